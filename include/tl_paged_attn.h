@@ -641,6 +641,221 @@ tl_status tl_paged_attn_decode_multi_int8(const void* q, const int8_t* k_codes,
                                           void* workspace, size_t workspace_bytes,
                                           uint32_t* error_word, void* stream);
 
+/* ---- Long contexts: what a decode step reads ------------------------------
+ * Two ways to read less than a sequence's whole history.  The pages that the
+ * other calls follow name neither, so their definitions stand here in full.
+ *
+ * Page selection keeps the cache whole and lets each step's query choose the
+ * pages it reads: tl_kv_page_bounds after the step's cache write,
+ * tl_kv_page_select for the query, tl_paged_attn_decode_pages over the pages
+ * selected.  Eviction makes the cache smaller for good: decode steps through
+ * tl_paged_attn_decode_mass gather each key's attention weight,
+ * tl_kv_evict_select picks the keys that stay and tl_kv_cache_compact moves
+ * them to the front of the sequence's pages.
+ */
+
+/*
+ * Bounds of the keys of pages.  For every page and KV head that a sequence's
+ * new keys touch (logical blocks first_new[b] / page_size ..
+ * (context_lens[b] - 1) / page_size), over the live keys j of the page (all of
+ * them, not the new ones alone), with K_j[e] the key's value (e4m3: the code's
+ * value; int8: code x its scale, one binary32 product):
+ *     M[e] = max_j K_j[e],  m[e] = min_j K_j[e]            e = 0..d-1
+ *     s = max_e max(|M[e]|, |m[e]|) / 127
+ *     bounds[page][g][0][e] = round-half-even(M[e] / s), clamped to +-127
+ *     bounds[page][g][1][e] = round-half-even(m[e] / s), clamped to +-127
+ *     bound_scales[page][g] = s
+ * with both divisions in binary32; s = 0 gives codes 0.  A non-finite key
+ * value counts as 0 and sets TL_DEVERR_VALUE_RANGE.  Bounds of other pages are
+ * left as they were.  A decode step passes first_new[b] = the length before
+ * the step (one page of each sequence is read again); first_new NULL, or 0,
+ * takes every page of the sequence.  A sequence with context_lens[b] <=
+ * first_new[b] is skipped; one longer than its table sets
+ * TL_DEVERR_CONTEXT_RANGE and is skipped.  A page that two sequences share is
+ * written by both (the same values where both see the same live keys of it).
+ *   k_cache       [num_pages][page_size][h_kv][d] in `dtype` (TL_BF16, TL_F32
+ *                 or TL_FP8_E4M3); tl_kv_page_bounds_int8: int8 codes and
+ *                 scales as tl_kv_cache_write_int8 writes them
+ *   first_new     [B] int32, or NULL
+ *   context_lens  [B] int32, the new keys included
+ *   bounds        [num_pages][h_kv][2][d] int8, in place
+ *   bound_scales  [num_pages][h_kv] float32, in place
+ * Supported: d in {64, 128}, page_size in [1, 256], num_pages*page_size <
+ * 2^31, B*max_pages_per_seq < 2^31.  Otherwise TL_ERR_UNSUPPORTED.
+ */
+tl_status tl_kv_page_bounds(const void* k_cache, const int32_t* block_table,
+                            int32_t max_pages_per_seq, const int32_t* first_new,
+                            const int32_t* context_lens, int8_t* bounds, float* bound_scales,
+                            int32_t B, int32_t h_kv, int32_t d, int32_t num_pages,
+                            int32_t page_size, tl_dtype dtype, uint32_t* error_word,
+                            void* stream);
+tl_status tl_kv_page_bounds_int8(const int8_t* k_codes, const float* k_scales,
+                                 const int32_t* block_table, int32_t max_pages_per_seq,
+                                 const int32_t* first_new, const int32_t* context_lens,
+                                 int8_t* bounds, float* bound_scales, int32_t B, int32_t h_kv,
+                                 int32_t d, int32_t num_pages, int32_t page_size,
+                                 uint32_t* error_word, void* stream);
+
+/* Bytes of workspace tl_kv_page_select needs (one float32 per sequence, KV
+ * head and table entry); 0 for invalid sizes. */
+size_t tl_kv_page_select_workspace_size(int32_t B, int32_t h_kv, int32_t max_pages_per_seq);
+
+/*
+ * The n_select pages of each sequence and KV head that a decode query is to
+ * read.  With nb = ceil(context_lens[b] / page_size) blocks, the score of
+ * block i for KV head g is
+ *     t_h = max_e |q[b][h][e]| / 127,  a_h[e] = round-half-even(q[b][h][e] / t_h)
+ *     I_h = sum_e a_h[e] x (a_h[e] >= 0 ? max code : min code of channel e)
+ *     score = max over the heads h of g of (float(I_h) x bound scale) x t_h
+ * (codes clamped to +-127, all in binary32, I_h exact: every implementation
+ * gives the same bits): the largest score a key of the page could have, in
+ * int8.  Blocks i < keep_first and i >= nb - keep_last are selected whatever
+ * their score, then the largest scores, equal ones by the lowest i.  With nb
+ * <= n_select every block is.  A non-finite query value counts as 0 and sets
+ * TL_DEVERR_VALUE_RANGE; a table entry outside the pool sets
+ * TL_DEVERR_PAGE_RANGE and scores lowest.
+ *   q             [B][h_q][d] in q_dtype (TL_BF16 or TL_F32)
+ *   bounds, bound_scales  as tl_kv_page_bounds writes them (read only)
+ *   page_table    [B][h_kv][n_select] int32: the selected blocks' block-table
+ *                 entries in ascending block order, then -1
+ *   page_lens     [B] int32: the keys they hold (the last block, always
+ *                 selected, may be part full); 0 for a sequence of length <= 0
+ *                 or longer than its table (TL_DEVERR_CONTEXT_RANGE)
+ *   keep_last     at least 1; keep_first + keep_last <= n_select
+ *   workspace     tl_kv_page_select_workspace_size bytes, 256-byte aligned;
+ *                 calls that overlap in time must not share one
+ * Supported: d in {64, 128}, h_q % h_kv == 0 with h_q/h_kv <= 16, page_size in
+ * [1, 256], B <= 65535.  Otherwise TL_ERR_UNSUPPORTED.
+ */
+tl_status tl_kv_page_select(const void* q, tl_dtype q_dtype, const int8_t* bounds,
+                            const float* bound_scales, const int32_t* block_table,
+                            int32_t max_pages_per_seq, const int32_t* context_lens,
+                            int32_t n_select, int32_t keep_first, int32_t keep_last,
+                            int32_t* page_table, int32_t* page_lens, int32_t B, int32_t h_q,
+                            int32_t h_kv, int32_t d, int32_t num_pages, int32_t page_size,
+                            void* workspace, size_t workspace_bytes, uint32_t* error_word,
+                            void* stream);
+
+/*
+ * tl_paged_attn_decode over a table per KV head: query head h of sequence b
+ * attends the keys at places 0 .. page_lens[b] - 1 of the pages
+ * page_table[b][g][0 ..], g = h / (h_q/h_kv), page_size keys a page.  What
+ * tl_kv_page_select writes; any table of the form works.  There is no window
+ * (places are not positions).  The workspace is tl_paged_attn_decode's; the
+ * other arguments, support and errors too (page_lens[b] past n_pages_per_head
+ * * page_size sets TL_DEVERR_CONTEXT_RANGE, output 0).
+ *   page_table  [B][h_kv][n_pages_per_head] int32
+ *   page_lens   [B] int32
+ */
+tl_status tl_paged_attn_decode_pages(const void* q, const void* k_cache, const void* v_cache,
+                                     const int32_t* page_table, int32_t n_pages_per_head,
+                                     const int32_t* page_lens, float* out, int32_t B,
+                                     int32_t h_q, int32_t h_kv, int32_t d, int32_t num_pages,
+                                     int32_t page_size, float scale, tl_dtype dtype,
+                                     void* workspace, size_t workspace_bytes,
+                                     uint32_t* error_word, void* stream);
+tl_status tl_paged_attn_decode_pages_int8(const void* q, const int8_t* k_codes,
+                                          const int8_t* v_codes, const float* k_scales,
+                                          const float* v_scales, const int32_t* page_table,
+                                          int32_t n_pages_per_head, const int32_t* page_lens,
+                                          float* out, int32_t B, int32_t h_q, int32_t h_kv,
+                                          int32_t d, int32_t num_pages, int32_t page_size,
+                                          float scale, void* workspace, size_t workspace_bytes,
+                                          uint32_t* error_word, void* stream);
+
+/*
+ * tl_paged_attn_decode_multi (q_len 1 .. 16 / (h_q/h_kv) tokens; q_len 1 is a
+ * decode step) that also adds every key's attention weight to a mass:
+ *     mass[b][g][j] += sum over tokens t and the query heads h of KV head g of
+ *                      softmax(s_th)_j
+ * for each position j that a token sees; other entries are not touched.  The
+ * additions have a fixed order: the result repeats bit for bit.
+ *   q             [B][q_len][h_q][d];  out [B][q_len][h_q][d] float32
+ *   mass          [B][h_kv][mass_len] float32, in place.  A sequence longer
+ *                 than mass_len (or its table) sets TL_DEVERR_CONTEXT_RANGE:
+ *                 output 0, mass as it was.  Two calls that overlap in time
+ *                 must not share a mass (or a workspace).
+ *   workspace     tl_paged_attn_decode_mass_workspace_size bytes (0: invalid
+ *                 sizes): the decode's, and one float32 per query head, token
+ *                 and mass place for the scores
+ *   other arguments, support (f32 pools with q_len 1) and errors as
+ *   tl_paged_attn_decode_multi / _int8.
+ */
+size_t tl_paged_attn_decode_mass_workspace_size(int32_t B, int32_t q_len, int32_t h_q,
+                                                int32_t h_kv, int32_t d, int32_t mass_len);
+tl_status tl_paged_attn_decode_mass(const void* q, const void* k_cache, const void* v_cache,
+                                    const int32_t* block_table, int32_t max_pages_per_seq,
+                                    const int32_t* context_lens, float* out, float* mass,
+                                    int32_t mass_len, int32_t B, int32_t q_len, int32_t h_q,
+                                    int32_t h_kv, int32_t d, int32_t num_pages,
+                                    int32_t page_size, int32_t window, float scale,
+                                    tl_dtype dtype, void* workspace, size_t workspace_bytes,
+                                    uint32_t* error_word, void* stream);
+tl_status tl_paged_attn_decode_mass_int8(const void* q, const int8_t* k_codes,
+                                         const int8_t* v_codes, const float* k_scales,
+                                         const float* v_scales, const int32_t* block_table,
+                                         int32_t max_pages_per_seq, const int32_t* context_lens,
+                                         float* out, float* mass, int32_t mass_len, int32_t B,
+                                         int32_t q_len, int32_t h_q, int32_t h_kv, int32_t d,
+                                         int32_t num_pages, int32_t page_size, int32_t window,
+                                         float scale, void* workspace, size_t workspace_bytes,
+                                         uint32_t* error_word, void* stream);
+
+/*
+ * The keys of each sequence and KV head that stay when its cache is cut to
+ * n_keep: with L = context_lens[b], positions j < keep_first and j >= L -
+ * keep_last, then the largest mass[b][g][j], equal ones by the lowest j (NaN
+ * below everything).  With L <= n_keep every position stays.
+ *   mass      [B][h_kv][mass_len] float32 (read only); a sequence longer than
+ *             mass_len sets TL_DEVERR_CONTEXT_RANGE and counts as empty
+ *   keep      [B][h_kv][n_keep] int32: the positions in ascending order, then -1
+ *   new_lens  [B] int32: min(L, n_keep), 0 for L <= 0
+ *   keep_first + keep_last <= n_keep
+ */
+tl_status tl_kv_evict_select(const float* mass, int32_t mass_len, const int32_t* context_lens,
+                             int32_t n_keep, int32_t keep_first, int32_t keep_last,
+                             int32_t* keep, int32_t* new_lens, int32_t B, int32_t h_kv,
+                             uint32_t* error_word, void* stream);
+
+/*
+ * The kept keys' rows moved, in place, to the front of their sequence's pages:
+ * for every j < new_lens[b] and KV head g,
+ *     K and V row of position j = those of position keep[b][g][j] before the call
+ * (int8 pools: and their scales), and with a mass,
+ *     mass[b][g][j] = mass[b][g][keep[b][g][j]],  mass[b][g][j'] = 0 for
+ *     new_lens[b] <= j' < context_lens[b].
+ * Rows at new_lens[b] and behind stay as they were; the block-table entries
+ * past the new length are the caller's to free, and the caller's context
+ * length becomes new_lens[b].  The heads of a position then hold different
+ * tokens' rows: a window over positions no longer means a window over tokens.
+ * Needs j <= keep[b][g][j] < context_lens[b], as tl_kv_evict_select gives; an
+ * entry outside that is skipped and sets TL_DEVERR_CONTEXT_RANGE.  A new_lens
+ * entry outside [0, min(n_keep, context_lens[b])], or a length past the table
+ * (or mass_len), sets the same bit and leaves the sequence as it was.  The
+ * pages below the length belong to the sequence alone: a page shared with
+ * another one is a caller error (its rows would move under the other).
+ *   k_cache, v_cache  [num_pages][page_size][h_kv][d] in `dtype` (TL_BF16,
+ *                     TL_F32 or TL_FP8_E4M3; _int8: codes and scales), in place
+ *   keep              [B][h_kv][n_keep] int32;  new_lens [B] int32
+ *   mass              NULL, or [B][h_kv][mass_len] float32, in place
+ * TL_ERR_INVALID_ARG when d * elem is not a multiple of 16 bytes;
+ * TL_ERR_UNSUPPORTED past 4,096 bytes a row, page_size > 256 or
+ * num_pages*page_size >= 2^31.
+ */
+tl_status tl_kv_cache_compact(void* k_cache, void* v_cache, const int32_t* block_table,
+                              int32_t max_pages_per_seq, const int32_t* context_lens,
+                              const int32_t* keep, int32_t n_keep, const int32_t* new_lens,
+                              float* mass, int32_t mass_len, int32_t B, int32_t h_kv, int32_t d,
+                              int32_t num_pages, int32_t page_size, tl_dtype dtype,
+                              uint32_t* error_word, void* stream);
+tl_status tl_kv_cache_compact_int8(int8_t* k_codes, int8_t* v_codes, float* k_scales,
+                                   float* v_scales, const int32_t* block_table,
+                                   int32_t max_pages_per_seq, const int32_t* context_lens,
+                                   const int32_t* keep, int32_t n_keep, const int32_t* new_lens,
+                                   float* mass, int32_t mass_len, int32_t B, int32_t h_kv,
+                                   int32_t d, int32_t num_pages, int32_t page_size,
+                                   uint32_t* error_word, void* stream);
+
 #ifdef __cplusplus
 }
 #endif

@@ -22,6 +22,11 @@ from .api import (TL_BF16, TL_FP8_E4M3, tl_kv_cache_write_fp8, TL_DEVERR_CONTEXT
                   tl_paged_attn_decode_multi_workspace_size,
                   tl_paged_attn_prefill_workspace_size_ex,
                   tl_paged_attn_prefill_workspace_size_keys,
+                  tl_kv_page_bounds, tl_kv_page_bounds_int8, tl_kv_page_select,
+                  tl_kv_page_select_workspace_size, tl_paged_attn_decode_pages,
+                  tl_paged_attn_decode_pages_int8, tl_paged_attn_decode_mass,
+                  tl_paged_attn_decode_mass_int8, tl_paged_attn_decode_mass_workspace_size,
+                  tl_kv_evict_select, tl_kv_cache_compact, tl_kv_cache_compact_int8,
                   tl_version)
 from . import build as _build_module
 

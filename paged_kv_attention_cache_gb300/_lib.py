@@ -70,6 +70,30 @@ SIGNATURES = {
                                         ctypes.c_int),
     "tl_paged_attn_prefill_int8": ([vp, vp, vp, vp, vp, vp, i32, vp, vp, i32, i32, i32, i32, i32,
                                     i32, i32, i32, f32, vp, sz, u32p, vp], ctypes.c_int),
+    "tl_kv_page_bounds": ([vp, vp, i32, vp, vp, vp, vp, i32, i32, i32, i32, i32, ctypes.c_int,
+                           u32p, vp], ctypes.c_int),
+    "tl_kv_page_bounds_int8": ([vp, vp, vp, i32, vp, vp, vp, vp, i32, i32, i32, i32, i32, u32p,
+                                vp], ctypes.c_int),
+    "tl_kv_page_select_workspace_size": ([i32, i32, i32], sz),
+    "tl_kv_page_select": ([vp, ctypes.c_int, vp, vp, vp, i32, vp, i32, i32, i32, vp, vp, i32, i32,
+                           i32, i32, i32, i32, vp, sz, u32p, vp], ctypes.c_int),
+    "tl_paged_attn_decode_pages": ([vp, vp, vp, vp, i32, vp, vp, i32, i32, i32, i32, i32, i32,
+                                    f32, ctypes.c_int, vp, sz, u32p, vp], ctypes.c_int),
+    "tl_paged_attn_decode_pages_int8": ([vp, vp, vp, vp, vp, vp, i32, vp, vp, i32, i32, i32, i32,
+                                         i32, i32, f32, vp, sz, u32p, vp], ctypes.c_int),
+    "tl_paged_attn_decode_mass_workspace_size": ([i32, i32, i32, i32, i32, i32], sz),
+    "tl_paged_attn_decode_mass": ([vp, vp, vp, vp, i32, vp, vp, vp, i32, i32, i32, i32, i32, i32,
+                                   i32, i32, i32, f32, ctypes.c_int, vp, sz, u32p, vp],
+                                  ctypes.c_int),
+    "tl_paged_attn_decode_mass_int8": ([vp, vp, vp, vp, vp, vp, i32, vp, vp, vp, i32, i32, i32,
+                                        i32, i32, i32, i32, i32, i32, f32, vp, sz, u32p, vp],
+                                       ctypes.c_int),
+    "tl_kv_evict_select": ([vp, i32, vp, i32, i32, i32, vp, vp, i32, i32, u32p, vp],
+                           ctypes.c_int),
+    "tl_kv_cache_compact": ([vp, vp, vp, i32, vp, vp, i32, vp, vp, i32, i32, i32, i32, i32, i32,
+                             ctypes.c_int, u32p, vp], ctypes.c_int),
+    "tl_kv_cache_compact_int8": ([vp, vp, vp, vp, vp, i32, vp, vp, i32, vp, vp, i32, i32, i32,
+                                  i32, i32, i32, u32p, vp], ctypes.c_int),
     "tl_paged_attn_prefill_ring": ([vp, vp, vp, vp, i32, vp, vp, i32, i32, i32, i32, i32, i32,
                                     i32, i32, i32, f32, ctypes.c_int, vp, sz, u32p, vp],
                                    ctypes.c_int),

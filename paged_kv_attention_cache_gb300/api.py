@@ -627,3 +627,279 @@ def tl_paged_attn_decode_multi_int8(q: torch.Tensor, k_codes: torch.Tensor,
          int(window), float(scale), _ptr(workspace), _ws_bytes(workspace),
          _err_word(error_word, dev))
     return out
+
+
+# ------------------------------------------ long contexts: page selection --
+
+def _need_bounds(bounds, bound_scales, device, num_pages=None, hkv=None, d=None):
+    """bounds [num_pages, H_kv, 2, d] int8 and bound_scales [num_pages, H_kv] float32."""
+    _need(bounds, "bounds", torch.int8, (num_pages, hkv, 2, d), device)
+    _need(bound_scales, "bound_scales", torch.float32, tuple(bounds.shape[:2]), device)
+
+
+def _need_first_new(first_new, B, device):
+    if first_new is not None:
+        _need(first_new, "first_new", torch.int32, (B,), device)
+    return _ptr(first_new)
+
+
+def tl_kv_page_bounds(k_cache: torch.Tensor, block_table: torch.Tensor,
+                      context_lens: torch.Tensor, bounds: torch.Tensor,
+                      bound_scales: torch.Tensor, first_new: Optional[torch.Tensor] = None,
+                      error_word: Optional[torch.Tensor] = None, stream=None) -> None:
+    """In place: each channel's largest and smallest key (bounds [num_pages,
+    H_kv, 2, d] int8 codes, bound_scales [num_pages, H_kv] float32) of every
+    page that holds a key at first_new[b] (default 0) or behind."""
+    dev = k_cache.device
+    _need(k_cache, "k_cache", None, (None, None, None, None), dev)
+    P, ps, hkv, d = k_cache.shape
+    _need_bounds(bounds, bound_scales, dev, P, hkv, d)
+    _need(context_lens, "context_lens", torch.int32, (None,), dev)
+    B = context_lens.shape[0]
+    _need_table(block_table, context_lens, B, dev)
+    _run("tl_kv_page_bounds", dev, stream,
+         _ptr(k_cache), _ptr(block_table), block_table.shape[1], _need_first_new(first_new, B, dev),
+         _ptr(context_lens), _ptr(bounds), _ptr(bound_scales), B, hkv, d, P, ps,
+         _DTYPES.get(k_cache.dtype, -1), _err_word(error_word, dev))
+
+
+def tl_kv_page_bounds_int8(k_codes: torch.Tensor, k_scales: torch.Tensor,
+                           block_table: torch.Tensor, context_lens: torch.Tensor,
+                           bounds: torch.Tensor, bound_scales: torch.Tensor,
+                           first_new: Optional[torch.Tensor] = None,
+                           error_word: Optional[torch.Tensor] = None, stream=None) -> None:
+    """tl_kv_page_bounds of an int8 pool (a key's value is code x its scale)."""
+    dev = k_codes.device
+    _need(k_codes, "k_codes", torch.int8, (None, None, None, None), dev)
+    P, ps, hkv, d = k_codes.shape
+    _need(k_scales, "k_scales", torch.float32, (P, hkv, ps), dev)
+    _need_bounds(bounds, bound_scales, dev, P, hkv, d)
+    _need(context_lens, "context_lens", torch.int32, (None,), dev)
+    B = context_lens.shape[0]
+    _need_table(block_table, context_lens, B, dev)
+    _run("tl_kv_page_bounds_int8", dev, stream,
+         _ptr(k_codes), _ptr(k_scales), _ptr(block_table), block_table.shape[1],
+         _need_first_new(first_new, B, dev), _ptr(context_lens), _ptr(bounds), _ptr(bound_scales),
+         B, hkv, d, P, ps, _err_word(error_word, dev))
+
+
+@functools.lru_cache(maxsize=1024)
+def tl_kv_page_select_workspace_size(B: int, h_kv: int, max_pages_per_seq: int) -> int:
+    return int(_lib.load().tl_kv_page_select_workspace_size(B, h_kv, max_pages_per_seq))
+
+
+def _int_out(t, name, shape, device):
+    if t is None:
+        return torch.empty(shape, dtype=torch.int32, device=device)
+    _need(t, name, torch.int32, shape, device)
+    return t
+
+
+def tl_kv_page_select(q: torch.Tensor, bounds: torch.Tensor, bound_scales: torch.Tensor,
+                      block_table: torch.Tensor, context_lens: torch.Tensor, page_size: int,
+                      n_select: int, keep_first: int = 0, keep_last: int = 1,
+                      page_table: Optional[torch.Tensor] = None,
+                      page_lens: Optional[torch.Tensor] = None,
+                      workspace: Optional[torch.Tensor] = None,
+                      error_word: Optional[torch.Tensor] = None, stream=None):
+    """(page_table [B, H_kv, n_select], page_lens [B]) int32: the pages whose
+    bounds let a key score highest against q [B, H_q, d] (bf16 or f32), for
+    tl_paged_attn_decode_pages; the first keep_first and the last keep_last
+    blocks always among them."""
+    dev = q.device
+    _need(q, "q", None, (None, None, None), dev)
+    B, hq, d = q.shape
+    _need_bounds(bounds, bound_scales, dev, None, None, d)
+    P, hkv = bounds.shape[:2]
+    _need_table(block_table, context_lens, B, dev)
+    n = int(n_select)
+    page_table = _int_out(page_table, "page_table", (B, hkv, n), dev)
+    page_lens = _int_out(page_lens, "page_lens", (B,), dev)
+    width = block_table.shape[1]
+    workspace = _workspace(workspace, tl_kv_page_select_workspace_size(B, hkv, width), dev)
+    _run("tl_kv_page_select", dev, stream,
+         _ptr(q), _DTYPES.get(q.dtype, -1), _ptr(bounds), _ptr(bound_scales), _ptr(block_table),
+         width, _ptr(context_lens), n, int(keep_first), int(keep_last), _ptr(page_table),
+         _ptr(page_lens), B, hq, hkv, d, P, int(page_size), _ptr(workspace), _ws_bytes(workspace),
+         _err_word(error_word, dev))
+    return page_table, page_lens
+
+
+def _need_page_table(page_table, page_lens, B, hkv, device):
+    _need(page_table, "page_table", torch.int32, (B, hkv, None), device)
+    if page_table.shape[2] < 1:
+        raise ValueError("page_table needs at least one column")
+    _need(page_lens, "page_lens", torch.int32, (B,), device)
+
+
+def tl_paged_attn_decode_pages(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tensor,
+                               page_table: torch.Tensor, page_lens: torch.Tensor, scale: float,
+                               out: Optional[torch.Tensor] = None,
+                               workspace: Optional[torch.Tensor] = None,
+                               error_word: Optional[torch.Tensor] = None,
+                               stream=None) -> torch.Tensor:
+    """out[B, H_q, d] (float32): one query per sequence over the page_lens[b]
+    keys of the pages page_table[b, g] (a row per KV head)."""
+    dev = q.device
+    P, ps, hkv, d = _need_pools(k_cache, v_cache, dev)
+    _need(q, "q", _query_dtype(k_cache.dtype), (None, None, d), dev)
+    B, hq, _ = q.shape
+    _need_page_table(page_table, page_lens, B, hkv, dev)
+    out = _decode_out(out, (B, hq, d), dev)
+    workspace = _workspace(workspace, tl_paged_attn_decode_workspace_size(B, hq, hkv, d), dev)
+    _run("tl_paged_attn_decode_pages", dev, stream,
+         _ptr(q), _ptr(k_cache), _ptr(v_cache), _ptr(page_table), page_table.shape[2],
+         _ptr(page_lens), _ptr(out), B, hq, hkv, d, P, ps, float(scale),
+         _DTYPES.get(k_cache.dtype, -1), _ptr(workspace), _ws_bytes(workspace),
+         _err_word(error_word, dev))
+    return out
+
+
+def tl_paged_attn_decode_pages_int8(q: torch.Tensor, k_codes: torch.Tensor,
+                                    v_codes: torch.Tensor, k_scales: torch.Tensor,
+                                    v_scales: torch.Tensor, page_table: torch.Tensor,
+                                    page_lens: torch.Tensor, scale: float,
+                                    out: Optional[torch.Tensor] = None,
+                                    workspace: Optional[torch.Tensor] = None,
+                                    error_word: Optional[torch.Tensor] = None,
+                                    stream=None) -> torch.Tensor:
+    """tl_paged_attn_decode_pages over int8 pools (bf16 q)."""
+    dev = q.device
+    P, ps, hkv, d = _need_int8_pools(k_codes, v_codes, k_scales, v_scales, dev)
+    _need(q, "q", torch.bfloat16, (None, None, d), dev)
+    B, hq, _ = q.shape
+    _need_page_table(page_table, page_lens, B, hkv, dev)
+    out = _decode_out(out, (B, hq, d), dev)
+    workspace = _workspace(workspace, tl_paged_attn_decode_workspace_size(B, hq, hkv, d), dev)
+    _run("tl_paged_attn_decode_pages_int8", dev, stream,
+         _ptr(q), _ptr(k_codes), _ptr(v_codes), _ptr(k_scales), _ptr(v_scales), _ptr(page_table),
+         page_table.shape[2], _ptr(page_lens), _ptr(out), B, hq, hkv, d, P, ps, float(scale),
+         _ptr(workspace), _ws_bytes(workspace), _err_word(error_word, dev))
+    return out
+
+
+# ------------------------------------------------ long contexts: eviction --
+
+@functools.lru_cache(maxsize=1024)
+def tl_paged_attn_decode_mass_workspace_size(B: int, q_len: int, h_q: int, h_kv: int, d: int,
+                                             mass_len: int) -> int:
+    return int(_lib.load().tl_paged_attn_decode_mass_workspace_size(B, q_len, h_q, h_kv, d,
+                                                                    mass_len))
+
+
+def tl_paged_attn_decode_mass(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tensor,
+                              block_table: torch.Tensor, context_lens: torch.Tensor,
+                              mass: torch.Tensor, scale: float, window: int = 0,
+                              out: Optional[torch.Tensor] = None,
+                              workspace: Optional[torch.Tensor] = None,
+                              error_word: Optional[torch.Tensor] = None,
+                              stream=None) -> torch.Tensor:
+    """tl_paged_attn_decode_multi (q [B, q_len, H_q, d]) that adds every key's
+    softmax probabilities to mass [B, H_kv, mass_len] (float32, in place)."""
+    dev, P, ps, hkv, d = _decode_args(q, k_cache, v_cache, block_table, context_lens,
+                                      q_tokens=True)
+    B, q_len, hq, _ = q.shape
+    _need(mass, "mass", torch.float32, (B, hkv, None), dev)
+    out = _decode_out(out, (B, q_len, hq, d), dev)
+    n = mass.shape[2]
+    workspace = _workspace(
+        workspace, tl_paged_attn_decode_mass_workspace_size(B, q_len, hq, hkv, d, n), dev)
+    _run("tl_paged_attn_decode_mass", dev, stream,
+         _ptr(q), _ptr(k_cache), _ptr(v_cache), _ptr(block_table), block_table.shape[1],
+         _ptr(context_lens), _ptr(out), _ptr(mass), n, B, q_len, hq, hkv, d, P, ps, int(window),
+         float(scale), _DTYPES.get(k_cache.dtype, -1), _ptr(workspace), _ws_bytes(workspace),
+         _err_word(error_word, dev))
+    return out
+
+
+def tl_paged_attn_decode_mass_int8(q: torch.Tensor, k_codes: torch.Tensor,
+                                   v_codes: torch.Tensor, k_scales: torch.Tensor,
+                                   v_scales: torch.Tensor, block_table: torch.Tensor,
+                                   context_lens: torch.Tensor, mass: torch.Tensor, scale: float,
+                                   window: int = 0, out: Optional[torch.Tensor] = None,
+                                   workspace: Optional[torch.Tensor] = None,
+                                   error_word: Optional[torch.Tensor] = None,
+                                   stream=None) -> torch.Tensor:
+    """tl_paged_attn_decode_mass over int8 pools (bf16 q [B, q_len, H_q, d])."""
+    dev = q.device
+    P, ps, hkv, d = _need_int8_pools(k_codes, v_codes, k_scales, v_scales, dev)
+    _need(q, "q", torch.bfloat16, (None, None, None, d), dev)
+    B, q_len, hq, _ = q.shape
+    _need_table(block_table, context_lens, B, dev)
+    _need(mass, "mass", torch.float32, (B, hkv, None), dev)
+    out = _decode_out(out, (B, q_len, hq, d), dev)
+    n = mass.shape[2]
+    workspace = _workspace(
+        workspace, tl_paged_attn_decode_mass_workspace_size(B, q_len, hq, hkv, d, n), dev)
+    _run("tl_paged_attn_decode_mass_int8", dev, stream,
+         _ptr(q), _ptr(k_codes), _ptr(v_codes), _ptr(k_scales), _ptr(v_scales), _ptr(block_table),
+         block_table.shape[1], _ptr(context_lens), _ptr(out), _ptr(mass), n, B, q_len, hq, hkv, d,
+         P, ps, int(window), float(scale), _ptr(workspace), _ws_bytes(workspace),
+         _err_word(error_word, dev))
+    return out
+
+
+def tl_kv_evict_select(mass: torch.Tensor, context_lens: torch.Tensor, n_keep: int,
+                       keep_first: int = 0, keep_last: int = 0,
+                       keep: Optional[torch.Tensor] = None,
+                       new_lens: Optional[torch.Tensor] = None,
+                       error_word: Optional[torch.Tensor] = None, stream=None):
+    """(keep [B, H_kv, n_keep], new_lens [B]) int32: the positions of largest
+    mass [B, H_kv, mass_len] (float32), ascending, the first keep_first and
+    the last keep_last of each sequence always among them."""
+    dev = mass.device
+    _need(mass, "mass", torch.float32, (None, None, None), dev)
+    B, hkv, n = mass.shape
+    _need(context_lens, "context_lens", torch.int32, (B,), dev)
+    keep = _int_out(keep, "keep", (B, hkv, int(n_keep)), dev)
+    new_lens = _int_out(new_lens, "new_lens", (B,), dev)
+    _run("tl_kv_evict_select", dev, stream,
+         _ptr(mass), n, _ptr(context_lens), int(n_keep), int(keep_first), int(keep_last),
+         _ptr(keep), _ptr(new_lens), B, hkv, _err_word(error_word, dev))
+    return keep, new_lens
+
+
+def _need_keep(keep, new_lens, mass, B, hkv, device):
+    _need(keep, "keep", torch.int32, (B, hkv, None), device)
+    _need(new_lens, "new_lens", torch.int32, (B,), device)
+    if mass is None:
+        return None, 0
+    _need(mass, "mass", torch.float32, (B, hkv, None), device)
+    return _ptr(mass), mass.shape[2]
+
+
+def tl_kv_cache_compact(k_cache: torch.Tensor, v_cache: torch.Tensor, block_table: torch.Tensor,
+                        context_lens: torch.Tensor, keep: torch.Tensor, new_lens: torch.Tensor,
+                        mass: Optional[torch.Tensor] = None,
+                        error_word: Optional[torch.Tensor] = None, stream=None) -> None:
+    """In place: row j < new_lens[b] of each KV head becomes the row of
+    position keep[b, g, j], in K, V and (when given) mass."""
+    dev = k_cache.device
+    P, ps, hkv, d = _need_pools(k_cache, v_cache, dev)
+    _need(context_lens, "context_lens", torch.int32, (None,), dev)
+    B = context_lens.shape[0]
+    _need_table(block_table, context_lens, B, dev)
+    mass_ptr, mass_len = _need_keep(keep, new_lens, mass, B, hkv, dev)
+    _run("tl_kv_cache_compact", dev, stream,
+         _ptr(k_cache), _ptr(v_cache), _ptr(block_table), block_table.shape[1],
+         _ptr(context_lens), _ptr(keep), keep.shape[2], _ptr(new_lens), mass_ptr, mass_len, B,
+         hkv, d, P, ps, _DTYPES.get(k_cache.dtype, -1), _err_word(error_word, dev))
+
+
+def tl_kv_cache_compact_int8(k_codes: torch.Tensor, v_codes: torch.Tensor,
+                             k_scales: torch.Tensor, v_scales: torch.Tensor,
+                             block_table: torch.Tensor, context_lens: torch.Tensor,
+                             keep: torch.Tensor, new_lens: torch.Tensor,
+                             mass: Optional[torch.Tensor] = None,
+                             error_word: Optional[torch.Tensor] = None, stream=None) -> None:
+    """tl_kv_cache_compact over int8 pools: the rows' scales move with them."""
+    dev = k_codes.device
+    P, ps, hkv, d = _need_int8_pools(k_codes, v_codes, k_scales, v_scales, dev)
+    _need(context_lens, "context_lens", torch.int32, (None,), dev)
+    B = context_lens.shape[0]
+    _need_table(block_table, context_lens, B, dev)
+    mass_ptr, mass_len = _need_keep(keep, new_lens, mass, B, hkv, dev)
+    _run("tl_kv_cache_compact_int8", dev, stream,
+         _ptr(k_codes), _ptr(v_codes), _ptr(k_scales), _ptr(v_scales), _ptr(block_table),
+         block_table.shape[1], _ptr(context_lens), _ptr(keep), keep.shape[2], _ptr(new_lens),
+         mass_ptr, mass_len, B, hkv, d, P, ps, _err_word(error_word, dev))
