@@ -20,8 +20,10 @@ struct EvictParams {
   uint32_t* error_word;
 };
 
-__global__ void __launch_bounds__(kSelMaxThreads) evict_select_kernel(EvictParams P, int csize) {
+template <int T>
+__global__ void __launch_bounds__(T) evict_select_kernel(EvictParams P, int csize, int key_cap) {
   __shared__ SelectShared sh;
+  extern __shared__ __align__(16) uint32_t sel_keys[];
   const int row = blockIdx.x / csize, rank = blockIdx.x % csize;
   const int b = row / P.h_kv;
   const int L = P.context_lens[b];
@@ -32,8 +34,8 @@ __global__ void __launch_bounds__(kSelMaxThreads) evict_select_kernel(EvictParam
   }
   const float* x = P.mass + (size_t)row * P.mass_len;
   int32_t* to = P.keep + (size_t)row * P.n;
-  select_row(
-      sh, len, P.n, P.first, P.last, rank, csize, [&](int i) { return __ldg(x + i); },
+  select_row<T>(
+      sh, sel_keys, key_cap, x, len, P.n, P.first, P.last, rank, csize,
       [&](int pos, int i) { to[pos] = i; }, [&](int pos) { to[pos] = -1; });
 }
 
@@ -253,10 +255,12 @@ extern "C" tl_status tl_kv_evict_select(const float* mass, int32_t mass_len,
   P.error_word = error_word;
   const int64_t rows = (int64_t)B * h_kv;
   const SelectShape s = select_shape(rows, mass_len);
-  int csize = s.cluster;
-  void* args[] = {&P, &csize};
-  if (launch_rows(reinterpret_cast<const void*>(evict_select_kernel), rows, s, args, false,
-                  (cudaStream_t)stream) != cudaSuccess)
+  int csize = s.cluster, key_cap = s.keys;
+  void* args[] = {&P, &csize, &key_cap};
+  const void* const kernels[3] = {reinterpret_cast<const void*>(evict_select_kernel<256>),
+                                  reinterpret_cast<const void*>(evict_select_kernel<512>),
+                                  reinterpret_cast<const void*>(evict_select_kernel<1024>)};
+  if (launch_rows(kernels, rows, s, args, false, (cudaStream_t)stream) != cudaSuccess)
     return TL_ERR_CUDA;
   return launch_status();
 }

@@ -57,6 +57,28 @@ TL_DEVINLINE void widen_vec(const uint4& x, float scale, float* f) {
   }
 }
 
+// Four int8 codes as two fp16 pairs (codes 0, 1 and 2, 3), exact: a code c +
+// 128 as the low byte under the high byte 0x64 is the fp16 1024 + c + 128.
+// The biased form leaves the 1152 in.
+TL_DEVINLINE void i8x4_as_f16x2x2_biased(uint32_t w, uint32_t& lo, uint32_t& hi) {
+  const uint32_t u = w ^ 0x80808080u;
+  lo = __byte_perm(u, 0x64646464u, 0x4140u);
+  hi = __byte_perm(u, 0x64646464u, 0x4342u);
+}
+TL_DEVINLINE void i8x4_as_f16x2x2(uint32_t w, uint32_t& lo, uint32_t& hi) {
+  i8x4_as_f16x2x2_biased(w, lo, hi);
+  asm("sub.rn.f16x2 %0, %0, %1;\n" : "+r"(lo) : "r"(0x64806480u));
+  asm("sub.rn.f16x2 %0, %0, %1;\n" : "+r"(hi) : "r"(0x64806480u));
+}
+TL_DEVINLINE void mma_f16_16816(float* c, uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3,
+                                uint32_t b0, uint32_t b1) {
+  asm volatile(
+      "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, "
+      "{%8,%9}, {%0,%1,%2,%3};\n"
+      : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+
 // max / min that return NaN when either is
 TL_DEVINLINE float max_nan(float a, float b) {
   float r;
@@ -206,7 +228,7 @@ __global__ void __launch_bounds__(kBoundsThreads) page_bounds_kernel(BoundsParam
       sum += n[j];
     }
     uint32_t total;
-    uint32_t at = select_block_scan(sum, tmp, total);
+    uint32_t at = select_block_scan(sum, tmp, total);  // the loop's barriers free tmp
 #pragma unroll
     for (int j = 0; j < PER; ++j) {
       start[tid * PER + j] = (int)at;
@@ -247,124 +269,313 @@ struct ScoreParams {
   const float* scales;
   const int32_t* block_table;
   const int32_t* context_lens;
-  float* scores;  // [B][h_kv][max_pages_per_seq]
+  float* scores;  // [B][h_kv][row_stride]
+  int64_t row_stride;
   int32_t max_pages_per_seq, B, h_q, h_kv, group, num_pages, page_size;
   uint32_t* error_word;
 };
 
-constexpr int kScoreWarps = 8;
-constexpr int kScoreTile = 128;  // pages of a CTA
+// A row of scores starts on 16 bytes.
+inline int64_t score_stride(int max_pages_per_seq) { return ((int64_t)max_pages_per_seq + 3) / 4 * 4; }
 
+constexpr int kScoreWarps = 8;
+constexpr int kScoreUnit = 8;     // pages; a CTA takes a run of units
+constexpr int kScoreSeqs = 1024;  // sequences placed per round
+constexpr int kScoreStages = 3;   // at most
+
+// Heads a CTA scores (grid.y covers the others), and the warps that share one.
 __host__ __device__ inline int score_heads(int h_kv) { return h_kv < kScoreWarps ? h_kv : kScoreWarps; }
+
+// Shared memory of a stage: 32 pages per warp of a head, each page's codes of
+// the CTA's heads (one run of the bounds pool) and 16 bytes more, so that 32
+// lanes reading the same word of 32 pages fall on different banks.
+__host__ __device__ inline int score_page_bytes(int heads, int d) { return heads * 2 * d + 16; }
+__host__ __device__ inline int score_stage_bytes(int heads, int d) {
+  return 32 * (kScoreWarps / heads) * score_page_bytes(heads, d);
+}
+__host__ __device__ inline int score_query_bytes(int heads, int group, int d) {
+  return heads * group * d;
+}
 
 // Blocks a sequence has, or 0 when its length is past its table.
 TL_DEVINLINE int blocks_of(int L, int max_pages, int page_size) {
   return L <= 0 || (int64_t)L > (int64_t)max_pages * page_size ? 0 : (L - 1) / page_size + 1;
 }
 
-// Scores of a tile of a sequence's pages.  A CTA quantises the query rows of
-// its heads once; its warps each take one head and walk the tile's pages, D/16
-// lanes to a page (16 max codes and 16 min codes a lane), neighbouring warps
-// on neighbouring heads of the same page, whose codes are one run of memory.
-template <int D, int G, bool QF32>
-__global__ void __launch_bounds__(kScoreWarps * 32) page_score_kernel(ScoreParams P) {
-  constexpr int LP = D / 16, PW = 32 / LP, U = 4;  // lanes a page, pages a load, loads in flight
-  __shared__ __align__(16) int8_t q_codes[kScoreWarps * G][D];
-  __shared__ float q_scale[kScoreWarps * G];
-  const int b = blockIdx.z, lane = threadIdx.x & 31, w = threadIdx.x >> 5;
-  const int L = P.context_lens[b];
-  const int nb = blocks_of(L, P.max_pages_per_seq, P.page_size);
-  const int p0 = blockIdx.x * kScoreTile, p1 = min(p0 + kScoreTile, nb);
-  if (p0 >= p1) return;
+// Scores of every page of every sequence, one CTA per SM.  Each takes an even
+// share of the batch's pages as one run (a scan of the sequences' block
+// counts places it: the host knows no length), so it quantises a sequence's
+// query rows once or twice a call.  A page's codes of the CTA's heads are one
+// run of memory (2 KiB at 8 heads of 128) and arrive by one bulk copy into a
+// ring of stages; then a warp takes a KV head: 16 pages are the rows of an
+// m16n8k16, the group's query heads its columns, the sum over the channels of
+// max code x (q code >= 0) and min code x (q code < 0) its k steps.
+//
+// The arithmetic is exact.  A code c enters as the fp16 1152 + c (two byte
+// permutes for four codes; taking the 1152 out there would cost two more
+// operations) and its sum with the query's codes is taken out at the end.
+// Even and odd steps accumulate apart: at d = 128 each sum is at most 64
+// channels x 127 x 1279 = 10.4 million, a whole number below 2^24, exact in
+// f32 however it is added up.
+template <int D, int NT, bool QF32>
+__global__ void __launch_bounds__(kScoreWarps * 32, 1) page_score_kernel(ScoreParams P, int nst) {
+  extern __shared__ __align__(16) unsigned char score_sm[];
+  __shared__ int start[kScoreSeqs + 1];  // first unit of each sequence of the round
+  __shared__ uint32_t tmp[32];
+  constexpr int KS = D / 16;  // k steps of the max codes, and of the min codes
+  __shared__ float q_scale[kScoreWarps * 8 * NT];
+  __shared__ unsigned long long full[kScoreStages];
+  __shared__ int abort_flag;
+  const int tid = threadIdx.x, lane = tid & 31, w = tid >> 5;
   const int hs = score_heads(P.h_kv), g0 = blockIdx.y * hs, heads = min(hs, P.h_kv - g0);
-  // query rows: code = rint(q / t) clamped to +-127, t = max|q| / 127
-  for (int r = w; r < heads * P.group; r += kScoreWarps) {
-    const size_t row = ((size_t)b * P.h_q + (size_t)g0 * P.group + r) * D;
-    float x[D / 32], m = 0.f;
-    bool bad = false;
+  const int per_head = kScoreWarps / hs;
+  const int gi = w % hs, sub = w / hs;
+  const bool works = sub < per_head && gi < heads;  // computes
+  const bool issues = sub < per_head && gi == 0;    // copies 32 pages of a stage
+  const int page_bytes = score_page_bytes(hs, D), stage_bytes = score_stage_bytes(hs, D);
+  const int stage_pages = 32 * per_head;
+  const uint32_t copy_bytes = (uint32_t)heads * 2 * D;
+  unsigned char* q_codes = score_sm + nst * stage_bytes;
+  // the selection may take the SMs that this grid leaves (it waits for the
+  // grid's end before it reads a score)
+  asm volatile("griddepcontrol.launch_dependents;\n" ::: "memory");
+  if (tid == 0) {
+    abort_flag = 0;
+    for (int s = 0; s < nst; ++s) mbar_init(smem_u32(&full[s]), per_head);
+    fence_mbar_init();
+  }
+  uint32_t issued = 0, done = 0;  // stages
+  bool stop = false;
+  for (int base = 0; base < P.B && !stop; base += kScoreSeqs) {
+    constexpr int PER = kScoreSeqs / (kScoreWarps * 32);
+    uint32_t n[PER], sum = 0;
 #pragma unroll
-    for (int i = 0; i < D / 32; ++i) {
-      const size_t e = row + lane + 32 * i;
-      x[i] = QF32 ? __ldg(static_cast<const float*>(P.q) + e)
-                  : __uint_as_float((uint32_t)__ldg(static_cast<const unsigned short*>(P.q) + e) << 16);
-      if (!isfinite(x[i])) {  // counts as 0
-        bad = true;
-        x[i] = 0.f;
+    for (int j = 0; j < PER; ++j) {
+      const int b = base + tid * PER + j;
+      const int nb = b < P.B ? blocks_of(P.context_lens[b], P.max_pages_per_seq, P.page_size) : 0;
+      n[j] = (uint32_t)(nb + kScoreUnit - 1) / kScoreUnit;
+      sum += n[j];
+    }
+    uint32_t total;
+    __syncthreads();  // the previous round's start and tmp are read
+    uint32_t at = select_block_scan(sum, tmp, total);
+#pragma unroll
+    for (int j = 0; j < PER; ++j) {
+      start[tid * PER + j] = (int)at;
+      at += n[j];
+    }
+    if (tid == 0) start[kScoreSeqs] = (int)total;
+    __syncthreads();
+    int u = (int)((int64_t)total * blockIdx.x / gridDim.x);
+    const int u1 = (int)((int64_t)total * (blockIdx.x + 1) / gridDim.x);
+    while (u < u1 && !stop) {
+      int lo = 0, hi = kScoreSeqs;  // the last sequence that starts at or before u
+      while (hi - lo > 1) {
+        const int mid = (lo + hi) >> 1;
+        if (start[mid] <= u) lo = mid;
+        else hi = mid;
       }
-      m = fmaxf(m, fabsf(x[i]));
-    }
-    m = warp_max(m);
-    const float t = __fdiv_rn(m, 127.f);
-#pragma unroll
-    for (int i = 0; i < D / 32; ++i) {
-      const float c = t > 0.f ? fminf(fmaxf(rintf(__fdiv_rn(x[i], t)), -127.f), 127.f) : 0.f;
-      q_codes[r][lane + 32 * i] = (int8_t)__float2int_rn(c);
-    }
-    if (lane == 0) q_scale[r] = t;
-    if (__any_sync(0xffffffffu, bad) && lane == 0) report(P.error_word, TL_DEVERR_VALUE_RANGE);
-  }
-  __syncthreads();
-  const int per_head = kScoreWarps / hs;  // warps that share a head
-  if (w >= hs * per_head) return;
-  const int gi = w % hs, sub = w / hs, g = g0 + gi;
-  if (gi >= heads) return;
-  const int col = lane % LP, row = lane / LP;
-  // the query codes of this lane's 16 channels, split by sign
-  uint32_t qp[G][4], qn[G][4];
-  float t[G];
-#pragma unroll
-  for (int r = 0; r < G; ++r) {
-    t[r] = r < P.group ? q_scale[gi * P.group + r] : 0.f;
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const uint32_t c =
-          r < P.group ? *reinterpret_cast<const uint32_t*>(&q_codes[gi * P.group + r][col * 16 + 4 * i])
-                      : 0u;
-      const uint32_t neg = __vcmplts4(c, 0u);  // 0xff in the bytes below 0
-      qp[r][i] = c & ~neg;
-      qn[r][i] = c & neg;
-    }
-  }
-  float* out = P.scores + ((size_t)b * P.h_kv + g) * P.max_pages_per_seq;
-  const int32_t* table = P.block_table + (size_t)b * P.max_pages_per_seq;
-  for (int q0 = p0 + sub * PW * U; q0 < p1; q0 += per_head * PW * U) {
-    uint4 mx[U], mn[U];
-    float sc[U];
-    bool ok[U];
-#pragma unroll
-    for (int u = 0; u < U; ++u) {
-      const int i = q0 + u * PW + row;
-      const int page = i < p1 ? __ldg(table + i) : -1;
-      ok[u] = page >= 0 && page < P.num_pages;
-      if (i < p1 && !ok[u] && col == 0) report(P.error_word, TL_DEVERR_PAGE_RANGE);
-      const size_t at = (size_t)(ok[u] ? page : 0) * P.h_kv + g;
-      const uint4* src = reinterpret_cast<const uint4*>(P.bounds + at * 2 * D) + col;
-      mx[u] = __ldg(src);
-      mn[u] = __ldg(src + LP);
-      sc[u] = __ldg(P.scales + at);
-    }
-#pragma unroll
-    for (int u = 0; u < U; ++u) {
-      const uint32_t a[4] = {mx[u].x, mx[u].y, mx[u].z, mx[u].w};
-      const uint32_t c[4] = {mn[u].x, mn[u].y, mn[u].z, mn[u].w};
-      float best = -INFINITY;
-#pragma unroll
-      for (int r = 0; r < G; ++r) {
-        if (r >= P.group) break;  // groups between two instantiations (5 runs the form of 8)
-        int dot = 0;
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          dot = __dp4a((int)qp[r][i], (int)a[i], dot);
-          dot = __dp4a((int)qn[r][i], (int)c[i], dot);
+      const int b = base + lo;
+      const int nb = blocks_of(P.context_lens[b], P.max_pages_per_seq, P.page_size);
+      const int u2 = min(u1, start[lo + 1]);
+      const int p0 = (u - start[lo]) * kScoreUnit, p1 = min((u2 - start[lo]) * kScoreUnit, nb);
+      u = u2;
+      const int steps = (p1 - p0 + stage_pages - 1) / stage_pages;
+      const int32_t* table = P.block_table + (size_t)b * P.max_pages_per_seq;
+      // this lane's page of step k, -1 past the run or outside the pool
+      auto page_at = [&](int k) {
+        const int i = p0 + k * stage_pages + sub * 32 + lane;
+        if (sub >= per_head || i >= p1) return -1;
+        const int page = __ldg(table + i);
+        if (page >= 0 && page < P.num_pages) return page;
+        if (gi == 0) report(P.error_word, TL_DEVERR_PAGE_RANGE);
+        return -1;
+      };
+      auto issue = [&](int k, int page) {
+        if (issues) {
+          const uint32_t bar = smem_u32(&full[issued % nst]);
+          const uint32_t live = __ballot_sync(0xffffffffu, page >= 0);
+          if (lane == 0) mbar_arrive_expect_tx(bar, (uint32_t)__popc(live) * copy_bytes);
+          if (page >= 0)
+            bulk_g2s(smem_u32(score_sm) + (issued % nst) * stage_bytes +
+                         (sub * 32 + lane) * page_bytes,
+                     P.bounds + ((size_t)page * P.h_kv + g0) * 2 * D, copy_bytes, bar);
         }
-#pragma unroll
-        for (int o = 1; o < LP; o <<= 1) dot += __shfl_xor_sync(0xffffffffu, dot, o);
-        // a whole number below 2^24: exact as a float
-        best = fmaxf(best, __fmul_rn(__fmul_rn((float)dot, sc[u]), t[r]));
+        ++issued;
+      };
+      // the first stages' copies run while the query is quantised; the pages
+      // are looked up a step before they are copied
+      int page_cur = page_at(0), page_nxt = page_at(1), page_iss = page_cur;
+      for (int k = 0; k < nst && k < steps; ++k) {
+        page_iss = k == 0 ? page_cur : k == 1 ? page_nxt : page_at(k);
+        issue(k, page_iss);
       }
-      const int i = q0 + u * PW + row;
-      if (i < p1 && col == 0) out[i] = ok[u] ? best : -INFINITY;
+      page_iss = page_at(nst);
+      // query rows: code = rint(q / t) clamped to +-127, t = max|q| / 127; four
+      // threads a row, so that the rows' loads are all in flight at once
+      for (int r0 = 0; r0 < heads * P.group; r0 += kScoreWarps * 8) {
+        constexpr int E = D / 4;  // a thread's channels
+        const int r = min(r0 + (tid >> 2), heads * P.group - 1), e0 = (tid & 3) * E;
+        const size_t row = ((size_t)b * P.h_q + (size_t)g0 * P.group + r) * D + e0;
+        float x[E], m = 0.f;
+        if (QF32) {
+          const float4* src = reinterpret_cast<const float4*>(static_cast<const float*>(P.q) + row);
+#pragma unroll
+          for (int i = 0; i < E / 4; ++i)
+            *reinterpret_cast<float4*>(x + 4 * i) = __ldg(src + i);
+        } else {
+          const uint4* src =
+              reinterpret_cast<const uint4*>(static_cast<const unsigned short*>(P.q) + row);
+#pragma unroll
+          for (int i = 0; i < E / 8; ++i) widen_vec<kBf16>(__ldg(src + i), 0.f, x + 8 * i);
+        }
+        bool bad = false;
+#pragma unroll
+        for (int i = 0; i < E; ++i) {
+          if (!isfinite(x[i])) {  // counts as 0
+            bad = true;
+            x[i] = 0.f;
+          }
+          m = fmaxf(m, fabsf(x[i]));
+        }
+        m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 1));
+        m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 2));
+        const float t = __fdiv_rn(m, 127.f);
+#pragma unroll
+        for (int i = 0; i < E / 4; ++i) {
+          uint32_t code = 0;
+#pragma unroll
+          for (int j = 0; j < 4; ++j) {
+            const float c =
+                t > 0.f ? fminf(fmaxf(rintf(__fdiv_rn(x[4 * i + j], t)), -127.f), 127.f) : 0.f;
+            code |= (uint32_t)(uint8_t)(int8_t)__float2int_rn(c) << (8 * j);
+          }
+          *reinterpret_cast<uint32_t*>(q_codes + r * D + e0 + 4 * i) = code;
+        }
+        if ((tid & 3) == 0) q_scale[r] = t;
+        if (bad) report(P.error_word, TL_DEVERR_VALUE_RANGE);
+      }
+      __syncthreads();
+      const int g = g0 + gi;
+      // The query codes of this warp's head as B fragments of an m16n8k16: the
+      // column is a query head of the group, k step ks < D/16 takes the codes
+      // >= 0 (they meet the max codes), the others those below 0.  A lane's
+      // four channels of a step are those of one 4-byte read of a page's
+      // codes: the same permutation of the summed channels on both sides.
+      uint32_t qb[NT][2 * KS][2];
+      float bias_even[NT][2], bias_odd[NT][2];  // 1152 x the codes' sum over those steps
+#pragma unroll
+      for (int nt = 0; nt < NT; ++nt) {
+        const int r = 8 * nt + (lane >> 2);
+        float even = 0.f, odd = 0.f;
+#pragma unroll
+        for (int ks = 0; ks < KS; ++ks) {
+          const uint32_t a = works && r < P.group
+                                 ? *reinterpret_cast<const uint32_t*>(
+                                       q_codes + (gi * P.group + r) * D + 16 * ks + 4 * (lane & 3))
+                                 : 0u;
+          const uint32_t neg = __vcmplts4(a, 0u);
+          i8x4_as_f16x2x2(a & ~neg, qb[nt][ks][0], qb[nt][ks][1]);
+          i8x4_as_f16x2x2(a & neg, qb[nt][KS + ks][0], qb[nt][KS + ks][1]);
+          const float s = (float)__dp4a((int)a, 0x01010101, 0);
+          if (ks & 1) odd += s;
+          else even += s;
+        }
+        // the sums over the four lanes of a column, then to the lanes that
+        // hold its results (columns 2t and 2t + 1 of lane t)
+        even += __shfl_xor_sync(0xffffffffu, even, 1);
+        even += __shfl_xor_sync(0xffffffffu, even, 2);
+        odd += __shfl_xor_sync(0xffffffffu, odd, 1);
+        odd += __shfl_xor_sync(0xffffffffu, odd, 2);
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+          bias_even[nt][e] = 1152.f * __shfl_sync(0xffffffffu, even, 8 * (lane & 3) + 4 * e);
+          bias_odd[nt][e] = 1152.f * __shfl_sync(0xffffffffu, odd, 8 * (lane & 3) + 4 * e);
+        }
+      }
+      float* out = P.scores + ((size_t)b * P.h_kv + g) * P.row_stride;
+      float sc = works && page_cur >= 0 ? __ldg(P.scales + (size_t)page_cur * P.h_kv + g) : 0.f;
+      for (int k = 0; k < steps; ++k) {
+        // one step ahead: the next pages' scales and the table entries behind
+        const float sc_nxt =
+            works && page_nxt >= 0 ? __ldg(P.scales + (size_t)page_nxt * P.h_kv + g) : 0.f;
+        const int page_nn = page_at(k + 2), page_in = page_at(k + nst + 1);
+        const bool ok = mbar_wait(smem_u32(&full[done % nst]), (done / nst) & 1, &abort_flag);
+        if (works && ok) {
+          const uint32_t src = smem_u32(score_sm) + (done % nst) * stage_bytes +
+                               sub * 32 * page_bytes + gi * 2 * D;
+#pragma unroll
+          for (int half = 0; half < 2; ++half) {  // 16 pages each, the MMA's rows
+            float acc[NT][2][4];
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+              for (int e = 0; e < 4; ++e) acc[nt][0][e] = acc[nt][1][e] = 0.f;
+            const uint32_t rows = src + (half * 16 + (lane & 15)) * page_bytes + (lane >> 4) * 16;
+#pragma unroll
+            for (int ks = 0; ks < 2 * KS; ks += 2) {
+              uint32_t x[4];
+              ldmatrix_x4(rows + ks * 16, x[0], x[1], x[2], x[3]);
+#pragma unroll
+              for (int h = 0; h < 2; ++h) {
+                uint32_t a0, a1, a2, a3;
+                i8x4_as_f16x2x2_biased(x[2 * h], a0, a2);
+                i8x4_as_f16x2x2_biased(x[2 * h + 1], a1, a3);
+#pragma unroll
+                for (int nt = 0; nt < NT; ++nt)
+                  mma_f16_16816(acc[nt][h], a0, a1, a2, a3, qb[nt][ks + h][0], qb[nt][ks + h][1]);
+              }
+            }
+            // lane (g, t): pages g and g + 8, heads 2t and 2t + 1
+            const float s0 = __shfl_sync(0xffffffffu, sc, half * 16 + (lane >> 2));
+            const float s1 = __shfl_sync(0xffffffffu, sc, half * 16 + (lane >> 2) + 8);
+            float b0 = -INFINITY, b1 = -INFINITY;
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+              for (int e = 0; e < 2; ++e) {
+                const int r = 8 * nt + 2 * (lane & 3) + e;
+                if (r < P.group) {
+                  const float t = q_scale[gi * P.group + r];
+                  const float d0 = (acc[nt][0][e] - bias_even[nt][e]) + (acc[nt][1][e] - bias_odd[nt][e]);
+                  const float d1 =
+                      (acc[nt][0][2 + e] - bias_even[nt][e]) + (acc[nt][1][2 + e] - bias_odd[nt][e]);
+                  b0 = fmaxf(b0, __fmul_rn(__fmul_rn(d0, s0), t));
+                  b1 = fmaxf(b1, __fmul_rn(__fmul_rn(d1, s1), t));
+                }
+              }
+#pragma unroll
+            for (int o = 1; o < 4; o <<= 1) {
+              b0 = fmaxf(b0, __shfl_xor_sync(0xffffffffu, b0, o));
+              b1 = fmaxf(b1, __shfl_xor_sync(0xffffffffu, b1, o));
+            }
+            const int row = half * 16 + (lane >> 2) + 8 * (lane & 1);
+            const int i = p0 + k * stage_pages + sub * 32 + row;
+            const int page = __shfl_sync(0xffffffffu, page_cur, row);
+            if ((lane & 3) < 2 && i < p1) out[i] = page >= 0 ? (lane & 1 ? b1 : b0) : -INFINITY;
+          }
+        }
+        ++done;
+        // every warp is past the stage (and, at the last step, past the
+        // query's codes): it may be filled again
+        if (__syncthreads_or(!ok)) {
+          stop = true;
+          break;
+        }
+        if (k + nst < steps) issue(k + nst, page_iss);
+        page_iss = page_in;
+        page_cur = page_nxt;
+        page_nxt = page_nn;
+        sc = sc_nxt;
+      }
     }
+  }
+  // copies in flight land before the CTA leaves (a wait that gave up)
+  if (stop) {
+    bool drained = true;
+    for (uint32_t i = done; i < issued; ++i)
+      drained &= mbar_drain(smem_u32(&full[i % nst]), (i / nst) & 1);
+    if (tid == 0) report(P.error_word, TL_DEVERR_TIMEOUT);
   }
 }
 
@@ -372,6 +583,7 @@ __global__ void __launch_bounds__(kScoreWarps * 32) page_score_kernel(ScoreParam
 
 struct PageSelectParams {
   const float* scores;
+  int64_t row_stride;
   const int32_t* block_table;
   const int32_t* context_lens;
   int32_t* table;  // [B][h_kv][n]
@@ -380,8 +592,10 @@ struct PageSelectParams {
   uint32_t* error_word;
 };
 
-__global__ void __launch_bounds__(kSelMaxThreads) page_select_kernel(PageSelectParams P, int csize) {
+template <int T>
+__global__ void __launch_bounds__(T) page_select_kernel(PageSelectParams P, int csize, int key_cap) {
   __shared__ SelectShared sh;
+  extern __shared__ __align__(16) uint32_t sel_keys[];
   asm volatile("griddepcontrol.wait;\n" ::: "memory");
   const int row = blockIdx.x / csize, rank = blockIdx.x % csize;
   const int b = row / P.h_kv;
@@ -391,11 +605,11 @@ __global__ void __launch_bounds__(kSelMaxThreads) page_select_kernel(PageSelectP
     P.lens[b] = nb == 0 ? 0 : nb <= P.n ? L : (P.n - 1) * P.page_size + (L - 1) % P.page_size + 1;
     if (nb == 0 && L > 0) report(P.error_word, TL_DEVERR_CONTEXT_RANGE);
   }
-  const float* x = P.scores + (size_t)row * P.max_pages_per_seq;
+  const float* x = P.scores + (size_t)row * P.row_stride;
   const int32_t* from = P.block_table + (size_t)b * P.max_pages_per_seq;
   int32_t* to = P.table + (size_t)row * P.n;
-  select_row(
-      sh, nb, P.n, P.first, P.last, rank, csize, [&](int i) { return __ldcg(x + i); },
+  select_row<T>(
+      sh, sel_keys, key_cap, x, nb, P.n, P.first, P.last, rank, csize,
       [&](int pos, int i) { to[pos] = __ldg(from + i); }, [&](int pos) { to[pos] = -1; });
 }
 
@@ -453,30 +667,44 @@ static tl_status bounds_impl(const void* k, const float* k_scales, const int32_t
   return launch_status();
 }
 
+template <int D, int NT, bool QF32>
+static bool launch_score(const ScoreParams& P, cudaStream_t st) {
+  auto kernel = page_score_kernel<D, NT, QF32>;
+  const int hs = score_heads(P.h_kv);
+  const int q_bytes = score_query_bytes(hs, P.group, D), stage = score_stage_bytes(hs, D);
+  // 227 KiB less the static state
+  int nst = kScoreStages;
+  while (nst > 2 && nst * stage + q_bytes > 227 * 1024 - 6144) --nst;
+  const int smem = nst * stage + q_bytes;
+  if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem) != cudaSuccess)
+    return false;
+  const dim3 grid((unsigned)num_sms(), (unsigned)((P.h_kv + hs - 1) / hs));
+  kernel<<<grid, kScoreWarps * 32, smem, st>>>(P, nst);
+  return launch_status() == TL_OK;
+}
+
 template <int D, bool QF32>
-static void launch_score(const ScoreParams& P, dim3 grid, cudaStream_t st) {
-  const int threads = kScoreWarps * 32;
-  if (P.group <= 1) page_score_kernel<D, 1, QF32><<<grid, threads, 0, st>>>(P);
-  else if (P.group <= 2) page_score_kernel<D, 2, QF32><<<grid, threads, 0, st>>>(P);
-  else if (P.group <= 4) page_score_kernel<D, 4, QF32><<<grid, threads, 0, st>>>(P);
-  else if (P.group <= 8) page_score_kernel<D, 8, QF32><<<grid, threads, 0, st>>>(P);
-  else page_score_kernel<D, 16, QF32><<<grid, threads, 0, st>>>(P);
+static bool launch_score_group(const ScoreParams& P, cudaStream_t st) {
+  return P.group <= 8 ? launch_score<D, 1, QF32>(P, st) : launch_score<D, 2, QF32>(P, st);
 }
 
 SelectShape select_shape(int64_t rows, int64_t cap) {
   SelectShape s;
-  s.threads = cap <= 4096 ? 256 : cap <= 8192 ? 512 : kSelMaxThreads;
   s.cluster = 1;
-  // more CTAs a row while the rows leave SMs empty and a slice stays long
-  while (s.cluster < 8 && cap > (int64_t)4096 * s.cluster && rows * s.cluster * 2 <= num_sms())
-    s.cluster *= 2;
-  // a row past the registers of its CTAs is split further whatever the rows
-  while (s.cluster < 8 && cap > (int64_t)kSelRegs * kSelMaxThreads * s.cluster) s.cluster *= 2;
+  // as many CTAs a row as its keys' shared memory asks for
+  while (s.cluster < kSelClusterMax && cap > (int64_t)kSelKeysMax * s.cluster) s.cluster *= 2;
+  const int64_t slice = ((cap + s.cluster - 1) / s.cluster + 127) / 128 * 128;
+  s.keys = (int)std::min<int64_t>(slice, kSelKeysMax);
+  s.threads = slice <= 1024 ? 256 : rows * s.cluster > 2 * num_sms() ? 512 : 1024;
   return s;
 }
 
-cudaError_t launch_rows(const void* kernel, int64_t rows, const SelectShape& s, void** args,
-                        bool dependent, cudaStream_t st) {
+cudaError_t launch_rows(const void* const (&kernels)[3], int64_t rows, const SelectShape& s,
+                        void** args, bool dependent, cudaStream_t st) {
+  const void* kernel = kernels[s.threads == 256 ? 0 : s.threads == 512 ? 1 : 2];
+  const int smem = s.keys * (int)sizeof(uint32_t);
+  cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+  if (e != cudaSuccess) return e;
   cudaLaunchAttribute attr[2];
   int n = 0;
   if (s.cluster > 1) {
@@ -494,6 +722,7 @@ cudaError_t launch_rows(const void* kernel, int64_t rows, const SelectShape& s, 
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3((unsigned)(rows * s.cluster));
   cfg.blockDim = dim3((unsigned)s.threads);
+  cfg.dynamicSmemBytes = (size_t)smem;
   cfg.stream = st;
   cfg.attrs = attr;
   cfg.numAttrs = (unsigned)n;
@@ -533,7 +762,7 @@ extern "C" tl_status tl_kv_page_bounds_int8(const int8_t* k_codes, const float* 
 extern "C" size_t tl_kv_page_select_workspace_size(int32_t B, int32_t h_kv,
                                                    int32_t max_pages_per_seq) {
   if (B <= 0 || h_kv <= 0 || max_pages_per_seq <= 0) return 0;
-  return tl::align_up(sizeof(float) * (size_t)B * h_kv * max_pages_per_seq, 256);
+  return tl::align_up(sizeof(float) * (size_t)B * h_kv * tl::score_stride(max_pages_per_seq), 256);
 }
 
 extern "C" tl_status tl_kv_page_select(const void* q, tl_dtype q_dtype, const int8_t* bounds,
@@ -556,7 +785,8 @@ extern "C" tl_status tl_kv_page_select(const void* q, tl_dtype q_dtype, const in
       (reinterpret_cast<uintptr_t>(context_lens) & 3u))
     return TL_ERR_INVALID_ARG;
   if (q_dtype != TL_BF16 && q_dtype != TL_F32) return TL_ERR_UNSUPPORTED;
-  if ((d != 64 && d != 128) || h_q / h_kv > 16 || page_size > 256 || B > 65535 ||
+  if ((d != 64 && d != 128) || h_q / h_kv > 16 || page_size > 256 ||
+      (int64_t)B * max_pages_per_seq > INT32_MAX ||
       (int64_t)num_pages * page_size >= ((int64_t)1 << 31) ||
       (int64_t)n_select * page_size >= ((int64_t)1 << 31) ||
       (int64_t)B * h_kv > INT32_MAX / 8 || (h_kv + kScoreWarps - 1) / kScoreWarps > 65535)
@@ -572,6 +802,7 @@ extern "C" tl_status tl_kv_page_select(const void* q, tl_dtype q_dtype, const in
   S.block_table = block_table;
   S.context_lens = context_lens;
   S.scores = static_cast<float*>(workspace);
+  S.row_stride = score_stride(max_pages_per_seq);
   S.max_pages_per_seq = max_pages_per_seq;
   S.B = B;
   S.h_q = h_q;
@@ -580,19 +811,15 @@ extern "C" tl_status tl_kv_page_select(const void* q, tl_dtype q_dtype, const in
   S.num_pages = num_pages;
   S.page_size = page_size;
   S.error_word = error_word;
-  const int hs = score_heads(h_kv);
-  const dim3 grid((unsigned)((max_pages_per_seq + kScoreTile - 1) / kScoreTile),
-                  (unsigned)((h_kv + hs - 1) / hs), (unsigned)B);
-  if (d == 128) {
-    if (q_dtype == TL_F32) launch_score<128, true>(S, grid, st);
-    else launch_score<128, false>(S, grid, st);
-  } else {
-    if (q_dtype == TL_F32) launch_score<64, true>(S, grid, st);
-    else launch_score<64, false>(S, grid, st);
-  }
-  if (launch_status() != TL_OK) return TL_ERR_CUDA;
+  const bool f32 = q_dtype == TL_F32;
+  const bool ran = d == 128 ? (f32 ? launch_score_group<128, true>(S, st)
+                                   : launch_score_group<128, false>(S, st))
+                            : (f32 ? launch_score_group<64, true>(S, st)
+                                   : launch_score_group<64, false>(S, st));
+  if (!ran) return TL_ERR_CUDA;
   PageSelectParams P;
   P.scores = S.scores;
+  P.row_stride = S.row_stride;
   P.block_table = block_table;
   P.context_lens = context_lens;
   P.table = page_table;
@@ -606,10 +833,11 @@ extern "C" tl_status tl_kv_page_select(const void* q, tl_dtype q_dtype, const in
   P.error_word = error_word;
   const int64_t rows = (int64_t)B * h_kv;
   const SelectShape s = select_shape(rows, max_pages_per_seq);
-  int csize = s.cluster;
-  void* args[] = {&P, &csize};
-  if (launch_rows(reinterpret_cast<const void*>(page_select_kernel), rows, s, args, true, st) !=
-      cudaSuccess)
-    return TL_ERR_CUDA;
+  int csize = s.cluster, key_cap = s.keys;
+  void* args[] = {&P, &csize, &key_cap};
+  const void* const kernels[3] = {reinterpret_cast<const void*>(page_select_kernel<256>),
+                                  reinterpret_cast<const void*>(page_select_kernel<512>),
+                                  reinterpret_cast<const void*>(page_select_kernel<1024>)};
+  if (launch_rows(kernels, rows, s, args, true, st) != cudaSuccess) return TL_ERR_CUDA;
   return launch_status();
 }

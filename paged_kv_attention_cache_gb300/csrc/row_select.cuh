@@ -10,16 +10,22 @@
 // (+0 and -0 are one key), so the result is exact and does not depend on how
 // the row is split.
 //
-// Method: a radix selection over the keys' range.  One pass finds the row's
-// smallest and largest key; the range between them is cut into 2,048 equal
-// bins (linear in the key, so in the logarithm of the value), a histogram in
-// shared memory finds the bin that the n-th value falls into, and that bin is
-// cut again until its members are all taken or all equal.  Two or three
-// passes do for any distribution, and a row whose values sit in registers is
-// read from memory once.  A row is one cluster of 1-8 CTAs (its slices'
-// histograms are summed through distributed shared memory); each CTA then
-// counts its taken values, and ballots and one scan place them in index
-// order.
+// Method: what is sought is one (key, index) pair, the last one taken; then an
+// index is taken when its key is larger, or equal with an index not behind.
+// A radix selection narrows the range of keys that holds it: the smallest and
+// largest key are found first, the range between them is cut into up to 4,096
+// equal bins (linear in the key, so about even over a heavy-tailed row's
+// values), a histogram in shared memory tells the bin, and that bin is cut
+// again until it holds at most 128 values, which are ranked against each
+// other (once, for rows of some 10,000 spread values).  Where the bin is one
+// key (a row of equal values) the search goes on over the indices.
+//
+// Layout: a row is one cluster of 1-8 CTAs, their histograms summed through
+// distributed shared memory.  A CTA keeps its slice's keys in shared memory
+// (a value is read from memory once), a lane four of them at a time, so that
+// a thread needs few registers and several rows share an SM: the steps of one
+// row are short sweeps between barriers, bound by latency, and other rows
+// fill its waits.  Slices past the shared memory read their values again.
 #pragma once
 
 #include <cooperative_groups.h>
@@ -28,28 +34,34 @@
 
 namespace tl {
 
-constexpr int kSelBins = 2048;
-constexpr int kSelBinBits = 11;
-constexpr int kSelRegs = 16;        // values a thread keeps in registers
-constexpr int kSelMaxThreads = 1024;
+constexpr int kSelBins = 4096;
+constexpr int kSelBinBits = 12;
+constexpr int kSelRank = 128;        // values ranked against each other at the end
+constexpr int kSelKeysMax = 16384;   // keys of a slice kept in shared memory (64 KiB)
+constexpr int kSelClusterMax = 8;
 
-// A value's key: unsigned order = float order, NaN lowest, -0 = +0.
+// Keys: 0 no value (behind the row), 1 NaN, then the floats in order (-0 =
+// +0), all ones an index that is taken whatever its value.
+constexpr uint32_t kSelForced = 0xffffffffu;
 TL_DEVINLINE uint32_t select_key(float x) {
-  if (x != x) return 0u;
+  if (x != x) return 1u;
   const uint32_t u = __float_as_uint(x == 0.f ? 0.f : x);
   return (u & 0x80000000u) ? ~u : (u | 0x80000000u);
 }
 
 struct SelectShared {
-  uint32_t hist[2][kSelBins];  // two, so that one is cleared while peers read the other
-  uint32_t minmax[2];          // this CTA's smallest and largest key
-  uint32_t totals[2];          // this CTA's taken values and values equal to the threshold
-  uint32_t warp_a[32], warp_b[32];
-  uint32_t found[3];           // bin, values above it, values in it
-  uint32_t counts[kSelRegs][32];  // per round of one value a thread and warp: above | equal << 16
+  __align__(16) uint32_t hist[2][kSelBins];  // two: one is cleared while peers read the other
+  uint32_t minmax[2];     // this CTA's smallest and largest key
+  uint32_t total;         // this CTA's taken values
+  uint32_t tmp[2][32];    // block scans, alternating
+  uint32_t found[3];      // bin, values above it, values in it
+  uint32_t n_cand;        // (rank 0's are used) the values ranked at the end
+  uint32_t cand[2][kSelRank];  // their keys and indices
+  uint32_t last[2];       // key and index of the last value taken
 };
 
-// The block's exclusive scan of x in thread order; every thread gets the total.
+// The block's exclusive scan of x in thread order; every thread gets the
+// total.  One barrier; `tmp` must not be the previous scan's.
 TL_DEVINLINE uint32_t select_block_scan(uint32_t x, uint32_t* tmp, uint32_t& total) {
   const int lane = threadIdx.x & 31, wid = threadIdx.x >> 5, nw = blockDim.x >> 5;
   uint32_t inc = x;
@@ -60,25 +72,28 @@ TL_DEVINLINE uint32_t select_block_scan(uint32_t x, uint32_t* tmp, uint32_t& tot
   }
   if (lane == 31) tmp[wid] = inc;
   __syncthreads();
-  uint32_t before = 0, all = 0;
-  for (int w = 0; w < nw; ++w) {
-    const uint32_t v = tmp[w];
-    if (w < wid) before += v;
-    all += v;
+  const uint32_t mine = lane < nw ? tmp[lane] : 0u;
+  uint32_t all = mine;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const uint32_t y = __shfl_up_sync(0xffffffffu, all, o);
+    if (lane >= o) all += y;
   }
-  __syncthreads();  // tmp is reused
-  total = all;
-  return before + inc - x;
+  total = __shfl_sync(0xffffffffu, all, 31);
+  return __shfl_sync(0xffffffffu, all - mine, wid) + inc - x;
 }
 
-// One row, by the CTAs of one cluster (rank `rank` of `csize`; csize 1 needs
-// no cluster launch).  value(i): the row's value i; emit(pos, i): index i is
+// One row x[0 .. len), by the CTAs of one cluster (rank `rank` of `csize`;
+// csize 1 needs no cluster launch), T threads each.  keys: key_cap words of
+// 16-byte aligned shared memory, a multiple of 128.  emit(pos, i): index i is
 // taken at place pos; tail(pos): place pos stays empty.
-template <class Value, class Emit, class Tail>
-__device__ void select_row(SelectShared& sh, int len, int n, int first, int last, int rank,
-                           int csize, Value value, Emit emit, Tail tail) {
+template <int T, class Emit, class Tail>
+__device__ void select_row(SelectShared& sh, uint32_t* keys, int key_cap, const float* x, int len,
+                           int n, int first, int last, int rank, int csize, Emit emit,
+                           Tail tail) {
   namespace cg = cooperative_groups;
-  const int tid = threadIdx.x, T = blockDim.x, lane = tid & 31, wid = tid >> 5, nw = T >> 5;
+  constexpr int NW = T / 32, PER = kSelBins / T;
+  const int tid = threadIdx.x, lane = tid & 31, wid = tid >> 5;
   auto cluster_sync = [&]() {
     if (csize > 1) cg::this_cluster().sync();
     else __syncthreads();
@@ -93,217 +108,272 @@ __device__ void select_row(SelectShared& sh, int len, int n, int first, int last
     }
     return;  // the same for every CTA of the cluster: no barrier is left waiting
   }
-  // this CTA's slice of the row, a multiple of 32 values long
-  const int slice = ((len + csize - 1) / csize + 31) / 32 * 32;
+  // this CTA's slice of the row, and this warp's run of it: whole steps of 128
+  // values, four neighbours a lane
+  const int slice = ((len + csize - 1) / csize + 127) / 128 * 128;
   const int i0 = min(rank * slice, len), i1 = min(i0 + slice, len);
+  const int run = ((i1 - i0 + NW - 1) / NW + 127) / 128 * 128;
+  const int w0 = i0 + min(wid * run, i1 - i0), w1 = min(w0 + run, i1);
   const int m0 = first, m1 = len - last;  // the middle: ranked by value
-  uint32_t reg[kSelRegs];
-#pragma unroll
-  for (int u = 0; u < kSelRegs; ++u) {
-    const int i = i0 + u * T + tid;
-    reg[u] = i < i1 ? select_key(value(i)) : 0u;
-  }
-  // f(i, key, in the slice) for this thread's values, steps of T apart, all
-  // lanes of a warp together
-  auto each = [&](auto f) {
-#pragma unroll
-    for (int u = 0; u < kSelRegs; ++u) {
-      const int i = i0 + u * T + tid;
-      f(i, reg[u], i < i1);
-    }
-    for (int w0 = i0 + kSelRegs * T + wid * 32; w0 < i1; w0 += T) {
-      const int i = w0 + lane;
-      f(i, i < i1 ? select_key(value(i)) : 0u, i < i1);
-    }
+  const bool vec = (reinterpret_cast<uintptr_t>(x + i0) & 15u) == 0;
+  auto load4 = [&](int i) {
+    if (vec && i + 3 < len) return __ldcg(reinterpret_cast<const float4*>(x + i));
+    float4 f;
+    f.x = i < len ? __ldcg(x + i) : 0.f;
+    f.y = i + 1 < len ? __ldcg(x + i + 1) : 0.f;
+    f.z = i + 2 < len ? __ldcg(x + i + 2) : 0.f;
+    f.w = i + 3 < len ? __ldcg(x + i + 3) : 0.f;
+    return f;
+  };
+  auto key_of = [&](float f, int i) {
+    return i >= len ? 0u : i < m0 || i >= m1 ? kSelForced : select_key(f);
+  };
+  auto keys_of = [&](const float4& f, int i) {
+    return make_uint4(key_of(f.x, i), key_of(f.y, i + 1), key_of(f.z, i + 2), key_of(f.w, i + 3));
+  };
+  // a lane reads back only the keys it stored
+  auto keys_at = [&](int i) {
+    return i - i0 < key_cap ? *reinterpret_cast<const uint4*>(keys + (i - i0))
+                            : keys_of(load4(i), i);
   };
 
   for (int b = tid; b < 2 * kSelBins; b += T) (&sh.hist[0][0])[b] = 0u;
-  uint32_t kmin = 0xffffffffu, kmax = 0u;
-  each([&](int i, uint32_t k, bool in) {
-    if (in && i >= m0 && i < m1) {
-      kmin = min(kmin, k);
-      kmax = max(kmax, k);
+  if (tid == 0) {
+    sh.n_cand = 0u;
+    sh.minmax[0] = kSelForced;
+    sh.minmax[1] = 0u;
+  }
+  uint32_t kmin = kSelForced, kmax = 0u;
+  constexpr int U = 4;  // loads in flight
+  for (int w = w0; w < w1; w += 128 * U) {
+    float4 f[U];
+#pragma unroll
+    for (int u = 0; u < U; ++u) f[u] = load4(w + 128 * u + 4 * lane);
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      const int i = w + 128 * u + 4 * lane;
+      if (w + 128 * u >= w1) break;
+      const uint4 k = keys_of(f[u], i);
+      if (i - i0 < key_cap) *reinterpret_cast<uint4*>(keys + (i - i0)) = k;
+      const uint32_t kk[4] = {k.x, k.y, k.z, k.w};
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        if (kk[j] - 1u < kSelForced - 1u) {  // neither none nor forced
+          kmin = min(kmin, kk[j]);
+          kmax = max(kmax, kk[j]);
+        }
+      }
     }
-  });
+  }
   kmin = __reduce_min_sync(0xffffffffu, kmin);
   kmax = __reduce_max_sync(0xffffffffu, kmax);
-  if (lane == 0) {
-    sh.warp_a[wid] = kmin;
-    sh.warp_b[wid] = kmax;
-  }
   __syncthreads();
-  if (wid == 0) {
-    kmin = __reduce_min_sync(0xffffffffu, lane < nw ? sh.warp_a[lane] : 0xffffffffu);
-    kmax = __reduce_max_sync(0xffffffffu, lane < nw ? sh.warp_b[lane] : 0u);
-    if (lane == 0) {
-      sh.minmax[0] = kmin;
-      sh.minmax[1] = kmax;
-    }
+  if (lane == 0) {
+    atomicMin(&sh.minmax[0], kmin);
+    atomicMax(&sh.minmax[1], kmax);
   }
   cluster_sync();
-  kmin = 0xffffffffu;
-  kmax = 0u;
-  for (int r = 0; r < csize; ++r) {
-    kmin = min(kmin, peer(sh.minmax, r)[0]);
-    kmax = max(kmax, peer(sh.minmax, r)[1]);
+  kmin = sh.minmax[0];
+  kmax = sh.minmax[1];
+  if (csize > 1) {
+#pragma unroll
+    for (int r = 0; r < kSelClusterMax; ++r) {
+      if (r < csize) {
+        const uint32_t* m = peer(sh.minmax, r);
+        kmin = min(kmin, m[0]);
+        kmax = max(kmax, m[1]);
+      }
+    }
   }
 
-  uint32_t need = (uint32_t)(n - first - last);  // places left for the middle's values
-  // The bin searched: keys lo .. lo + span (inclusive).  Ends with a
-  // threshold: values above it are taken, of those equal to it the first
-  // `need` (need 0: none, or none left to take).
-  uint32_t lo = kmin, span = kmax - kmin, above = 0xffffffffu;  // taken: key > above
-  bool ties = false;
-  if (need > 0) {
-    for (int pass = 0;; ++pass) {
-      const int bits = 32 - __clz(span);
-      const int shift = bits > kSelBinBits ? bits - kSelBinBits : 0;
-      uint32_t* hist = sh.hist[pass & 1];
-      each([&](int i, uint32_t k, bool in) {
-        const uint32_t off = k - lo;
-        in = in && i >= m0 && i < m1 && off <= span;
-        // a warp whose values all share a bin (equal values do) counts once
-        const uint32_t bin = in ? off >> shift : kSelBins;
-        int same;
-        __match_all_sync(0xffffffffu, bin, &same);
-        if (in && (!same || lane == 0)) atomicAdd(hist + bin, same ? 32u : 1u);
+  // The search: the need-th largest of the cnt values in lo .. lo + span.
+  // by_index: among the values of key `equal`, over len - 1 - index.
+  uint32_t need = (uint32_t)(n - first - last), cnt = (uint32_t)(m1 - m0);
+  uint32_t lo = kmin, span = kmax - kmin, equal = 0u;
+  bool by_index = false;
+  uint32_t count = 0;  // this warp's taken values
+  // the last pair taken; none so far: above every value, below the forced
+  uint32_t last_key = kSelForced - 1u;
+  int last_idx = -1;
+  // f(place in the range, index, key) for this warp's values in the range
+  auto in_range = [&](auto f) {
+#pragma unroll 2
+    for (int w = w0; w < w1; w += 128) {
+      const int i = w + 4 * lane;
+      const uint4 k = keys_at(i);
+      const uint32_t kk[4] = {k.x, k.y, k.z, k.w};
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        if (!by_index) {
+          if (kk[j] - lo <= span) f(kk[j] - lo, i + j, kk[j]);
+        } else if (kk[j] == equal) {
+          const uint32_t v = (uint32_t)(len - 1 - i - j);
+          if (v - lo <= span) f(v - lo, i + j, kk[j]);
+        }
+      }
+    }
+  };
+  for (int pass = 0; need > 0; ++pass) {
+    if (need == cnt) {  // all of the range
+      last_key = by_index ? equal : lo;
+      last_idx = by_index ? len - 1 - (int)lo : len;
+      break;
+    }
+    if (cnt <= (uint32_t)kSelRank) {  // rank them
+      uint32_t* n_cand = peer(&sh.n_cand, 0);
+      uint32_t* cand = peer(&sh.cand[0][0], 0);
+      in_range([&](uint32_t, int i, uint32_t k) {
+        const uint32_t at = atomicAdd(n_cand, 1u);
+        if (at < (uint32_t)kSelRank) {
+          cand[at] = k;
+          cand[kSelRank + at] = (uint32_t)i;
+        }
       });
       cluster_sync();
-      // from the top bin down: thread t takes the per = kSelBins / T bins
-      // below kSelBins - t * per (T divides kSelBins)
-      const int per = kSelBins / T;
-      uint32_t sum = 0;
-      for (int j = 0; j < per; ++j) {
-        const int b = kSelBins - 1 - tid * per - j;
-        for (int r = 0; r < csize; ++r) sum += peer(hist, r)[b];
+      uint32_t* ck = &sh.cand[0][0];
+      if (csize > 1 && rank != 0) {  // a copy of rank 0's list
+        for (int c = tid; c < (int)cnt; c += T) {
+          ck[c] = cand[c];
+          ck[kSelRank + c] = cand[kSelRank + c];
+        }
+        __syncthreads();
       }
-      uint32_t total;
-      uint32_t before = select_block_scan(sum, sh.warp_a, total);
-      if (before < need && need <= before + sum) {
-        for (int j = 0; j < per; ++j) {
-          const int b = kSelBins - 1 - tid * per - j;
-          uint32_t c = 0;
-          for (int r = 0; r < csize; ++r) c += peer(hist, r)[b];
-          if (before + c >= need) {
-            sh.found[0] = (uint32_t)b;
-            sh.found[1] = before;
-            sh.found[2] = c;
-            break;
-          }
-          before += c;
+      if (tid < (int)cnt) {
+        const uint32_t k = ck[tid], at = ck[kSelRank + tid];
+        uint32_t better = 0;
+#pragma unroll 4
+        for (uint32_t c = 0; c < cnt; ++c)
+          better += ck[c] > k || (ck[c] == k && ck[kSelRank + c] < at) ? 1u : 0u;
+        if (better == need - 1) {
+          sh.last[0] = k;
+          sh.last[1] = at;
         }
       }
-      // the other histogram is cleared for the next pass: its readers were
-      // past it two barriers ago
-      if (pass > 0)
-        for (int b = tid; b < kSelBins; b += T) sh.hist[(pass + 1) & 1][b] = 0u;
-      cluster_sync();
-      const uint32_t bin = sh.found[0];
-      need -= sh.found[1];
-      lo += bin << shift;
-      span = min(span - (bin << shift), (1u << shift) - 1u);
-      if (sh.found[2] == need) {  // the whole bin
-        above = lo - 1u;  // lo = 0 (NaN keys): taken by the ties rule below
-        need = 0;
-        if (lo == 0u) {
-          above = 0u;
-          ties = true;
-          need = 0xffffffffu;
-        }
-        break;
-      }
-      if (shift == 0) {  // one key: its first `need` values by index
-        above = lo;
-        ties = true;
-        break;
-      }
+      __syncthreads();
+      last_key = sh.last[0];
+      last_idx = (int)sh.last[1];
+      break;
     }
+    if (span == 0u && !by_index) {  // one key: on over the indices
+      by_index = true;
+      equal = lo;
+      lo = 0u;
+      span = (uint32_t)(len - 1);
+    }
+    const int bits = 32 - __clz(span);
+    const int shift = bits > kSelBinBits ? bits - kSelBinBits : 0;
+    uint32_t* hist = sh.hist[pass & 1];
+    in_range([&](uint32_t off, int, uint32_t) { atomicAdd(hist + (off >> shift), 1u); });
+    cluster_sync();
+    // from the top bin down: thread t takes the PER bins that end below
+    // kSelBins - t * PER
+    const int b0 = kSelBins - (tid + 1) * PER;
+    uint32_t c[PER], sum = 0;
+#pragma unroll
+    for (int j = 0; j < PER; ++j) c[j] = 0u;
+    if (csize > 1) {
+#pragma unroll
+      for (int r = 0; r < kSelClusterMax; ++r) {
+        if (r < csize) {
+          const uint4* h = reinterpret_cast<const uint4*>(peer(hist, r) + b0);
+#pragma unroll
+          for (int j = 0; j < PER / 4; ++j) {
+            const uint4 v = h[j];
+            c[4 * j] += v.x;
+            c[4 * j + 1] += v.y;
+            c[4 * j + 2] += v.z;
+            c[4 * j + 3] += v.w;
+          }
+        }
+      }
+    } else {
+#pragma unroll
+      for (int j = 0; j < PER; ++j) c[j] = hist[b0 + j];
+    }
+#pragma unroll
+    for (int j = 0; j < PER; ++j) sum += c[j];
+    uint32_t total;
+    uint32_t before = select_block_scan(sum, sh.tmp[pass & 1], total);
+    if (before < need && need <= before + sum) {
+      uint32_t bin = 0, above = 0, in = 0;
+#pragma unroll
+      for (int j = PER - 1; j >= 0; --j) {
+        if (before < need && need <= before + c[j]) {
+          bin = (uint32_t)(b0 + j);
+          above = before;
+          in = c[j];
+        }
+        before += c[j];
+      }
+      sh.found[0] = bin;
+      sh.found[1] = above;
+      sh.found[2] = in;
+    }
+    // the other histogram is cleared for the next pass: its readers are past
+    // it since the barrier above
+    if (pass > 0)
+      for (int b = tid; b < kSelBins; b += T) sh.hist[(pass + 1) & 1][b] = 0u;
+    cluster_sync();
+    const uint32_t bin = sh.found[0];
+    need -= sh.found[1];
+    cnt = sh.found[2];
+    lo += bin << shift;
+    span = min(span - (bin << shift), (1u << shift) - 1u);
   }
 
-  // Place the taken values in index order: rounds of kSelRegs values a
-  // thread; in a round, value u of warp w comes after every value of earlier
-  // (u, w).  A taken value's place is the number of values before it that are
-  // above the threshold (or at a forced index) plus the ties before it, up to
-  // need.
-  auto is_above = [&](int i, uint32_t k) { return i < m0 || i >= m1 || k > above; };
-  auto is_tie = [&](int i, uint32_t k) { return ties && i >= m0 && i < m1 && k == above; };
-  uint32_t base_above = 0, base_tie = 0;
-  if (csize > 1) {
-    uint32_t a = 0, e = 0;
-    each([&](int i, uint32_t k, bool in) {
-      if (in && is_above(i, k)) ++a;
-      else if (in && is_tie(i, k)) ++e;
-    });
-    a = __reduce_add_sync(0xffffffffu, a);
-    e = __reduce_add_sync(0xffffffffu, e);
-    if (lane == 0) {
-      sh.warp_a[wid] = a;
-      sh.warp_b[wid] = e;
-    }
-    __syncthreads();
-    if (wid == 0) {
-      a = __reduce_add_sync(0xffffffffu, lane < nw ? sh.warp_a[lane] : 0u);
-      e = __reduce_add_sync(0xffffffffu, lane < nw ? sh.warp_b[lane] : 0u);
-      if (lane == 0) {
-        sh.totals[0] = a;
-        sh.totals[1] = e;
-      }
-    }
-    cluster_sync();
-    for (int r = 0; r < rank; ++r) {
-      base_above += peer(sh.totals, r)[0];
-      base_tie += peer(sh.totals, r)[1];
-    }
-  }
-  auto round = [&](int r0, auto key_of) {
-#pragma unroll
-    for (int u = 0; u < kSelRegs; ++u) {
-      const int i = r0 + u * T + tid;
-      const bool in = i < i1;
-      const uint32_t k = key_of(u, i);
-      const uint32_t ba = __ballot_sync(0xffffffffu, in && is_above(i, k));
-      const uint32_t be = __ballot_sync(0xffffffffu, in && is_tie(i, k));
-      if (lane == 0) sh.counts[u][wid] = (uint32_t)__popc(ba) | ((uint32_t)__popc(be) << 16);
-    }
-    __syncthreads();
-    // exclusive scan of the (u, warp) counts: at most 512 entries of at most
-    // 32 each, so both halves of the packed sums stay below 2^16
-    const int entries = kSelRegs * nw;
-    const uint32_t c = tid < entries ? sh.counts[tid / nw][tid % nw] : 0u;
-    uint32_t total;
-    const uint32_t off = select_block_scan(c, sh.warp_a, total);
-    if (tid < entries) sh.counts[tid / nw][tid % nw] = off;
-    __syncthreads();
-#pragma unroll
-    for (int u = 0; u < kSelRegs; ++u) {
-      const int i = r0 + u * T + tid;
-      const bool in = i < i1;
-      const uint32_t k = key_of(u, i);
-      const bool fa = in && is_above(i, k), fe = in && is_tie(i, k);
-      const uint32_t ba = __ballot_sync(0xffffffffu, fa), be = __ballot_sync(0xffffffffu, fe);
-      const uint32_t o = sh.counts[u][wid], below = (1u << lane) - 1u;
-      const uint32_t pa = base_above + (o & 0xffffu) + (uint32_t)__popc(ba & below);
-      const uint32_t pe = base_tie + (o >> 16) + (uint32_t)__popc(be & below);
-      if (fa || (fe && pe < need)) emit((int)(pa + min(pe, need)), i);
-    }
-    base_above += total & 0xffffu;
-    base_tie += total >> 16;
-    __syncthreads();  // counts are rewritten by the next round
+  // Place the taken values in index order: each warp counts its run's, a scan
+  // over the warps (and the cluster's earlier CTAs) gives its first place.
+  auto taken = [&](uint32_t k, int i) {
+    return k > last_key || (k == last_key && i <= last_idx);
   };
-  round(i0, [&](int u, int) { return reg[u]; });
-  for (int r0 = i0 + kSelRegs * T; r0 < i1; r0 += kSelRegs * T)
-    round(r0, [&](int, int i) { return i < i1 ? select_key(value(i)) : 0u; });
+#pragma unroll 2
+  for (int w = w0; w < w1; w += 128) {
+    const int i = w + 4 * lane;
+    const uint4 k = keys_at(i);
+    count += (taken(k.x, i) ? 1u : 0u) + (taken(k.y, i + 1) ? 1u : 0u) +
+             (taken(k.z, i + 2) ? 1u : 0u) + (taken(k.w, i + 3) ? 1u : 0u);
+  }
+  count = __reduce_add_sync(0xffffffffu, count);
+  __syncthreads();  // sh.tmp is free
+  uint32_t total;
+  uint32_t at = select_block_scan(lane == 0 ? count : 0u, sh.tmp[0], total);
+  at = __shfl_sync(0xffffffffu, at, 0);
+  if (csize > 1) {
+    if (tid == 0) sh.total = total;
+    cg::this_cluster().sync();
+#pragma unroll
+    for (int r = 0; r < kSelClusterMax; ++r)
+      if (r < rank) at += *peer(&sh.total, r);
+  }
+  const uint32_t below = (1u << lane) - 1u;
+  for (int w = w0; w < w1 && count > 0; w += 128) {
+    const int i = w + 4 * lane;
+    const uint4 k = keys_at(i);
+    const bool t0 = taken(k.x, i), t1 = taken(k.y, i + 1), t2 = taken(k.z, i + 2),
+               t3 = taken(k.w, i + 3);
+    const uint32_t s0 = __ballot_sync(0xffffffffu, t0), s1 = __ballot_sync(0xffffffffu, t1);
+    const uint32_t s2 = __ballot_sync(0xffffffffu, t2), s3 = __ballot_sync(0xffffffffu, t3);
+    int pos = (int)at + __popc(s0 & below) + __popc(s1 & below) + __popc(s2 & below) +
+              __popc(s3 & below);
+    if (t0) emit(pos++, i);
+    if (t1) emit(pos++, i + 1);
+    if (t2) emit(pos++, i + 2);
+    if (t3) emit(pos, i + 3);
+    at += (uint32_t)(__popc(s0) + __popc(s1) + __popc(s2) + __popc(s3));
+  }
   if (csize > 1) cg::this_cluster().sync();  // peers may still read this CTA's totals
 }
 
-// Threads per CTA and CTAs per row for rows of up to cap values.
+// Threads per CTA, CTAs per row and keys kept per CTA for `rows` rows of up to
+// cap values.
 struct SelectShape {
-  int threads, cluster;
+  int threads, cluster, keys;
 };
 SelectShape select_shape(int64_t rows, int64_t cap);
-// Launch of a kernel of `rows` clusters; dependent: a programmatic dependent
-// of the stream's previous kernel.
-cudaError_t launch_rows(const void* kernel, int64_t rows, const SelectShape& s, void** args,
-                        bool dependent, cudaStream_t st);
+// Launch of a kernel (its three forms: 256, 512 and 1,024 threads) over `rows`
+// clusters; dependent: a programmatic dependent of the stream's previous
+// kernel.
+cudaError_t launch_rows(const void* const (&kernels)[3], int64_t rows, const SelectShape& s,
+                        void** args, bool dependent, cudaStream_t st);
 
 }  // namespace tl

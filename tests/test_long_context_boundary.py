@@ -60,7 +60,7 @@ def test_page_select_refusals(lib):
                       ("pt", 1540), ("pl", 1796)):
         assert s(**{name: off}) == BAD, name
     assert s(qd=tl.TL_FP8_E4M3) == UNS and s(d=256) == UNS and s(hq=34) == UNS
-    assert s(ps=300) == UNS and s(B=65536) == UNS and s(n=1 << 28) == UNS
+    assert s(ps=300) == UNS and s(B=1 << 20, maxp=1 << 12) == UNS and s(n=1 << 28) == UNS
     need = tl.tl_kv_page_select_workspace_size(2, 2, 8)
     assert need == 256  # 2 x 2 x 8 floats
     assert s(ws=None) == WS and s(ws=2064) == WS and s(wsb=need - 1) == WS
