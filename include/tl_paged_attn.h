@@ -681,7 +681,7 @@ tl_status tl_paged_attn_decode_multi_int8(const void* q, const int8_t* k_codes,
  *   bounds        [num_pages][h_kv][2][d] int8, in place
  *   bound_scales  [num_pages][h_kv] float32, in place
  * Supported: d in {64, 128}, page_size in [1, 256], num_pages*page_size <
- * 2^31, B*max_pages_per_seq < 2^31.  Otherwise TL_ERR_UNSUPPORTED.
+ * 2^31, B*max_pages_per_seq*h_kv < 2^31.  Otherwise TL_ERR_UNSUPPORTED.
  */
 tl_status tl_kv_page_bounds(const void* k_cache, const int32_t* block_table,
                             int32_t max_pages_per_seq, const int32_t* first_new,

@@ -48,13 +48,11 @@ __global__ void __launch_bounds__(T) evict_select_kernel(EvictParams P, int csiz
 // batch's rows, and after a barrier stores them.  Every keep[j] >= j, so the
 // rows a batch stores (positions below the batch's end) are never sources of
 // a later batch, whatever the list's order: no row is lost, no order between
-// CTAs is needed, no copy of the pool is made.  The next batch's loads are
-// issued before the barrier that the current batch's stores follow, so a
-// batch of reads is always in flight.  Rows that stay (keep[j] = j) are
-// neither read nor written.
-constexpr int kCompactThreads = 256;
-constexpr int kCompactUnroll = 4;  // 16-byte vectors in flight per thread
-
+// CTAs is needed, no copy of the pool is made.  Reads may run ahead of the
+// stores as far as registers go: a batch's list entries are loaded two
+// batches ahead and its rows one batch ahead, before the barrier that the
+// stores of the batch before them follow.  Rows that stay (keep[j] = j) are
+// neither read nor written.  Bound: HBM, 2 x (K and V row) per moved row.
 struct CompactParams {
   void* pool[2];    // k, v: [num_pages][page_size][h_kv][row_bytes]
   float* scale[2];  // int8 pools: [num_pages][h_kv][page_size]
@@ -69,16 +67,71 @@ struct CompactParams {
   uint32_t* error_word;
 };
 
-// The slot of a sequence's position j, or -1 when its page is not one.
-TL_DEVINLINE int compact_slot(const CompactParams& P, const int32_t* table, int j) {
+// Page and offset of a sequence's position j; page -1 when it is not one of
+// the pool's.
+struct CompactPlace {
+  int page, off;
+};
+TL_DEVINLINE CompactPlace compact_place(const CompactParams& P, const int32_t* table, int j) {
   const int blk = P.ps_shift >= 0 ? j >> P.ps_shift : j / P.page_size;
   const int page = __ldg(table + blk);
-  if (page < 0 || page >= P.num_pages) return -1;
-  return page * P.page_size + (j - blk * P.page_size);
+  return {page >= 0 && page < P.num_pages ? page : -1, j - blk * P.page_size};
 }
 
-__global__ void __launch_bounds__(kCompactThreads) compact_kernel(CompactParams P) {
-  constexpr int U = kCompactUnroll;
+// The walk: rows_per_pass rows of a pass, this thread's being row r of it
+// (r < 0: none), U passes a batch.  slot(j): where position j's element is (-1: nowhere); at(slot): the
+// element.  Entries outside [j, L) and positions without a page are reported
+// by `reports` threads and skipped.
+template <int U, class Vec, class Index, class Slot, class At>
+TL_DEVINLINE void compact_walk(const int32_t* keep, int new_len, int L, int rows_per_pass, int r,
+                               bool reports, uint32_t* error_word, Slot slot, At at) {
+  const int batch = rows_per_pass * U;
+  auto entry = [&](int j) { return r >= 0 && j < new_len ? __ldg(keep + j) : j; };
+  // the rows of the batch at j0, whose list entries are s
+  auto load = [&](int j0, const int* s, Vec* x, Index* d) {
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      const int j = j0 + u * rows_per_pass + r;
+      d[u] = -1;
+      if (s[u] == j) continue;  // stays, or not a row of this thread
+      if (s[u] < j || s[u] >= L) {
+        if (reports) report(error_word, TL_DEVERR_CONTEXT_RANGE);
+        continue;
+      }
+      const Index from = slot(s[u]), to = slot(j);
+      if (from < 0 || to < 0) {
+        if (reports) report(error_word, TL_DEVERR_PAGE_RANGE);
+        continue;
+      }
+      d[u] = to;
+      x[u] = __ldcg(at(from));
+    }
+  };
+  Vec v[U], nv[U];
+  Index dst[U], ndst[U];
+  int s[U], ns[U];
+#pragma unroll
+  for (int u = 0; u < U; ++u) s[u] = entry(u * rows_per_pass + r);
+#pragma unroll
+  for (int u = 0; u < U; ++u) ns[u] = entry(batch + u * rows_per_pass + r);
+  load(0, s, v, dst);
+  for (int j0 = 0; j0 < new_len; j0 += batch) {
+#pragma unroll
+    for (int u = 0; u < U; ++u) s[u] = entry(j0 + 2 * batch + u * rows_per_pass + r);
+    load(j0 + batch, ns, nv, ndst);
+    __syncthreads();  // every thread's loads of this batch come before any store of it
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      if (dst[u] >= 0) *at(dst[u]) = v[u];
+      v[u] = nv[u];
+      dst[u] = ndst[u];
+      ns[u] = s[u];
+    }
+  }
+}
+
+template <int T, int U>
+__global__ void __launch_bounds__(T) compact_kernel(CompactParams P) {
   const int tid = threadIdx.x;
   const int row = blockIdx.x, b = row / P.h_kv, g = row % P.h_kv;
   const int L = P.context_lens[b], new_len = P.new_lens[b];
@@ -91,81 +144,40 @@ __global__ void __launch_bounds__(kCompactThreads) compact_kernel(CompactParams 
   }
   const int32_t* keep = P.keep + (size_t)row * P.n;
   const int32_t* table = P.block_table + (size_t)b * P.max_pages_per_seq;
-  if ((int)blockIdx.y == 2 * P.slices) {  // the masses move with their keys
+  const int kind = blockIdx.y;  // the pools' slices, then K and V scales, then the mass
+  if (kind < 2 * P.slices) {
+    const bool is_v = kind >= P.slices;
+    const int lanes = P.row_vecs / P.slices;  // threads of a row
+    const int per = T / lanes;                // rows of a pass
+    uint4* pool = static_cast<uint4*>(is_v ? P.pool[1] : P.pool[0]) + (size_t)g * P.row_vecs +
+                  (kind - (is_v ? P.slices : 0)) * lanes + tid % lanes;
+    const int64_t stride = (int64_t)P.h_kv * P.row_vecs;
+    compact_walk<U, uint4, int>(
+        keep, new_len, L, per, tid / lanes < per ? tid / lanes : -1, tid % lanes == 0,
+        P.error_word,
+        [&](int j) {
+          const CompactPlace p = compact_place(P, table, j);
+          return p.page < 0 ? -1 : p.page * P.page_size + p.off;
+        },
+        [&](int slot) { return pool + slot * stride; });
+  } else if (P.scale[0] && kind < 2 * P.slices + 2) {
+    float* scale = (kind == 2 * P.slices ? P.scale[0] : P.scale[1]) + (size_t)g * P.page_size;
+    compact_walk<U, float, int64_t>(
+        keep, new_len, L, T, tid, false, nullptr,
+        [&](int j) -> int64_t {
+          const CompactPlace p = compact_place(P, table, j);
+          return p.page < 0 ? -1 : (int64_t)p.page * P.h_kv * P.page_size + p.off;
+        },
+        [&](int64_t slot) { return scale + slot; });
+  } else {
     float* m = P.mass + (size_t)row * P.mass_len;
-    for (int j0 = 0; j0 < new_len; j0 += kCompactThreads * U) {
-      float v[U];
-      bool mv[U];
-#pragma unroll
-      for (int u = 0; u < U; ++u) {
-        const int j = j0 + u * kCompactThreads + tid;
-        const int s = j < new_len ? __ldg(keep + j) : 0;
-        mv[u] = j < new_len && s > j && s < L;
-        v[u] = mv[u] ? __ldcg(m + s) : 0.f;
-      }
-      __syncthreads();
-#pragma unroll
-      for (int u = 0; u < U; ++u)
-        if (mv[u]) m[j0 + u * kCompactThreads + tid] = v[u];
-    }
-    // positions that no key holds any more gather nothing: the last batch's
-    // loads are behind a barrier, so they may be cleared
+    compact_walk<U, float, int>(
+        keep, new_len, L, T, tid, false, nullptr, [&](int j) { return j; },
+        [&](int j) { return m + j; });
+    // positions that no key holds any more gather nothing; the last batch's
+    // loads are behind the walk's barrier
     __syncthreads();
-    for (int j = new_len + tid; j < L; j += kCompactThreads) m[j] = 0.f;
-    return;
-  }
-  const int which = blockIdx.y / P.slices, slice = blockIdx.y % P.slices;
-  const int lanes = P.row_vecs / P.slices;  // threads of a row
-  const int per = kCompactThreads / lanes;  // rows of a pass
-  const int r = tid / lanes, c = slice * lanes + tid % lanes;
-  const bool active = r < per;
-  uint4* pool = static_cast<uint4*>(which ? P.pool[1] : P.pool[0]);
-  float* scale = which ? P.scale[1] : P.scale[0];
-  const bool moves_scale = scale && slice == 0 && tid % lanes == 0;
-  const int batch = per * U;
-  uint4 v[U], nv[U];
-  float sv[U], nsv[U];
-  int dst[U], ndst[U];  // the row's slot, -1: nothing to store
-  auto load = [&](int j0, uint4* x, float* sx, int* d) {
-#pragma unroll
-    for (int u = 0; u < U; ++u) {
-      const int j = j0 + u * per + r;
-      d[u] = -1;
-      if (!active || j >= new_len) continue;
-      const int s = __ldg(keep + j);
-      if (s == j) continue;
-      if (s < j || s >= L) {
-        if (tid % lanes == 0) report(P.error_word, TL_DEVERR_CONTEXT_RANGE);
-        continue;
-      }
-      const int from = compact_slot(P, table, s), to = compact_slot(P, table, j);
-      if (from < 0 || to < 0) {
-        if (tid % lanes == 0) report(P.error_word, TL_DEVERR_PAGE_RANGE);
-        continue;
-      }
-      d[u] = to;
-      x[u] = __ldcg(pool + ((size_t)from * P.h_kv + g) * P.row_vecs + c);
-      if (moves_scale)
-        sx[u] = __ldcg(scale + ((size_t)(from / P.page_size) * P.h_kv + g) * P.page_size +
-                       from % P.page_size);
-    }
-  };
-  load(0, v, sv, dst);
-  for (int j0 = 0; j0 < new_len; j0 += batch) {
-    load(j0 + batch, nv, nsv, ndst);
-    __syncthreads();  // every thread's loads of this batch come before any store of it
-#pragma unroll
-    for (int u = 0; u < U; ++u) {
-      if (dst[u] >= 0) {
-        pool[((size_t)dst[u] * P.h_kv + g) * P.row_vecs + c] = v[u];
-        if (moves_scale)
-          scale[((size_t)(dst[u] / P.page_size) * P.h_kv + g) * P.page_size +
-                dst[u] % P.page_size] = sv[u];
-      }
-      v[u] = nv[u];
-      sv[u] = nsv[u];
-      dst[u] = ndst[u];
-    }
+    for (int j = new_len + tid; j < L; j += T) m[j] = 0.f;
   }
 }
 
@@ -187,7 +199,7 @@ static tl_status compact_impl(void* k, void* v, float* k_scales, float* v_scales
   if (elem == 0) return TL_ERR_UNSUPPORTED;
   const int64_t row_bytes = (int64_t)d * elem;
   if (row_bytes % 16 != 0) return TL_ERR_INVALID_ARG;
-  if (row_bytes / 16 > kCompactThreads || page_size > 256 ||
+  if (row_bytes > 4096 || page_size > 256 ||
       (int64_t)num_pages * page_size >= ((int64_t)1 << 31) || (int64_t)B * h_kv > INT32_MAX)
     return TL_ERR_UNSUPPORTED;
   CompactParams P;
@@ -212,14 +224,20 @@ static tl_status compact_impl(void* k, void* v, float* k_scales, float* v_scales
   P.row_vecs = (int32_t)(row_bytes / 16);
   P.error_word = error_word;
   // a row is shared by more CTAs while the (sequence, head) rows leave SMs
-  // empty, down to 64 bytes of a row
+  // empty, down to 32 bytes (a sector) of a row; then a CTA takes all of an SM's threads
   const int64_t rows = (int64_t)B * h_kv;
   P.slices = 1;
-  while (P.row_vecs % (2 * P.slices) == 0 && P.row_vecs / (2 * P.slices) >= 4 &&
+  while (P.row_vecs % (2 * P.slices) == 0 && P.row_vecs / (2 * P.slices) >= 2 &&
          rows * 2 * P.slices < 2 * num_sms())
     P.slices *= 2;
-  const dim3 grid((unsigned)rows, (unsigned)(2 * P.slices + (mass ? 1 : 0)));
-  compact_kernel<<<grid, kCompactThreads, 0, (cudaStream_t)stream>>>(P);
+  const dim3 grid((unsigned)rows, (unsigned)(2 * P.slices + (k_scales ? 2 : 0) + (mass ? 1 : 0)));
+  // otherwise small CTAs, whose barriers hold few rows back: one sequence of
+  // 8,192 rows kept takes 23 us with 1,024 threads and 33 with 512, 64
+  // sequences of 2,048 take 152 us with 128 threads, 169 with 256, 212 with 64
+  if (rows * 2 * P.slices <= 2 * num_sms() || P.row_vecs / P.slices > 128)
+    compact_kernel<1024, 2><<<grid, 1024, 0, (cudaStream_t)stream>>>(P);
+  else
+    compact_kernel<128, 4><<<grid, 128, 0, (cudaStream_t)stream>>>(P);
   return launch_status();
 }
 

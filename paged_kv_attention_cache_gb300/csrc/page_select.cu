@@ -72,7 +72,7 @@ TL_DEVINLINE void i8x4_as_f16x2x2(uint32_t w, uint32_t& lo, uint32_t& hi) {
 }
 TL_DEVINLINE void mma_f16_16816(float* c, uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3,
                                 uint32_t b0, uint32_t b1) {
-  asm volatile(
+  asm(
       "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, "
       "{%8,%9}, {%0,%1,%2,%3};\n"
       : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
@@ -90,6 +90,85 @@ TL_DEVINLINE float min_nan(float a, float b) {
   asm("min.NaN.f32 %0, %1, %2;\n" : "=f"(r) : "f"(a), "f"(b));
   return r;
 }
+
+// Running max and min of a lane's 16-byte vectors.  16-bit values go two at a
+// time (a packed max and min per pair; e4m3 codes are fp16 values too); f32 and
+// scaled int8 values one at a time.
+template <int KIND>
+struct Extremes {
+  static constexpr int V = PoolElem<KIND>::kPerVec;
+  static constexpr bool kPacked = KIND == kBf16 || KIND == kE4m3;
+  static constexpr int N = kPacked ? V / 2 : V;
+  uint32_t top[N], low[N];  // packed pairs, or f32 bits
+  TL_DEVINLINE static uint32_t max_of(uint32_t a, uint32_t b) {
+    if (KIND == kBf16) asm("max.NaN.bf16x2 %0, %0, %1;\n" : "+r"(a) : "r"(b));
+    else if (KIND == kE4m3) asm("max.NaN.f16x2 %0, %0, %1;\n" : "+r"(a) : "r"(b));
+    else return __float_as_uint(max_nan(__uint_as_float(a), __uint_as_float(b)));
+    return a;
+  }
+  TL_DEVINLINE static uint32_t min_of(uint32_t a, uint32_t b) {
+    if (KIND == kBf16) asm("min.NaN.bf16x2 %0, %0, %1;\n" : "+r"(a) : "r"(b));
+    else if (KIND == kE4m3) asm("min.NaN.f16x2 %0, %0, %1;\n" : "+r"(a) : "r"(b));
+    else return __float_as_uint(min_nan(__uint_as_float(a), __uint_as_float(b)));
+    return a;
+  }
+  TL_DEVINLINE void clear() {  // -inf, +inf
+    constexpr uint32_t inf = KIND == kBf16 ? 0x7f807f80u : KIND == kE4m3 ? 0x7c007c00u : 0x7f800000u;
+    constexpr uint32_t sign = kPacked ? 0x80008000u : 0x80000000u;
+#pragma unroll
+    for (int i = 0; i < N; ++i) {
+      top[i] = inf | sign;
+      low[i] = inf;
+    }
+  }
+  TL_DEVINLINE void add(const uint4& x, float scale) {
+    const uint32_t w[4] = {x.x, x.y, x.z, x.w};
+    uint32_t v[N];
+    if constexpr (KIND == kBf16 || KIND == kF32) {
+#pragma unroll
+      for (int i = 0; i < N; ++i) v[i] = w[i];
+    } else if constexpr (KIND == kE4m3) {
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+        asm("{\n .reg .b16 l, h;\n mov.b32 {l, h}, %2;\n cvt.rn.f16x2.e4m3x2 %0, l;\n"
+            " cvt.rn.f16x2.e4m3x2 %1, h;\n}\n"
+            : "=r"(v[2 * i]), "=r"(v[2 * i + 1])
+            : "r"(w[i]));
+    } else {
+      float f[V];
+      widen_vec<KIND>(x, scale, f);
+#pragma unroll
+      for (int i = 0; i < N; ++i) v[i] = __float_as_uint(f[i]);
+    }
+#pragma unroll
+    for (int i = 0; i < N; ++i) {
+      top[i] = max_of(top[i], v[i]);
+      low[i] = min_of(low[i], v[i]);
+    }
+  }
+  TL_DEVINLINE void fold(int o) {  // with the lane `o` away
+#pragma unroll
+    for (int i = 0; i < N; ++i) {
+      top[i] = max_of(top[i], __shfl_xor_sync(0xffffffffu, top[i], o));
+      low[i] = min_of(low[i], __shfl_xor_sync(0xffffffffu, low[i], o));
+    }
+  }
+  TL_DEVINLINE static void floats(const uint32_t* x, float* f) {
+#pragma unroll
+    for (int i = 0; i < N; ++i) {
+      if (KIND == kBf16) {
+        f[2 * i] = __uint_as_float(x[i] << 16);
+        f[2 * i + 1] = __uint_as_float(x[i] & 0xffff0000u);
+      } else if (KIND == kE4m3) {
+        asm("{\n .reg .b16 l, h;\n mov.b32 {l, h}, %2;\n cvt.f32.f16 %0, l;\n cvt.f32.f16 %1, h;\n}\n"
+            : "=f"(f[2 * i]), "=f"(f[2 * i + 1])
+            : "r"(x[i]));
+      } else {
+        f[i] = __uint_as_float(x[i]);
+      }
+    }
+  }
+};
 
 struct BoundsParams {
   const void* k;
@@ -116,41 +195,7 @@ TL_DEVINLINE void page_bounds(const BoundsParams& P, int page, int g, int live, 
                               col * 16;
   const float* ks = KIND == kInt8 ? P.k_scales + ((size_t)page * P.h_kv + g) * P.page_size : nullptr;
   float top[V], low[V];
-  // clean: the values as they are; otherwise a non-finite one counts as 0
-  auto reduce = [&](bool clean) {
-#pragma unroll
-    for (int e = 0; e < V; ++e) {
-      top[e] = -INFINITY;
-      low[e] = INFINITY;
-    }
-    for (int r0 = 0; r0 < live; r0 += RPW * U) {
-      uint4 x[U];
-      float sc[U];
-#pragma unroll
-      for (int u = 0; u < U; ++u) {
-        const int r = min(r0 + u * RPW + row, live - 1);  // a repeated row changes nothing
-        x[u] = __ldg(reinterpret_cast<const uint4*>(base + (size_t)r * stride));
-        sc[u] = KIND == kInt8 ? __ldg(ks + r) : 0.f;
-      }
-#pragma unroll
-      for (int u = 0; u < U; ++u) {
-        float f[V];
-        widen_vec<KIND>(x[u], sc[u], f);
-#pragma unroll
-        for (int e = 0; e < V; ++e) {
-          const float v = clean || fabsf(f[e]) <= 3.402823466e38f ? f[e] : 0.f;
-          top[e] = max_nan(top[e], v);
-          low[e] = min_nan(low[e], v);
-        }
-      }
-    }
-#pragma unroll
-    for (int o = LPR; o < 32; o <<= 1)
-#pragma unroll
-      for (int e = 0; e < V; ++e) {
-        top[e] = max_nan(top[e], __shfl_xor_sync(0xffffffffu, top[e], o));
-        low[e] = min_nan(low[e], __shfl_xor_sync(0xffffffffu, low[e], o));
-      }
+  auto largest = [&]() {  // of the magnitudes, over the whole row
     float m = 0.f;
 #pragma unroll
     for (int e = 0; e < V; ++e) m = max_nan(m, max_nan(fabsf(top[e]), fabsf(low[e])));
@@ -158,10 +203,52 @@ TL_DEVINLINE void page_bounds(const BoundsParams& P, int page, int g, int live, 
     for (int o = 1; o < LPR; o <<= 1) m = max_nan(m, __shfl_xor_sync(0xffffffffu, m, o));
     return m;
   };
-  float m = reduce(true);
-  if (!(m <= 3.402823466e38f)) {  // a NaN or an infinity among the live keys
+  Extremes<KIND> ext;
+  ext.clear();
+  for (int r0 = 0; r0 < live; r0 += RPW * U) {
+    uint4 x[U];
+    float sc[U];
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      const int r = min(r0 + u * RPW + row, live - 1);  // a repeated row changes nothing
+      x[u] = __ldg(reinterpret_cast<const uint4*>(base + (size_t)r * stride));
+      sc[u] = KIND == kInt8 ? __ldg(ks + r) : 0.f;
+    }
+#pragma unroll
+    for (int u = 0; u < U; ++u) ext.add(x[u], sc[u]);
+  }
+#pragma unroll
+  for (int o = LPR; o < 32; o <<= 1) ext.fold(o);
+  ext.floats(ext.top, top);
+  ext.floats(ext.low, low);
+  float m = largest();
+  if (!(m <= 3.402823466e38f)) {  // a NaN or an infinity among the live keys: it counts as 0
     if (lane == 0) report(P.error_word, TL_DEVERR_VALUE_RANGE);
-    m = reduce(false);
+#pragma unroll
+    for (int e = 0; e < V; ++e) {
+      top[e] = -INFINITY;
+      low[e] = INFINITY;
+    }
+    for (int r0 = 0; r0 < live; r0 += RPW) {
+      const int r = min(r0 + row, live - 1);
+      float f[V];
+      widen_vec<KIND>(__ldg(reinterpret_cast<const uint4*>(base + (size_t)r * stride)),
+                      KIND == kInt8 ? __ldg(ks + r) : 0.f, f);
+#pragma unroll
+      for (int e = 0; e < V; ++e) {
+        const float v = fabsf(f[e]) <= 3.402823466e38f ? f[e] : 0.f;
+        top[e] = fmaxf(top[e], v);
+        low[e] = fminf(low[e], v);
+      }
+    }
+#pragma unroll
+    for (int o = LPR; o < 32; o <<= 1)
+#pragma unroll
+      for (int e = 0; e < V; ++e) {
+        top[e] = fmaxf(top[e], __shfl_xor_sync(0xffffffffu, top[e], o));
+        low[e] = fminf(low[e], __shfl_xor_sync(0xffffffffu, low[e], o));
+      }
+    m = largest();
   }
   const float s = __fdiv_rn(m, 127.f);
   if (row < 2) {  // the first row group writes the max codes, the second the min codes
@@ -193,15 +280,22 @@ TL_DEVINLINE void page_bounds(const BoundsParams& P, int page, int g, int live, 
   }
 }
 
+// The first of n things that share `i` of `shares` takes (the first n % shares
+// shares take one more).
+TL_DEVINLINE uint32_t even_share(uint32_t n, uint32_t i, uint32_t shares) {
+  const uint32_t q = n / shares;
+  return q * i + min(i, n - q * shares);
+}
+
 constexpr int kBoundsThreads = 256;
 constexpr int kBoundsSeqs = 1024;  // sequences placed per round
 
 // Blocks first_new / page_size .. (L - 1) / page_size of every sequence,
-// times the heads, spread over the grid's warps: each CTA scans the
+// times the heads, in even runs over the grid's warps: each CTA scans the
 // sequences' block counts into shared memory, and a warp finds the sequence
-// of its next (block, head) by a binary search.  The batch may be ragged (a
-// prompt among decode steps): the work is even whatever the lengths, and the
-// host needs to know none of them.
+// of its run by a binary search.  The batch may be ragged (a prompt among
+// decode steps): the work is even whatever the lengths, and the host needs to
+// know none of them.
 template <int D, int KIND>
 __global__ void __launch_bounds__(kBoundsThreads) page_bounds_kernel(BoundsParams P) {
   __shared__ int start[kBoundsSeqs + 1];  // first block of each sequence of the round
@@ -236,9 +330,14 @@ __global__ void __launch_bounds__(kBoundsThreads) page_bounds_kernel(BoundsParam
     }
     if (tid == 0) start[kBoundsSeqs] = (int)total;
     __syncthreads();
-    for (int64_t t = warp; t < (int64_t)total * P.h_kv; t += nwarps) {
-      const int i = (int)(t / P.h_kv), g = (int)(t % P.h_kv);
-      int lo = 0, hi = kBoundsSeqs;  // the last sequence that starts at or before i
+    // this warp's run of (block, head) pairs, heads innermost: a page's heads
+    // are one run of memory
+    const uint32_t tasks = total * (uint32_t)P.h_kv;
+    uint32_t t = even_share(tasks, (uint32_t)warp, (uint32_t)nwarps);
+    const uint32_t t1 = even_share(tasks, (uint32_t)warp + 1, (uint32_t)nwarps);
+    while (t < t1) {
+      const int i = (int)(t / (uint32_t)P.h_kv);
+      int lo = 0, hi = kBoundsSeqs;  // the last sequence that starts at or before block i
       while (hi - lo > 1) {
         const int mid = (lo + hi) >> 1;
         if (start[mid] <= i) lo = mid;
@@ -247,15 +346,21 @@ __global__ void __launch_bounds__(kBoundsThreads) page_bounds_kernel(BoundsParam
       // sequences without blocks start where the next one does: the last of
       // equal starts is the one that has them
       const int b = base + lo;
-      const int f = P.first_new ? max(P.first_new[b], 0) : 0;
-      const int blk = f / P.page_size + (i - start[lo]);
-      const int live = min(P.page_size, P.context_lens[b] - blk * P.page_size);
-      const int page = __ldg(P.block_table + (size_t)b * P.max_pages_per_seq + blk);
-      if (page < 0 || page >= P.num_pages) {
-        if (lane == 0) report(P.error_word, TL_DEVERR_PAGE_RANGE);
-        continue;
+      const int f = P.first_new ? max(P.first_new[b], 0) : 0, L = P.context_lens[b];
+      int g = (int)(t - (uint32_t)i * (uint32_t)P.h_kv);
+      const int first = f / P.page_size + (i - start[lo]);
+      const int n_blk = start[lo + 1] - i;  // of the sequence from here
+      const int32_t* table = P.block_table + (size_t)b * P.max_pages_per_seq + first;
+      int page = __ldg(table);
+      for (int k = 0; k < n_blk && t < t1; ++k, g = 0) {
+        const int next = k + 1 < n_blk ? __ldg(table + k + 1) : -1;
+        const int live = min(P.page_size, L - (first + k) * P.page_size);
+        const bool ok = page >= 0 && page < P.num_pages;
+        if (!ok && lane == 0) report(P.error_word, TL_DEVERR_PAGE_RANGE);
+        for (; g < P.h_kv && t < t1; ++g, ++t)
+          if (ok) page_bounds<D, KIND>(P, page, g, live, lane);
+        page = next;
       }
-      page_bounds<D, KIND>(P, page, g, live, lane);
     }
     __syncthreads();  // start is rewritten by the next round
   }
@@ -279,19 +384,19 @@ struct ScoreParams {
 inline int64_t score_stride(int max_pages_per_seq) { return ((int64_t)max_pages_per_seq + 3) / 4 * 4; }
 
 constexpr int kScoreWarps = 8;
-constexpr int kScoreUnit = 8;     // pages; a CTA takes a run of units
+constexpr int kScoreUnit = 4;     // pages; a CTA takes a run of units
 constexpr int kScoreSeqs = 1024;  // sequences placed per round
 constexpr int kScoreStages = 3;   // at most
 
 // Heads a CTA scores (grid.y covers the others), and the warps that share one.
 __host__ __device__ inline int score_heads(int h_kv) { return h_kv < kScoreWarps ? h_kv : kScoreWarps; }
 
-// Shared memory of a stage: 32 pages per warp of a head, each page's codes of
-// the CTA's heads (one run of the bounds pool) and 16 bytes more, so that 32
-// lanes reading the same word of 32 pages fall on different banks.
+// Shared memory of a stage: 16 pages per warp of a head, each page's codes of
+// the CTA's heads (one run of the bounds pool) and 16 bytes more, so that the
+// same 16 bytes of 8 pages fall on different banks.
 __host__ __device__ inline int score_page_bytes(int heads, int d) { return heads * 2 * d + 16; }
 __host__ __device__ inline int score_stage_bytes(int heads, int d) {
-  return 32 * (kScoreWarps / heads) * score_page_bytes(heads, d);
+  return 16 * (kScoreWarps / heads) * score_page_bytes(heads, d);
 }
 __host__ __device__ inline int score_query_bytes(int heads, int group, int d) {
   return heads * group * d;
@@ -302,7 +407,7 @@ TL_DEVINLINE int blocks_of(int L, int max_pages, int page_size) {
   return L <= 0 || (int64_t)L > (int64_t)max_pages * page_size ? 0 : (L - 1) / page_size + 1;
 }
 
-// Scores of every page of every sequence, one CTA per SM.  Each takes an even
+// Scores of every page of every sequence, two CTAs per SM.  Each takes an even
 // share of the batch's pages as one run (a scan of the sequences' block
 // counts places it: the host knows no length), so it quantises a sequence's
 // query rows once or twice a call.  A page's codes of the CTA's heads are one
@@ -318,7 +423,7 @@ TL_DEVINLINE int blocks_of(int L, int max_pages, int page_size) {
 // channels x 127 x 1279 = 10.4 million, a whole number below 2^24, exact in
 // f32 however it is added up.
 template <int D, int NT, bool QF32>
-__global__ void __launch_bounds__(kScoreWarps * 32, 1) page_score_kernel(ScoreParams P, int nst) {
+__global__ void __launch_bounds__(kScoreWarps * 32, 2) page_score_kernel(ScoreParams P, int nst) {
   extern __shared__ __align__(16) unsigned char score_sm[];
   __shared__ int start[kScoreSeqs + 1];  // first unit of each sequence of the round
   __shared__ uint32_t tmp[32];
@@ -331,9 +436,9 @@ __global__ void __launch_bounds__(kScoreWarps * 32, 1) page_score_kernel(ScorePa
   const int per_head = kScoreWarps / hs;
   const int gi = w % hs, sub = w / hs;
   const bool works = sub < per_head && gi < heads;  // computes
-  const bool issues = sub < per_head && gi == 0;    // copies 32 pages of a stage
+  const int copies = 2 * per_head;                  // pages of a stage that each warp copies
   const int page_bytes = score_page_bytes(hs, D), stage_bytes = score_stage_bytes(hs, D);
-  const int stage_pages = 32 * per_head;
+  const int stage_pages = 16 * per_head;
   const uint32_t copy_bytes = (uint32_t)heads * 2 * D;
   unsigned char* q_codes = score_sm + nst * stage_bytes;
   // the selection may take the SMs that this grid leaves (it waits for the
@@ -341,10 +446,12 @@ __global__ void __launch_bounds__(kScoreWarps * 32, 1) page_score_kernel(ScorePa
   asm volatile("griddepcontrol.launch_dependents;\n" ::: "memory");
   if (tid == 0) {
     abort_flag = 0;
-    for (int s = 0; s < nst; ++s) mbar_init(smem_u32(&full[s]), per_head);
+    for (int s = 0; s < nst; ++s) mbar_init(smem_u32(&full[s]), kScoreWarps);
     fence_mbar_init();
   }
-  uint32_t issued = 0, done = 0;  // stages
+  uint32_t issued = 0, done = 0;  // stages, and their places in the ring
+  int slot_in = 0, slot_out = 0;
+  uint32_t parity = 0;  // of the phase that slot_out waits for
   bool stop = false;
   for (int base = 0; base < P.B && !stop; base += kScoreSeqs) {
     constexpr int PER = kScoreSeqs / (kScoreWarps * 32);
@@ -366,8 +473,8 @@ __global__ void __launch_bounds__(kScoreWarps * 32, 1) page_score_kernel(ScorePa
     }
     if (tid == 0) start[kScoreSeqs] = (int)total;
     __syncthreads();
-    int u = (int)((int64_t)total * blockIdx.x / gridDim.x);
-    const int u1 = (int)((int64_t)total * (blockIdx.x + 1) / gridDim.x);
+    int u = (int)even_share(total, blockIdx.x, gridDim.x);
+    const int u1 = (int)even_share(total, blockIdx.x + 1, gridDim.x);
     while (u < u1 && !stop) {
       int lo = 0, hi = kScoreSeqs;  // the last sequence that starts at or before u
       while (hi - lo > 1) {
@@ -382,35 +489,33 @@ __global__ void __launch_bounds__(kScoreWarps * 32, 1) page_score_kernel(ScorePa
       u = u2;
       const int steps = (p1 - p0 + stage_pages - 1) / stage_pages;
       const int32_t* table = P.block_table + (size_t)b * P.max_pages_per_seq;
-      // this lane's page of step k, -1 past the run or outside the pool
-      auto page_at = [&](int k) {
-        const int i = p0 + k * stage_pages + sub * 32 + lane;
-        if (sub >= per_head || i >= p1) return -1;
+      // the page at place j of step k, -1 past the run or outside the pool
+      auto page_at = [&](int k, int j) {
+        const int i = p0 + k * stage_pages + j;
+        if (j < 0 || i >= p1) return -1;
         const int page = __ldg(table + i);
-        if (page >= 0 && page < P.num_pages) return page;
-        if (gi == 0) report(P.error_word, TL_DEVERR_PAGE_RANGE);
-        return -1;
+        return page >= 0 && page < P.num_pages ? page : -1;
       };
+      const int mine = works && lane < 16 ? sub * 16 + lane : -1;  // scored
+      const int copied = w * copies + lane;
+      // each warp copies its share of a stage's pages: one lane a page, and the
+      // copies of one warp are issued one after another
       auto issue = [&](int k, int page) {
-        if (issues) {
-          const uint32_t bar = smem_u32(&full[issued % nst]);
-          const uint32_t live = __ballot_sync(0xffffffffu, page >= 0);
-          if (lane == 0) mbar_arrive_expect_tx(bar, (uint32_t)__popc(live) * copy_bytes);
-          if (page >= 0)
-            bulk_g2s(smem_u32(score_sm) + (issued % nst) * stage_bytes +
-                         (sub * 32 + lane) * page_bytes,
-                     P.bounds + ((size_t)page * P.h_kv + g0) * 2 * D, copy_bytes, bar);
-        }
+        const uint32_t bar = smem_u32(&full[slot_in]);
+        const bool inside = lane < copies && p0 + k * stage_pages + copied < p1;
+        if (inside && page < 0) report(P.error_word, TL_DEVERR_PAGE_RANGE);
+        const uint32_t live = __ballot_sync(0xffffffffu, inside && page >= 0);
+        if (lane == 0) mbar_arrive_expect_tx(bar, (uint32_t)__popc(live) * copy_bytes);
+        if (inside && page >= 0)
+          bulk_g2s(smem_u32(score_sm) + slot_in * stage_bytes + copied * page_bytes,
+                   P.bounds + ((size_t)page * P.h_kv + g0) * 2 * D, copy_bytes, bar);
         ++issued;
+        slot_in = slot_in + 1 == nst ? 0 : slot_in + 1;
       };
-      // the first stages' copies run while the query is quantised; the pages
+      // the first stages' copies run while the query is quantised; later pages
       // are looked up a step before they are copied
-      int page_cur = page_at(0), page_nxt = page_at(1), page_iss = page_cur;
-      for (int k = 0; k < nst && k < steps; ++k) {
-        page_iss = k == 0 ? page_cur : k == 1 ? page_nxt : page_at(k);
-        issue(k, page_iss);
-      }
-      page_iss = page_at(nst);
+      for (int k = 0; k < nst && k < steps; ++k) issue(k, page_at(k, copied));
+      int page_cur = page_at(0, mine), page_nxt = page_at(1, mine), page_iss = page_at(nst, copied);
       // query rows: code = rint(q / t) clamped to +-127, t = max|q| / 127; four
       // threads a row, so that the rows' loads are all in flight at once
       for (int r0 = 0; r0 < heads * P.group; r0 += kScoreWarps * 8) {
@@ -464,6 +569,7 @@ __global__ void __launch_bounds__(kScoreWarps * 32, 1) page_score_kernel(ScorePa
       // codes: the same permutation of the summed channels on both sides.
       uint32_t qb[NT][2 * KS][2];
       float bias_even[NT][2], bias_odd[NT][2];  // 1152 x the codes' sum over those steps
+      float t_q[NT][2];                         // the scales of columns 2t and 2t + 1
 #pragma unroll
       for (int nt = 0; nt < NT; ++nt) {
         const int r = 8 * nt + (lane >> 2);
@@ -491,6 +597,8 @@ __global__ void __launch_bounds__(kScoreWarps * 32, 1) page_score_kernel(ScorePa
         for (int e = 0; e < 2; ++e) {
           bias_even[nt][e] = 1152.f * __shfl_sync(0xffffffffu, even, 8 * (lane & 3) + 4 * e);
           bias_odd[nt][e] = 1152.f * __shfl_sync(0xffffffffu, odd, 8 * (lane & 3) + 4 * e);
+          const int rq = 8 * nt + 2 * (lane & 3) + e;
+          t_q[nt][e] = works && rq < P.group ? q_scale[gi * P.group + rq] : 0.f;
         }
       }
       float* out = P.scores + ((size_t)b * P.h_kv + g) * P.row_stride;
@@ -499,66 +607,70 @@ __global__ void __launch_bounds__(kScoreWarps * 32, 1) page_score_kernel(ScorePa
         // one step ahead: the next pages' scales and the table entries behind
         const float sc_nxt =
             works && page_nxt >= 0 ? __ldg(P.scales + (size_t)page_nxt * P.h_kv + g) : 0.f;
-        const int page_nn = page_at(k + 2), page_in = page_at(k + nst + 1);
-        const bool ok = mbar_wait(smem_u32(&full[done % nst]), (done / nst) & 1, &abort_flag);
+        const int page_nn = page_at(k + 2, mine), page_in = page_at(k + nst + 1, copied);
+        const bool ok = mbar_wait(smem_u32(&full[slot_out]), parity, &abort_flag);
         if (works && ok) {
-          const uint32_t src = smem_u32(score_sm) + (done % nst) * stage_bytes +
-                               sub * 32 * page_bytes + gi * 2 * D;
+          // 16 pages are the MMA's rows; every fragment is loaded before the
+          // first is used
+          const uint32_t rows = smem_u32(score_sm) + slot_out * stage_bytes +
+                                (sub * 16 + (lane & 15)) * page_bytes + gi * 2 * D +
+                                (lane >> 4) * 16;
+          uint32_t x[KS][4];
 #pragma unroll
-          for (int half = 0; half < 2; ++half) {  // 16 pages each, the MMA's rows
-            float acc[NT][2][4];
+          for (int ks = 0; ks < KS; ++ks)
+            ldmatrix_x4(rows + ks * 32, x[ks][0], x[ks][1], x[ks][2], x[ks][3]);
+          float acc[NT][2][4];
 #pragma unroll
-            for (int nt = 0; nt < NT; ++nt)
+          for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-              for (int e = 0; e < 4; ++e) acc[nt][0][e] = acc[nt][1][e] = 0.f;
-            const uint32_t rows = src + (half * 16 + (lane & 15)) * page_bytes + (lane >> 4) * 16;
+            for (int e = 0; e < 4; ++e) acc[nt][0][e] = acc[nt][1][e] = 0.f;
 #pragma unroll
-            for (int ks = 0; ks < 2 * KS; ks += 2) {
-              uint32_t x[4];
-              ldmatrix_x4(rows + ks * 16, x[0], x[1], x[2], x[3]);
+          for (int ks = 0; ks < KS; ++ks)
 #pragma unroll
-              for (int h = 0; h < 2; ++h) {
-                uint32_t a0, a1, a2, a3;
-                i8x4_as_f16x2x2_biased(x[2 * h], a0, a2);
-                i8x4_as_f16x2x2_biased(x[2 * h + 1], a1, a3);
+            for (int h = 0; h < 2; ++h) {
+              uint32_t a0, a1, a2, a3;
+              i8x4_as_f16x2x2_biased(x[ks][2 * h], a0, a2);
+              i8x4_as_f16x2x2_biased(x[ks][2 * h + 1], a1, a3);
 #pragma unroll
-                for (int nt = 0; nt < NT; ++nt)
-                  mma_f16_16816(acc[nt][h], a0, a1, a2, a3, qb[nt][ks + h][0], qb[nt][ks + h][1]);
+              for (int nt = 0; nt < NT; ++nt)
+                mma_f16_16816(acc[nt][h], a0, a1, a2, a3, qb[nt][2 * ks + h][0],
+                              qb[nt][2 * ks + h][1]);
+            }
+          // lane (g, t): pages g and g + 8, heads 2t and 2t + 1
+          const float s0 = __shfl_sync(0xffffffffu, sc, lane >> 2);
+          const float s1 = __shfl_sync(0xffffffffu, sc, (lane >> 2) + 8);
+          float b0 = -INFINITY, b1 = -INFINITY;
+#pragma unroll
+          for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+              const int r = 8 * nt + 2 * (lane & 3) + e;
+              if (r < P.group) {
+                const float d0 =
+                    (acc[nt][0][e] - bias_even[nt][e]) + (acc[nt][1][e] - bias_odd[nt][e]);
+                const float d1 =
+                    (acc[nt][0][2 + e] - bias_even[nt][e]) + (acc[nt][1][2 + e] - bias_odd[nt][e]);
+                b0 = fmaxf(b0, __fmul_rn(__fmul_rn(d0, s0), t_q[nt][e]));
+                b1 = fmaxf(b1, __fmul_rn(__fmul_rn(d1, s1), t_q[nt][e]));
               }
             }
-            // lane (g, t): pages g and g + 8, heads 2t and 2t + 1
-            const float s0 = __shfl_sync(0xffffffffu, sc, half * 16 + (lane >> 2));
-            const float s1 = __shfl_sync(0xffffffffu, sc, half * 16 + (lane >> 2) + 8);
-            float b0 = -INFINITY, b1 = -INFINITY;
 #pragma unroll
-            for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-              for (int e = 0; e < 2; ++e) {
-                const int r = 8 * nt + 2 * (lane & 3) + e;
-                if (r < P.group) {
-                  const float t = q_scale[gi * P.group + r];
-                  const float d0 = (acc[nt][0][e] - bias_even[nt][e]) + (acc[nt][1][e] - bias_odd[nt][e]);
-                  const float d1 =
-                      (acc[nt][0][2 + e] - bias_even[nt][e]) + (acc[nt][1][2 + e] - bias_odd[nt][e]);
-                  b0 = fmaxf(b0, __fmul_rn(__fmul_rn(d0, s0), t));
-                  b1 = fmaxf(b1, __fmul_rn(__fmul_rn(d1, s1), t));
-                }
-              }
-#pragma unroll
-            for (int o = 1; o < 4; o <<= 1) {
-              b0 = fmaxf(b0, __shfl_xor_sync(0xffffffffu, b0, o));
-              b1 = fmaxf(b1, __shfl_xor_sync(0xffffffffu, b1, o));
-            }
-            const int row = half * 16 + (lane >> 2) + 8 * (lane & 1);
-            const int i = p0 + k * stage_pages + sub * 32 + row;
-            const int page = __shfl_sync(0xffffffffu, page_cur, row);
-            if ((lane & 3) < 2 && i < p1) out[i] = page >= 0 ? (lane & 1 ? b1 : b0) : -INFINITY;
+          for (int o = 1; o < 4; o <<= 1) {
+            b0 = fmaxf(b0, __shfl_xor_sync(0xffffffffu, b0, o));
+            b1 = fmaxf(b1, __shfl_xor_sync(0xffffffffu, b1, o));
           }
+          const int row = (lane >> 2) + 8 * (lane & 1);
+          const int i = p0 + k * stage_pages + sub * 16 + row;
+          const int page = __shfl_sync(0xffffffffu, page_cur, row);
+          if ((lane & 3) < 2 && i < p1) out[i] = page >= 0 ? (lane & 1 ? b1 : b0) : -INFINITY;
         }
         ++done;
+        slot_out = slot_out + 1 == nst ? 0 : slot_out + 1;
+        parity ^= slot_out == 0 ? 1u : 0u;
         // every warp is past the stage (and, at the last step, past the
         // query's codes): it may be filled again
         if (__syncthreads_or(!ok)) {
+          --done;  // drained below
           stop = true;
           break;
         }
@@ -575,6 +687,7 @@ __global__ void __launch_bounds__(kScoreWarps * 32, 1) page_score_kernel(ScorePa
     bool drained = true;
     for (uint32_t i = done; i < issued; ++i)
       drained &= mbar_drain(smem_u32(&full[i % nst]), (i / nst) & 1);
+    (void)drained;
     if (tid == 0) report(P.error_word, TL_DEVERR_TIMEOUT);
   }
 }
@@ -608,9 +721,16 @@ __global__ void __launch_bounds__(T) page_select_kernel(PageSelectParams P, int 
   const float* x = P.scores + (size_t)row * P.row_stride;
   const int32_t* from = P.block_table + (size_t)b * P.max_pages_per_seq;
   int32_t* to = P.table + (size_t)row * P.n;
-  select_row<T>(
+  if (nb <= P.n) {  // every block
+    for (int i = rank * T + threadIdx.x; i < P.n; i += csize * T)
+      to[i] = i < nb ? __ldg(from + i) : -1;
+    return;
+  }
+  const int2 mine = select_row<T>(
       sh, sel_keys, key_cap, x, nb, P.n, P.first, P.last, rank, csize,
-      [&](int pos, int i) { to[pos] = __ldg(from + i); }, [&](int pos) { to[pos] = -1; });
+      [&](int pos, int i) { to[pos] = i; }, [](int) {});
+  __syncthreads();  // the CTA's blocks are in place: their table entries
+  for (int pos = mine.x + threadIdx.x; pos < mine.y; pos += T) to[pos] = __ldg(from + to[pos]);
 }
 
 }  // namespace tl
@@ -634,8 +754,10 @@ static tl_status bounds_impl(const void* k, const float* k_scales, const int32_t
     return TL_ERR_INVALID_ARG;
   if ((d != 64 && d != 128) || page_size > 256 || kind < 0) return TL_ERR_UNSUPPORTED;
   if ((int64_t)num_pages * page_size >= ((int64_t)1 << 31)) return TL_ERR_UNSUPPORTED;
-  // block counts are summed in 32 bits
-  if ((int64_t)B * max_pages_per_seq > INT32_MAX) return TL_ERR_UNSUPPORTED;
+  // (block, head) pairs are counted in 32 bits
+  if ((int64_t)B * max_pages_per_seq > INT32_MAX ||
+      (int64_t)B * max_pages_per_seq * h_kv > INT32_MAX)
+    return TL_ERR_UNSUPPORTED;
   BoundsParams P;
   P.k = k;
   P.k_scales = k_scales;
@@ -672,13 +794,14 @@ static bool launch_score(const ScoreParams& P, cudaStream_t st) {
   auto kernel = page_score_kernel<D, NT, QF32>;
   const int hs = score_heads(P.h_kv);
   const int q_bytes = score_query_bytes(hs, P.group, D), stage = score_stage_bytes(hs, D);
-  // 227 KiB less the static state
+  // two CTAs share an SM's 228 KiB (each with up to 6 KiB of static state and
+  // the system's 1 KiB): 16 warps, whose waits fill each other's
   int nst = kScoreStages;
-  while (nst > 2 && nst * stage + q_bytes > 227 * 1024 - 6144) --nst;
+  while (nst > 2 && nst * stage + q_bytes > 107 * 1024) --nst;
   const int smem = nst * stage + q_bytes;
   if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem) != cudaSuccess)
     return false;
-  const dim3 grid((unsigned)num_sms(), (unsigned)((P.h_kv + hs - 1) / hs));
+  const dim3 grid((unsigned)num_sms() * 2, (unsigned)((P.h_kv + hs - 1) / hs));
   kernel<<<grid, kScoreWarps * 32, smem, st>>>(P, nst);
   return launch_status() == TL_OK;
 }
@@ -691,11 +814,13 @@ static bool launch_score_group(const ScoreParams& P, cudaStream_t st) {
 SelectShape select_shape(int64_t rows, int64_t cap) {
   SelectShape s;
   s.cluster = 1;
-  // as many CTAs a row as its keys' shared memory asks for
+  // as many CTAs a row as its keys' shared memory asks for: a cluster's
+  // barriers and remote reads cost more than the sweeps that it would divide
+  // (8 rows of 128K values: 23.9 us by 4 CTAs each, 24.7 by 8)
   while (s.cluster < kSelClusterMax && cap > (int64_t)kSelKeysMax * s.cluster) s.cluster *= 2;
   const int64_t slice = ((cap + s.cluster - 1) / s.cluster + 127) / 128 * 128;
   s.keys = (int)std::min<int64_t>(slice, kSelKeysMax);
-  s.threads = slice <= 1024 ? 256 : rows * s.cluster > 2 * num_sms() ? 512 : 1024;
+  s.threads = slice <= 1024 ? 256 : slice <= 4096 && rows * s.cluster > 2 * num_sms() ? 512 : 1024;
   return s;
 }
 

@@ -2247,7 +2247,7 @@ static int decode_warps(int rows) {
 // the additions is fixed (row 0, 1, ...).
 static __global__ void __launch_bounds__(256) decode_mass_kernel(DecodeParams P, float* mass,
                                                                  int64_t mass_len) {
-  constexpr int U = 4;  // keys per lane and round
+  constexpr int U = 4, R = 4;  // keys per lane and rows per round of loads
   asm volatile("griddepcontrol.wait;\n" ::: "memory");
   const int lane = threadIdx.x & 31;
   const int nwarps = gridDim.x * (blockDim.x >> 5);
@@ -2261,33 +2261,43 @@ static __global__ void __launch_bounds__(256) decode_mass_kernel(DecodeParams P,
       const float2 st = __ldcg(reinterpret_cast<const float2*>(P.stats) +
                                (size_t)it.b * P.hq_all + (lane / P.group) * P.h_q +
                                it.g * P.group + lane % P.group);
-      m = st.x;
-      inv = st.y > 0.f ? 1.f / st.y : 0.f;
+      if (st.y > 0.f) {
+        m = st.x;
+        inv = 1.f / st.y;
+      }
     }
     const size_t bg = (size_t)it.b * P.h_kv + it.g;
     const float* srow = P.scores + bg * P.rows * P.score_stride;
     float* mrow = mass + bg * mass_len;
     const int first = max(it.lo, it.c_begin * kChunk);
     const int last = min(it.p, it.c_end * kChunk - 1);
-    for (int j0 = first; j0 <= last; j0 += 32 * U) {
-      float acc[U];
+    for (int j0 = first + lane; j0 - lane <= last; j0 += 32 * U) {
+      float acc[U], was[U];
 #pragma unroll
-      for (int u = 0; u < U; ++u) acc[u] = 0.f;
-      for (int r = 0; r < P.rows; ++r) {
-        const float mr = __shfl_sync(0xffffffffu, m, r), ir = __shfl_sync(0xffffffffu, inv, r);
-        if (ir == 0.f) continue;
+      for (int u = 0; u < U; ++u) {
+        acc[u] = 0.f;
+        was[u] = j0 + 32 * u <= last ? mrow[j0 + 32 * u] : 0.f;
+      }
+      for (int r0 = 0; r0 < P.rows; r0 += R) {
+        float s[R][U];
 #pragma unroll
-        for (int u = 0; u < U; ++u) {
-          const int j = j0 + 32 * u + lane;
-          if (j <= last)
-            acc[u] = fmaf(fast_exp2(__ldcg(srow + r * P.score_stride + j) - mr), ir, acc[u]);
+        for (int r = 0; r < R; ++r)
+#pragma unroll
+          for (int u = 0; u < U; ++u)
+            s[r][u] = r0 + r < P.rows && j0 + 32 * u <= last
+                          ? __ldcg(srow + (r0 + r) * P.score_stride + j0 + 32 * u)
+                          : -INFINITY;
+#pragma unroll
+        for (int r = 0; r < R; ++r) {  // a row past the last has inv 0
+          const float mr = __shfl_sync(0xffffffffu, m, r0 + r);
+          const float ir = __shfl_sync(0xffffffffu, inv, r0 + r);
+#pragma unroll
+          for (int u = 0; u < U; ++u) acc[u] = fmaf(fast_exp2(s[r][u] - mr), ir, acc[u]);
         }
       }
 #pragma unroll
-      for (int u = 0; u < U; ++u) {
-        const int j = j0 + 32 * u + lane;
-        if (j <= last) mrow[j] += acc[u];
-      }
+      for (int u = 0; u < U; ++u)
+        if (j0 + 32 * u <= last) mrow[j0 + 32 * u] = was[u] + acc[u];
     }
   }
 }
@@ -2299,7 +2309,7 @@ static cudaError_t launch_mass(const DecodeParams& P, float* mass, int64_t mass_
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3((unsigned)num_sms() * 4);
+  cfg.gridDim = dim3((unsigned)num_sms() * 6);  // a warp an item, about
   cfg.blockDim = dim3(256);
   cfg.stream = st;
   cfg.attrs = attr;

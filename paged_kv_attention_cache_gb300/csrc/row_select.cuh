@@ -37,20 +37,20 @@ namespace tl {
 constexpr int kSelBins = 4096;
 constexpr int kSelBinBits = 12;
 constexpr int kSelRank = 128;        // values ranked against each other at the end
-constexpr int kSelKeysMax = 16384;   // keys of a slice kept in shared memory (64 KiB)
+constexpr int kSelKeysMax = 32768;   // keys of a slice kept in shared memory (128 KiB)
 constexpr int kSelClusterMax = 8;
 
 // Keys: 0 no value (behind the row), 1 NaN, then the floats in order (-0 =
 // +0), all ones an index that is taken whatever its value.
 constexpr uint32_t kSelForced = 0xffffffffu;
-TL_DEVINLINE uint32_t select_key(float x) {
-  if (x != x) return 1u;
-  const uint32_t u = __float_as_uint(x == 0.f ? 0.f : x);
-  return (u & 0x80000000u) ? ~u : (u | 0x80000000u);
+TL_DEVINLINE uint32_t select_key_number(float x) {  // x is not NaN
+  const uint32_t u = __float_as_uint(x + 0.f);      // -0 + 0 is +0
+  return u ^ ((uint32_t)((int32_t)u >> 31) | 0x80000000u);
 }
+TL_DEVINLINE uint32_t select_key(float x) { return x != x ? 1u : select_key_number(x); }
 
 struct SelectShared {
-  __align__(16) uint32_t hist[2][kSelBins];  // two: one is cleared while peers read the other
+  __align__(16) uint32_t hist[kSelBins];
   uint32_t minmax[2];     // this CTA's smallest and largest key
   uint32_t total;         // this CTA's taken values
   uint32_t tmp[2][32];    // block scans, alternating
@@ -86,9 +86,11 @@ TL_DEVINLINE uint32_t select_block_scan(uint32_t x, uint32_t* tmp, uint32_t& tot
 // One row x[0 .. len), by the CTAs of one cluster (rank `rank` of `csize`;
 // csize 1 needs no cluster launch), T threads each.  keys: key_cap words of
 // 16-byte aligned shared memory, a multiple of 128.  emit(pos, i): index i is
-// taken at place pos; tail(pos): place pos stays empty.
+// taken at place pos; tail(pos): place pos stays empty.  Returns the places
+// that this CTA filled, first and one past the last ({0, 0} where len <= n:
+// each thread filled places rank * T + tid, + csize * T, ...).
 template <int T, class Emit, class Tail>
-__device__ void select_row(SelectShared& sh, uint32_t* keys, int key_cap, const float* x, int len,
+__device__ int2 select_row(SelectShared& sh, uint32_t* keys, int key_cap, const float* x, int len,
                            int n, int first, int last, int rank, int csize, Emit emit,
                            Tail tail) {
   namespace cg = cooperative_groups;
@@ -106,7 +108,7 @@ __device__ void select_row(SelectShared& sh, uint32_t* keys, int key_cap, const 
       if (i < len) emit(i, i);
       else tail(i);
     }
-    return;  // the same for every CTA of the cluster: no barrier is left waiting
+    return make_int2(0, 0);  // every CTA of the cluster: no barrier is left waiting
   }
   // this CTA's slice of the row, and this warp's run of it: whole steps of 128
   // values, four neighbours a lane
@@ -131,13 +133,17 @@ __device__ void select_row(SelectShared& sh, uint32_t* keys, int key_cap, const 
   auto keys_of = [&](const float4& f, int i) {
     return make_uint4(key_of(f.x, i), key_of(f.y, i + 1), key_of(f.z, i + 2), key_of(f.w, i + 3));
   };
-  // a lane reads back only the keys it stored
+  // a lane reads back the keys it stored; behind a barrier, any of its warp's
   auto keys_at = [&](int i) {
     return i - i0 < key_cap ? *reinterpret_cast<const uint4*>(keys + (i - i0))
                             : keys_of(load4(i), i);
   };
 
-  for (int b = tid; b < 2 * kSelBins; b += T) (&sh.hist[0][0])[b] = 0u;
+  auto clear_hist = [&]() {
+    for (int b = tid; b < kSelBins / 4; b += T)
+      reinterpret_cast<uint4*>(sh.hist)[b] = make_uint4(0u, 0u, 0u, 0u);
+  };
+  clear_hist();
   if (tid == 0) {
     sh.n_cand = 0u;
     sh.minmax[0] = kSelForced;
@@ -151,18 +157,30 @@ __device__ void select_row(SelectShared& sh, uint32_t* keys, int key_cap, const 
     for (int u = 0; u < U; ++u) f[u] = load4(w + 128 * u + 4 * lane);
 #pragma unroll
     for (int u = 0; u < U; ++u) {
-      const int i = w + 128 * u + 4 * lane;
-      if (w + 128 * u >= w1) break;
-      const uint4 k = keys_of(f[u], i);
-      if (i - i0 < key_cap) *reinterpret_cast<uint4*>(keys + (i - i0)) = k;
-      const uint32_t kk[4] = {k.x, k.y, k.z, k.w};
+      const int ws = w + 128 * u, i = ws + 4 * lane;
+      if (ws >= w1) break;
+      uint4 k;
+      if (ws >= m0 && ws + 128 <= m1) {  // all of the step is in the middle
+        k = make_uint4(select_key_number(f[u].x), select_key_number(f[u].y),
+                       select_key_number(f[u].z), select_key_number(f[u].w));
+        const float any = (f[u].x + f[u].y) + (f[u].z + f[u].w);
+        if (any != any)  // a NaN (or opposite infinities) among the four
+          k = make_uint4(select_key(f[u].x), select_key(f[u].y), select_key(f[u].z),
+                         select_key(f[u].w));
+        kmin = min(min(min(kmin, k.x), min(k.y, k.z)), k.w);
+        kmax = max(max(max(kmax, k.x), max(k.y, k.z)), k.w);
+      } else {
+        k = keys_of(f[u], i);
+        const uint32_t kk[4] = {k.x, k.y, k.z, k.w};
 #pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        if (kk[j] - 1u < kSelForced - 1u) {  // neither none nor forced
-          kmin = min(kmin, kk[j]);
-          kmax = max(kmax, kk[j]);
+        for (int j = 0; j < 4; ++j) {
+          if (kk[j] - 1u < kSelForced - 1u) {  // neither none nor forced
+            kmin = min(kmin, kk[j]);
+            kmax = max(kmax, kk[j]);
+          }
         }
       }
+      if (i - i0 < key_cap) *reinterpret_cast<uint4*>(keys + (i - i0)) = k;
     }
   }
   kmin = __reduce_min_sync(0xffffffffu, kmin);
@@ -191,7 +209,8 @@ __device__ void select_row(SelectShared& sh, uint32_t* keys, int key_cap, const 
   uint32_t need = (uint32_t)(n - first - last), cnt = (uint32_t)(m1 - m0);
   uint32_t lo = kmin, span = kmax - kmin, equal = 0u;
   bool by_index = false;
-  uint32_t count = 0;  // this warp's taken values
+  uint32_t count = 0;  // this warp's taken values, once `counted`
+  bool counted = false;
   // the last pair taken; none so far: above every value, below the forced
   uint32_t last_key = kSelForced - 1u;
   int last_idx = -1;
@@ -222,13 +241,58 @@ __device__ void select_row(SelectShared& sh, uint32_t* keys, int key_cap, const 
     if (cnt <= (uint32_t)kSelRank) {  // rank them
       uint32_t* n_cand = peer(&sh.n_cand, 0);
       uint32_t* cand = peer(&sh.cand[0][0], 0);
-      in_range([&](uint32_t, int i, uint32_t k) {
-        const uint32_t at = atomicAdd(n_cand, 1u);
-        if (at < (uint32_t)kSelRank) {
-          cand[at] = k;
-          cand[kSelRank + at] = (uint32_t)i;
+      if (by_index) {
+        in_range([&](uint32_t, int i, uint32_t k) {
+          const uint32_t at = atomicAdd(n_cand, 1u);
+          if (at < (uint32_t)kSelRank) {
+            cand[at] = k;
+            cand[kSelRank + at] = (uint32_t)i;
+          }
+        });
+      } else {  // the same sweep counts the values above the range
+        counted = true;
+        const uint32_t hi = lo + span;
+        // a lane keeps the last two it meets and lists them behind the sweep
+        // (listing each as it is met stalls the warp every other step); one
+        // that meets more walks its values again
+        uint32_t met = 0u, k0 = 0u, k1 = 0u;
+        int x0 = 0, x1 = 0;
+        auto look1 = [&](uint32_t k, int i) {
+          count += k > hi ? 1u : 0u;
+          if (k - lo <= span) {
+            k1 = k0;
+            x1 = x0;
+            k0 = k;
+            x0 = i;
+            ++met;
+          }
+        };
+#pragma unroll 4
+        for (int w = w0; w < w1; w += 128) {
+          const int i = w + 4 * lane;
+          const uint4 k = keys_at(i);
+          look1(k.x, i);
+          look1(k.y, i + 1);
+          look1(k.z, i + 2);
+          look1(k.w, i + 3);
         }
-      });
+        auto list = [&](uint32_t k, int i) {
+          const uint32_t at = atomicAdd(n_cand, 1u);
+          if (at < (uint32_t)kSelRank) {
+            cand[at] = k;
+            cand[kSelRank + at] = (uint32_t)i;
+          }
+        };
+        if (met == 1u || met == 2u) list(k0, x0);
+        if (met == 2u) list(k1, x1);
+        if (met > 2u)
+          for (int i = w0 + 4 * lane; i < w1; i += 128) {
+            const uint4 k = keys_at(i);
+            const uint32_t kk[4] = {k.x, k.y, k.z, k.w};
+            for (int j = 0; j < 4; ++j)
+              if (kk[j] - lo <= span) list(kk[j], i + j);
+          }
+      }
       cluster_sync();
       uint32_t* ck = &sh.cand[0][0];
       if (csize > 1 && rank != 0) {  // a copy of rank 0's list
@@ -238,20 +302,32 @@ __device__ void select_row(SelectShared& sh, uint32_t* keys, int key_cap, const 
         }
         __syncthreads();
       }
-      if (tid < (int)cnt) {
-        const uint32_t k = ck[tid], at = ck[kSelRank + tid];
-        uint32_t better = 0;
+      // T / kSelRank threads a value, each against its share of the others
+      constexpr int kShare = T / kSelRank;
+      const int mine = tid / kShare;
+      uint32_t k = 0u, at = 0u, better = 0u;
+      if (mine < (int)cnt) {
+        k = ck[mine];
+        at = ck[kSelRank + mine];
 #pragma unroll 4
-        for (uint32_t c = 0; c < cnt; ++c)
+        for (int c = tid % kShare; c < (int)cnt; c += kShare)
           better += ck[c] > k || (ck[c] == k && ck[kSelRank + c] < at) ? 1u : 0u;
-        if (better == need - 1) {
-          sh.last[0] = k;
-          sh.last[1] = at;
-        }
+      }
+#pragma unroll
+      for (int o = 1; o < kShare; o <<= 1) better += __shfl_xor_sync(0xffffffffu, better, o);
+      if (mine < (int)cnt && better == need - 1) {  // its threads write the same
+        sh.last[0] = k;
+        sh.last[1] = at;
       }
       __syncthreads();
       last_key = sh.last[0];
       last_idx = (int)sh.last[1];
+      if (counted)  // the ranked values that are taken and this warp's
+        for (int c = lane; c < (int)cnt; c += 32) {
+          const int i = (int)ck[kSelRank + c];
+          if (i >= w0 && i < w1 && (ck[c] > last_key || (ck[c] == last_key && i <= last_idx)))
+            ++count;
+        }
       break;
     }
     if (span == 0u && !by_index) {  // one key: on over the indices
@@ -262,7 +338,12 @@ __device__ void select_row(SelectShared& sh, uint32_t* keys, int key_cap, const 
     }
     const int bits = 32 - __clz(span);
     const int shift = bits > kSelBinBits ? bits - kSelBinBits : 0;
-    uint32_t* hist = sh.hist[pass & 1];
+    if (pass > 0) {
+      if (csize > 1) cg::this_cluster().sync();  // peers are past the last pass's histogram
+      clear_hist();
+      __syncthreads();
+    }
+    uint32_t* hist = sh.hist;
     in_range([&](uint32_t off, int, uint32_t) { atomicAdd(hist + (off >> shift), 1u); });
     cluster_sync();
     // from the top bin down: thread t takes the PER bins that end below
@@ -309,11 +390,7 @@ __device__ void select_row(SelectShared& sh, uint32_t* keys, int key_cap, const 
       sh.found[1] = above;
       sh.found[2] = in;
     }
-    // the other histogram is cleared for the next pass: its readers are past
-    // it since the barrier above
-    if (pass > 0)
-      for (int b = tid; b < kSelBins; b += T) sh.hist[(pass + 1) & 1][b] = 0u;
-    cluster_sync();
+    __syncthreads();
     const uint32_t bin = sh.found[0];
     need -= sh.found[1];
     cnt = sh.found[2];
@@ -321,47 +398,72 @@ __device__ void select_row(SelectShared& sh, uint32_t* keys, int key_cap, const 
     span = min(span - (bin << shift), (1u << shift) - 1u);
   }
 
-  // Place the taken values in index order: each warp counts its run's, a scan
-  // over the warps (and the cluster's earlier CTAs) gives its first place.
   auto taken = [&](uint32_t k, int i) {
     return k > last_key || (k == last_key && i <= last_idx);
   };
+  // Place the taken values in index order: each warp's count (most came with
+  // the last sweep), a scan over the warps, the cluster's earlier CTAs.
+  if (!counted) {
 #pragma unroll 2
-  for (int w = w0; w < w1; w += 128) {
-    const int i = w + 4 * lane;
-    const uint4 k = keys_at(i);
-    count += (taken(k.x, i) ? 1u : 0u) + (taken(k.y, i + 1) ? 1u : 0u) +
-             (taken(k.z, i + 2) ? 1u : 0u) + (taken(k.w, i + 3) ? 1u : 0u);
+    for (int w = w0; w < w1; w += 128) {
+      const int i = w + 4 * lane;
+      const uint4 k = keys_at(i);
+      count += (taken(k.x, i) ? 1u : 0u) + (taken(k.y, i + 1) ? 1u : 0u) +
+               (taken(k.z, i + 2) ? 1u : 0u) + (taken(k.w, i + 3) ? 1u : 0u);
+    }
   }
   count = __reduce_add_sync(0xffffffffu, count);
   __syncthreads();  // sh.tmp is free
   uint32_t total;
-  uint32_t at = select_block_scan(lane == 0 ? count : 0u, sh.tmp[0], total);
+  int at = (int)select_block_scan(lane == 0 ? count : 0u, sh.tmp[0], total);
   at = __shfl_sync(0xffffffffu, at, 0);
+  int base = 0;
   if (csize > 1) {
     if (tid == 0) sh.total = total;
     cg::this_cluster().sync();
 #pragma unroll
     for (int r = 0; r < kSelClusterMax; ++r)
-      if (r < rank) at += *peer(&sh.total, r);
+      if (r < rank) base += (int)*peer(&sh.total, r);
+    at += base;
+    // no peer's shared memory is read behind this point
+    asm volatile("barrier.cluster.arrive.release.aligned;\n" ::: "memory");
   }
   const uint32_t below = (1u << lane) - 1u;
-  for (int w = w0; w < w1 && count > 0; w += 128) {
+  const int end = at + (int)count;
+  for (int w = w0; w < w1 && at < end; w += 128) {
     const int i = w + 4 * lane;
     const uint4 k = keys_at(i);
-    const bool t0 = taken(k.x, i), t1 = taken(k.y, i + 1), t2 = taken(k.z, i + 2),
-               t3 = taken(k.w, i + 3);
-    const uint32_t s0 = __ballot_sync(0xffffffffu, t0), s1 = __ballot_sync(0xffffffffu, t1);
-    const uint32_t s2 = __ballot_sync(0xffffffffu, t2), s3 = __ballot_sync(0xffffffffu, t3);
-    int pos = (int)at + __popc(s0 & below) + __popc(s1 & below) + __popc(s2 & below) +
-              __popc(s3 & below);
-    if (t0) emit(pos++, i);
-    if (t1) emit(pos++, i + 1);
-    if (t2) emit(pos++, i + 2);
-    if (t3) emit(pos, i + 3);
-    at += (uint32_t)(__popc(s0) + __popc(s1) + __popc(s2) + __popc(s3));
+    bool t0, t1, t2, t3;
+    if (w <= last_idx && last_idx < w + 128) {  // the step of the last one taken
+      t0 = taken(k.x, i);
+      t1 = taken(k.y, i + 1);
+      t2 = taken(k.z, i + 2);
+      t3 = taken(k.w, i + 3);
+    } else {  // equal values are all taken before it, and none behind it
+      const uint32_t over = w > last_idx ? last_key : last_key - 1u;  // last_key >= 1
+      t0 = k.x > over;
+      t1 = k.y > over;
+      t2 = k.z > over;
+      t3 = k.w > over;
+    }
+    // the lanes' counts (0 to 4) added up bit by bit
+    const uint32_t c = (t0 ? 1u : 0u) + (t1 ? 1u : 0u) + (t2 ? 1u : 0u) + (t3 ? 1u : 0u);
+    const uint32_t s0 = __ballot_sync(0xffffffffu, c & 1u);
+    const uint32_t s1 = __ballot_sync(0xffffffffu, c & 2u);
+    const uint32_t s2 = __ballot_sync(0xffffffffu, c & 4u);
+    if ((s0 | s1 | s2) == 0u) continue;
+    if (c != 0u) {
+      int pos = at + __popc(s0 & below) + 2 * __popc(s1 & below) + 4 * __popc(s2 & below);
+      if (t0) emit(pos++, i);
+      if (t1) emit(pos++, i + 1);
+      if (t2) emit(pos++, i + 2);
+      if (t3) emit(pos, i + 3);
+    }
+    at += __popc(s0) + 2 * __popc(s1) + 4 * __popc(s2);
   }
-  if (csize > 1) cg::this_cluster().sync();  // peers may still read this CTA's totals
+  if (csize > 1)  // the CTA stays until its peers have read its totals
+    asm volatile("barrier.cluster.wait.acquire.aligned;\n" ::: "memory");
+  return make_int2(base, base + (int)total);
 }
 
 // Threads per CTA, CTAs per row and keys kept per CTA for `rows` rows of up to

@@ -301,7 +301,7 @@ def random_keep(lens, hkv, n, seed):
     ("bf16", 128, 16, 8, True), ("bf16", 64, 8, 2, False), ("bf16", 96, 16, 3, True),
     ("bf16", 8, 5, 1, True), ("f32", 128, 16, 2, True), ("f32", 64, 3, 5, False),
     ("e4m3", 128, 16, 4, True), ("e4m3", 16, 32, 2, False), ("int8", 128, 16, 4, True),
-    ("int8", 48, 24, 3, True), ("int8", 16, 16, 2, False),
+    ("int8", 48, 24, 3, True), ("int8", 16, 16, 2, False), ("f32", 1024, 4, 40, False),
 ])
 @pytest.mark.parametrize("n", [1, 70, 400])
 def test_compact_moves_the_rows(kind, d, ps, hkv, with_mass, n):
