@@ -20,7 +20,7 @@ struct EvictParams {
   uint32_t* error_word;
 };
 
-template <int T>
+template <int T, bool FITS>
 __global__ void __launch_bounds__(T) evict_select_kernel(EvictParams P, int csize, int key_cap) {
   __shared__ SelectShared sh;
   extern __shared__ __align__(16) uint32_t sel_keys[];
@@ -34,7 +34,7 @@ __global__ void __launch_bounds__(T) evict_select_kernel(EvictParams P, int csiz
   }
   const float* x = P.mass + (size_t)row * P.mass_len;
   int32_t* to = P.keep + (size_t)row * P.n;
-  select_row<T>(
+  select_row<T, FITS>(
       sh, sel_keys, key_cap, x, len, P.n, P.first, P.last, rank, csize,
       [&](int pos, int i) { to[pos] = i; }, [&](int pos) { to[pos] = -1; });
 }
@@ -275,9 +275,10 @@ extern "C" tl_status tl_kv_evict_select(const float* mass, int32_t mass_len,
   const SelectShape s = select_shape(rows, mass_len);
   int csize = s.cluster, key_cap = s.keys;
   void* args[] = {&P, &csize, &key_cap};
-  const void* const kernels[3] = {reinterpret_cast<const void*>(evict_select_kernel<256>),
-                                  reinterpret_cast<const void*>(evict_select_kernel<512>),
-                                  reinterpret_cast<const void*>(evict_select_kernel<1024>)};
+  const void* const kernels[4] = {reinterpret_cast<const void*>(evict_select_kernel<256, true>),
+                                  reinterpret_cast<const void*>(evict_select_kernel<512, true>),
+                                  reinterpret_cast<const void*>(evict_select_kernel<1024, true>),
+                                  reinterpret_cast<const void*>(evict_select_kernel<1024, false>)};
   if (launch_rows(kernels, rows, s, args, false, (cudaStream_t)stream) != cudaSuccess)
     return TL_ERR_CUDA;
   return launch_status();

@@ -79,6 +79,24 @@ TL_DEVINLINE void mma_f16_16816(float* c, uint32_t a0, uint32_t a1, uint32_t a2,
       : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
 }
 
+// round-half-even(x / s) as the f32 quotient rounds, clamped to +-127, for s >
+// 0 and |x / s| <= 128: the product with 1 / s is within 2 x 10^-5 of the
+// quotient, so it rounds alike unless it lies within 5 x 10^-4 of a half,
+// where (and for an s whose reciprocal is out of range) the division is done.
+struct Quotient {
+  float s, inv;
+  bool fast;
+  TL_DEVINLINE explicit Quotient(float scale) : s(scale), inv(0.f), fast(scale > 1e-30f && scale < 1e30f) {
+    if (fast) inv = __fdividef(1.f, s);
+  }
+  TL_DEVINLINE int code(float x) const {
+    const float r = x * inv;
+    float c = rintf(r);
+    if (!fast || fabsf(r - c) > 0.4995f) c = s > 0.f ? rintf(__fdiv_rn(x, s)) : 0.f;
+    return __float2int_rn(fminf(fmaxf(c, -127.f), 127.f));
+  }
+};
+
 // max / min that return NaN when either is
 TL_DEVINLINE float max_nan(float a, float b) {
   float r;
@@ -251,13 +269,13 @@ TL_DEVINLINE void page_bounds(const BoundsParams& P, int page, int g, int live, 
     m = largest();
   }
   const float s = __fdiv_rn(m, 127.f);
+  const Quotient quot(s);
   if (row < 2) {  // the first row group writes the max codes, the second the min codes
     uint32_t packed[(V + 3) / 4];
 #pragma unroll
     for (int e = 0; e < V; ++e) {
       const float b = row == 0 ? top[e] : low[e];
-      const float c = s > 0.f ? fminf(fmaxf(rintf(__fdiv_rn(b, s)), -127.f), 127.f) : 0.f;
-      const uint32_t byte = (uint32_t)(uint8_t)(int8_t)__float2int_rn(c);
+      const uint32_t byte = (uint32_t)(uint8_t)(int8_t)quot.code(b);
       if (e % 4 == 0) packed[e / 4] = byte;
       else packed[e / 4] |= byte << (8 * (e % 4));
     }
@@ -268,8 +286,7 @@ TL_DEVINLINE void page_bounds(const BoundsParams& P, int page, int g, int live, 
     if (RPW == 1) {  // an f32 row of 128 takes the whole warp: it writes both
 #pragma unroll
       for (int e = 0; e < V; ++e) {
-        const float c = s > 0.f ? fminf(fmaxf(rintf(__fdiv_rn(low[e], s)), -127.f), 127.f) : 0.f;
-        const uint32_t byte = (uint32_t)(uint8_t)(int8_t)__float2int_rn(c);
+        const uint32_t byte = (uint32_t)(uint8_t)(int8_t)quot.code(low[e]);
         if (e % 4 == 0) packed[e / 4] = byte;
         else packed[e / 4] |= byte << (8 * (e % 4));
       }
@@ -297,7 +314,7 @@ constexpr int kBoundsSeqs = 1024;  // sequences placed per round
 // decode steps): the work is even whatever the lengths, and the host needs to
 // know none of them.
 template <int D, int KIND>
-__global__ void __launch_bounds__(kBoundsThreads) page_bounds_kernel(BoundsParams P) {
+__global__ void __launch_bounds__(kBoundsThreads, KIND == kInt8 || KIND == kE4m3 ? 3 : 4) page_bounds_kernel(BoundsParams P) {
   __shared__ int start[kBoundsSeqs + 1];  // first block of each sequence of the round
   __shared__ uint32_t tmp[32];
   const int tid = threadIdx.x, lane = tid & 31;
@@ -546,14 +563,13 @@ __global__ void __launch_bounds__(kScoreWarps * 32, 2) page_score_kernel(ScorePa
         m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 1));
         m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 2));
         const float t = __fdiv_rn(m, 127.f);
+        const Quotient quot(t);
 #pragma unroll
         for (int i = 0; i < E / 4; ++i) {
           uint32_t code = 0;
 #pragma unroll
           for (int j = 0; j < 4; ++j) {
-            const float c =
-                t > 0.f ? fminf(fmaxf(rintf(__fdiv_rn(x[4 * i + j], t)), -127.f), 127.f) : 0.f;
-            code |= (uint32_t)(uint8_t)(int8_t)__float2int_rn(c) << (8 * j);
+            code |= (uint32_t)(uint8_t)(int8_t)quot.code(x[4 * i + j]) << (8 * j);
           }
           *reinterpret_cast<uint32_t*>(q_codes + r * D + e0 + 4 * i) = code;
         }
@@ -705,7 +721,7 @@ struct PageSelectParams {
   uint32_t* error_word;
 };
 
-template <int T>
+template <int T, bool FITS>
 __global__ void __launch_bounds__(T) page_select_kernel(PageSelectParams P, int csize, int key_cap) {
   __shared__ SelectShared sh;
   extern __shared__ __align__(16) uint32_t sel_keys[];
@@ -726,7 +742,7 @@ __global__ void __launch_bounds__(T) page_select_kernel(PageSelectParams P, int 
       to[i] = i < nb ? __ldg(from + i) : -1;
     return;
   }
-  const int2 mine = select_row<T>(
+  const int2 mine = select_row<T, FITS>(
       sh, sel_keys, key_cap, x, nb, P.n, P.first, P.last, rank, csize,
       [&](int pos, int i) { to[pos] = i; }, [](int) {});
   __syncthreads();  // the CTA's blocks are in place: their table entries
@@ -774,7 +790,7 @@ static tl_status bounds_impl(const void* k, const float* k_scales, const int32_t
   P.error_word = error_word;
   const int64_t most = ((int64_t)B * max_pages_per_seq * h_kv + kBoundsThreads / 32 - 1) /
                        (kBoundsThreads / 32);
-  const unsigned grid = (unsigned)std::min<int64_t>(most, (int64_t)num_sms() * 6);
+  const unsigned grid = (unsigned)std::min<int64_t>(most, (int64_t)num_sms() * 4);  // one wave
   cudaStream_t st = (cudaStream_t)stream;
 #define TL_BOUNDS(K)                                                              \
   do {                                                                            \
@@ -820,13 +836,14 @@ SelectShape select_shape(int64_t rows, int64_t cap) {
   while (s.cluster < kSelClusterMax && cap > (int64_t)kSelKeysMax * s.cluster) s.cluster *= 2;
   const int64_t slice = ((cap + s.cluster - 1) / s.cluster + 127) / 128 * 128;
   s.keys = (int)std::min<int64_t>(slice, kSelKeysMax);
+  s.fits = slice <= kSelKeysMax;  // else 1,024 threads, by the rule below
   s.threads = slice <= 1024 ? 256 : slice <= 4096 && rows * s.cluster > 2 * num_sms() ? 512 : 1024;
   return s;
 }
 
-cudaError_t launch_rows(const void* const (&kernels)[3], int64_t rows, const SelectShape& s,
+cudaError_t launch_rows(const void* const (&kernels)[4], int64_t rows, const SelectShape& s,
                         void** args, bool dependent, cudaStream_t st) {
-  const void* kernel = kernels[s.threads == 256 ? 0 : s.threads == 512 ? 1 : 2];
+  const void* kernel = kernels[!s.fits ? 3 : s.threads == 256 ? 0 : s.threads == 512 ? 1 : 2];
   const int smem = s.keys * (int)sizeof(uint32_t);
   cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
   if (e != cudaSuccess) return e;
@@ -960,9 +977,10 @@ extern "C" tl_status tl_kv_page_select(const void* q, tl_dtype q_dtype, const in
   const SelectShape s = select_shape(rows, max_pages_per_seq);
   int csize = s.cluster, key_cap = s.keys;
   void* args[] = {&P, &csize, &key_cap};
-  const void* const kernels[3] = {reinterpret_cast<const void*>(page_select_kernel<256>),
-                                  reinterpret_cast<const void*>(page_select_kernel<512>),
-                                  reinterpret_cast<const void*>(page_select_kernel<1024>)};
+  const void* const kernels[4] = {reinterpret_cast<const void*>(page_select_kernel<256, true>),
+                                  reinterpret_cast<const void*>(page_select_kernel<512, true>),
+                                  reinterpret_cast<const void*>(page_select_kernel<1024, true>),
+                                  reinterpret_cast<const void*>(page_select_kernel<1024, false>)};
   if (launch_rows(kernels, rows, s, args, true, st) != cudaSuccess) return TL_ERR_CUDA;
   return launch_status();
 }

@@ -85,11 +85,11 @@ TL_DEVINLINE uint32_t select_block_scan(uint32_t x, uint32_t* tmp, uint32_t& tot
 
 // One row x[0 .. len), by the CTAs of one cluster (rank `rank` of `csize`;
 // csize 1 needs no cluster launch), T threads each.  keys: key_cap words of
-// 16-byte aligned shared memory, a multiple of 128.  emit(pos, i): index i is
+// 16-byte aligned shared memory, a multiple of 128 (FITS: no slice is longer).  emit(pos, i): index i is
 // taken at place pos; tail(pos): place pos stays empty.  Returns the places
 // that this CTA filled, first and one past the last ({0, 0} where len <= n:
 // each thread filled places rank * T + tid, + csize * T, ...).
-template <int T, class Emit, class Tail>
+template <int T, bool FITS, class Emit, class Tail>
 __device__ int2 select_row(SelectShared& sh, uint32_t* keys, int key_cap, const float* x, int len,
                            int n, int first, int last, int rank, int csize, Emit emit,
                            Tail tail) {
@@ -135,7 +135,7 @@ __device__ int2 select_row(SelectShared& sh, uint32_t* keys, int key_cap, const 
   };
   // a lane reads back the keys it stored; behind a barrier, any of its warp's
   auto keys_at = [&](int i) {
-    return i - i0 < key_cap ? *reinterpret_cast<const uint4*>(keys + (i - i0))
+    return FITS || i - i0 < key_cap ? *reinterpret_cast<const uint4*>(keys + (i - i0))
                             : keys_of(load4(i), i);
   };
 
@@ -180,7 +180,7 @@ __device__ int2 select_row(SelectShared& sh, uint32_t* keys, int key_cap, const 
           }
         }
       }
-      if (i - i0 < key_cap) *reinterpret_cast<uint4*>(keys + (i - i0)) = k;
+      if (FITS || i - i0 < key_cap) *reinterpret_cast<uint4*>(keys + (i - i0)) = k;
     }
   }
   kmin = __reduce_min_sync(0xffffffffu, kmin);
@@ -214,24 +214,20 @@ __device__ int2 select_row(SelectShared& sh, uint32_t* keys, int key_cap, const 
   // the last pair taken; none so far: above every value, below the forced
   uint32_t last_key = kSelForced - 1u;
   int last_idx = -1;
-  // f(place in the range, index, key) for this warp's values in the range
-  auto in_range = [&](auto f) {
-#pragma unroll 2
+  // f(index, key) for this warp's values that the range may hold
+  auto each = [&](auto f) {
+#pragma unroll 4
     for (int w = w0; w < w1; w += 128) {
       const int i = w + 4 * lane;
       const uint4 k = keys_at(i);
-      const uint32_t kk[4] = {k.x, k.y, k.z, k.w};
-#pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        if (!by_index) {
-          if (kk[j] - lo <= span) f(kk[j] - lo, i + j, kk[j]);
-        } else if (kk[j] == equal) {
-          const uint32_t v = (uint32_t)(len - 1 - i - j);
-          if (v - lo <= span) f(v - lo, i + j, kk[j]);
-        }
-      }
+      f(i, k.x);
+      f(i + 1, k.y);
+      f(i + 2, k.z);
+      f(i + 3, k.w);
     }
   };
+  // places of equal keys: from the row's end, so that the lowest is the largest
+  auto place = [&](int i) { return (uint32_t)(len - 1 - i); };
   for (int pass = 0; need > 0; ++pass) {
     if (need == cnt) {  // all of the range
       last_key = by_index ? equal : lo;
@@ -242,7 +238,8 @@ __device__ int2 select_row(SelectShared& sh, uint32_t* keys, int key_cap, const 
       uint32_t* n_cand = peer(&sh.n_cand, 0);
       uint32_t* cand = peer(&sh.cand[0][0], 0);
       if (by_index) {
-        in_range([&](uint32_t, int i, uint32_t k) {
+        each([&](int i, uint32_t k) {
+          if (k != equal || place(i) - lo > span) return;
           const uint32_t at = atomicAdd(n_cand, 1u);
           if (at < (uint32_t)kSelRank) {
             cand[at] = k;
@@ -267,15 +264,7 @@ __device__ int2 select_row(SelectShared& sh, uint32_t* keys, int key_cap, const 
             ++met;
           }
         };
-#pragma unroll 4
-        for (int w = w0; w < w1; w += 128) {
-          const int i = w + 4 * lane;
-          const uint4 k = keys_at(i);
-          look1(k.x, i);
-          look1(k.y, i + 1);
-          look1(k.z, i + 2);
-          look1(k.w, i + 3);
-        }
+        each([&](int i, uint32_t k) { look1(k, i); });
         auto list = [&](uint32_t k, int i) {
           const uint32_t at = atomicAdd(n_cand, 1u);
           if (at < (uint32_t)kSelRank) {
@@ -344,7 +333,15 @@ __device__ int2 select_row(SelectShared& sh, uint32_t* keys, int key_cap, const 
       __syncthreads();
     }
     uint32_t* hist = sh.hist;
-    in_range([&](uint32_t off, int, uint32_t) { atomicAdd(hist + (off >> shift), 1u); });
+    if (!by_index) {
+      each([&](int, uint32_t k) {
+        if (k - lo <= span) atomicAdd(hist + ((k - lo) >> shift), 1u);
+      });
+    } else {
+      each([&](int i, uint32_t k) {
+        if (k == equal && place(i) - lo <= span) atomicAdd(hist + ((place(i) - lo) >> shift), 1u);
+      });
+    }
     cluster_sync();
     // from the top bin down: thread t takes the PER bins that end below
     // kSelBins - t * PER
@@ -404,13 +401,7 @@ __device__ int2 select_row(SelectShared& sh, uint32_t* keys, int key_cap, const 
   // Place the taken values in index order: each warp's count (most came with
   // the last sweep), a scan over the warps, the cluster's earlier CTAs.
   if (!counted) {
-#pragma unroll 2
-    for (int w = w0; w < w1; w += 128) {
-      const int i = w + 4 * lane;
-      const uint4 k = keys_at(i);
-      count += (taken(k.x, i) ? 1u : 0u) + (taken(k.y, i + 1) ? 1u : 0u) +
-               (taken(k.z, i + 2) ? 1u : 0u) + (taken(k.w, i + 3) ? 1u : 0u);
-    }
+    each([&](int i, uint32_t k) { count += taken(k, i) ? 1u : 0u; });
   }
   count = __reduce_add_sync(0xffffffffu, count);
   __syncthreads();  // sh.tmp is free
@@ -470,12 +461,13 @@ __device__ int2 select_row(SelectShared& sh, uint32_t* keys, int key_cap, const 
 // cap values.
 struct SelectShape {
   int threads, cluster, keys;
+  bool fits;  // every slice's keys are kept
 };
 SelectShape select_shape(int64_t rows, int64_t cap);
-// Launch of a kernel (its three forms: 256, 512 and 1,024 threads) over `rows`
-// clusters; dependent: a programmatic dependent of the stream's previous
-// kernel.
-cudaError_t launch_rows(const void* const (&kernels)[3], int64_t rows, const SelectShape& s,
+// Launch of a kernel over `rows` clusters (its forms: 256, 512 and 1,024
+// threads, then 1,024 threads with slices that do not fit); dependent: a
+// programmatic dependent of the stream's previous kernel.
+cudaError_t launch_rows(const void* const (&kernels)[4], int64_t rows, const SelectShape& s,
                         void** args, bool dependent, cudaStream_t st);
 
 }  // namespace tl
