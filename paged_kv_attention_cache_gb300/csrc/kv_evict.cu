@@ -22,7 +22,7 @@ struct EvictParams {
 
 template <int T, bool FITS>
 __global__ void __launch_bounds__(T) evict_select_kernel(EvictParams P, int csize, int key_cap) {
-  __shared__ SelectShared sh;
+  __shared__ SelectShared<T> sh;
   extern __shared__ __align__(16) uint32_t sel_keys[];
   const int row = blockIdx.x / csize, rank = blockIdx.x % csize;
   const int b = row / P.h_kv;

@@ -70,13 +70,12 @@ TL_DEVINLINE void i8x4_as_f16x2x2(uint32_t w, uint32_t& lo, uint32_t& hi) {
   asm("sub.rn.f16x2 %0, %0, %1;\n" : "+r"(lo) : "r"(0x64806480u));
   asm("sub.rn.f16x2 %0, %0, %1;\n" : "+r"(hi) : "r"(0x64806480u));
 }
-TL_DEVINLINE void mma_f16_16816(float* c, uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3,
-                                uint32_t b0, uint32_t b1) {
-  asm(
-      "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, "
-      "{%8,%9}, {%0,%1,%2,%3};\n"
-      : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
-      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+// D(16x8, s32) += A(16x32, s8, row) * B(32x8, s8, col)
+TL_DEVINLINE void mma_s8_16832(int* c, const uint32_t* a, const uint32_t* b) {
+  asm("mma.sync.aligned.m16n8k32.row.col.s32.s8.s8.s32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, "
+      "{%0,%1,%2,%3};\n"
+      : "+r"(c[0]), "+r"(c[1]), "+r"(c[2]), "+r"(c[3])
+      : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b[0]), "r"(b[1]));
 }
 
 // round-half-even(x / s) as the f32 quotient rounds, clamped to +-127, for s >
@@ -444,7 +443,7 @@ __global__ void __launch_bounds__(kScoreWarps * 32, 2) page_score_kernel(ScorePa
   extern __shared__ __align__(16) unsigned char score_sm[];
   __shared__ int start[kScoreSeqs + 1];  // first unit of each sequence of the round
   __shared__ uint32_t tmp[32];
-  constexpr int KS = D / 16;  // k steps of the max codes, and of the min codes
+  constexpr int KS = D / 32;  // k steps of the max codes, and of the min codes
   __shared__ float q_scale[kScoreWarps * 8 * NT];
   __shared__ unsigned long long full[kScoreStages];
   __shared__ int abort_flag;
@@ -490,49 +489,73 @@ __global__ void __launch_bounds__(kScoreWarps * 32, 2) page_score_kernel(ScorePa
     }
     if (tid == 0) start[kScoreSeqs] = (int)total;
     __syncthreads();
-    int u = (int)even_share(total, blockIdx.x, gridDim.x);
+    const int u0 = (int)even_share(total, blockIdx.x, gridDim.x);
     const int u1 = (int)even_share(total, blockIdx.x + 1, gridDim.x);
-    while (u < u1 && !stop) {
+    // The CTA's units as segments, one sequence each: pages p0 .. p1 of
+    // sequence b in steps of a stage.  Two cursors walk them: copies are
+    // issued a ring ahead of the computation, on into the next segments.
+    struct Segment {
+      int next, b, p0, p1, steps;  // next: the first unit behind it
+      const int32_t* table;
+    };
+    auto open = [&](Segment& s) {
+      const int u = s.next;
+      if (u >= u1) return false;
       int lo = 0, hi = kScoreSeqs;  // the last sequence that starts at or before u
       while (hi - lo > 1) {
         const int mid = (lo + hi) >> 1;
         if (start[mid] <= u) lo = mid;
         else hi = mid;
       }
-      const int b = base + lo;
-      const int nb = blocks_of(P.context_lens[b], P.max_pages_per_seq, P.page_size);
-      const int u2 = min(u1, start[lo + 1]);
-      const int p0 = (u - start[lo]) * kScoreUnit, p1 = min((u2 - start[lo]) * kScoreUnit, nb);
-      u = u2;
-      const int steps = (p1 - p0 + stage_pages - 1) / stage_pages;
-      const int32_t* table = P.block_table + (size_t)b * P.max_pages_per_seq;
-      // the page at place j of step k, -1 past the run or outside the pool
-      auto page_at = [&](int k, int j) {
-        const int i = p0 + k * stage_pages + j;
-        if (j < 0 || i >= p1) return -1;
-        const int page = __ldg(table + i);
-        return page >= 0 && page < P.num_pages ? page : -1;
-      };
-      const int mine = works && lane < 16 ? sub * 16 + lane : -1;  // scored
-      const int copied = w * copies + lane;
-      // each warp copies its share of a stage's pages: one lane a page, and the
-      // copies of one warp are issued one after another
-      auto issue = [&](int k, int page) {
-        const uint32_t bar = smem_u32(&full[slot_in]);
-        const bool inside = lane < copies && p0 + k * stage_pages + copied < p1;
-        if (inside && page < 0) report(P.error_word, TL_DEVERR_PAGE_RANGE);
-        const uint32_t live = __ballot_sync(0xffffffffu, inside && page >= 0);
-        if (lane == 0) mbar_arrive_expect_tx(bar, (uint32_t)__popc(live) * copy_bytes);
-        if (inside && page >= 0)
-          bulk_g2s(smem_u32(score_sm) + slot_in * stage_bytes + copied * page_bytes,
-                   P.bounds + ((size_t)page * P.h_kv + g0) * 2 * D, copy_bytes, bar);
-        ++issued;
-        slot_in = slot_in + 1 == nst ? 0 : slot_in + 1;
-      };
-      // the first stages' copies run while the query is quantised; later pages
-      // are looked up a step before they are copied
-      for (int k = 0; k < nst && k < steps; ++k) issue(k, page_at(k, copied));
-      int page_cur = page_at(0, mine), page_nxt = page_at(1, mine), page_iss = page_at(nst, copied);
+      s.b = base + lo;
+      s.next = min(u1, start[lo + 1]);
+      s.p0 = (u - start[lo]) * kScoreUnit;
+      s.p1 = min((s.next - start[lo]) * kScoreUnit,
+                 blocks_of(P.context_lens[s.b], P.max_pages_per_seq, P.page_size));
+      s.steps = (s.p1 - s.p0 + stage_pages - 1) / stage_pages;
+      s.table = P.block_table + (size_t)s.b * P.max_pages_per_seq;
+      return true;
+    };
+    // the page at place j of step k, -1 past the segment or outside the pool
+    auto page_at = [&](const Segment& s, int k, int j) {
+      const int i = s.p0 + k * stage_pages + j;
+      if (j < 0 || i >= s.p1) return -1;
+      const int page = __ldg(s.table + i);
+      return page >= 0 && page < P.num_pages ? page : -1;
+    };
+    const int mine = works && lane < 16 ? sub * 16 + lane : -1;  // scored
+    const int copied = w * copies + lane;
+    Segment in;
+    in.next = u0;
+    bool in_live = open(in);
+    int in_k = 0, in_page = in_live ? page_at(in, 0, copied) : -1;  // looked up a step early
+    // each warp copies its share of a stage's pages: one lane a page, and the
+    // copies of one warp are issued one after another
+    auto issue_next = [&]() {
+      if (!in_live) return;
+      const uint32_t bar = smem_u32(&full[slot_in]);
+      const bool inside = lane < copies && in.p0 + in_k * stage_pages + copied < in.p1;
+      if (inside && in_page < 0) report(P.error_word, TL_DEVERR_PAGE_RANGE);
+      const uint32_t live = __ballot_sync(0xffffffffu, inside && in_page >= 0);
+      if (lane == 0) mbar_arrive_expect_tx(bar, (uint32_t)__popc(live) * copy_bytes);
+      if (inside && in_page >= 0)
+        bulk_g2s(smem_u32(score_sm) + slot_in * stage_bytes + copied * page_bytes,
+                 P.bounds + ((size_t)in_page * P.h_kv + g0) * 2 * D, copy_bytes, bar);
+      ++issued;
+      slot_in = slot_in + 1 == nst ? 0 : slot_in + 1;
+      if (++in_k == in.steps) {
+        in_k = 0;
+        in_live = open(in);
+      }
+      if (in_live) in_page = page_at(in, in_k, copied);
+    };
+    for (int k = 0; k < nst; ++k) issue_next();
+    Segment seg;
+    seg.next = u0;
+    while (!stop && open(seg)) {
+      const int b = seg.b, p0 = seg.p0, p1 = seg.p1;
+      int page_cur = page_at(seg, 0, mine), page_nxt = page_at(seg, 1, mine);
+      float sc = page_cur >= 0 ? __ldg(P.scales + (size_t)page_cur * P.h_kv + g0 + gi) : 0.f;
       // query rows: code = rint(q / t) clamped to +-127, t = max|q| / 127; four
       // threads a row, so that the rows' loads are all in flight at once
       for (int r0 = 0; r0 < heads * P.group; r0 += kScoreWarps * 8) {
@@ -578,52 +601,38 @@ __global__ void __launch_bounds__(kScoreWarps * 32, 2) page_score_kernel(ScorePa
       }
       __syncthreads();
       const int g = g0 + gi;
-      // The query codes of this warp's head as B fragments of an m16n8k16: the
-      // column is a query head of the group, k step ks < D/16 takes the codes
-      // >= 0 (they meet the max codes), the others those below 0.  A lane's
-      // four channels of a step are those of one 4-byte read of a page's
-      // codes: the same permutation of the summed channels on both sides.
+      // The query codes of this warp's head as B fragments of an m16n8k32: the
+      // column is a query head of the group; the first D/32 k steps take the
+      // codes >= 0 (they meet the max codes), the others those below 0.
       uint32_t qb[NT][2 * KS][2];
-      float bias_even[NT][2], bias_odd[NT][2];  // 1152 x the codes' sum over those steps
-      float t_q[NT][2];                         // the scales of columns 2t and 2t + 1
+      float t_q[NT][2];  // the scales of columns 2t and 2t + 1
 #pragma unroll
       for (int nt = 0; nt < NT; ++nt) {
         const int r = 8 * nt + (lane >> 2);
-        float even = 0.f, odd = 0.f;
 #pragma unroll
-        for (int ks = 0; ks < KS; ++ks) {
-          const uint32_t a = works && r < P.group
-                                 ? *reinterpret_cast<const uint32_t*>(
-                                       q_codes + (gi * P.group + r) * D + 16 * ks + 4 * (lane & 3))
-                                 : 0u;
-          const uint32_t neg = __vcmplts4(a, 0u);
-          i8x4_as_f16x2x2(a & ~neg, qb[nt][ks][0], qb[nt][ks][1]);
-          i8x4_as_f16x2x2(a & neg, qb[nt][KS + ks][0], qb[nt][KS + ks][1]);
-          const float s = (float)__dp4a((int)a, 0x01010101, 0);
-          if (ks & 1) odd += s;
-          else even += s;
-        }
-        // the sums over the four lanes of a column, then to the lanes that
-        // hold its results (columns 2t and 2t + 1 of lane t)
-        even += __shfl_xor_sync(0xffffffffu, even, 1);
-        even += __shfl_xor_sync(0xffffffffu, even, 2);
-        odd += __shfl_xor_sync(0xffffffffu, odd, 1);
-        odd += __shfl_xor_sync(0xffffffffu, odd, 2);
+        for (int ks = 0; ks < KS; ++ks)
+#pragma unroll
+          for (int h = 0; h < 2; ++h) {
+            const uint32_t a = works && r < P.group
+                                   ? *reinterpret_cast<const uint32_t*>(
+                                         q_codes + (gi * P.group + r) * D + 32 * ks + 16 * h +
+                                         4 * (lane & 3))
+                                   : 0u;
+            const uint32_t neg = __vcmplts4(a, 0u);
+            qb[nt][ks][h] = a & ~neg;
+            qb[nt][KS + ks][h] = a & neg;
+          }
 #pragma unroll
         for (int e = 0; e < 2; ++e) {
-          bias_even[nt][e] = 1152.f * __shfl_sync(0xffffffffu, even, 8 * (lane & 3) + 4 * e);
-          bias_odd[nt][e] = 1152.f * __shfl_sync(0xffffffffu, odd, 8 * (lane & 3) + 4 * e);
           const int rq = 8 * nt + 2 * (lane & 3) + e;
           t_q[nt][e] = works && rq < P.group ? q_scale[gi * P.group + rq] : 0.f;
         }
       }
       float* out = P.scores + ((size_t)b * P.h_kv + g) * P.row_stride;
-      float sc = works && page_cur >= 0 ? __ldg(P.scales + (size_t)page_cur * P.h_kv + g) : 0.f;
-      for (int k = 0; k < steps; ++k) {
+      for (int k = 0; k < seg.steps; ++k) {
         // one step ahead: the next pages' scales and the table entries behind
-        const float sc_nxt =
-            works && page_nxt >= 0 ? __ldg(P.scales + (size_t)page_nxt * P.h_kv + g) : 0.f;
-        const int page_nn = page_at(k + 2, mine), page_in = page_at(k + nst + 1, copied);
+        const float sc_nxt = page_nxt >= 0 ? __ldg(P.scales + (size_t)page_nxt * P.h_kv + g) : 0.f;
+        const int page_nn = page_at(seg, k + 2, mine);
         const bool ok = mbar_wait(smem_u32(&full[slot_out]), parity, &abort_flag);
         if (works && ok) {
           // 16 pages are the MMA's rows; every fragment is loaded before the
@@ -631,27 +640,20 @@ __global__ void __launch_bounds__(kScoreWarps * 32, 2) page_score_kernel(ScorePa
           const uint32_t rows = smem_u32(score_sm) + slot_out * stage_bytes +
                                 (sub * 16 + (lane & 15)) * page_bytes + gi * 2 * D +
                                 (lane >> 4) * 16;
-          uint32_t x[KS][4];
+          uint32_t x[2 * KS][4];
 #pragma unroll
-          for (int ks = 0; ks < KS; ++ks)
+          for (int ks = 0; ks < 2 * KS; ++ks)
             ldmatrix_x4(rows + ks * 32, x[ks][0], x[ks][1], x[ks][2], x[ks][3]);
-          float acc[NT][2][4];
+          int acc[NT][2][4];  // two chains
 #pragma unroll
           for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-            for (int e = 0; e < 4; ++e) acc[nt][0][e] = acc[nt][1][e] = 0.f;
+            for (int e = 0; e < 4; ++e) acc[nt][0][e] = acc[nt][1][e] = 0;
 #pragma unroll
-          for (int ks = 0; ks < KS; ++ks)
+          for (int ks = 0; ks < 2 * KS; ++ks)
 #pragma unroll
-            for (int h = 0; h < 2; ++h) {
-              uint32_t a0, a1, a2, a3;
-              i8x4_as_f16x2x2_biased(x[ks][2 * h], a0, a2);
-              i8x4_as_f16x2x2_biased(x[ks][2 * h + 1], a1, a3);
-#pragma unroll
-              for (int nt = 0; nt < NT; ++nt)
-                mma_f16_16816(acc[nt][h], a0, a1, a2, a3, qb[nt][2 * ks + h][0],
-                              qb[nt][2 * ks + h][1]);
-            }
+            for (int nt = 0; nt < NT; ++nt)
+              mma_s8_16832(acc[nt][ks & 1], x[ks], qb[nt][ks]);
           // lane (g, t): pages g and g + 8, heads 2t and 2t + 1
           const float s0 = __shfl_sync(0xffffffffu, sc, lane >> 2);
           const float s1 = __shfl_sync(0xffffffffu, sc, (lane >> 2) + 8);
@@ -662,10 +664,9 @@ __global__ void __launch_bounds__(kScoreWarps * 32, 2) page_score_kernel(ScorePa
             for (int e = 0; e < 2; ++e) {
               const int r = 8 * nt + 2 * (lane & 3) + e;
               if (r < P.group) {
-                const float d0 =
-                    (acc[nt][0][e] - bias_even[nt][e]) + (acc[nt][1][e] - bias_odd[nt][e]);
-                const float d1 =
-                    (acc[nt][0][2 + e] - bias_even[nt][e]) + (acc[nt][1][2 + e] - bias_odd[nt][e]);
+                // whole numbers below 2^24: exact as floats
+                const float d0 = (float)(acc[nt][0][e] + acc[nt][1][e]);
+                const float d1 = (float)(acc[nt][0][2 + e] + acc[nt][1][2 + e]);
                 b0 = fmaxf(b0, __fmul_rn(__fmul_rn(d0, s0), t_q[nt][e]));
                 b1 = fmaxf(b1, __fmul_rn(__fmul_rn(d1, s1), t_q[nt][e]));
               }
@@ -690,8 +691,7 @@ __global__ void __launch_bounds__(kScoreWarps * 32, 2) page_score_kernel(ScorePa
           stop = true;
           break;
         }
-        if (k + nst < steps) issue(k + nst, page_iss);
-        page_iss = page_in;
+        issue_next();
         page_cur = page_nxt;
         page_nxt = page_nn;
         sc = sc_nxt;
@@ -723,7 +723,7 @@ struct PageSelectParams {
 
 template <int T, bool FITS>
 __global__ void __launch_bounds__(T) page_select_kernel(PageSelectParams P, int csize, int key_cap) {
-  __shared__ SelectShared sh;
+  __shared__ SelectShared<T> sh;
   extern __shared__ __align__(16) uint32_t sel_keys[];
   asm volatile("griddepcontrol.wait;\n" ::: "memory");
   const int row = blockIdx.x / csize, rank = blockIdx.x % csize;
@@ -837,7 +837,8 @@ SelectShape select_shape(int64_t rows, int64_t cap) {
   const int64_t slice = ((cap + s.cluster - 1) / s.cluster + 127) / 128 * 128;
   s.keys = (int)std::min<int64_t>(slice, kSelKeysMax);
   s.fits = slice <= kSelKeysMax;  // else 1,024 threads, by the rule below
-  s.threads = slice <= 1024 ? 256 : slice <= 4096 && rows * s.cluster > 2 * num_sms() ? 512 : 1024;
+  const bool many = rows * s.cluster > 2 * num_sms();
+  s.threads = slice <= 1024 || (many && slice <= 2048) ? 256 : many && slice <= 8192 ? 512 : 1024;
   return s;
 }
 

@@ -13,7 +13,7 @@
 // Method: what is sought is one (key, index) pair, the last one taken; then an
 // index is taken when its key is larger, or equal with an index not behind.
 // A radix selection narrows the range of keys that holds it: the smallest and
-// largest key are found first, the range between them is cut into up to 4,096
+// largest key are found first, the range between them is cut into 1,024 to 4,096
 // equal bins (linear in the key, so about even over a heavy-tailed row's
 // values), a histogram in shared memory tells the bin, and that bin is cut
 // again until it holds at most 128 values, which are ranked against each
@@ -34,8 +34,11 @@
 
 namespace tl {
 
-constexpr int kSelBins = 4096;
-constexpr int kSelBinBits = 12;
+// Bins of a pass: four a thread (1,024 to 4,096), so that a short row, which
+// needs few, clears and scans few.
+__host__ __device__ constexpr int select_bin_bits(int threads) {
+  return threads >= 1024 ? 12 : threads >= 512 ? 11 : 10;
+}
 constexpr int kSelRank = 128;        // values ranked against each other at the end
 constexpr int kSelKeysMax = 32768;   // keys of a slice kept in shared memory (128 KiB)
 constexpr int kSelClusterMax = 8;
@@ -49,8 +52,11 @@ TL_DEVINLINE uint32_t select_key_number(float x) {  // x is not NaN
 }
 TL_DEVINLINE uint32_t select_key(float x) { return x != x ? 1u : select_key_number(x); }
 
+template <int T>
 struct SelectShared {
-  __align__(16) uint32_t hist[kSelBins];
+  static constexpr int kBinBits = select_bin_bits(T), kBins = 1 << kBinBits;
+  static_assert(kBins == 4 * T, "a thread takes four bins");
+  __align__(16) uint32_t hist[kBins];
   uint32_t minmax[2];     // this CTA's smallest and largest key
   uint32_t total;         // this CTA's taken values
   uint32_t tmp[2][32];    // block scans, alternating
@@ -90,11 +96,12 @@ TL_DEVINLINE uint32_t select_block_scan(uint32_t x, uint32_t* tmp, uint32_t& tot
 // that this CTA filled, first and one past the last ({0, 0} where len <= n:
 // each thread filled places rank * T + tid, + csize * T, ...).
 template <int T, bool FITS, class Emit, class Tail>
-__device__ int2 select_row(SelectShared& sh, uint32_t* keys, int key_cap, const float* x, int len,
+__device__ int2 select_row(SelectShared<T>& sh, uint32_t* keys, int key_cap, const float* x, int len,
                            int n, int first, int last, int rank, int csize, Emit emit,
                            Tail tail) {
   namespace cg = cooperative_groups;
-  constexpr int NW = T / 32, PER = kSelBins / T;
+  constexpr int NW = T / 32, PER = 4;
+  constexpr int kSelBins = SelectShared<T>::kBins, kSelBinBits = SelectShared<T>::kBinBits;
   const int tid = threadIdx.x, lane = tid & 31, wid = tid >> 5;
   auto cluster_sync = [&]() {
     if (csize > 1) cg::this_cluster().sync();
