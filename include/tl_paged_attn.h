@@ -697,8 +697,10 @@ tl_status tl_kv_page_bounds_int8(const int8_t* k_codes, const float* k_scales,
                                  uint32_t* error_word, void* stream);
 
 /* Bytes of workspace tl_kv_page_select needs (one float32 per sequence, KV
- * head and table entry); 0 for invalid sizes. */
-size_t tl_kv_page_select_workspace_size(int32_t B, int32_t h_kv, int32_t max_pages_per_seq);
+ * head and table entry, and the query's codes and scales); 0 for invalid
+ * sizes. */
+size_t tl_kv_page_select_workspace_size(int32_t B, int32_t h_q, int32_t h_kv, int32_t d,
+                                        int32_t max_pages_per_seq);
 
 /*
  * The n_select pages of each sequence and KV head that a decode query is to

@@ -74,7 +74,7 @@ SIGNATURES = {
                            u32p, vp], ctypes.c_int),
     "tl_kv_page_bounds_int8": ([vp, vp, vp, i32, vp, vp, vp, vp, i32, i32, i32, i32, i32, u32p,
                                 vp], ctypes.c_int),
-    "tl_kv_page_select_workspace_size": ([i32, i32, i32], sz),
+    "tl_kv_page_select_workspace_size": ([i32, i32, i32, i32, i32], sz),
     "tl_kv_page_select": ([vp, ctypes.c_int, vp, vp, vp, i32, vp, i32, i32, i32, vp, vp, i32, i32,
                            i32, i32, i32, i32, vp, sz, u32p, vp], ctypes.c_int),
     "tl_paged_attn_decode_pages": ([vp, vp, vp, vp, i32, vp, vp, i32, i32, i32, i32, i32, i32,

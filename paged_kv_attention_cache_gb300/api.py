@@ -684,8 +684,9 @@ def tl_kv_page_bounds_int8(k_codes: torch.Tensor, k_scales: torch.Tensor,
 
 
 @functools.lru_cache(maxsize=1024)
-def tl_kv_page_select_workspace_size(B: int, h_kv: int, max_pages_per_seq: int) -> int:
-    return int(_lib.load().tl_kv_page_select_workspace_size(B, h_kv, max_pages_per_seq))
+def tl_kv_page_select_workspace_size(B: int, h_q: int, h_kv: int, d: int,
+                                     max_pages_per_seq: int) -> int:
+    return int(_lib.load().tl_kv_page_select_workspace_size(B, h_q, h_kv, d, max_pages_per_seq))
 
 
 def _int_out(t, name, shape, device):
@@ -716,7 +717,7 @@ def tl_kv_page_select(q: torch.Tensor, bounds: torch.Tensor, bound_scales: torch
     page_table = _int_out(page_table, "page_table", (B, hkv, n), dev)
     page_lens = _int_out(page_lens, "page_lens", (B,), dev)
     width = block_table.shape[1]
-    workspace = _workspace(workspace, tl_kv_page_select_workspace_size(B, hkv, width), dev)
+    workspace = _workspace(workspace, tl_kv_page_select_workspace_size(B, hq, hkv, d, width), dev)
     _run("tl_kv_page_select", dev, stream,
          _ptr(q), _DTYPES.get(q.dtype, -1), _ptr(bounds), _ptr(bound_scales), _ptr(block_table),
          width, _ptr(context_lens), n, int(keep_first), int(keep_last), _ptr(page_table),

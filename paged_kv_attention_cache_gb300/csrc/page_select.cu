@@ -386,6 +386,8 @@ __global__ void __launch_bounds__(kBoundsThreads, KIND == kInt8 || KIND == kE4m3
 
 struct ScoreParams {
   const void* q;  // [B][h_q][d], bf16 or f32
+  int8_t* q_codes;  // [B][h_q][d]
+  float* q_scales;  // [B][h_q]
   const int8_t* bounds;
   const float* scales;
   const int32_t* block_table;
@@ -399,10 +401,59 @@ struct ScoreParams {
 // A row of scores starts on 16 bytes.
 inline int64_t score_stride(int max_pages_per_seq) { return ((int64_t)max_pages_per_seq + 3) / 4 * 4; }
 
-constexpr int kScoreWarps = 8;
+// Query rows as int8 codes, one warp a row: code = rint(q / t) clamped to
+// +-127, t = max|q| / 127; a value that is not finite counts as 0.
+template <int D, bool QF32>
+__global__ void __launch_bounds__(256) page_query_kernel(ScoreParams P) {
+  constexpr int E = D / 32;  // a lane's channels
+  // the scores' kernel may start: it waits for these codes after its first copies
+  asm volatile("griddepcontrol.launch_dependents;\n" ::: "memory");
+  const int lane = threadIdx.x & 31;
+  const int64_t row = (int64_t)blockIdx.x * 8 + (threadIdx.x >> 5);
+  if (row >= (int64_t)P.B * P.h_q) return;
+  float x[E];
+  if (QF32) {
+    const float* src = static_cast<const float*>(P.q) + row * D + lane * E;
+#pragma unroll
+    for (int i = 0; i < E; i += 2) *reinterpret_cast<float2*>(x + i) = __ldg(reinterpret_cast<const float2*>(src + i));
+  } else {
+    const uint32_t* src = reinterpret_cast<const uint32_t*>(
+        static_cast<const unsigned short*>(P.q) + row * D + lane * E);
+#pragma unroll
+    for (int i = 0; i < E / 2; ++i) {
+      const uint32_t w = __ldg(src + i);
+      x[2 * i] = __uint_as_float(w << 16);
+      x[2 * i + 1] = __uint_as_float(w & 0xffff0000u);
+    }
+  }
+  bool bad = false;
+  float m = 0.f;
+#pragma unroll
+  for (int i = 0; i < E; ++i) {
+    if (!isfinite(x[i])) {
+      bad = true;
+      x[i] = 0.f;
+    }
+    m = fmaxf(m, fabsf(x[i]));
+  }
+  m = __uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(m)));  // m >= 0
+  const float t = __fdiv_rn(m, 127.f);
+  const Quotient quot(t);
+  uint32_t code = 0;
+#pragma unroll
+  for (int i = 0; i < E; ++i) code |= (uint32_t)(uint8_t)(int8_t)quot.code(x[i]) << (8 * i);
+  int8_t* dst = P.q_codes + row * D + lane * E;
+  if (E == 4) *reinterpret_cast<uint32_t*>(dst) = code;
+  else *reinterpret_cast<uint16_t*>(dst) = (uint16_t)code;
+  if (lane == 0) P.q_scales[row] = t;
+  if (__any_sync(0xffffffffu, bad) && lane == 0) report(P.error_word, TL_DEVERR_VALUE_RANGE);
+}
+
+constexpr int kScoreWarps = 8;    // that compute; one more copies
+constexpr int kScoreThreads = (kScoreWarps + 1) * 32;
 constexpr int kScoreUnit = 4;     // pages; a CTA takes a run of units
 constexpr int kScoreSeqs = 1024;  // sequences placed per round
-constexpr int kScoreStages = 3;   // at most
+constexpr int kScoreStages = 3;
 
 // Heads a CTA scores (grid.y covers the others), and the warps that share one.
 __host__ __device__ inline int score_heads(int h_kv) { return h_kv < kScoreWarps ? h_kv : kScoreWarps; }
@@ -414,9 +465,6 @@ __host__ __device__ inline int score_page_bytes(int heads, int d) { return heads
 __host__ __device__ inline int score_stage_bytes(int heads, int d) {
   return 16 * (kScoreWarps / heads) * score_page_bytes(heads, d);
 }
-__host__ __device__ inline int score_query_bytes(int heads, int group, int d) {
-  return heads * group * d;
-}
 
 // Blocks a sequence has, or 0 when its length is past its table.
 TL_DEVINLINE int blocks_of(int L, int max_pages, int page_size) {
@@ -425,225 +473,203 @@ TL_DEVINLINE int blocks_of(int L, int max_pages, int page_size) {
 
 // Scores of every page of every sequence, two CTAs per SM.  Each takes an even
 // share of the batch's pages as one run (a scan of the sequences' block
-// counts places it: the host knows no length), so it quantises a sequence's
-// query rows once or twice a call.  A page's codes of the CTA's heads are one
-// run of memory (2 KiB at 8 heads of 128) and arrive by one bulk copy into a
-// ring of stages; then a warp takes a KV head: 16 pages are the rows of an
-// m16n8k16, the group's query heads its columns, the sum over the channels of
-// max code x (q code >= 0) and min code x (q code < 0) its k steps.
-//
-// The arithmetic is exact.  A code c enters as the fp16 1152 + c (two byte
-// permutes for four codes; taking the 1152 out there would cost two more
-// operations) and its sum with the query's codes is taken out at the end.
-// Even and odd steps accumulate apart: at d = 128 each sum is at most 64
-// channels x 127 x 1279 = 10.4 million, a whole number below 2^24, exact in
-// f32 however it is added up.
-template <int D, int NT, bool QF32>
-__global__ void __launch_bounds__(kScoreWarps * 32, 2) page_score_kernel(ScoreParams P, int nst) {
+// counts places it: the host knows no length).  One warp looks the pages up
+// and copies them: a page's codes of the CTA's heads are one run of memory
+// (2 KiB at 8 heads of 128), one bulk copy into a ring of stages, on from one
+// sequence's pages to the next's.  The other warps take a KV head each, with
+// no barrier among them: 16 pages are the rows of an m16n8k32 over int8, the
+// group's query heads its columns, the sum over the channels of max code x (q
+// code >= 0) and min code x (q code < 0) its k steps, in whole numbers.
+template <int D, int NT>
+__global__ void __launch_bounds__(kScoreThreads, 2) page_score_kernel(ScoreParams P) {
+  constexpr int KS = D / 32;  // k steps of the max codes, and of the min codes
+  constexpr int NST = kScoreStages;
   extern __shared__ __align__(16) unsigned char score_sm[];
   __shared__ int start[kScoreSeqs + 1];  // first unit of each sequence of the round
   __shared__ uint32_t tmp[32];
-  constexpr int KS = D / 32;  // k steps of the max codes, and of the min codes
-  __shared__ float q_scale[kScoreWarps * 8 * NT];
-  __shared__ unsigned long long full[kScoreStages];
+  __shared__ unsigned long long full[NST], empty[NST];
   __shared__ int abort_flag;
   const int tid = threadIdx.x, lane = tid & 31, w = tid >> 5;
   const int hs = score_heads(P.h_kv), g0 = blockIdx.y * hs, heads = min(hs, P.h_kv - g0);
   const int per_head = kScoreWarps / hs;
-  const int gi = w % hs, sub = w / hs;
-  const bool works = sub < per_head && gi < heads;  // computes
-  const int copies = 2 * per_head;                  // pages of a stage that each warp copies
   const int page_bytes = score_page_bytes(hs, D), stage_bytes = score_stage_bytes(hs, D);
   const int stage_pages = 16 * per_head;
-  const uint32_t copy_bytes = (uint32_t)heads * 2 * D;
-  unsigned char* q_codes = score_sm + nst * stage_bytes;
+  const uint32_t sm0 = smem_u32(score_sm);
   // the selection may take the SMs that this grid leaves (it waits for the
   // grid's end before it reads a score)
   asm volatile("griddepcontrol.launch_dependents;\n" ::: "memory");
   if (tid == 0) {
     abort_flag = 0;
-    for (int s = 0; s < nst; ++s) mbar_init(smem_u32(&full[s]), kScoreWarps);
+    for (int s = 0; s < NST; ++s) {
+      mbar_init(smem_u32(&full[s]), 1);
+      mbar_init(smem_u32(&empty[s]), (uint32_t)(heads * per_head));
+    }
     fence_mbar_init();
   }
-  uint32_t issued = 0, done = 0;  // stages, and their places in the ring
-  int slot_in = 0, slot_out = 0;
-  uint32_t parity = 0;  // of the phase that slot_out waits for
-  bool stop = false;
-  for (int base = 0; base < P.B && !stop; base += kScoreSeqs) {
-    constexpr int PER = kScoreSeqs / (kScoreWarps * 32);
+  int slot = 0;          // of the ring, in step in every warp
+  uint32_t parity = 0;   // of the slot's phase
+  uint32_t stages = 0;   // copied (the copying warp)
+  auto advance = [&]() {
+    slot = slot + 1 == NST ? 0 : slot + 1;
+    parity ^= slot == 0 ? 1u : 0u;
+  };
+  bool stop = false, waited = false;
+  for (int base = 0; base < P.B; base += kScoreSeqs) {
+    constexpr int PER = (kScoreSeqs + kScoreThreads - 1) / kScoreThreads;
     uint32_t n[PER], sum = 0;
 #pragma unroll
     for (int j = 0; j < PER; ++j) {
-      const int b = base + tid * PER + j;
-      const int nb = b < P.B ? blocks_of(P.context_lens[b], P.max_pages_per_seq, P.page_size) : 0;
+      const int i = tid * PER + j, b = base + i;
+      const int nb = i < kScoreSeqs && b < P.B
+                         ? blocks_of(P.context_lens[b], P.max_pages_per_seq, P.page_size)
+                         : 0;
       n[j] = (uint32_t)(nb + kScoreUnit - 1) / kScoreUnit;
       sum += n[j];
     }
     uint32_t total;
-    __syncthreads();  // the previous round's start and tmp are read
+    // the previous round's start and tmp are read; a wait that gave up in any
+    // warp ends the rounds for all
+    if (__syncthreads_or(stop)) break;
     uint32_t at = select_block_scan(sum, tmp, total);
 #pragma unroll
     for (int j = 0; j < PER; ++j) {
-      start[tid * PER + j] = (int)at;
+      if (tid * PER + j < kScoreSeqs) start[tid * PER + j] = (int)at;
       at += n[j];
     }
     if (tid == 0) start[kScoreSeqs] = (int)total;
     __syncthreads();
-    const int u0 = (int)even_share(total, blockIdx.x, gridDim.x);
     const int u1 = (int)even_share(total, blockIdx.x + 1, gridDim.x);
     // The CTA's units as segments, one sequence each: pages p0 .. p1 of
-    // sequence b in steps of a stage.  Two cursors walk them: copies are
-    // issued a ring ahead of the computation, on into the next segments.
+    // sequence b in steps of a stage.  The copying warp and the others walk
+    // them at their own pace.
     struct Segment {
       int next, b, p0, p1, steps;  // next: the first unit behind it
       const int32_t* table;
-    };
-    auto open = [&](Segment& s) {
-      const int u = s.next;
+    } seg;
+    seg.next = (int)even_share(total, blockIdx.x, gridDim.x);
+    auto open = [&]() {
+      const int u = seg.next;
       if (u >= u1) return false;
-      int lo = 0, hi = kScoreSeqs;  // the last sequence that starts at or before u
+      int lo = 0, hi = min(kScoreSeqs, P.B - base);  // the last sequence that starts at or before u
       while (hi - lo > 1) {
         const int mid = (lo + hi) >> 1;
         if (start[mid] <= u) lo = mid;
         else hi = mid;
       }
-      s.b = base + lo;
-      s.next = min(u1, start[lo + 1]);
-      s.p0 = (u - start[lo]) * kScoreUnit;
-      s.p1 = min((s.next - start[lo]) * kScoreUnit,
-                 blocks_of(P.context_lens[s.b], P.max_pages_per_seq, P.page_size));
-      s.steps = (s.p1 - s.p0 + stage_pages - 1) / stage_pages;
-      s.table = P.block_table + (size_t)s.b * P.max_pages_per_seq;
+      seg.b = base + lo;
+      seg.next = min(u1, start[lo + 1]);
+      seg.p0 = (u - start[lo]) * kScoreUnit;
+      seg.p1 = min((seg.next - start[lo]) * kScoreUnit,
+                   blocks_of(P.context_lens[seg.b], P.max_pages_per_seq, P.page_size));
+      seg.steps = (seg.p1 - seg.p0 + stage_pages - 1) / stage_pages;
+      seg.table = P.block_table + (size_t)seg.b * P.max_pages_per_seq;
       return true;
     };
-    // the page at place j of step k, -1 past the segment or outside the pool
-    auto page_at = [&](const Segment& s, int k, int j) {
-      const int i = s.p0 + k * stage_pages + j;
-      if (j < 0 || i >= s.p1) return -1;
-      const int page = __ldg(s.table + i);
-      return page >= 0 && page < P.num_pages ? page : -1;
-    };
-    const int mine = works && lane < 16 ? sub * 16 + lane : -1;  // scored
-    const int copied = w * copies + lane;
-    Segment in;
-    in.next = u0;
-    bool in_live = open(in);
-    int in_k = 0, in_page = in_live ? page_at(in, 0, copied) : -1;  // looked up a step early
-    // each warp copies its share of a stage's pages: one lane a page, and the
-    // copies of one warp are issued one after another
-    auto issue_next = [&]() {
-      if (!in_live) return;
-      const uint32_t bar = smem_u32(&full[slot_in]);
-      const bool inside = lane < copies && in.p0 + in_k * stage_pages + copied < in.p1;
-      if (inside && in_page < 0) report(P.error_word, TL_DEVERR_PAGE_RANGE);
-      const uint32_t live = __ballot_sync(0xffffffffu, inside && in_page >= 0);
-      if (lane == 0) mbar_arrive_expect_tx(bar, (uint32_t)__popc(live) * copy_bytes);
-      if (inside && in_page >= 0)
-        bulk_g2s(smem_u32(score_sm) + slot_in * stage_bytes + copied * page_bytes,
-                 P.bounds + ((size_t)in_page * P.h_kv + g0) * 2 * D, copy_bytes, bar);
-      ++issued;
-      slot_in = slot_in + 1 == nst ? 0 : slot_in + 1;
-      if (++in_k == in.steps) {
-        in_k = 0;
-        in_live = open(in);
-      }
-      if (in_live) in_page = page_at(in, in_k, copied);
-    };
-    for (int k = 0; k < nst; ++k) issue_next();
-    Segment seg;
-    seg.next = u0;
-    while (!stop && open(seg)) {
-      const int b = seg.b, p0 = seg.p0, p1 = seg.p1;
-      int page_cur = page_at(seg, 0, mine), page_nxt = page_at(seg, 1, mine);
-      float sc = page_cur >= 0 ? __ldg(P.scales + (size_t)page_cur * P.h_kv + g0 + gi) : 0.f;
-      // query rows: code = rint(q / t) clamped to +-127, t = max|q| / 127; four
-      // threads a row, so that the rows' loads are all in flight at once
-      for (int r0 = 0; r0 < heads * P.group; r0 += kScoreWarps * 8) {
-        constexpr int E = D / 4;  // a thread's channels
-        const int r = min(r0 + (tid >> 2), heads * P.group - 1), e0 = (tid & 3) * E;
-        const size_t row = ((size_t)b * P.h_q + (size_t)g0 * P.group + r) * D + e0;
-        float x[E], m = 0.f;
-        if (QF32) {
-          const float4* src = reinterpret_cast<const float4*>(static_cast<const float*>(P.q) + row);
-#pragma unroll
-          for (int i = 0; i < E / 4; ++i)
-            *reinterpret_cast<float4*>(x + 4 * i) = __ldg(src + i);
-        } else {
-          const uint4* src =
-              reinterpret_cast<const uint4*>(static_cast<const unsigned short*>(P.q) + row);
-#pragma unroll
-          for (int i = 0; i < E / 8; ++i) widen_vec<kBf16>(__ldg(src + i), 0.f, x + 8 * i);
-        }
-        bool bad = false;
-#pragma unroll
-        for (int i = 0; i < E; ++i) {
-          if (!isfinite(x[i])) {  // counts as 0
-            bad = true;
-            x[i] = 0.f;
+    if (w == kScoreWarps) {
+      // ---------------------------------------------------------- copies
+      const uint32_t copy_bytes = (uint32_t)heads * 2 * D;
+      while (!stop && open()) {
+        const int n_pages = seg.p1 - seg.p0;
+        // 32 entries of the table at a time, the next ones on their way
+        int ahead = lane < n_pages ? __ldg(seg.table + seg.p0 + lane) : -1;
+        int window = -1, held = 0;
+        for (int k = 0; k < seg.steps; ++k) {
+          if (!mbar_wait(smem_u32(&empty[slot]), parity ^ 1u, &abort_flag)) {
+            stop = true;
+            break;
           }
-          m = fmaxf(m, fabsf(x[i]));
-        }
-        m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 1));
-        m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 2));
-        const float t = __fdiv_rn(m, 127.f);
-        const Quotient quot(t);
-#pragma unroll
-        for (int i = 0; i < E / 4; ++i) {
-          uint32_t code = 0;
-#pragma unroll
-          for (int j = 0; j < 4; ++j) {
-            code |= (uint32_t)(uint8_t)(int8_t)quot.code(x[4 * i + j]) << (8 * j);
+          const int n_here = min(stage_pages, n_pages - k * stage_pages);
+          uint32_t bytes = 0;
+          for (int c0 = 0; c0 < n_here; c0 += 32) {  // this stage's pages, a lane each
+            const int i = k * stage_pages + c0;      // of the segment
+            if (i >= held) {
+              window = ahead;
+              held += 32;
+              ahead = held + lane < n_pages ? __ldg(seg.table + seg.p0 + held + lane) : -1;
+            }
+            const int page = __shfl_sync(0xffffffffu, window, (i & 31) + lane);
+            const bool inside = lane < min(n_here - c0, min(32, stage_pages));
+            const bool ok = inside && page >= 0 && page < P.num_pages;
+            if (inside && !ok) report(P.error_word, TL_DEVERR_PAGE_RANGE);
+            bytes += (uint32_t)__popc(__ballot_sync(0xffffffffu, ok)) * copy_bytes;
+            if (c0 + 32 >= n_here && lane == 0) mbar_arrive_expect_tx(smem_u32(&full[slot]), bytes);
+            if (ok)
+              bulk_g2s(sm0 + slot * stage_bytes + (c0 + lane) * page_bytes,
+                       P.bounds + ((size_t)page * P.h_kv + g0) * 2 * D, copy_bytes,
+                       smem_u32(&full[slot]));
           }
-          *reinterpret_cast<uint32_t*>(q_codes + r * D + e0 + 4 * i) = code;
-        }
-        if ((tid & 3) == 0) q_scale[r] = t;
-        if (bad) report(P.error_word, TL_DEVERR_VALUE_RANGE);
-      }
-      __syncthreads();
-      const int g = g0 + gi;
-      // The query codes of this warp's head as B fragments of an m16n8k32: the
-      // column is a query head of the group; the first D/32 k steps take the
-      // codes >= 0 (they meet the max codes), the others those below 0.
-      uint32_t qb[NT][2 * KS][2];
-      float t_q[NT][2];  // the scales of columns 2t and 2t + 1
-#pragma unroll
-      for (int nt = 0; nt < NT; ++nt) {
-        const int r = 8 * nt + (lane >> 2);
-#pragma unroll
-        for (int ks = 0; ks < KS; ++ks)
-#pragma unroll
-          for (int h = 0; h < 2; ++h) {
-            const uint32_t a = works && r < P.group
-                                   ? *reinterpret_cast<const uint32_t*>(
-                                         q_codes + (gi * P.group + r) * D + 32 * ks + 16 * h +
-                                         4 * (lane & 3))
-                                   : 0u;
-            const uint32_t neg = __vcmplts4(a, 0u);
-            qb[nt][ks][h] = a & ~neg;
-            qb[nt][KS + ks][h] = a & neg;
-          }
-#pragma unroll
-        for (int e = 0; e < 2; ++e) {
-          const int rq = 8 * nt + 2 * (lane & 3) + e;
-          t_q[nt][e] = works && rq < P.group ? q_scale[gi * P.group + rq] : 0.f;
+          ++stages;
+          advance();
         }
       }
-      float* out = P.scores + ((size_t)b * P.h_kv + g) * P.row_stride;
-      for (int k = 0; k < seg.steps; ++k) {
-        // one step ahead: the next pages' scales and the table entries behind
-        const float sc_nxt = page_nxt >= 0 ? __ldg(P.scales + (size_t)page_nxt * P.h_kv + g) : 0.f;
-        const int page_nn = page_at(seg, k + 2, mine);
-        const bool ok = mbar_wait(smem_u32(&full[slot_out]), parity, &abort_flag);
-        if (works && ok) {
-          // 16 pages are the MMA's rows; every fragment is loaded before the
-          // first is used
-          const uint32_t rows = smem_u32(score_sm) + slot_out * stage_bytes +
-                                (sub * 16 + (lane & 15)) * page_bytes + gi * 2 * D +
-                                (lane >> 4) * 16;
+    } else {
+      // ---------------------------------------------------------- scores
+      const int gi = w % hs, sub = w / hs, g = g0 + gi;
+      const bool works = sub < per_head && gi < heads;
+      while (works && !stop && open()) {
+        // lane i < 16: page i of this warp's 16 of a step, -1 where there is none
+        auto page_at = [&](int k) {
+          const int i = seg.p0 + k * stage_pages + sub * 16 + lane;
+          if (lane >= 16 || i >= seg.p1) return -1;
+          const int page = __ldg(seg.table + i);
+          return page >= 0 && page < P.num_pages ? page : -1;
+        };
+        int page_cur = page_at(0), page_nxt = page_at(1);
+        float sc = page_cur >= 0 ? __ldg(P.scales + (size_t)page_cur * P.h_kv + g) : 0.f;
+        if (!waited) asm volatile("griddepcontrol.wait;\n" ::: "memory");  // the query's codes
+        waited = true;
+        // B fragments of the head's query codes: the column is a query head of
+        // the group; the first D/32 k steps take the codes >= 0 (they meet the
+        // max codes), the others those below 0
+        uint32_t qb[NT][2 * KS][2];
+        float t_q[NT][2];  // the scales of columns 2t and 2t + 1
+        const size_t q0 = (size_t)seg.b * P.h_q + (size_t)g * P.group;
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt) {
+          const int r = 8 * nt + (lane >> 2);
+#pragma unroll
+          for (int ks = 0; ks < KS; ++ks)
+#pragma unroll
+            for (int h = 0; h < 2; ++h)
+              qb[nt][ks][h] = r < P.group ? __ldcg(reinterpret_cast<const uint32_t*>(
+                                                P.q_codes + (q0 + r) * D + 32 * ks + 16 * h +
+                                                4 * (lane & 3)))
+                                          : 0u;
+#pragma unroll
+          for (int e = 0; e < 2; ++e) {
+            const int rq = 8 * nt + 2 * (lane & 3) + e;
+            t_q[nt][e] = rq < P.group ? __ldcg(P.q_scales + q0 + rq) : 0.f;
+          }
+#pragma unroll
+          for (int ks = 0; ks < KS; ++ks)
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+              const uint32_t a = qb[nt][ks][h], neg = __vcmplts4(a, 0u);
+              qb[nt][ks][h] = a & ~neg;
+              qb[nt][KS + ks][h] = a & neg;
+            }
+        }
+        float* out = P.scores + ((size_t)seg.b * P.h_kv + g) * P.row_stride;
+        for (int k = 0; k < seg.steps; ++k) {
+          // a step ahead: the next pages' scales, and the table entries behind them
+          const float sc_nxt =
+              page_nxt >= 0 ? __ldg(P.scales + (size_t)page_nxt * P.h_kv + g) : 0.f;
+          const int page_nn = page_at(k + 2);
+          if (!mbar_wait(smem_u32(&full[slot]), parity, &abort_flag)) {
+            stop = true;
+            break;
+          }
+          // 16 pages are the MMA's rows; every fragment is loaded, and the
+          // stage given back, before the first is used
+          const uint32_t rows = sm0 + slot * stage_bytes + (sub * 16 + (lane & 15)) * page_bytes +
+                                gi * 2 * D + (lane >> 4) * 16;
           uint32_t x[2 * KS][4];
 #pragma unroll
           for (int ks = 0; ks < 2 * KS; ++ks)
             ldmatrix_x4(rows + ks * 32, x[ks][0], x[ks][1], x[ks][2], x[ks][3]);
+          __syncwarp();
+          if (lane == 0) mbar_arrive(smem_u32(&empty[slot]));
+          advance();
           int acc[NT][2][4];  // two chains
 #pragma unroll
           for (int nt = 0; nt < NT; ++nt)
@@ -652,8 +678,7 @@ __global__ void __launch_bounds__(kScoreWarps * 32, 2) page_score_kernel(ScorePa
 #pragma unroll
           for (int ks = 0; ks < 2 * KS; ++ks)
 #pragma unroll
-            for (int nt = 0; nt < NT; ++nt)
-              mma_s8_16832(acc[nt][ks & 1], x[ks], qb[nt][ks]);
+            for (int nt = 0; nt < NT; ++nt) mma_s8_16832(acc[nt][ks & 1], x[ks], qb[nt][ks]);
           // lane (g, t): pages g and g + 8, heads 2t and 2t + 1
           const float s0 = __shfl_sync(0xffffffffu, sc, lane >> 2);
           const float s1 = __shfl_sync(0xffffffffu, sc, (lane >> 2) + 8);
@@ -662,8 +687,7 @@ __global__ void __launch_bounds__(kScoreWarps * 32, 2) page_score_kernel(ScorePa
           for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
             for (int e = 0; e < 2; ++e) {
-              const int r = 8 * nt + 2 * (lane & 3) + e;
-              if (r < P.group) {
+              if (8 * nt + 2 * (lane & 3) + e < P.group) {
                 // whole numbers below 2^24: exact as floats
                 const float d0 = (float)(acc[nt][0][e] + acc[nt][1][e]);
                 const float d1 = (float)(acc[nt][0][2 + e] + acc[nt][1][2 + e]);
@@ -677,35 +701,25 @@ __global__ void __launch_bounds__(kScoreWarps * 32, 2) page_score_kernel(ScorePa
             b1 = fmaxf(b1, __shfl_xor_sync(0xffffffffu, b1, o));
           }
           const int row = (lane >> 2) + 8 * (lane & 1);
-          const int i = p0 + k * stage_pages + sub * 16 + row;
+          const int i = seg.p0 + k * stage_pages + sub * 16 + row;
           const int page = __shfl_sync(0xffffffffu, page_cur, row);
-          if ((lane & 3) < 2 && i < p1) out[i] = page >= 0 ? (lane & 1 ? b1 : b0) : -INFINITY;
+          if ((lane & 3) < 2 && i < seg.p1) out[i] = page >= 0 ? (lane & 1 ? b1 : b0) : -INFINITY;
+          page_cur = page_nxt;
+          page_nxt = page_nn;
+          sc = sc_nxt;
         }
-        ++done;
-        slot_out = slot_out + 1 == nst ? 0 : slot_out + 1;
-        parity ^= slot_out == 0 ? 1u : 0u;
-        // every warp is past the stage (and, at the last step, past the
-        // query's codes): it may be filled again
-        if (__syncthreads_or(!ok)) {
-          --done;  // drained below
-          stop = true;
-          break;
-        }
-        issue_next();
-        page_cur = page_nxt;
-        page_nxt = page_nn;
-        sc = sc_nxt;
       }
     }
   }
-  // copies in flight land before the CTA leaves (a wait that gave up)
-  if (stop) {
-    bool drained = true;
-    for (uint32_t i = done; i < issued; ++i)
-      drained &= mbar_drain(smem_u32(&full[i % nst]), (i / nst) & 1);
-    (void)drained;
-    if (tid == 0) report(P.error_word, TL_DEVERR_TIMEOUT);
-  }
+  // a wait that gave up: the copies in flight land before the CTA leaves (each
+  // is the latest phase of its barrier)
+  if (stop && w == kScoreWarps)
+    for (uint32_t i = stages > NST ? stages - NST : 0; i < stages; ++i)
+      (void)mbar_drain(smem_u32(&full[i % NST]), (i / NST) & 1);
+  // no CTA ends before the query's kernel has, whether it read its codes or not
+  asm volatile("griddepcontrol.wait;\n" ::: "memory");
+  __syncthreads();  // every wait above is bounded
+  if (tid == 0 && abort_flag) report(P.error_word, TL_DEVERR_TIMEOUT);
 }
 
 // ------------------------------------------------------------------ select --
@@ -805,26 +819,29 @@ static tl_status bounds_impl(const void* k, const float* k_scales, const int32_t
   return launch_status();
 }
 
-template <int D, int NT, bool QF32>
-static bool launch_score(const ScoreParams& P, cudaStream_t st) {
-  auto kernel = page_score_kernel<D, NT, QF32>;
+template <int D, bool QF32>
+static bool launch_scores(const ScoreParams& P, cudaStream_t st) {
+  const int64_t rows = (int64_t)P.B * P.h_q;
+  page_query_kernel<D, QF32><<<(unsigned)((rows + 7) / 8), 256, 0, st>>>(P);
+  if (launch_status() != TL_OK) return false;
+  auto kernel = P.group <= 8 ? page_score_kernel<D, 1> : page_score_kernel<D, 2>;
   const int hs = score_heads(P.h_kv);
-  const int q_bytes = score_query_bytes(hs, P.group, D), stage = score_stage_bytes(hs, D);
-  // two CTAs share an SM's 228 KiB (each with up to 6 KiB of static state and
-  // the system's 1 KiB): 16 warps, whose waits fill each other's
-  int nst = kScoreStages;
-  while (nst > 2 && nst * stage + q_bytes > 107 * 1024) --nst;
-  const int smem = nst * stage + q_bytes;
+  // two CTAs share an SM's 228 KiB: at most 3 x 33.5 KiB of stages each, 5 KiB
+  // of static state and the system's 1 KiB
+  const int smem = kScoreStages * score_stage_bytes(hs, D);
   if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem) != cudaSuccess)
     return false;
-  const dim3 grid((unsigned)num_sms() * 2, (unsigned)((P.h_kv + hs - 1) / hs));
-  kernel<<<grid, kScoreWarps * 32, smem, st>>>(P, nst);
-  return launch_status() == TL_OK;
-}
-
-template <int D, bool QF32>
-static bool launch_score_group(const ScoreParams& P, cudaStream_t st) {
-  return P.group <= 8 ? launch_score<D, 1, QF32>(P, st) : launch_score<D, 2, QF32>(P, st);
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3((unsigned)num_sms() * 2, (unsigned)((P.h_kv + hs - 1) / hs));
+  cfg.blockDim = dim3(kScoreThreads);
+  cfg.dynamicSmemBytes = (size_t)smem;
+  cfg.stream = st;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, kernel, P) == cudaSuccess;
 }
 
 SelectShape select_shape(int64_t rows, int64_t cap) {
@@ -902,10 +919,24 @@ extern "C" tl_status tl_kv_page_bounds_int8(const int8_t* k_codes, const float* 
                          tl::kInt8, error_word, stream);
 }
 
-extern "C" size_t tl_kv_page_select_workspace_size(int32_t B, int32_t h_kv,
+namespace tl {
+// Workspace of a selection: the scores, the query's scales and its codes.
+struct SelectWorkspace {
+  size_t q_scales, q_codes, bytes;
+};
+static SelectWorkspace select_ws_layout(int B, int h_q, int h_kv, int d, int max_pages) {
+  SelectWorkspace w;
+  w.q_scales = align_up(sizeof(float) * (size_t)B * h_kv * score_stride(max_pages), 256);
+  w.q_codes = align_up(w.q_scales + sizeof(float) * (size_t)B * h_q, 256);
+  w.bytes = align_up(w.q_codes + (size_t)B * h_q * d, 256);
+  return w;
+}
+}  // namespace tl
+
+extern "C" size_t tl_kv_page_select_workspace_size(int32_t B, int32_t h_q, int32_t h_kv, int32_t d,
                                                    int32_t max_pages_per_seq) {
-  if (B <= 0 || h_kv <= 0 || max_pages_per_seq <= 0) return 0;
-  return tl::align_up(sizeof(float) * (size_t)B * h_kv * tl::score_stride(max_pages_per_seq), 256);
+  if (B <= 0 || h_q <= 0 || h_kv <= 0 || d <= 0 || max_pages_per_seq <= 0 || h_q % h_kv) return 0;
+  return tl::select_ws_layout(B, h_q, h_kv, d, max_pages_per_seq).bytes;
 }
 
 extern "C" tl_status tl_kv_page_select(const void* q, tl_dtype q_dtype, const int8_t* bounds,
@@ -935,7 +966,7 @@ extern "C" tl_status tl_kv_page_select(const void* q, tl_dtype q_dtype, const in
       (int64_t)B * h_kv > INT32_MAX / 8 || (h_kv + kScoreWarps - 1) / kScoreWarps > 65535)
     return TL_ERR_UNSUPPORTED;
   if (!workspace || (reinterpret_cast<uintptr_t>(workspace) & 255u) ||
-      workspace_bytes < tl_kv_page_select_workspace_size(B, h_kv, max_pages_per_seq))
+      workspace_bytes < tl_kv_page_select_workspace_size(B, h_q, h_kv, d, max_pages_per_seq))
     return TL_ERR_WORKSPACE;
   cudaStream_t st = (cudaStream_t)stream;
   ScoreParams S;
@@ -944,7 +975,10 @@ extern "C" tl_status tl_kv_page_select(const void* q, tl_dtype q_dtype, const in
   S.scales = bound_scales;
   S.block_table = block_table;
   S.context_lens = context_lens;
+  const SelectWorkspace ws = select_ws_layout(B, h_q, h_kv, d, max_pages_per_seq);
   S.scores = static_cast<float*>(workspace);
+  S.q_scales = reinterpret_cast<float*>(static_cast<char*>(workspace) + ws.q_scales);
+  S.q_codes = reinterpret_cast<int8_t*>(static_cast<char*>(workspace) + ws.q_codes);
   S.row_stride = score_stride(max_pages_per_seq);
   S.max_pages_per_seq = max_pages_per_seq;
   S.B = B;
@@ -955,10 +989,8 @@ extern "C" tl_status tl_kv_page_select(const void* q, tl_dtype q_dtype, const in
   S.page_size = page_size;
   S.error_word = error_word;
   const bool f32 = q_dtype == TL_F32;
-  const bool ran = d == 128 ? (f32 ? launch_score_group<128, true>(S, st)
-                                   : launch_score_group<128, false>(S, st))
-                            : (f32 ? launch_score_group<64, true>(S, st)
-                                   : launch_score_group<64, false>(S, st));
+  const bool ran = d == 128 ? (f32 ? launch_scores<128, true>(S, st) : launch_scores<128, false>(S, st))
+                            : (f32 ? launch_scores<64, true>(S, st) : launch_scores<64, false>(S, st));
   if (!ran) return TL_ERR_CUDA;
   PageSelectParams P;
   P.scores = S.scores;

@@ -376,7 +376,7 @@ def test_a_step_captured_in_a_graph_and_on_another_stream():
     out = torch.empty((3, hkv * group, d), device="cuda")
     pages = torch.empty((3, hkv, 8), dtype=torch.int32, device="cuda")
     ln = torch.empty(3, dtype=torch.int32, device="cuda")
-    ws1 = tl.alloc_workspace(tl.tl_kv_page_select_workspace_size(3, hkv, tb.shape[1]), "cuda")
+    ws1 = tl.alloc_workspace(tl.tl_kv_page_select_workspace_size(3, hkv * group, hkv, d, tb.shape[1]), "cuda")
     ws2 = tl.alloc_workspace(tl.tl_paged_attn_decode_workspace_size(3, hkv * group, hkv, d), "cuda")
 
     def step():

@@ -61,11 +61,12 @@ def test_page_select_refusals(lib):
         assert s(**{name: off}) == BAD, name
     assert s(qd=tl.TL_FP8_E4M3) == UNS and s(d=256) == UNS and s(hq=34) == UNS
     assert s(ps=300) == UNS and s(B=1 << 20, maxp=1 << 12) == UNS and s(n=1 << 28) == UNS
-    need = tl.tl_kv_page_select_workspace_size(2, 2, 8)
-    assert need == 256  # 2 x 2 x 8 floats
+    size = tl.tl_kv_page_select_workspace_size
+    need = size(2, 8, 2, 128, 8)
+    assert need == 256 + 256 + 2 * 8 * 128  # 2 x 2 x 8 scores, 2 x 8 scales, the codes
     assert s(ws=None) == WS and s(ws=2064) == WS and s(wsb=need - 1) == WS
-    assert tl.tl_kv_page_select_workspace_size(0, 2, 8) == 0
-    assert tl.tl_kv_page_select_workspace_size(64, 8, 8192) == 64 * 8 * 8192 * 4
+    assert size(0, 8, 2, 128, 8) == 0 and size(2, 7, 2, 128, 8) == 0
+    assert size(64, 32, 8, 128, 8192) == 64 * 8 * 8192 * 4 + 64 * 32 * 4 + 64 * 32 * 128
 
 
 def test_decode_pages_refusals(lib):
