@@ -592,6 +592,12 @@ __global__ void __launch_bounds__(kScoreThreads, 2) page_score_kernel(ScoreParam
             const bool ok = inside && page >= 0 && page < P.num_pages;
             if (inside && !ok) report(P.error_word, TL_DEVERR_PAGE_RANGE);
             bytes += (uint32_t)__popc(__ballot_sync(0xffffffffu, ok)) * copy_bytes;
+#ifdef TL_TEST_STALL_FIRST_STAGE
+            // failure-path test build only: the first stage of CTA 0 expects 16
+            // bytes that no copy delivers, so the waits for it run out (the
+            // copies it does issue all land before the CTA exits)
+            if (blockIdx.x == 0 && blockIdx.y == 0 && stages == 0 && c0 == 0) bytes += 16;
+#endif
             if (c0 + 32 >= n_here && lane == 0) mbar_arrive_expect_tx(smem_u32(&full[slot]), bytes);
             if (ok)
               bulk_g2s(sm0 + slot * stage_bytes + (c0 + lane) * page_bytes,
@@ -711,14 +717,14 @@ __global__ void __launch_bounds__(kScoreThreads, 2) page_score_kernel(ScoreParam
       }
     }
   }
-  // a wait that gave up: the copies in flight land before the CTA leaves (each
-  // is the latest phase of its barrier)
-  if (stop && w == kScoreWarps)
-    for (uint32_t i = stages > NST ? stages - NST : 0; i < stages; ++i)
-      (void)mbar_drain(smem_u32(&full[i % NST]), (i / NST) & 1);
   // no CTA ends before the query's kernel has, whether it read its codes or not
   asm volatile("griddepcontrol.wait;\n" ::: "memory");
   __syncthreads();  // every wait above is bounded
+  // a wait that gave up: the copies in flight land before the CTA leaves (each
+  // is the latest phase of its barrier)
+  if (abort_flag && w == kScoreWarps)
+    for (uint32_t i = stages > NST ? stages - NST : 0; i < stages; ++i)
+      (void)mbar_drain(smem_u32(&full[i % NST]), (i / NST) & 1);
   if (tid == 0 && abort_flag) report(P.error_word, TL_DEVERR_TIMEOUT);
 }
 

@@ -443,3 +443,96 @@ def test_an_eviction_captured_in_a_graph():
     assert torch.equal(keep, k2) and torch.equal(new, n2)
     data, _, wm = compact_ref(pools, table, lens, k2.cpu(), n2.cpu().tolist(), ref_mass.cpu())
     assert same(p["k"], data["k"]) and torch.equal(mass.cpu(), wm)
+
+
+# ------------------------------------------------------------------- edges --
+
+def test_mass_and_compaction_past_32_bit_offsets():
+    """Pools of more than 2^32 elements, only their last pages filled; a mass of as many places
+    a row as the longest of contexts."""
+    P, ps, hkv, d = 270000, 16, 8, 128
+    lens = [500, 90]
+    small, n = ref.tables(lens, ps, seed=1, spare=0)
+    table = torch.where(small >= 0, P - 1 - small, -1).int()
+    pools = ref.Pools("bf16", n, ps, hkv, d, seed=2)
+    k = torch.empty((P, ps, hkv, d), dtype=torch.bfloat16, device="cuda")
+    v = torch.empty_like(k)
+    far = (P - 1 - torch.arange(n)).cuda()
+    k[far], v[far] = pools.data["k"].cuda(), pools.data["v"].cuda()
+    q = torch.randn((2, 1, 32, d), generator=torch.Generator().manual_seed(3)).bfloat16()
+    mass0 = torch.rand((2, hkv, 500), generator=torch.Generator().manual_seed(4))
+    mass = mass0.cuda()
+    err = word()
+    out = tl.tl_paged_attn_decode_mass(q.cuda(), k, v, table.cuda(), i32(lens), mass, 0.09,
+                                       error_word=err)
+    check_mass(out, mass, mass0, pools, q, small, lens, 0.09, 0, "far")
+    keep, new = check_evict(mass.cpu(), lens, 200, 2, 20)
+    data, _, want = compact_ref(pools, small, lens, keep.cpu(), new.cpu().tolist(), mass.cpu())
+    tl.tl_kv_cache_compact(k, v, table.cuda(), i32(lens), keep, new, mass=mass, error_word=err)
+    assert int(err.item()) == 0
+    assert same(k[far], data["k"]) and same(v[far], data["v"]) and torch.equal(mass.cpu(), want)
+
+
+def test_mass_of_several_calls_adds_up_and_two_streams():
+    lens = [800, 30]
+    table, P = ref.tables(lens, 16, seed=1)
+    pools = ref.Pools("bf16", P, 16, 2, 128, seed=2)
+    p = pools.gpu()
+    tb, ln = table.cuda(), i32(lens)
+    g = torch.Generator().manual_seed(3)
+    qs = [torch.randn((2, 1, 8, 128), generator=g).bfloat16().cuda() for _ in range(2)]
+    masses = [torch.zeros((2, 2, 800), device="cuda") for _ in range(2)]
+    streams = [torch.cuda.Stream(), torch.cuda.Stream()]
+    torch.cuda.synchronize()
+    for _ in range(10):
+        for i, s in enumerate(streams):
+            with torch.cuda.stream(s):
+                tl.tl_paged_attn_decode_mass(qs[i], p["k"], p["v"], tb, ln, masses[i], 0.09,
+                                             stream=s)
+    torch.cuda.synchronize()
+    for i in range(2):
+        once = torch.zeros((2, 2, 800), device="cuda")
+        tl.tl_paged_attn_decode_mass(qs[i], p["k"], p["v"], tb, ln, once, 0.09)
+        want = once.clone()
+        for _ in range(9):
+            want += once  # the same additions in the same order
+        assert torch.equal(masses[i], want)
+
+
+def test_a_verify_step_longer_than_the_sequence():
+    """Tokens before the sequence's first position see nothing: output 0, no weight."""
+    lens = [1, 2, 3, 40]
+    table, P = ref.tables(lens, 16, seed=1)
+    pools = ref.Pools("bf16", P, 16, 2, 128, seed=2)
+    q = torch.randn((4, 4, 4, 128), generator=torch.Generator().manual_seed(3)).bfloat16()
+    mass0 = torch.zeros((4, 2, 40))
+    mass = mass0.cuda()
+    out = run_mass(pools, q, table, lens, mass, 0.09)
+    check_mass(out, mass, mass0, pools, q, table, lens, 0.09, 0, "short")
+    assert torch.all(out[0, :3] == 0) and torch.all(out[1, :2] == 0)
+
+
+def test_compact_twice_over_the_same_list():
+    """A second call gathers from the moved rows: every call reads the pools as they are."""
+    lens = [300, 300]
+    table, P = ref.tables(lens, 16, seed=1)
+    pools = ref.Pools("int8", P, 16, 2, 128, seed=2)
+    keep, new = random_keep(lens, 2, 120, seed=3)
+    p = pools.gpu()
+    args = (table.cuda(), i32(lens), keep.cuda(), i32(new))
+    for _ in range(2):
+        tl.tl_kv_cache_compact_int8(p["k"], p["v"], p["ks"], p["vs"], *args)
+        data, scales, _ = compact_ref(pools, table, lens, keep, new, None)
+        pools.data, pools.scales = data, scales
+    assert all(same(p[n], data[n]) and same(p[n + "s"], scales[n]) for n in data)
+
+
+def test_keeping_as_much_as_there_is_moves_nothing():
+    lens = [64, 100]
+    table, P = ref.tables(lens, 16, seed=1)
+    pools = ref.Pools("bf16", P, 16, 1, 64, seed=2)
+    mass = weights((2, 1, 100), 3)
+    keep, new = check_evict(mass, lens, 128, 0, 0)
+    assert new.cpu().tolist() == lens
+    p, m = run_compact(pools, table, lens, keep.cpu(), new.cpu().tolist(), mass)
+    assert same(p["k"], pools.data["k"]) and torch.equal(m.cpu(), mass)

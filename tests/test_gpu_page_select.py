@@ -405,3 +405,130 @@ def test_a_step_captured_in_a_graph_and_on_another_stream():
         want_t, want_l = ref.page_select(qn, want_b, want_s, table, lens, ps, 8, 0, 1, P)
         assert torch.equal(pages.cpu(), want_t)
         check_pages(out, pools, qn, want_t, want_l, 0.09, f"replay {seed}")
+
+
+# ------------------------------------------------------------------- edges --
+
+def test_scores_at_the_largest_codes():
+    """Every code and query at +-127: the sums' largest magnitudes, whole numbers all the same."""
+    P, hkv = 40, 2
+    bnd = torch.full((P, hkv, 2, 128), 127, dtype=torch.int8)
+    bnd[:, :, 1] = -127
+    bnd[::3, 0, 0, 5], bnd[1::3, 1, 1, 77] = 126, -126
+    sc = torch.full((P, hkv), 0.03)
+    sc[7::11] = 0.030000001
+    q = torch.ones(1, 16, 128)
+    q[0, 1::2, ::2] = -1
+    table = torch.randperm(P, generator=torch.Generator().manual_seed(1)).int().view(1, P)
+    for n in (1, 11, 39):
+        check_select(q, bnd, sc, table, [P * 16], 16, n, 0, 1)
+        check_select(q.bfloat16(), bnd, sc, table, [P * 16 - 9], 16, n, 0, 1)
+
+
+def test_query_scales_out_of_the_ordinary():
+    """Rows whose scale is subnormal, tiny, huge or zero: the codes are those of the division."""
+    P = 50
+    bnd, sc = random_bounds(P, 4, 64, seed=3)
+    g = torch.Generator().manual_seed(4)
+    q = torch.randn((4, 4, 64), generator=g)
+    mul = torch.tensor([1e-42, 1e-36, 1e35, 0.0]).view(1, 4, 1)
+    table = torch.stack([torch.randperm(P, generator=g).int() for _ in range(4)])
+    check_select(q * mul, bnd, sc, table, [P * 16] * 4, 16, 9, 0, 1)
+
+
+@pytest.mark.parametrize("mul", [1e-44, 1e-37, 3e37])
+def test_bounds_of_keys_of_extreme_size(mul):
+    lens = [37]
+    table, P = ref.tables(lens, 16, seed=1)
+    pools = ref.Pools("f32", P, 16, 2, 64, seed=2, only_k=True)
+    pools.data["k"].mul_(mul / 10)
+    b0, s0 = start_bounds(P, 2, 64)
+    got_b, got_s = run_bounds("f32", pools, table, lens, None, b0, s0)
+    want_b, want_s = ref.bounds(pools.values("k"), table, lens, None, 16, b0, s0)
+    assert torch.equal(got_s, want_s) and torch.equal(got_b, want_b)
+
+
+@pytest.mark.parametrize("kind", ["bf16", "e4m3"])
+def test_halves_round_to_even(kind):
+    """Keys whose quotients fall on halves (few bits, small multiples of the largest)."""
+    table, P = ref.tables([16 * 40], 16, seed=1)
+    pools = ref.Pools("f32", P, 16, 1, 128, seed=2, only_k=True)
+    g = torch.Generator().manual_seed(3)
+    x = torch.randint(-254, 255, (P, 16, 1, 128), generator=g) * 0.5
+    x[:, 0, 0, 0] = 127.0 if kind == "bf16" else 112.0
+    pools.kind, pools.data["k"] = kind, x.clamp(-127, 127).to(ref.TYPES[kind])
+    b0, s0 = start_bounds(P, 1, 128)
+    got_b, got_s = run_bounds(kind, pools, table, [16 * 40], None, b0, s0)
+    want_b, want_s = ref.bounds(pools.values("k"), table, [16 * 40], None, 16, b0, s0)
+    assert torch.equal(got_s, want_s) and torch.equal(got_b, want_b)
+
+
+def test_more_sequences_than_a_round_select():
+    lens = [(11 * b) % 90 for b in range(1100)]
+    table, P = ref.tables(lens, 8, seed=1)
+    bnd, sc = random_bounds(P, 1, 64, seed=2)
+    q = torch.randn((1100, 2, 64), generator=torch.Generator().manual_seed(3)).bfloat16()
+    check_select(q, bnd, sc, table, lens, 8, 4, 1, 1)
+
+
+def test_calls_on_two_streams_at_once():
+    """Two steps at once, each with its own workspaces and outputs."""
+    lens = [3000, 900]
+    table, P = ref.tables(lens, 16, seed=31)
+    pools = ref.Pools("bf16", P, 16, 2, 128, seed=32)
+    p = pools.gpu()
+    bnd = torch.zeros((P, 2, 2, 128), dtype=torch.int8, device="cuda")
+    sc = torch.zeros((P, 2), device="cuda")
+    tb, ln_in = table.cuda(), i32(lens)
+    tl.tl_kv_page_bounds(p["k"], tb, ln_in, bnd, sc)
+    g = torch.Generator().manual_seed(33)
+    qs = [torch.randn((2, 8, 128), generator=g).bfloat16() for _ in range(2)]
+    dq = [q.cuda() for q in qs]
+    streams = [torch.cuda.Stream(), torch.cuda.Stream()]
+    out = [[] for _ in range(2)]
+    torch.cuda.synchronize()
+    for _ in range(20):
+        for i, s in enumerate(streams):
+            with torch.cuda.stream(s):
+                pages, ln = tl.tl_kv_page_select(dq[i], bnd, sc, tb, ln_in, 16, 20, stream=s)
+                o = tl.tl_paged_attn_decode_pages(dq[i], p["k"], p["v"], pages, ln, 0.09, stream=s)
+                out[i].append((pages, o))
+    torch.cuda.synchronize()
+    for i in range(2):
+        want_t, want_l = ref.page_select(qs[i], bnd.cpu(), sc.cpu(), table, lens, 16, 20, 0, 1, P)
+        check_pages(out[i][0][1], pools, qs[i], want_t, want_l, 0.09, f"stream {i}")
+        for pages, o in out[i]:
+            assert torch.equal(pages.cpu(), want_t) and torch.equal(o, out[i][0][1])
+
+
+def test_pages_past_32_bit_offsets():
+    """Pools of more than 2^32 elements, only their last pages filled."""
+    P, ps, hkv, d = 270000, 16, 8, 128  # 4.4e9 elements a pool
+    lens = [700, 333]
+    need = [-(-n // ps) for n in lens]
+    table = torch.full((2, max(need)), -1, dtype=torch.int32)
+    order = torch.randperm(sum(need), generator=torch.Generator().manual_seed(1))
+    small = torch.full((2, max(need)), -1, dtype=torch.int32)
+    at = 0
+    for b, n in enumerate(need):
+        small[b, :n] = order[at:at + n].int()
+        table[b, :n] = P - 1 - small[b, :n]
+        at += n
+    n = sum(need)
+    pools = ref.Pools("bf16", n, ps, hkv, d, seed=2)
+    k = torch.empty((P, ps, hkv, d), dtype=torch.bfloat16, device="cuda")
+    v = torch.empty_like(k)
+    bnd = torch.empty((P, hkv, 2, d), dtype=torch.int8, device="cuda")
+    sc = torch.empty((P, hkv), device="cuda")
+    far = P - 1 - torch.arange(n)
+    k[far.cuda()], v[far.cuda()] = pools.data["k"].cuda(), pools.data["v"].cuda()
+    tl.tl_kv_page_bounds(k, table.cuda(), i32(lens), bnd, sc)
+    want_b, want_s = ref.bounds(pools.values("k"), small, lens, None, ps,
+                                torch.zeros((n, hkv, 2, d), dtype=torch.int8), torch.zeros((n, hkv)))
+    assert torch.equal(bnd[far.cuda()].cpu(), want_b) and torch.equal(sc[far.cuda()].cpu(), want_s)
+    q = torch.randn((2, 32, d), generator=torch.Generator().manual_seed(3)).bfloat16()
+    pages, ln = tl.tl_kv_page_select(q.cuda(), bnd, sc, table.cuda(), i32(lens), ps, 10)
+    want_t, want_l = ref.page_select(q, want_b, want_s, small, lens, ps, 10, 0, 1, n)
+    assert torch.equal(pages.cpu(), torch.where(want_t >= 0, P - 1 - want_t, -1))
+    out = tl.tl_paged_attn_decode_pages(q.cuda(), k, v, pages, ln, 0.09)
+    check_pages(out, pools, q, want_t, want_l, 0.09, "far")
