@@ -44,9 +44,13 @@
 // Every reduction has a fixed order, so results repeat bit for bit and do not
 // depend on the pool's page placement.
 //
+// The EX form of a call with few sequences has no plan launch, and one with a
+// mass a last launch more (decode_mass_kernel).
+//
 // Template argument EX (paged_decode_ex.cu): the form that reads a table per
 // (sequence, KV head) and / or leaves every score and each output row's
-// softmax statistics in memory.  The plain form compiles none of it.
+// softmax statistics in memory; 2: without a plan launch, for few sequences.
+// The plain form (0) compiles none of it.
 #pragma once
 
 #include <algorithm>
@@ -175,7 +179,10 @@ struct DecodeParams {
   // log2 units, [B][H_kv][rows][score_stride] by key position (-inf where a
   // row does not see a key of the pieces' chunks).  stats: each output row's
   // running max (log2 units) and sum, [B][hq_all][2].
+  // self_plan: no plan launch; every attention CTA derives the pieces itself
+  // (at most kSelfPlanMax sequences).
   int32_t head_tables;
+  int32_t self_plan, target_splits;
   float* scores;
   int64_t score_stride;
   float* stats;
@@ -376,6 +383,90 @@ __device__ __forceinline__ void write_piece_descs(const DecodeParams& P, const i
 constexpr int kWarpPlanMax = 128;
 constexpr int kWriteWarps = 8;  // writing warps per CTA of a warp-planned launch
 
+// The piece layout from the sequences' ranges rng[b] = {lo, p}, by one warp:
+// rec[b] as write_piece_descs takes it, s_plan = {split, small, bulk pieces (-1:
+// refused), small pieces}; with `publish`, the workspace's offsets, count and
+// counter too.
+__device__ __forceinline__ void warp_plan(const DecodeParams& P, int target_splits,
+                                          int first_dynamic, const int2* rng, int4* rec,
+                                          int* s_plan, bool publish, int lane) {
+  const int K = (P.B + 31) >> 5, b0 = min(lane * K, P.B), b1 = min(b0 + K, P.B);
+  long long C = 0, T = 0;
+#pragma unroll 1
+  for (int b = b0; b < b1; ++b) {
+    const int n = rng[b].y < 0 ? 0 : rng[b].y / kChunk - rng[b].x / kChunk + 1;
+    C += n;
+    T += tail_chunks(n);
+  }
+  C = warp_sum64(C);
+  T = warp_sum64(T);
+  const long long half = max(target_splits / 2, 1);
+  const int small = (int)max((long long)kSmallChunks, (T + P.B + half - 1) / half);
+  long long TP = 0;
+#pragma unroll 1
+  for (int b = b0; b < b1; ++b) {
+    const int n = rng[b].y < 0 ? 0 : rng[b].y / kChunk - rng[b].x / kChunk + 1;
+    TP += (tail_chunks(n) + small - 1) / small;
+  }
+  TP = warp_sum64(TP);
+  const long long budget = (long long)target_splits + P.B - TP;
+  const long long sb = (C - T + budget - 1) / budget;
+  const int split = (int)(sb < kMinSplitChunks ? kMinSplitChunks : sb);
+  long long x = 0;  // this lane's (bulk << 32 | small) pieces
+#pragma unroll 1
+  for (int b = b0; b < b1; ++b) {
+    const int n = rng[b].y < 0 ? 0 : rng[b].y / kChunk - rng[b].x / kChunk + 1;
+    const int t = tail_chunks(n);
+    x += ((long long)((n - t + split - 1) / split) << 32) | ((t + small - 1) / small);
+  }
+  long long inc = x;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const long long y = __shfl_up_sync(0xffffffffu, inc, o);
+    if (lane >= o) inc += y;
+  }
+  const long long tot = __shfl_sync(0xffffffffu, inc, 31);
+  const int NB = (int)(tot >> 32), NS = (int)(tot & 0xffffffffll);
+  if (NB + NS > decode_max_splits(P.B, P.h_kv)) {
+    // past the workspace's bound (see the block-wide path): refused
+    if (publish)
+      for (int b = lane; b <= P.B; b += 32) P.ws.split_off[b] = 0;
+    if (lane == 0) {
+      if (publish) {
+        report(P.error_word, TL_DEVERR_PLAN_CAPACITY);
+        P.ws.ctrl[0] = split;
+        P.ws.ctrl[1] = 0;
+        P.ws.ctrl[2] = first_dynamic;
+      }
+      s_plan[2] = -1;
+    }
+  } else {
+    long long pos = inc - x;
+#pragma unroll 1
+    for (int b = b0; b < b1; ++b) {
+      const int n = rng[b].y < 0 ? 0 : rng[b].y / kChunk - rng[b].x / kChunk + 1;
+      const int t = tail_chunks(n);
+      const int nb = (n - t + split - 1) / split, ntl = (t + small - 1) / small;
+      const int pos_b = (int)(pos >> 32), pos_t = (int)(pos & 0xffffffffll);
+      if (publish) P.ws.split_off[b] = pos_b + pos_t;
+      rec[b] = make_int4(pos_b, pos_t, nb, ntl);
+      pos += ((long long)nb << 32) | ntl;
+    }
+    if (lane == 0) {
+      if (publish) {
+        P.ws.split_off[P.B] = NB + NS;
+        P.ws.ctrl[0] = split;
+        P.ws.ctrl[1] = NB + NS;
+        P.ws.ctrl[2] = first_dynamic;
+      }
+      s_plan[0] = split;
+      s_plan[1] = small;
+      s_plan[2] = NB;
+      s_plan[3] = NS;
+    }
+  }
+}
+
 // One CTA.  Up to kWarpPlanMax sequences: warp 0 plans alone (above).
 // Larger batches: thread t keeps sequence t's range in registers (sequences
 // past the block size are re-read in each pass); three block reductions fix
@@ -502,78 +593,7 @@ static __global__ void __launch_bounds__(1024) decode_plan_kernel(DecodeParams P
       rng[tid] = make_int2(lo, p);
     }
     __syncthreads();
-    if (wid == 0) {
-      const int K = (P.B + 31) >> 5, b0 = min(lane * K, P.B), b1 = min(b0 + K, P.B);
-      long long C = 0, T = 0;
-#pragma unroll 1
-      for (int b = b0; b < b1; ++b) {
-        const int n = rng[b].y < 0 ? 0 : rng[b].y / kChunk - rng[b].x / kChunk + 1;
-        C += n;
-        T += tail_chunks(n);
-      }
-      C = warp_sum64(C);
-      T = warp_sum64(T);
-      const long long half = max(target_splits / 2, 1);
-      const int small = (int)max((long long)kSmallChunks, (T + P.B + half - 1) / half);
-      long long TP = 0;
-#pragma unroll 1
-      for (int b = b0; b < b1; ++b) {
-        const int n = rng[b].y < 0 ? 0 : rng[b].y / kChunk - rng[b].x / kChunk + 1;
-        TP += (tail_chunks(n) + small - 1) / small;
-      }
-      TP = warp_sum64(TP);
-      const long long budget = (long long)target_splits + P.B - TP;
-      const long long sb = (C - T + budget - 1) / budget;
-      const int split = (int)(sb < kMinSplitChunks ? kMinSplitChunks : sb);
-      long long x = 0;  // this lane's (bulk << 32 | small) pieces
-#pragma unroll 1
-      for (int b = b0; b < b1; ++b) {
-        const int n = rng[b].y < 0 ? 0 : rng[b].y / kChunk - rng[b].x / kChunk + 1;
-        const int t = tail_chunks(n);
-        x += ((long long)((n - t + split - 1) / split) << 32) | ((t + small - 1) / small);
-      }
-      long long inc = x;
-#pragma unroll
-      for (int o = 1; o < 32; o <<= 1) {
-        const long long y = __shfl_up_sync(0xffffffffu, inc, o);
-        if (lane >= o) inc += y;
-      }
-      const long long tot = __shfl_sync(0xffffffffu, inc, 31);
-      const int NB = (int)(tot >> 32), NS = (int)(tot & 0xffffffffll);
-      if (NB + NS > decode_max_splits(P.B, P.h_kv)) {
-        // past the workspace's bound (see the block-wide path): refused
-        for (int b = lane; b <= P.B; b += 32) P.ws.split_off[b] = 0;
-        if (lane == 0) {
-          report(P.error_word, TL_DEVERR_PLAN_CAPACITY);
-          P.ws.ctrl[0] = split;
-          P.ws.ctrl[1] = 0;
-          P.ws.ctrl[2] = first_dynamic;
-          s_plan[2] = -1;
-        }
-      } else {
-        long long pos = inc - x;
-#pragma unroll 1
-        for (int b = b0; b < b1; ++b) {
-          const int n = rng[b].y < 0 ? 0 : rng[b].y / kChunk - rng[b].x / kChunk + 1;
-          const int t = tail_chunks(n);
-          const int nb = (n - t + split - 1) / split, ntl = (t + small - 1) / small;
-          const int pos_b = (int)(pos >> 32), pos_t = (int)(pos & 0xffffffffll);
-          P.ws.split_off[b] = pos_b + pos_t;
-          rec[b] = make_int4(pos_b, pos_t, nb, ntl);
-          pos += ((long long)nb << 32) | ntl;
-        }
-        if (lane == 0) {
-          P.ws.split_off[P.B] = NB + NS;
-          P.ws.ctrl[0] = split;
-          P.ws.ctrl[1] = NB + NS;
-          P.ws.ctrl[2] = first_dynamic;
-          s_plan[0] = split;
-          s_plan[1] = small;
-          s_plan[2] = NB;
-          s_plan[3] = NS;
-        }
-      }
-    }
+    if (wid == 0) warp_plan(P, target_splits, first_dynamic, rng, rec, s_plan, true, lane);
     __syncthreads();
     if (s_plan[2] < 0) return;
     if (tid == 0) TL_TRACE_SET(TL_TRACE_PLAN_PLACED);
@@ -670,6 +690,16 @@ static __global__ void __launch_bounds__(1024) decode_plan_kernel(DecodeParams P
   }
 }
 
+// Sequences up to which an EX call has no plan launch: its CTAs plan for
+// themselves (one sequence a lane of one warp) and take a fixed share of the
+// items, which saves a launch and its 4-5 us but not the counter's evenness.
+// Measured with and without it (us a call, Llama-3-8B heads): 128 selected
+// pages of 1, 4, 8, 16, 32 sequences 16.4 / 19.0, 17.4 / 20.0, 19.3 / 21.0,
+// 30.5 / 32.3, 51.1 / 52.3; weight-gathering over whole bf16 contexts of up to
+// 8,192 keys 20.1 / 22.8, 27.9 / 29.5, 40.3 / 41.9, 67.4 / 68.6 and, at 32,
+// 127.4 / 121.6 (e4m3: 53.1 / 54.9 at 16, 89.5 / 83.1 at 32).
+constexpr int kSelfPlanMax = 16;
+
 struct ItemInfo {
   int b, g, lo, p, c_begin, c_end;  // chunks [c_begin, c_end)
   int s_global, nsplits;            // split index in the partial arrays; splits of b
@@ -688,6 +718,30 @@ __device__ __forceinline__ void describe_item(const DecodeParams& P, int item, I
   it.lo = d1.x;
   it.p = d1.y;
   it.s_global = d1.z;
+}
+
+// The same from a layout in shared memory (rec, rng and s_plan of warp_plan).
+__device__ __forceinline__ void describe_planned(const DecodeParams& P, const int4* rec,
+                                                 const int2* rng, const int* s_plan, int item,
+                                                 ItemInfo& it) {
+  const int s = item / P.h_kv, NB = s_plan[2];
+  const bool bulk = s < NB;
+  const int pidx = bulk ? s : s - NB;
+  int j = 0;  // the last sequence whose first piece of the kind is at or before it
+  for (int b = 1; b < P.B; ++b) j = (bulk ? rec[b].x : rec[b].y) <= pidx ? b : j;
+  const int4 r = rec[j];
+  const int lo = rng[j].x, p = rng[j].y;
+  const int n = p / kChunk - lo / kChunk + 1, c0 = lo / kChunk, c1 = c0 + n;
+  const int cm = c1 - tail_chunks(n);
+  const int k = pidx - (bulk ? r.x : r.y);
+  it.g = item - s * P.h_kv;
+  it.b = j;
+  it.lo = lo;
+  it.p = p;
+  it.c_begin = bulk ? c0 + k * s_plan[0] : cm + k * s_plan[1];
+  it.c_end = bulk ? min(cm, it.c_begin + s_plan[0]) : min(c1, it.c_begin + s_plan[1]);
+  it.s_global = r.x + r.y + (bulk ? k : r.z + k);
+  it.nsplits = r.z + r.w;
 }
 
 // ------------------------------------------------------ bf16 decode kernel --
@@ -880,7 +934,7 @@ struct WarpShared {
   int abort_flag;
 };
 
-template <int D, bool TWO_ROWS, bool KV8, bool I8, bool EX>
+template <int D, bool TWO_ROWS, bool KV8, bool I8, int EX>
 __global__ void __launch_bounds__(DecodeShape<TWO_ROWS, KV8>::kWarps * 32, 1)
     decode_bf16_kernel(DecodeParams P, const __grid_constant__ CUtensorMap kmap,
                        const __grid_constant__ CUtensorMap vmap, int box_rows) {
@@ -909,6 +963,27 @@ __global__ void __launch_bounds__(DecodeShape<TWO_ROWS, KV8>::kWarps * 32, 1)
   }
   __syncthreads();
 
+  // EX with few sequences: every CTA plans for itself, CTA 0 also for the
+  // launches that follow
+  constexpr bool self_plan = EX == 2;
+  __shared__ int4 plan_rec[self_plan ? kSelfPlanMax : 1];
+  __shared__ int2 plan_rng[self_plan ? kSelfPlanMax : 1];
+  __shared__ int plan_out[4];
+  if constexpr (self_plan) {
+    if (threadIdx.x < P.B) {
+      int lo, p;
+      seq_range(P, threadIdx.x, lo, p, blockIdx.x == 0);
+      plan_rng[threadIdx.x] = make_int2(lo, p);
+    }
+    __syncthreads();
+    if (w == 0)
+      warp_plan(P, P.target_splits, 0, plan_rng, plan_rec, plan_out, blockIdx.x == 0, lane);
+    __syncthreads();
+    if (blockIdx.x == 0 && plan_out[2] >= 0)
+      write_piece_descs(P, plan_rec, plan_rng, 0, P.B, 0, plan_out[2], 0, plan_out[3], plan_out[2],
+                        plan_out[0], plan_out[1], threadIdx.x, blockDim.x);
+  }
+
   // launched as a programmatic dependent of the plan kernel: its results
   // (work counter, descriptors, offsets) are read only after this wait
   asm volatile("griddepcontrol.wait;\n" ::: "memory");
@@ -922,7 +997,9 @@ __global__ void __launch_bounds__(DecodeShape<TWO_ROWS, KV8>::kWarps * 32, 1)
   const uint32_t scale_ring = smem_u32(scale_sm) + w * R * L::kScaleBytes;
   const uint32_t qbase = ring + R * L::kStageBytes;
   const unsigned char* qbase_ptr = smem0 + (qbase - sbase0);
-  const int total_items = __ldcg(P.ws.ctrl + 1) * P.h_kv;
+  const int total_items =
+      self_plan ? (plan_out[2] < 0 ? 0 : plan_out[2] + plan_out[3]) * P.h_kv
+                : __ldcg(P.ws.ctrl + 1) * P.h_kv;
   const __nv_bfloat16* qg = static_cast<const __nv_bfloat16*>(P.q);
   const int n_slots = P.num_pages * P.page_size;
   constexpr int CPS = L::kCps;
@@ -958,27 +1035,29 @@ __global__ void __launch_bounds__(DecodeShape<TWO_ROWS, KV8>::kWarps * 32, 1)
   int items_issued = 0;
   auto fetch_step = [&]() {
     if (nstate == 0) {
-      if (lane == 0) grab = atomicAdd(P.ws.ctrl + 2, 1);
+      if constexpr (self_plan) grab += gridDim.x * (blockDim.x >> 5);  // a fixed share of few
+      else if (lane == 0) grab = atomicAdd(P.ws.ctrl + 2, 1);
       nstate = 1;
     } else if (nstate == 1) {
       const int id = __shfl_sync(0xffffffffu, grab, 0);
       if (id >= total_items) {
         nstate = 4;
       } else {
-        describe_item(P, id, inext);
+        if constexpr (self_plan) describe_planned(P, plan_rec, plan_rng, plan_out, id, inext);
+        else describe_item(P, id, inext);
         nstate = 2;
       }
     } else if (nstate == 2) {
       nwin_blk0 = page_of(P, inext.c_begin * kChunk);
       const int blk = nwin_blk0 + lane;
-      nwin = blk <= page_of(P, inext.p) ? table_entry<EX>(P, inext.b, inext.g, blk) : -1;
+      nwin = blk <= page_of(P, inext.p) ? table_entry<EX != 0>(P, inext.b, inext.g, blk) : -1;
       nstate = 3;
     }
   };
   // the first item's descriptor loads alongside the item count (its piece
   // index is inside the workspace's descriptors whatever the count: the
   // grid's warps are fewer than the pieces target)
-  if (grab / P.h_kv < decode_max_splits(P.B, P.h_kv)) {
+  if (!self_plan && grab / P.h_kv < decode_max_splits(P.B, P.h_kv)) {
     describe_item(P, grab, inext);
     nstate = grab >= total_items ? 4 : 2;
   }
@@ -1029,7 +1108,7 @@ __global__ void __launch_bounds__(DecodeShape<TWO_ROWS, KV8>::kWarps * 32, 1)
       iwin_blk0 = bmin;
       const int blk = iwin_blk0 + lane;
       iwin = blk <= last_blk
-                 ? table_entry<EX>(P, icur.b, icur.g, blk)
+                 ? table_entry<EX != 0>(P, icur.b, icur.g, blk)
                  : -1;
     }
     uint32_t mask = 0u;  // live keys of the stage (16 bits per chunk)
@@ -2225,13 +2304,14 @@ struct NewRows {
 // Warps per CTA of a bf16 / one-byte kernel variant: its shape's count, or
 // as many as the dynamic shared memory holds (227 KiB less 2 KiB for the
 // static state, the int8 scale rings and the 1 KiB alignment pad).
-template <int D, bool TWO, bool K8, bool I8>
+template <int D, bool TWO, bool K8, bool I8, bool EX>
 static int decode_warps(int rows) {
   using S = DecodeShape<TWO, K8>;
   using L = WarpSmem<D, K8, I8, S::kRing>;
   static_assert(sizeof(WarpShared<S::kWarps, S::kRing>) <= 2048, "static state over 2 KiB");
   const int scales = I8 ? S::kWarps * S::kRing * L::kScaleBytes : 0;
-  return std::min(S::kWarps, (227 * 1024 - 3072 - scales) / L::warp_bytes(rows));
+  // (EX: and 1 KiB for the pieces it plans itself)
+  return std::min(S::kWarps, (227 * 1024 - 3072 - (EX ? 1024 : 0) - scales) / L::warp_bytes(rows));
 }
 
 // ------------------------------------------------------------------ mass --
@@ -2448,14 +2528,14 @@ static tl_status decode_impl(const void* q, const void* k_cache, const void* v_c
   const bool two = rows > 8;
   int warps = 0;
   if (dtype != TL_F32) {
-    warps = i8    ? (two ? decode_warps<128, true, true, true>(rows)
-                         : decode_warps<128, false, true, true>(rows))
-            : kv8 ? (two ? decode_warps<128, true, true, false>(rows)
-                         : decode_warps<128, false, true, false>(rows))
-            : d == 128 ? (two ? decode_warps<128, true, false, false>(rows)
-                              : decode_warps<128, false, false, false>(rows))
-                       : (two ? decode_warps<64, true, false, false>(rows)
-                              : decode_warps<64, false, false, false>(rows));
+    warps = i8    ? (two ? decode_warps<128, true, true, true, EX>(rows)
+                         : decode_warps<128, false, true, true, EX>(rows))
+            : kv8 ? (two ? decode_warps<128, true, true, false, EX>(rows)
+                         : decode_warps<128, false, true, false, EX>(rows))
+            : d == 128 ? (two ? decode_warps<128, true, false, false, EX>(rows)
+                              : decode_warps<128, false, false, false, EX>(rows))
+                       : (two ? decode_warps<64, true, false, false, EX>(rows)
+                              : decode_warps<64, false, false, false, EX>(rows));
   }
   const int target_splits = (kTargetItems + h_kv - 1) / h_kv;
   // plan block: up to kWarpPlanMax sequences one warp plans and 1024
@@ -2472,9 +2552,13 @@ static tl_status decode_impl(const void* q, const void* k_cache, const void* v_c
   const int wpc = B <= kWarpPlanMax ? kWriteWarps : plan_threads / 32;
   const int64_t write_ctas =
       P.n_new > 0 ? std::min<int64_t>(num_sms(), (write_warps + wpc - 1) / wpc) : 0;
-  decode_plan_kernel<<<(unsigned)(1 + write_ctas), plan_threads, 0, st>>>(P, target_splits,
-                                                                          num_sms() * warps);
-  if (launch_status() != TL_OK) return TL_ERR_CUDA;
+  P.target_splits = target_splits;
+  P.self_plan = EX && dtype != TL_F32 && B <= kSelfPlanMax ? 1 : 0;
+  if (!P.self_plan) {
+    decode_plan_kernel<<<(unsigned)(1 + write_ctas), plan_threads, 0, st>>>(P, target_splits,
+                                                                            num_sms() * warps);
+    if (launch_status() != TL_OK) return TL_ERR_CUDA;
+  }
 
   if (dtype == TL_BF16 || dtype == TL_FP8_E4M3) {
     // 3-D tensor maps of the pools: (d, H_kv, slot), boxes of one 128-byte
@@ -2492,7 +2576,9 @@ static tl_status decode_impl(const void* q, const void* k_cache, const void* v_c
     if (!enc) return TL_ERR_CUDA;
 #define TL_LAUNCH_W(DD, TWO, K8, I8V)                                                     \
   do {                                                                                    \
-    auto kern = decode_bf16_kernel<DD, TWO, K8, I8V, EX>;                                     \
+    auto kern = decode_bf16_kernel<DD, TWO, K8, I8V, EX ? 1 : 0>;                         \
+    if constexpr (EX)                                                                     \
+      if (P.self_plan) kern = decode_bf16_kernel<DD, TWO, K8, I8V, 2>;                    \
     const int sm =                                                                        \
         warps * WarpSmem<DD, K8, I8V, DecodeShape<TWO, K8>::kRing>::warp_bytes(rows) + 1024; \
     if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, sm) !=    \
@@ -2507,7 +2593,7 @@ static tl_status decode_impl(const void* q, const void* k_cache, const void* v_c
     cfg.dynamicSmemBytes = sm;                                                            \
     cfg.stream = st;                                                                      \
     cfg.attrs = attr;                                                                     \
-    cfg.numAttrs = 1;                                                                     \
+    cfg.numAttrs = P.self_plan ? 0 : 1; /* its predecessor is not the call's plan */      \
     if (cudaLaunchKernelEx(&cfg, kern, P, kmap, vmap, box_rows) != cudaSuccess)           \
       return TL_ERR_CUDA;                                                                 \
   } while (0)
