@@ -834,6 +834,13 @@ __device__ __forceinline__ void split_f16x2(float a, float b, uint32_t& hi, uint
   asm("cvt.rn.f16x2.f32 %0, %1, %2;\n" : "=r"(lo) : "f"(b - bh), "f"(a - ah));
 }
 
+// What the bf16 pairs hi and lo leave of (a, b), as a bf16 pair.
+__device__ __forceinline__ uint32_t rest_bf16x2(float a, float b, uint32_t hi, uint32_t lo) {
+  const float ra = a - __uint_as_float(hi << 16) - __uint_as_float(lo << 16);
+  const float rb = b - __uint_as_float(hi & 0xffff0000u) - __uint_as_float(lo & 0xffff0000u);
+  return pack_bf16x2(ra, rb);
+}
+
 template <bool F16>
 __device__ __forceinline__ void split16(float a, float b, uint32_t& hi, uint32_t& lo) {
   if (F16)
@@ -1194,6 +1201,10 @@ __global__ void __launch_bounds__(DecodeShape<TWO_ROWS, KV8>::kWarps * 32, 1)
   // row c; with at most 4 rows, columns 4-7 repeat rows 0-3 and carry the
   // low parts of P (dup).
   constexpr bool KT = S::kKeysAsRows;
+  // The plain form leaves the 1152 in the int8 codes and takes it out of the
+  // scores (faster by 2%, scores off by some 10^-5); EX, whose weights are a
+  // result of their own, widens exactly.
+  constexpr bool kBiased = I8 && KT && EX == 0;
   const bool dup = KT && P.rows <= 4;
   const int qrow = dup ? (qr & 3) : qr;  // the query row of this lane's B-operand column
   uint32_t gs_c = 0;
@@ -1246,7 +1257,7 @@ __global__ void __launch_bounds__(DecodeShape<TWO_ROWS, KV8>::kWarps * 32, 1)
     // lane's score columns 2t and 2t + 1 (the B fragments hold column g's
     // values at four d a K step; the sum over t completes a column)
     float kb0 = 0.f, kb1 = 0.f;
-    if constexpr (I8 && KT) {
+    if constexpr (kBiased) {
       float part = 0.f;
 #pragma unroll
       for (int ks = 0; ks < D / 16; ++ks)
@@ -1346,9 +1357,12 @@ __global__ void __launch_bounds__(DecodeShape<TWO_ROWS, KV8>::kWarps * 32, 1)
 #pragma unroll
           for (int h = 0; h < 2; ++h) {
             uint32_t a0, a1, a2, a3;
-            if constexpr (I8) {
+            if constexpr (kBiased) {
               i8x4_as_f16x2x2_biased(w[2 * h], a0, a2);
               i8x4_as_f16x2x2_biased(w[2 * h + 1], a1, a3);
+            } else if constexpr (I8) {
+              i8x4_as_f16x2x2(w[2 * h], a0, a2);
+              i8x4_as_f16x2x2(w[2 * h + 1], a1, a3);
             } else {
               e4m3x4_as_f16x2x2(w[2 * h], a0, a2);
               e4m3x4_as_f16x2x2(w[2 * h + 1], a1, a3);
@@ -1367,10 +1381,16 @@ __global__ void __launch_bounds__(DecodeShape<TWO_ROWS, KV8>::kWarps * 32, 1)
           const uint32_t sa = scale_ring + stage * L::kScaleBytes + ((sub0 + j) * kChunk + qr) * 4;
           asm volatile("ld.shared.f32 %0, [%1];\n" : "=f"(k0) : "r"(sa));
           asm volatile("ld.shared.f32 %0, [%1];\n" : "=f"(k1) : "r"(sa + 32));
-          s[j][0] = (s[j][0] + kb0) * k0;
-          s[j][1] = (s[j][1] + kb1) * k0;
-          s[j][2] = (s[j][2] + kb0) * k1;
-          s[j][3] = (s[j][3] + kb1) * k1;
+          if constexpr (kBiased) {
+            s[j][0] += kb0;
+            s[j][1] += kb1;
+            s[j][2] += kb0;
+            s[j][3] += kb1;
+          }
+          s[j][0] *= k0;
+          s[j][1] *= k0;
+          s[j][2] *= k1;
+          s[j][3] *= k1;
         }
       }
       constexpr uint32_t all_keys = nj == 1 ? 0xffffu : 0xffffffffu;
@@ -1797,6 +1817,15 @@ __global__ void __launch_bounds__(DecodeShape<TWO_ROWS, KV8>::kWarps * 32, 1)
           uint32_t h0, l0w, h2, l2w;
           split16<KV8>(p[jc][0][0], p[jc][0][1], h0, l0w);
           split16<KV8>(p[jc][1][0], p[jc][1][1], h2, l2w);
+          // EX: a third bf16 part, 24 significant bits together: outputs within
+          // 4 x 10^-7 of exact instead of 2.4 x 10^-6, for one more MMA where
+          // there were two and 1-2% of a call
+          constexpr bool three = EX != 0 && !KV8;
+          [[maybe_unused]] uint32_t r0 = 0u, r2 = 0u;
+          if constexpr (three) {
+            r0 = rest_bf16x2(p[jc][0][0], p[jc][0][1], h0, l0w);
+            r2 = rest_bf16x2(p[jc][1][0], p[jc][1][1], h2, l2w);
+          }
           if constexpr (KV8) {
             // V's B fragments from the e4m3 codes: a transposing ldmatrix of
             // 16-byte unit j (its 16-bit elements being code pairs) hands lane
@@ -1855,11 +1884,20 @@ __global__ void __launch_bounds__(DecodeShape<TWO_ROWS, KV8>::kWarps * 32, 1)
                     b1, b2, b3);
                 mma_16816<KV8>(o[2 * nd2], h0, l0w, h2, l2w, b0, b1);
                 mma_16816<KV8>(o[2 * nd2 + 1], h0, l0w, h2, l2w, b2, b3);
+                if constexpr (three) {
+                  mma_16816<KV8>(o[2 * nd2], r0, 0u, r2, 0u, b0, b1);
+                  mma_16816<KV8>(o[2 * nd2 + 1], r0, 0u, r2, 0u, b2, b3);
+                }
               }
             } else {
               uint32_t h1, l1w, h3, l3w;
               split16<KV8>(p[jc][0][2], p[jc][0][3], h1, l1w);
               split16<KV8>(p[jc][1][2], p[jc][1][3], h3, l3w);
+              [[maybe_unused]] uint32_t r1 = 0u, r3 = 0u;
+              if constexpr (three) {
+                r1 = rest_bf16x2(p[jc][0][2], p[jc][0][3], h1, l1w);
+                r3 = rest_bf16x2(p[jc][1][2], p[jc][1][3], h3, l3w);
+              }
   #pragma unroll
               for (int nd2 = 0; nd2 < D / 16; ++nd2) {
                 const int u = 2 * nd2 + (mi >> 1);
@@ -1871,6 +1909,10 @@ __global__ void __launch_bounds__(DecodeShape<TWO_ROWS, KV8>::kWarps * 32, 1)
                 mma_16816<KV8>(o[2 * nd2], l0w, l1w, l2w, l3w, b0, b1);
                 mma_16816<KV8>(o[2 * nd2 + 1], h0, h1, h2, h3, b2, b3);
                 mma_16816<KV8>(o[2 * nd2 + 1], l0w, l1w, l2w, l3w, b2, b3);
+                if constexpr (three) {
+                  mma_16816<KV8>(o[2 * nd2], r0, r1, r2, r3, b0, b1);
+                  mma_16816<KV8>(o[2 * nd2 + 1], r0, r1, r2, r3, b2, b3);
+                }
               }
             }
           }

@@ -49,6 +49,10 @@ class Pools:
             x = x * self.scales[n].permute(0, 2, 1)[..., None]
         return x
 
+    def units(self, n):
+        """Magnitudes that 16-bit weights multiply: the values, or an int8 pool's codes."""
+        return (self.data[n].float() if self.kind == "int8" else self.values(n)).double().abs()
+
     def gpu(self):
         out = {n: x.cuda() for n, x in self.data.items()}
         out.update({n + "s": x.cuda() for n, x in self.scales.items()})
@@ -164,31 +168,23 @@ def attend(q, k, v, scale, sees):
     return p, p @ v, p @ np.abs(v)
 
 
-def score_error(kind, q, k, scale, raw_codes=None):
+def score_error(q, k, scale):
     """A bound on the error of a score in the kernels (natural-log units): d products summed in
-    f32, each addition off by at most one unit of 2^-23 of the running magnitude.  int8 pools at
-    up to 8 rows hold a code c as 1152 + c, whose sum with q is taken out again."""
-    d = q.shape[-1]
-    mag = np.abs(q) @ np.abs(k).T
-    if kind == "int8":
-        # |code x scale| <= 127 x scale, held as up to 1279 x scale
-        mag = mag + 1280.0 * np.abs(q).sum(-1, keepdims=True) * raw_codes[None, :]
-    return (d + 4) * 2.0 ** -23 * mag.max() * scale
+    f32, each addition off by at most one unit of 2^-23 of the sum of magnitudes (codes widen
+    exactly, and a key's scale is one more product)."""
+    return (q.shape[-1] + 4) * 2.0 ** -23 * (np.abs(q) @ np.abs(k).T).max() * scale
 
 
-def weight_error(kind):
-    """Relative error of a weight as P.V takes it: two bf16 parts (each off by half a step of
-    2^-8) or two fp16 parts (2^-11 each, and fp16's subnormals below 2^-14)."""
-    return {"bf16": 2.0 ** -16, "f32": 0.0, "e4m3": 2.0 ** -21, "int8": 2.0 ** -21}[kind]
-
-
-def out_tolerance(kind, q, k, v_mag, scale, n, raw_scales=None):
-    """|out - exact| of each output: the weights' relative errors (their score's error twice:
-    in the weight and in the sum it is divided by; 2^-21 for the exponential; their own
-    rounding; n + 8 roundings of the sums) on sum_j p_j |v_j|."""
-    es = score_error(kind, q, k, scale, raw_scales)
-    rel = 2 * es + 2 * 2.0 ** -21 + weight_error(kind) + (n + 8) * 2.0 ** -23
-    return rel * v_mag + 1e-7
+def out_tolerance(kind, q, k, v_mag, scale, n, v_units):
+    """|out - exact| of each output.  Relative, on v_mag = sum_j p_j |v_j|: the score's error
+    twice (in the weight and in the sum it is divided by), 2^-21 twice for the exponentials, the
+    weight's parts (three of bf16: 2^-23; two of fp16: 2^-21; f32 none) and n + 8 roundings of the
+    sums.  Absolute: fp16 parts of a weight below 2^-14 of the largest are off by up to 2^-25,
+    times v_units = sum_j |v_j| (int8: of the codes, whose scales are in the weights)."""
+    parts = {"bf16": 2.0 ** -23, "f32": 0.0, "e4m3": 2.0 ** -21, "int8": 2.0 ** -21}[kind]
+    rel = 2 * score_error(q, k, scale) + 2 * 2.0 ** -21 + parts + (n + 8) * 2.0 ** -23
+    flat = 2.0 ** -25 * v_units if kind in ("e4m3", "int8") else 0.0
+    return rel * v_mag + flat + 1e-7
 
 
 def assert_within(got, want, tol, what):

@@ -46,6 +46,7 @@ def run_mass(pools, q, table, lens, mass, scale, window=0, err=None, p=None, **k
 def check_mass(out, mass, mass0, pools, q, table, lens, scale, window, what):
     k, v = pools.values("k").double().numpy(), pools.values("v").double().numpy()
     hkv, ps, d = pools.hkv, pools.ps, pools.d
+    units = pools.units("v").numpy()
     B, T, hq, _ = q.shape
     group = hq // hkv
     qn = q.double().numpy()
@@ -58,9 +59,7 @@ def check_mass(out, mass, mass0, pools, q, table, lens, scale, window, what):
         for g in range(hkv):
             kk = k[pg][:, :, g].reshape(-1, d)[:n]
             vv = v[pg][:, :, g].reshape(-1, d)[:n]
-            raw = None
-            if pools.kind == "int8":
-                raw = pools.scales["k"].numpy()[pg][:, g].reshape(-1)[:n].astype(np.float64)
+            flat = units[pg][:, :, g].reshape(-1, d)[:n].sum(0)
             add = np.zeros(n)
             seen = np.zeros(n, bool)
             es = 0.0
@@ -73,11 +72,11 @@ def check_mass(out, mass, mass0, pools, q, table, lens, scale, window, what):
                     sees &= key > pos - window
                 w, o, mag = ref.attend(qn[b, t, rows], kk, vv, scale,
                                        np.broadcast_to(sees, (group, n)))
-                tol = ref.out_tolerance(pools.kind, qn[b, t, rows], kk, mag, scale, n, raw)
+                tol = ref.out_tolerance(pools.kind, qn[b, t, rows], kk, mag, scale, n, flat)
                 ref.assert_within(out[b, t, rows], o, tol, f"{what} out b{b} t{t} g{g}")
                 add += w.sum(0)
                 seen |= sees
-                es = max(es, ref.score_error(pools.kind, qn[b, t, rows], kk, scale, raw))
+                es = max(es, ref.score_error(qn[b, t, rows], kk, scale))
             # a weight: its score's error and its sum's, 2^-21 of the exponentials, the sums'
             # roundings; then the additions to the mass
             rel = 2 * es + 2 * 2.0 ** -21 + (n + T * group + 8) * 2.0 ** -23

@@ -240,6 +240,7 @@ def run_pages(pools, q, pages, ln, scale, err=None, **kw):
 def check_pages(out, pools, q, pages, ln, scale, what):
     k, v = pools.values("k").double().numpy(), pools.values("v").double().numpy()
     hkv, ps, d = pools.hkv, pools.ps, pools.d
+    units = pools.units("v").numpy()
     group = q.shape[1] // hkv
     qn = q.double().numpy()
     for b in range(q.shape[0]):
@@ -249,14 +250,12 @@ def check_pages(out, pools, q, pages, ln, scale, what):
             pg = pages[b, g, :-(-n // ps)].long().numpy()
             kk = k[pg][:, :, g].reshape(-1, d)[:n]
             vv = v[pg][:, :, g].reshape(-1, d)[:n]
-            raw = None
-            if pools.kind == "int8":
-                raw = pools.scales["k"].numpy()[pg][:, g].reshape(-1)[:n].astype(np.float64)
             if n == 0:
                 assert torch.all(out[b, rows] == 0)
                 continue
             _, o, mag = ref.attend(qn[b, rows], kk, vv, scale, np.ones((group, n), bool))
-            tol = ref.out_tolerance(pools.kind, qn[b, rows], kk, mag, scale, n, raw)
+            tol = ref.out_tolerance(pools.kind, qn[b, rows], kk, mag, scale, n,
+                                    units[pg][:, :, g].reshape(-1, d)[:n].sum(0))
             ref.assert_within(out[b, rows], o, tol, f"{what} b{b} g{g}")
 
 
