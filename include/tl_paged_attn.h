@@ -119,7 +119,8 @@ tl_status tl_get_device_error(uint32_t* error_word, uint32_t* bits, int32_t clea
  * tl_decode_trace_reset zeroes the stamps (the combine's start to all ones)
  * after synchronising the device; tl_decode_trace_read synchronises the
  * device and copies the first n (1..TL_TRACE_SLOTS) stamps to host memory at
- * `stamps`.  Trace one call at a time: reset, call, read.  Both return
+ * `stamps`.  Trace one call at a time: reset, call, read; the decode calls of
+ * the section "Long contexts" are not recorded.  Both return
  * TL_ERR_UNSUPPORTED from a library built without the option (nothing else
  * is done), TL_ERR_INVALID_ARG for a NULL `stamps` or n out of range, and
  * TL_ERR_CUDA when the synchronisation or the copy fails.
@@ -672,7 +673,9 @@ tl_status tl_paged_attn_decode_multi_int8(const void* q, const int8_t* k_codes,
  * takes every page of the sequence.  A sequence with context_lens[b] <=
  * first_new[b] is skipped; one longer than its table sets
  * TL_DEVERR_CONTEXT_RANGE and is skipped.  A page that two sequences share is
- * written by both (the same values where both see the same live keys of it).
+ * written by both: the same values where both see the same live keys of it, as
+ * a full page of a shared prefix; where they do not, a mix of the two, a caller
+ * error.
  *   k_cache       [num_pages][page_size][h_kv][d] in `dtype` (TL_BF16, TL_F32
  *                 or TL_FP8_E4M3); tl_kv_page_bounds_int8: int8 codes and
  *                 scales as tl_kv_cache_write_int8 writes them
@@ -813,6 +816,8 @@ tl_status tl_paged_attn_decode_mass_int8(const void* q, const int8_t* k_codes,
  *   keep      [B][h_kv][n_keep] int32: the positions in ascending order, then -1
  *   new_lens  [B] int32: min(L, n_keep), 0 for L <= 0
  *   keep_first + keep_last <= n_keep
+ * Supported: mass_len and n_keep up to 2^30, B*h_kv < 2^28.  Otherwise
+ * TL_ERR_UNSUPPORTED.
  */
 tl_status tl_kv_evict_select(const float* mass, int32_t mass_len, const int32_t* context_lens,
                              int32_t n_keep, int32_t keep_first, int32_t keep_last,
@@ -829,7 +834,8 @@ tl_status tl_kv_evict_select(const float* mass, int32_t mass_len, const int32_t*
  * Rows at new_lens[b] and behind stay as they were; the block-table entries
  * past the new length are the caller's to free, and the caller's context
  * length becomes new_lens[b].  The heads of a position then hold different
- * tokens' rows: a window over positions no longer means a window over tokens.
+ * tokens' rows: a window over positions no longer means a window over tokens,
+ * and page bounds (tl_kv_page_bounds) of the sequence are to be made anew.
  * Needs j <= keep[b][g][j] < context_lens[b], as tl_kv_evict_select gives; an
  * entry outside that is skipped and sets TL_DEVERR_CONTEXT_RANGE.  A new_lens
  * entry outside [0, min(n_keep, context_lens[b])], or a length past the table
@@ -841,8 +847,8 @@ tl_status tl_kv_evict_select(const float* mass, int32_t mass_len, const int32_t*
  *   keep              [B][h_kv][n_keep] int32;  new_lens [B] int32
  *   mass              NULL, or [B][h_kv][mass_len] float32, in place
  * TL_ERR_INVALID_ARG when d * elem is not a multiple of 16 bytes;
- * TL_ERR_UNSUPPORTED past 4,096 bytes a row, page_size > 256 or
- * num_pages*page_size >= 2^31.
+ * TL_ERR_UNSUPPORTED past 4,096 bytes a row, page_size > 256,
+ * num_pages*page_size >= 2^31 or n_keep > 2^30.
  */
 tl_status tl_kv_cache_compact(void* k_cache, void* v_cache, const int32_t* block_table,
                               int32_t max_pages_per_seq, const int32_t* context_lens,

@@ -79,9 +79,9 @@ TL_DEVINLINE CompactPlace compact_place(const CompactParams& P, const int32_t* t
 }
 
 // The walk: rows_per_pass rows of a pass, this thread's being row r of it
-// (r < 0: none), U passes a batch.  slot(j): where position j's element is (-1: nowhere); at(slot): the
-// element.  Entries outside [j, L) and positions without a page are reported
-// by `reports` threads and skipped.
+// (r < 0: none), U passes a batch.  slot(j): where position j's element is
+// (-1: nowhere); at(slot): the element.  Entries outside [j, L) and positions
+// without a page are reported by `reports` threads and skipped.
 template <int U, class Vec, class Index, class Slot, class At>
 TL_DEVINLINE void compact_walk(const int32_t* keep, int new_len, int L, int rows_per_pass, int r,
                                bool reports, uint32_t* error_word, Slot slot, At at) {
@@ -200,7 +200,8 @@ static tl_status compact_impl(void* k, void* v, float* k_scales, float* v_scales
   const int64_t row_bytes = (int64_t)d * elem;
   if (row_bytes % 16 != 0) return TL_ERR_INVALID_ARG;
   if (row_bytes > 4096 || page_size > 256 ||
-      (int64_t)num_pages * page_size >= ((int64_t)1 << 31) || (int64_t)B * h_kv > INT32_MAX)
+      (int64_t)num_pages * page_size >= ((int64_t)1 << 31) || (int64_t)B * h_kv > INT32_MAX ||
+      n_keep > (1 << 30))
     return TL_ERR_UNSUPPORTED;
   CompactParams P;
   P.pool[0] = k;

@@ -832,10 +832,13 @@ static bool launch_scores(const ScoreParams& P, cudaStream_t st) {
   if (launch_status() != TL_OK) return false;
   auto kernel = P.group <= 8 ? page_score_kernel<D, 1> : page_score_kernel<D, 2>;
   const int hs = score_heads(P.h_kv);
-  // two CTAs share an SM's 228 KiB: at most 3 x 33.5 KiB of stages each, 5 KiB
-  // of static state and the system's 1 KiB
+  // two CTAs share an SM's 228 KiB: at most (one head) 3 x 34 KiB of stages
+  // each, 5 KiB of static state and the system's 1 KiB.  The limit is the same
+  // whatever the heads: threads that launch different ones at once set it
   const int smem = kScoreStages * score_stage_bytes(hs, D);
-  if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem) != cudaSuccess)
+  const int most = kScoreStages * score_stage_bytes(1, D);
+  if (smem > most ||
+      cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, most) != cudaSuccess)
     return false;
   cudaLaunchAttribute attr[1];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
@@ -869,7 +872,9 @@ cudaError_t launch_rows(const void* const (&kernels)[4], int64_t rows, const Sel
                         void** args, bool dependent, cudaStream_t st) {
   const void* kernel = kernels[!s.fits ? 3 : s.threads == 256 ? 0 : s.threads == 512 ? 1 : 2];
   const int smem = s.keys * (int)sizeof(uint32_t);
-  cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+  // the same limit for every shape: threads that launch different ones at once set it
+  cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                       kSelKeysMax * (int)sizeof(uint32_t));
   if (e != cudaSuccess) return e;
   cudaLaunchAttribute attr[2];
   int n = 0;

@@ -693,11 +693,11 @@ static __global__ void __launch_bounds__(1024) decode_plan_kernel(DecodeParams P
 // Sequences up to which an EX call has no plan launch: its CTAs plan for
 // themselves (one sequence a lane of one warp) and take a fixed share of the
 // items, which saves a launch and its 4-5 us but not the counter's evenness.
-// Measured with and without it (us a call, Llama-3-8B heads): 128 selected
-// pages of 1, 4, 8, 16, 32 sequences 16.4 / 19.0, 17.4 / 20.0, 19.3 / 21.0,
-// 30.5 / 32.3, 51.1 / 52.3; weight-gathering over whole bf16 contexts of up to
-// 8,192 keys 20.1 / 22.8, 27.9 / 29.5, 40.3 / 41.9, 67.4 / 68.6 and, at 32,
-// 127.4 / 121.6 (e4m3: 53.1 / 54.9 at 16, 89.5 / 83.1 at 32).
+// Measured with / without it (us a call, 32 query and 8 KV heads of 128): 128
+// selected pages of 1, 4, 8, 16, 32 sequences 17.2 / 19.5, 18.5 / 21.0, 19.8 /
+// 22.0, 31.6 / 33.1, 52.6 / 53.9; weight-gathering over whole bf16 contexts of
+// up to 8,192 keys 21.3 / 23.6, 29.1 / 31.1, 40.9 / 42.7, 68.1 / 69.1 and, at
+// 32, 128.9 / 122.9 (e4m3: 53.4 / 54.2 at 16, 89.5 / 83.1 at 32).
 constexpr int kSelfPlanMax = 16;
 
 struct ItemInfo {
@@ -2343,17 +2343,27 @@ struct NewRows {
   void* v_dst = nullptr;
 };
 
-// Warps per CTA of a bf16 / one-byte kernel variant: its shape's count, or
-// as many as the dynamic shared memory holds (227 KiB less 2 KiB for the
-// static state, the int8 scale rings and the 1 KiB alignment pad).
+// Dynamic shared memory a bf16 / one-byte kernel variant may take: 227 KiB
+// less 2 KiB for the static state, the int8 scale rings and (EX) 1 KiB for the
+// pieces it plans itself.  A kernel is given all of it, whatever a call's own
+// part: threads that launch different sizes at once set the same attribute.
 template <int D, bool TWO, bool K8, bool I8, bool EX>
-static int decode_warps(int rows) {
+static constexpr int decode_smem_max() {
   using S = DecodeShape<TWO, K8>;
   using L = WarpSmem<D, K8, I8, S::kRing>;
   static_assert(sizeof(WarpShared<S::kWarps, S::kRing>) <= 2048, "static state over 2 KiB");
   const int scales = I8 ? S::kWarps * S::kRing * L::kScaleBytes : 0;
-  // (EX: and 1 KiB for the pieces it plans itself)
-  return std::min(S::kWarps, (227 * 1024 - 3072 - (EX ? 1024 : 0) - scales) / L::warp_bytes(rows));
+  return 227 * 1024 - 2048 - (EX ? 1024 : 0) - scales;
+}
+
+// Warps per CTA: the shape's count, or as many as that memory holds besides
+// the 1 KiB alignment pad.
+template <int D, bool TWO, bool K8, bool I8, bool EX>
+static int decode_warps(int rows) {
+  using S = DecodeShape<TWO, K8>;
+  using L = WarpSmem<D, K8, I8, S::kRing>;
+  return std::min(S::kWarps,
+                  (decode_smem_max<D, TWO, K8, I8, EX>() - 1024) / L::warp_bytes(rows));
 }
 
 // ------------------------------------------------------------------ mass --
@@ -2623,8 +2633,8 @@ static tl_status decode_impl(const void* q, const void* k_cache, const void* v_c
       if (P.self_plan) kern = decode_bf16_kernel<DD, TWO, K8, I8V, 2>;                    \
     const int sm =                                                                        \
         warps * WarpSmem<DD, K8, I8V, DecodeShape<TWO, K8>::kRing>::warp_bytes(rows) + 1024; \
-    if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, sm) !=    \
-        cudaSuccess)                                                                      \
+    if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize,           \
+                             decode_smem_max<DD, TWO, K8, I8V, EX>()) != cudaSuccess)     \
       return TL_ERR_CUDA;                                                                 \
     cudaLaunchAttribute attr[1];                                                          \
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;                      \

@@ -535,3 +535,54 @@ def test_keeping_as_much_as_there_is_moves_nothing():
     assert new.cpu().tolist() == lens
     p, m = run_compact(pools, table, lens, keep.cpu(), new.cpu().tolist(), mass)
     assert same(p["k"], pools.data["k"]) and torch.equal(m.cpu(), mass)
+
+
+def test_threads_calling_with_different_sizes_at_once():
+    """Each host thread's calls ask for another amount of shared memory (rows of 100 and 30,000
+    values; 1 and 4 query heads a KV head), on a stream of its own."""
+    import threading
+
+    def make(n, hkv, group, seed):
+        lens = [n, n // 2]
+        table, P = ref.tables(lens, 16, seed=seed)
+        p = ref.Pools("bf16", P, 16, hkv, 64, seed=seed).gpu()
+        q = torch.randn((2, 1, hkv * group, 64), generator=torch.Generator().manual_seed(seed))
+        return dict(p=p, q=q.bfloat16().cuda(), table=table.cuda(), lens=i32(lens),
+                    mass=weights((2, hkv, n), seed).cuda(), n=n)
+
+    def calls(c, stream):
+        bounds = torch.empty((c["p"]["k"].shape[0], c["p"]["k"].shape[2], 2, 64),
+                             dtype=torch.int8, device="cuda")
+        scales = torch.empty(bounds.shape[:2], device="cuda")
+        mass = c["mass"].clone()
+        tl.tl_kv_page_bounds(c["p"]["k"], c["table"], c["lens"], bounds, scales, stream=stream)
+        pages, lens = tl.tl_kv_page_select(c["q"][:, 0], bounds, scales, c["table"], c["lens"],
+                                           16, 4, stream=stream)
+        out = tl.tl_paged_attn_decode_mass(c["q"], c["p"]["k"], c["p"]["v"], c["table"],
+                                           c["lens"], mass, 0.1, stream=stream)
+        keep, new = tl.tl_kv_evict_select(mass, c["lens"], c["n"] // 3, stream=stream)
+        return [pages, lens, out, mass, keep, new]
+
+    cases = [make(100, 8, 1, 1), make(30000, 1, 4, 2)]
+    want = [calls(c, None) for c in cases]
+    torch.cuda.synchronize()
+    wrong = []
+
+    def work(i):
+        try:
+            stream = torch.cuda.Stream()
+            with torch.cuda.stream(stream):
+                for _ in range(40):
+                    got = calls(cases[i], stream)
+                    stream.synchronize()
+                    if not all(torch.equal(a, b) for a, b in zip(got, want[i])):
+                        wrong.append(f"case {i} differs")
+        except Exception as e:  # reported by the main thread
+            wrong.append(repr(e))
+
+    threads = [threading.Thread(target=work, args=(i,)) for i in (0, 1, 0, 1)]
+    for th in threads:
+        th.start()
+    for th in threads:
+        th.join()
+    assert not wrong, wrong[:3]

@@ -155,6 +155,14 @@ def test_compact_refusals(lib):
     assert i(ks=None) == BAD and i(vs=None) == BAD and i(ks=12290) == BAD
 
 
+def test_compact_refuses_lists_past_its_counters(lib):
+    ok = dict(k=256, v=512, bt=1024, maxp=8, cl=1280, keep=1536, n=(1 << 30) + 1, new=1792, m=None,
+              ml=0, B=1, hkv=1, d=128, P=16, ps=16, dt=tl.TL_BF16, err=None, st=None)
+    c = caller(lib.tl_kv_cache_compact,
+               "k v bt maxp cl keep n new m ml B hkv d P ps dt err st", ok)
+    assert c() == UNS and c(n=0) == BAD
+
+
 def test_the_binding_refuses_cpu_tensors_and_wrong_shapes():
     x = torch.zeros(4, 16, 2, 128, dtype=torch.bfloat16)
     t, n = torch.zeros(1, 4, dtype=torch.int32), torch.zeros(1, dtype=torch.int32)
