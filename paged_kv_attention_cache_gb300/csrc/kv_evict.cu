@@ -24,7 +24,7 @@ template <int T, bool FITS>
 __global__ void __launch_bounds__(T) evict_select_kernel(EvictParams P, int csize, int key_cap) {
   __shared__ SelectShared<T> sh;
   extern __shared__ __align__(16) uint32_t sel_keys[];
-  const int row = blockIdx.x / csize, rank = blockIdx.x % csize;
+  const int row = (int)blockIdx.x >> (31 - __clz(csize)), rank = (int)blockIdx.x & (csize - 1);
   const int b = row / P.h_kv;
   const int L = P.context_lens[b];
   const int len = L <= 0 || L > P.mass_len ? 0 : L;

@@ -746,7 +746,7 @@ __global__ void __launch_bounds__(T) page_select_kernel(PageSelectParams P, int 
   __shared__ SelectShared<T> sh;
   extern __shared__ __align__(16) uint32_t sel_keys[];
   asm volatile("griddepcontrol.wait;\n" ::: "memory");
-  const int row = blockIdx.x / csize, rank = blockIdx.x % csize;
+  const int row = (int)blockIdx.x >> (31 - __clz(csize)), rank = (int)blockIdx.x & (csize - 1);
   const int b = row / P.h_kv;
   const int L = P.context_lens[b];
   const int nb = blocks_of(L, P.max_pages_per_seq, P.page_size);

@@ -63,7 +63,7 @@ template <int T>
 struct SelectShared {
   static constexpr int kBinBits = select_bin_bits(T), kBins = 1 << kBinBits;
   static_assert(kBins == 4 * T, "a thread takes four bins");
-  __align__(16) uint32_t hist[kBins];
+  __align__(16) uint32_t hist[kBins + 32];  // the last 32: values outside a pass's range
   uint32_t minmax[2];     // this CTA's smallest and largest key
   uint32_t total;         // this CTA's taken values
   uint32_t tmp[2][32];    // block scans, alternating
@@ -96,8 +96,8 @@ TL_DEVINLINE uint32_t select_block_scan(uint32_t x, uint32_t* tmp, uint32_t& tot
   return __shfl_sync(0xffffffffu, all - mine, wid) + inc - x;
 }
 
-// One row x[0 .. len), by the CTAs of one cluster (rank `rank` of `csize`;
-// csize 1 needs no cluster launch), T threads each.  keys: key_cap words of
+// One row x[0 .. len), by the CTAs of one cluster (rank `rank` of `csize`, a
+// power of two; csize 1 needs no cluster launch), T threads each.  keys: key_cap words of
 // 16-byte aligned shared memory, a multiple of 128 (FITS: no slice is longer).  emit(pos, i): index i is
 // taken at place pos; tail(pos): place pos stays empty.  Returns the places
 // that this CTA filled, first and one past the last ({0, 0} where len <= n:
@@ -126,7 +126,7 @@ __device__ int2 select_row(SelectShared<T>& sh, uint32_t* keys, int key_cap, con
   }
   // this CTA's slice of the row, and this warp's run of it: whole steps of 128
   // values, four neighbours a lane
-  const int slice = ((len + csize - 1) / csize + 127) / 128 * 128;
+  const int slice = (((len + csize - 1) >> (31 - __clz(csize))) + 127) / 128 * 128;
   const int i0 = min(rank * slice, len), i1 = min(i0 + slice, len);
   const int run = ((i1 - i0 + NW - 1) / NW + 127) / 128 * 128;
   const int w0 = i0 + min(wid * run, i1 - i0), w1 = min(w0 + run, i1);
@@ -151,6 +151,9 @@ __device__ int2 select_row(SelectShared<T>& sh, uint32_t* keys, int key_cap, con
   auto keys_at = [&](int i) {
     return FITS || i - i0 < key_cap ? *reinterpret_cast<const uint4*>(keys + (i - i0))
                             : keys_of(load4(i), i);
+  };
+  auto key_at = [&](int i) {
+    return FITS || i - i0 < key_cap ? keys[i - i0] : key_of(__ldcg(x + i), i);
   };
 
   auto clear_hist = [&]() {
@@ -266,19 +269,15 @@ __device__ int2 select_row(SelectShared<T>& sh, uint32_t* keys, int key_cap, con
         // a lane keeps the last two it meets and lists them behind the sweep
         // (listing each as it is met stalls the warp every other step); one
         // that meets more walks its values again
-        uint32_t met = 0u, k0 = 0u, k1 = 0u;
+        uint32_t met = 0u;
         int x0 = 0, x1 = 0;
-        auto look1 = [&](uint32_t k, int i) {
+        each([&](int i, uint32_t k) {
           count += k > hi ? 1u : 0u;
-          if (k - lo <= span) {
-            k1 = k0;
-            x1 = x0;
-            k0 = k;
-            x0 = i;
-            ++met;
-          }
-        };
-        each([&](int i, uint32_t k) { look1(k, i); });
+          const bool in = k - lo <= span;
+          x1 = in ? x0 : x1;
+          x0 = in ? i : x0;
+          met += in ? 1u : 0u;
+        });
         auto list = [&](uint32_t k, int i) {
           const uint32_t at = atomicAdd(n_cand, 1u);
           if (at < (uint32_t)kSelRank) {
@@ -286,8 +285,8 @@ __device__ int2 select_row(SelectShared<T>& sh, uint32_t* keys, int key_cap, con
             cand[kSelRank + at] = (uint32_t)i;
           }
         };
-        if (met == 1u || met == 2u) list(k0, x0);
-        if (met == 2u) list(k1, x1);
+        if (met == 1u || met == 2u) list(key_at(x0), x0);
+        if (met == 2u) list(key_at(x1), x1);
         if (met > 2u)
           for (int i = w0 + 4 * lane; i < w1; i += 128) {
             const uint4 k = keys_at(i);
@@ -348,8 +347,11 @@ __device__ int2 select_row(SelectShared<T>& sh, uint32_t* keys, int key_cap, con
     }
     uint32_t* hist = sh.hist;
     if (!by_index) {
+      // a value outside the range counts in a spare bin of its lane: fewer
+      // instructions than a branch around the count
+      const uint32_t spare = (uint32_t)(kSelBins + lane);
       each([&](int, uint32_t k) {
-        if (k - lo <= span) atomicAdd(hist + ((k - lo) >> shift), 1u);
+        atomicAdd(hist + (k - lo <= span ? (k - lo) >> shift : spare), 1u);
       });
     } else {
       each([&](int i, uint32_t k) {
