@@ -153,7 +153,7 @@ __device__ int2 select_row(SelectShared<T>& sh, uint32_t* keys, int key_cap, con
                             : keys_of(load4(i), i);
   };
   auto key_at = [&](int i) {
-    return FITS || i - i0 < key_cap ? keys[i - i0] : key_of(__ldcg(x + i), i);
+    return FITS || i - i0 < key_cap ? keys[i - i0] : i < len ? key_of(__ldcg(x + i), i) : 0u;
   };
 
   auto clear_hist = [&]() {
@@ -438,35 +438,26 @@ __device__ int2 select_row(SelectShared<T>& sh, uint32_t* keys, int key_cap, con
   const uint32_t below = (1u << lane) - 1u;
   const int end = at + (int)count;
   for (int w = w0; w < w1 && at < end; w += 128) {
-    const int i = w + 4 * lane;
-    const uint4 k = keys_at(i);
-    bool t0, t1, t2, t3;
+    // a lane's values 32 apart: a ballot orders them, and the warp's stores
+    // run together
+    const int i = w + lane;
+    uint32_t k[4], m[4];
+#pragma unroll
+    for (int j = 0; j < 4; ++j) k[j] = key_at(i + 32 * j);
     if (w <= last_idx && last_idx < w + 128) {  // the step of the last one taken
-      t0 = taken(k.x, i);
-      t1 = taken(k.y, i + 1);
-      t2 = taken(k.z, i + 2);
-      t3 = taken(k.w, i + 3);
+#pragma unroll
+      for (int j = 0; j < 4; ++j) m[j] = __ballot_sync(0xffffffffu, taken(k[j], i + 32 * j));
     } else {  // equal values are all taken before it, and none behind it
       const uint32_t over = w > last_idx ? last_key : last_key - 1u;  // last_key >= 1
-      t0 = k.x > over;
-      t1 = k.y > over;
-      t2 = k.z > over;
-      t3 = k.w > over;
+#pragma unroll
+      for (int j = 0; j < 4; ++j) m[j] = __ballot_sync(0xffffffffu, k[j] > over);
     }
-    // the lanes' counts (0 to 4) added up bit by bit
-    const uint32_t c = (t0 ? 1u : 0u) + (t1 ? 1u : 0u) + (t2 ? 1u : 0u) + (t3 ? 1u : 0u);
-    const uint32_t s0 = __ballot_sync(0xffffffffu, c & 1u);
-    const uint32_t s1 = __ballot_sync(0xffffffffu, c & 2u);
-    const uint32_t s2 = __ballot_sync(0xffffffffu, c & 4u);
-    if ((s0 | s1 | s2) == 0u) continue;
-    if (c != 0u) {
-      int pos = at + __popc(s0 & below) + 2 * __popc(s1 & below) + 4 * __popc(s2 & below);
-      if (t0) emit(pos++, i);
-      if (t1) emit(pos++, i + 1);
-      if (t2) emit(pos++, i + 2);
-      if (t3) emit(pos, i + 3);
+    if ((m[0] | m[1] | m[2] | m[3]) == 0u) continue;
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      if (m[j] >> lane & 1u) emit(at + __popc(m[j] & below), i + 32 * j);
+      at += __popc(m[j]);
     }
-    at += __popc(s0) + 2 * __popc(s1) + 4 * __popc(s2);
   }
   if (csize > 1)  // the CTA stays until its peers have read its totals
     asm volatile("barrier.cluster.wait.acquire.aligned;\n" ::: "memory");
