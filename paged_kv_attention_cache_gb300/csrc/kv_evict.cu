@@ -53,6 +53,12 @@ __global__ void __launch_bounds__(T) evict_select_kernel(EvictParams P, int csiz
 // batches ahead and its rows one batch ahead, before the barrier that the
 // stores of the batch before them follow.  Rows that stay (keep[j] = j) are
 // neither read nor written.  Bound: HBM, 2 x (K and V row) per moved row.
+// Measured (bf16, 8 KV heads of 128): 64 sequences of 512-8,192 keys cut to
+// 2,048 in 151 us (871 MB at 5.8 TB/s), one of 32,768 cut to 8,192 in 23 us (69
+// MB, 3.0 TB/s: its CTAs wait for a batch's loads, 8 batches in a row, and a
+// row's 32-byte pieces fill the L1's tag rate by half).  Copies through a ring
+// in shared memory, two and more batches ahead of the stores, were slower
+// (165-190 and 25-27 us).
 struct CompactParams {
   void* pool[2];    // k, v: [num_pages][page_size][h_kv][row_bytes]
   float* scale[2];  // int8 pools: [num_pages][h_kv][page_size]

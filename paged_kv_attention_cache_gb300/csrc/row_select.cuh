@@ -27,12 +27,16 @@
 // barriers, bound by instructions and by the barriers' latency, not by the
 // values' bytes.  Slices past the shared memory read their values again.
 //
-// Measured on GB300: one row of 8,192 scores 8 us; 512 rows of 1,024-32,768
-// masses (35 MB) 43 us, 8 rows of 131,072 (clusters of 4) 22 us.  Tried and no
-// faster: halves of the keys in 16 bits (three rows an SM; 39 us and 24 us,
-// but 8-20% more for short rows), 16,384 keys a CTA and clusters of 2 (63 us:
-// a cluster's barriers and remote reads cost 2-5 thousand cycles each),
-// ballots into a bit mask for the places (50 us).
+// Measured on GB300: 512 rows of 1,024-32,768 masses (35 MB) 39 us, 8 rows of
+// 131,072 (clusters of 4) 21 us.  Of the 39, loading and the extremes take 13,
+// the histogram 8, the sweep for the bin's values 7, ranking them 3, placing 8;
+// the schedulers issue 60% of the time: a warp has 4 steps of 128 values a
+// sweep, and as many instructions around them.  Tried and no faster: halves of
+// the keys in 16 bits (three rows an SM; 8-20% more for short rows), 512
+// threads a row (46 us), 16,384 keys a CTA and clusters of 2 (a cluster's
+// barriers and remote reads cost 2-5 thousand cycles each), the longest rows
+// first (39.1 for 43 us then, before its own cost), ballots into a bit mask
+// for the places, unrolling the sweeps less, twice the loads in flight (1%).
 #pragma once
 
 #include <cooperative_groups.h>
