@@ -586,3 +586,40 @@ def test_threads_calling_with_different_sizes_at_once():
     for th in threads:
         th.join()
     assert not wrong, wrong[:3]
+
+
+@pytest.mark.parametrize("kind", ["bf16", "f32", "int8"])
+@pytest.mark.parametrize("B", [1, 16, 17, 130])
+def test_a_batch_with_nothing_to_read(kind, B):
+    """Every place of the batch is padding (length 0): zeros, empty lists, and all else as it was."""
+    pools = ref.Pools(kind, 4, 16, 2, 128, seed=2)
+    p = pools.gpu()
+    q = torch.randn((B, 4, 128), generator=torch.Generator().manual_seed(3))
+    q = (q if kind == "f32" else q.bfloat16()).cuda()
+    table, lens = torch.full((B, 3), -1, dtype=torch.int32, device="cuda"), i32([0] * B)
+    mass = torch.rand((B, 2, 48), generator=torch.Generator().manual_seed(4)).cuda()
+    before, w, int8 = mass.clone(), word(), kind == "int8"
+    scales = (p["ks"], p["vs"]) if int8 else ()
+    bounds = torch.full((4, 2, 2, 128), 5, dtype=torch.int8, device="cuda")
+    bscales = torch.full((4, 2), 0.5, device="cuda")
+    if int8:
+        tl.tl_kv_page_bounds_int8(p["k"], p["ks"], table, lens, bounds, bscales, error_word=w)
+    else:
+        tl.tl_kv_page_bounds(p["k"], table, lens, bounds, bscales, error_word=w)
+    assert torch.all(bounds == 5) and torch.all(bscales == 0.5)
+    pages, page_lens = tl.tl_kv_page_select(q, bounds, bscales, table, lens, 16, 2, error_word=w)
+    assert torch.all(pages == -1) and torch.all(page_lens == 0)
+    attend = tl.tl_paged_attn_decode_pages_int8 if int8 else tl.tl_paged_attn_decode_pages
+    out = torch.full((B, 4, 128), 7.0, device="cuda")
+    attend(q, p["k"], p["v"], *scales, pages, page_lens, 0.1, out=out, error_word=w)
+    assert torch.all(out == 0)
+    gather = tl.tl_paged_attn_decode_mass_int8 if int8 else tl.tl_paged_attn_decode_mass
+    out = torch.full((B, 1, 4, 128), 7.0, device="cuda")
+    gather(q[:, None], p["k"], p["v"], *scales, table, lens, mass, 0.1, out=out, error_word=w)
+    assert torch.all(out == 0) and torch.equal(mass, before)
+    keep, new = tl.tl_kv_evict_select(mass, lens, 8, error_word=w)
+    assert torch.all(keep == -1) and torch.all(new == 0)
+    compact = tl.tl_kv_cache_compact_int8 if int8 else tl.tl_kv_cache_compact
+    compact(p["k"], p["v"], *scales, table, lens, keep, new, mass=mass, error_word=w)
+    assert torch.equal(mass, before) and int(w.item()) == 0
+    assert all(same(p[n], pools.data[n]) for n in pools.data)
