@@ -2380,9 +2380,10 @@ static int decode_warps(int rows) {
 // Bound: L2 (the scores, 4 bytes a row and key) and the masses' 8 bytes a key
 // and head.  Measured: 14 of a call's 123 us for 64 e4m3 contexts of 512-8,192
 // keys, 32 query and 8 KV heads (37 MB of scores, 19 of masses); a bf16 context
-// of 32,768 takes 35.5 us in all (136 MB).  Folded into the merge's launch (its
-// last CTA of a sequence adding up) a call took 39.5 and 124.7 us, 36.7 and 121
-// with a launch of its own.
+// of 32,768 takes 35.5 us in all (136 MB).  One launch for the merge and this
+// (blocks of either kind, these folding the pieces' statistics themselves)
+// took 39.5 and 124.7 us a call where two launches took 36.7 and 121: every
+// block then holds the merge's registers.
 static __global__ void __launch_bounds__(256) decode_mass_kernel(DecodeParams P, float* mass,
                                                                  int64_t mass_len) {
   constexpr int U = 4, R = 4;  // keys per lane and rows per round of loads
