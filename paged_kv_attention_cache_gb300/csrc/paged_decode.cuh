@@ -1289,6 +1289,29 @@ __global__ void __launch_bounds__(DecodeShape<TWO_ROWS, KV8>::kWarps * 32, 1)
     const int pr1 = it.p - (P.q_len - 1 - rb / P.group);
     const int lr0 = (P.window > 0 && pr0 - P.window + 1 > 0) ? pr0 - P.window + 1 : 0;
     const int lr1 = (P.window > 0 && pr1 - P.window + 1 > 0) ? pr1 - P.window + 1 : 0;
+    // EX, int8: what P' = p x V scale is multiplied by before it is split into
+    // fp16 parts, a power of two (0: no live key yet).  The largest scale so
+    // far lies in [32, 64) after it, so that neither part falls below fp16's
+    // normal range (outputs within 5 x 10^-7 of exact; 2-5 x 10^-6 without) and
+    // p, at most 2^kLazyLog2, does not pass its largest value, whatever the
+    // pool's scales; 2% of a call, 5% with 16 rows.
+    constexpr bool kFitV = I8 && EX != 0;
+    [[maybe_unused]] float vfit = 0.f, vlim = 0.f;
+    [[maybe_unused]] auto fit_v = [&](float big) {  // big: the largest scale of this lane's live keys
+      if (!__any_sync(0xffffffffu, big > vlim)) return;
+      const uint32_t most = __reduce_max_sync(0xffffffffu, __float_as_uint(big));
+      const int e = min(5 - ((int)(most >> 23) - 127), 126);  // at least -122
+      const float f = __uint_as_float((uint32_t)(e + 127) << 23);
+      if (vfit > 0.f) {
+        const float r = f / vfit;
+#pragma unroll
+        for (int n = 0; n < NO; ++n)
+#pragma unroll
+          for (int x = 0; x < 4; ++x) o[n][x] *= r;
+      }
+      vfit = f;
+      vlim = 64.f / f;
+    };
     // EX: the score rows of rows ra and rb (null: none, or not this lane's)
     float *srow0 = nullptr, *srow1 = nullptr;
     if constexpr (EX) {
@@ -1511,6 +1534,13 @@ __global__ void __launch_bounds__(DecodeShape<TWO_ROWS, KV8>::kWarps * 32, 1)
           // to [0, 3e38] (NaN to 0), it leaves their p = 0 at 0
           v0 = fminf(fmaxf(v0, 0.f), 3.0e38f);
           v1 = fminf(fmaxf(v1, 0.f), 3.0e38f);
+          if constexpr (kFitV) {
+            v0 = p[jc][0] + p[jc][1] > 0.f ? v0 : 0.f;
+            v1 = p[jc][2] + p[jc][3] > 0.f ? v1 : 0.f;
+            fit_v(fmaxf(v0, v1));
+            v0 *= vfit;
+            v1 *= vfit;
+          }
           p[jc][0] *= v0;
           p[jc][1] *= v0;
           p[jc][2] *= v1;
@@ -1798,13 +1828,32 @@ __global__ void __launch_bounds__(DecodeShape<TWO_ROWS, KV8>::kWarps * 32, 1)
           if constexpr (I8) {
             // int8 pools: each probability times its key's V scale (a key
             // outside the live set has p = 0 and keeps it, whatever its scale)
+            float v[2][2];
   #pragma unroll
-            for (int n = 0; n < 2; ++n) {
-              float v0, v1;
+            for (int n = 0; n < 2; ++n)
               asm volatile("ld.shared.v2.f32 {%0, %1}, [%2];\n"
-                           : "=f"(v0), "=f"(v1)
+                           : "=f"(v[n][0]), "=f"(v[n][1])
                            : "r"(scale_ring + stage * L::kScaleBytes +
                                  ((CPS + sub0 + jc) * kChunk + n * 8 + qc) * 4));
+            if constexpr (kFitV) {
+              float big = 0.f;
+  #pragma unroll
+              for (int n = 0; n < 2; ++n)
+  #pragma unroll
+                for (int e = 0; e < 2; ++e) {
+                  v[n][e] = fminf(fmaxf(v[n][e], 0.f), 3.0e38f);
+                  const float any = TWO_ROWS ? p[jc][n][e] + p[jc][n][2 + e] : p[jc][n][e];
+                  if (any > 0.f) big = fmaxf(big, v[n][e]);
+                }
+              fit_v(big);
+  #pragma unroll
+              for (int n = 0; n < 2; ++n)
+  #pragma unroll
+                for (int e = 0; e < 2; ++e) v[n][e] *= vfit;
+            }
+  #pragma unroll
+            for (int n = 0; n < 2; ++n) {
+              const float v0 = v[n][0], v1 = v[n][1];
               p[jc][n][0] = p[jc][n][0] > 0.f ? p[jc][n][0] * v0 : 0.f;
               p[jc][n][1] = p[jc][n][1] > 0.f ? p[jc][n][1] * v1 : 0.f;
               if (TWO_ROWS) {
@@ -1930,6 +1979,8 @@ __global__ void __launch_bounds__(DecodeShape<TWO_ROWS, KV8>::kWarps * 32, 1)
     }
     if (stop) break;
     // ------------------------------------------------------ finish the item
+    float unfit = 1.f;
+    if constexpr (kFitV) unfit = vfit > 0.f ? 1.f / vfit : 1.f;
     if constexpr (KT) {
       // a column's sum spans the 8 lanes of one t; with dup, the low parts
       // (columns 4-7, lanes t = 2, 3) join their rows (lanes t - 2)
@@ -1962,8 +2013,8 @@ __global__ void __launch_bounds__(DecodeShape<TWO_ROWS, KV8>::kWarps * 32, 1)
       };
       if (it.nsplits == 1) {
         const float i0 = l0 > 0.f ? 1.f / l0 : 0.f, i1 = l1 > 0.f ? 1.f / l1 : 0.f;
-        if (live0) write_col(P.out + ((size_t)it.b * P.hq_all + h0r) * D, 0, i0, false, 0);
-        if (live1) write_col(P.out + ((size_t)it.b * P.hq_all + h1r) * D, 1, i1, false, 0);
+        if (live0) write_col(P.out + ((size_t)it.b * P.hq_all + h0r) * D, 0, i0 * unfit, false, 0);
+        if (live1) write_col(P.out + ((size_t)it.b * P.hq_all + h1r) * D, 1, i1 * unfit, false, 0);
         if constexpr (EX) {
           float2* st = reinterpret_cast<float2*>(P.stats) + (size_t)it.b * P.hq_all;
           if (P.stats && live0 && qr == 0) st[h0r] = make_float2(m0, l0);
@@ -1973,12 +2024,12 @@ __global__ void __launch_bounds__(DecodeShape<TWO_ROWS, KV8>::kWarps * 32, 1)
         const uint64_t keep = l2_evict_last();
         if (live0) {
           const size_t rowi = (size_t)it.s_global * P.hq_all + h0r;
-          write_col(P.ws.acc + rowi * D, 0, 1.f, true, keep);
+          write_col(P.ws.acc + rowi * D, 0, unfit, true, keep);
           if (qr == 0) st_f32x2_hint(P.ws.ml + rowi * 2, m0, l0, keep);
         }
         if (live1) {
           const size_t rowi = (size_t)it.s_global * P.hq_all + h1r;
-          write_col(P.ws.acc + rowi * D, 1, 1.f, true, keep);
+          write_col(P.ws.acc + rowi * D, 1, unfit, true, keep);
           if (qr == 0) st_f32x2_hint(P.ws.ml + rowi * 2, m1, l1, keep);
         }
       }
@@ -2029,9 +2080,10 @@ __global__ void __launch_bounds__(DecodeShape<TWO_ROWS, KV8>::kWarps * 32, 1)
       };
       if (single) {
         const float i0 = l0 > 0.f ? 1.f / l0 : 0.f, i1 = l1 > 0.f ? 1.f / l1 : 0.f;
-        if (qr < P.rows) write_row(P.out + ((size_t)it.b * P.hq_all + h0r) * D, false, i0, false, 0);
+        if (qr < P.rows)
+          write_row(P.out + ((size_t)it.b * P.hq_all + h0r) * D, false, i0 * unfit, false, 0);
         if (TWO_ROWS && qr + 8 < P.rows)
-          write_row(P.out + ((size_t)it.b * P.hq_all + h1r) * D, true, i1, false, 0);
+          write_row(P.out + ((size_t)it.b * P.hq_all + h1r) * D, true, i1 * unfit, false, 0);
         if constexpr (EX) {
           float2* st = reinterpret_cast<float2*>(P.stats) + (size_t)it.b * P.hq_all;
           if (P.stats && qr < P.rows && (lane & 3) == 0) st[h0r] = make_float2(m0, l0);
@@ -2043,12 +2095,12 @@ __global__ void __launch_bounds__(DecodeShape<TWO_ROWS, KV8>::kWarps * 32, 1)
         const uint64_t keep = l2_evict_last();
         if (qr < P.rows) {
           const size_t rowi = (size_t)it.s_global * P.hq_all + h0r;
-          write_row(P.ws.acc + rowi * D, false, 1.f, true, keep);
+          write_row(P.ws.acc + rowi * D, false, unfit, true, keep);
           if ((lane & 3) == 0) st_f32x2_hint(P.ws.ml + rowi * 2, m0, l0, keep);
         }
         if (TWO_ROWS && qr + 8 < P.rows) {
           const size_t rowi = (size_t)it.s_global * P.hq_all + h1r;
-          write_row(P.ws.acc + rowi * D, true, 1.f, true, keep);
+          write_row(P.ws.acc + rowi * D, true, unfit, true, keep);
           if ((lane & 3) == 0) st_f32x2_hint(P.ws.ml + rowi * 2, m1, l1, keep);
         }
       }

@@ -50,8 +50,12 @@ class Pools:
         return x
 
     def units(self, n):
-        """Magnitudes that 16-bit weights multiply: the values, or an int8 pool's codes."""
-        return (self.data[n].float() if self.kind == "int8" else self.values(n)).double().abs()
+        """Magnitudes that 16-bit weights multiply: the values; an int8 pool's codes, whose
+        weights carry their scales, the largest of them brought to at least 32."""
+        if self.kind != "int8":
+            return self.values(n).double().abs()
+        scales = self.scales[n]
+        return self.data[n].double().abs() * (scales[torch.isfinite(scales)].double().max() / 32)
 
     def gpu(self):
         out = {n: x.cuda() for n, x in self.data.items()}
@@ -180,7 +184,7 @@ def out_tolerance(kind, q, k, v_mag, scale, n, v_units):
     twice (in the weight and in the sum it is divided by), 2^-21 twice for the exponentials, the
     weight's parts (three of bf16: 2^-23; two of fp16: 2^-21; f32 none) and n + 8 roundings of the
     sums.  Absolute: fp16 parts of a weight below 2^-14 of the largest are off by up to 2^-25,
-    times v_units = sum_j |v_j| (int8: of the codes, whose scales are in the weights)."""
+    times v_units = sum_j |v_j| (see Pools.units)."""
     parts = {"bf16": 2.0 ** -23, "f32": 0.0, "e4m3": 2.0 ** -21, "int8": 2.0 ** -21}[kind]
     rel = 2 * score_error(q, k, scale) + 2 * 2.0 ** -21 + parts + (n + 8) * 2.0 ** -23
     flat = 2.0 ** -25 * v_units if kind in ("e4m3", "int8") else 0.0

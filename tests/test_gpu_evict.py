@@ -623,3 +623,32 @@ def test_a_batch_with_nothing_to_read(kind, B):
     compact(p["k"], p["v"], *scales, table, lens, keep, new, mass=mass, error_word=w)
     assert torch.equal(mass, before) and int(w.item()) == 0
     assert all(same(p[n], pools.data[n]) for n in pools.data)
+
+
+@pytest.mark.parametrize("group,T", [(4, 1), (4, 4), (16, 1)])
+def test_v_scales_of_any_size(group, T):
+    """Weights times V scales go through 16-bit parts: a power of two in every scale of a pool
+    multiplies the outputs and changes no bit, and scales 10^6 apart in one sequence, rising or
+    falling along it, keep the outputs within their tolerance."""
+    lens = [700, 40, 1500]
+    table, P = ref.tables(lens, 16, seed=1)
+    pools = ref.Pools("int8", P, 16, 2, 128, seed=2)
+    q = torch.randn((3, T, 2 * group, 128), generator=torch.Generator().manual_seed(3)).bfloat16()
+    mass0 = torch.zeros((3, 2, 1500))
+    base = pools.scales["v"]
+    outs = []
+    for f in (1.0, 2.0 ** -60, 2.0 ** 40):
+        pools.scales["v"] = base * f
+        mass = mass0.cuda()
+        outs.append(run_mass(pools, q, table, lens, mass, 0.09) / f)
+    assert torch.equal(outs[0], outs[1]) and torch.equal(outs[0], outs[2])
+    position = torch.zeros((P, 16))
+    for b, n in enumerate(lens):
+        blocks = -(-n // 16)
+        place = torch.arange(blocks * 16).view(blocks, 16) / max(lens)
+        position[table[b, :blocks].long()] = place
+    for sign in (1.0, -1.0):
+        pools.scales["v"] = base * torch.exp2(sign * 20 * (position - 0.5))[:, None, :]
+        mass = mass0.cuda()
+        out = run_mass(pools, q, table, lens, mass, 0.09)
+        check_mass(out, mass, mass0, pools, q, table, lens, 0.09, 0, f"scales {sign}")
