@@ -180,7 +180,7 @@ struct DecodeParams {
   // row does not see a key of the pieces' chunks).  stats: each output row's
   // running max (log2 units) and sum, [B][hq_all][2].
   // self_plan: no plan launch; every attention CTA derives the pieces itself
-  // (at most kSelfPlanMax sequences).
+  // (at most self_plan_max sequences).
   int32_t head_tables;
   int32_t self_plan, target_splits;
   float* scores;
@@ -258,6 +258,10 @@ constexpr int kTailPct = TL_DECODE_TAIL_PCT;          // share of a sequence in 
 __device__ __forceinline__ int tail_chunks(int n) {
   return n < 2 * kMinSplitChunks ? 0 : min(n, (kTailPct * n + 99) / 100);
 }
+// The same in a layout whose small pieces have `small` chunks (0: it has none).
+__device__ __forceinline__ int tail_chunks(int n, int small) {
+  return small > 0 ? tail_chunks(n) : 0;
+}
 
 // Sums of two values over the block (every thread gets them); red holds one
 // slot per warp for each.
@@ -327,6 +331,7 @@ __device__ __forceinline__ long long warp_sum64(long long x) {
 // before it (a binary search of rec).  Each piece also asks L2 for the
 // block-table entries its first chunk reads, so the attention kernel's
 // first table load of the item hits.
+template <bool EX = false>
 __device__ __forceinline__ void write_piece_descs(const DecodeParams& P, const int4* rec,
                                                   const int2* rng, int base, int nseq, int bulk0,
                                                   int nb, int small0, int ns, int NB, int split,
@@ -345,7 +350,8 @@ __device__ __forceinline__ void write_piece_descs(const DecodeParams& P, const i
     const int4 r = rec[j];
     const int lo_j = rng[j].x, p_j = rng[j].y, bj = base + j;
     const int n_j = p_j < 0 ? 0 : p_j / kChunk - lo_j / kChunk + 1;
-    const int c0 = lo_j / kChunk, c1 = c0 + n_j, cm = c1 - tail_chunks(n_j);
+    const int c0 = lo_j / kChunk, c1 = c0 + n_j;
+    const int cm = c1 - (EX ? tail_chunks(n_j, small) : tail_chunks(n_j));
     const int first = r.x + r.y, pieces = r.z + r.w;
     int cb, ce, slot, part;
     if (bulk) {
@@ -380,16 +386,35 @@ __device__ __forceinline__ void write_piece_descs(const DecodeParams& P, const i
 // same pieces as the block-wide path.  The loops stay rolled: the plan runs
 // once per call from a cold instruction cache, where straight-line code costs
 // more than the loop overhead.
+constexpr int kMaxChunks = 1 << 27;  // of a sequence: 2^31 keys
 constexpr int kWarpPlanMax = 128;
 constexpr int kWriteWarps = 8;  // writing warps per CTA of a warp-planned launch
+
+// Sequences up to which an EX call has no plan launch: its CTAs plan for
+// themselves and each warp takes one piece (two past 32 sequences), all of one
+// size.  It saves a launch and its 4-5 us and gives every warp work where there
+// is little; a long batch is dealt more evenly by the plan's counter and its
+// round of small pieces.  Measured without / with the plan's launch (us a call,
+// 32 query and 8 KV heads of 128): 128 selected pages of 1, 4, 16, 32, 64
+// sequences 11.6 / 19.5, 14.3 / 20.8, 29.7 / 33.2, 51.0 / 53.5, 95.0 / 93.7;
+// weight-gathering over whole bf16 contexts of 2,048-8,192 keys of 1, 8, 16,
+// 32, 64 sequences 17.3 / 23.6, 39.3 / 42.7, 66.3 / 69.3, 125 / 122, 254 / 234;
+// e4m3 contexts 18.1 / 24.1, 27.1 / 36.5, 40.5 / 54.2, 71.5 / 84.1 and, in two
+// rounds, 136 / 145.
+__host__ __device__ constexpr int self_plan_max(bool one_byte) { return one_byte ? 64 : 32; }
+constexpr int kOneRoundSeqs = 32;
+constexpr int kOneRoundMin = 2;  // chunks of a piece; 1 measured no faster
 
 // The piece layout from the sequences' ranges rng[b] = {lo, p}, by one warp:
 // rec[b] as write_piece_descs takes it, s_plan = {split, small, bulk pieces (-1:
 // refused), small pieces}; with `publish`, the workspace's offsets, count and
-// counter too.
+// counter too.  ONE_ROUND: every piece has the same size (small is 0), the
+// least that makes them no more than an item, or two, for each of `warps` (with
+// more sequences and heads than that, the layout above).
+template <bool ONE_ROUND = false>
 __device__ __forceinline__ void warp_plan(const DecodeParams& P, int target_splits,
                                           int first_dynamic, const int2* rng, int4* rec,
-                                          int* s_plan, bool publish, int lane) {
+                                          int* s_plan, bool publish, int lane, int warps = 0) {
   const int K = (P.B + 31) >> 5, b0 = min(lane * K, P.B), b1 = min(b0 + K, P.B);
   long long C = 0, T = 0;
 #pragma unroll 1
@@ -400,24 +425,54 @@ __device__ __forceinline__ void warp_plan(const DecodeParams& P, int target_spli
   }
   C = warp_sum64(C);
   T = warp_sum64(T);
-  const long long half = max(target_splits / 2, 1);
-  const int small = (int)max((long long)kSmallChunks, (T + P.B + half - 1) / half);
-  long long TP = 0;
+  int one = 0;  // that size, or 0
+  if (ONE_ROUND) {
+    const int rounds = P.B > kOneRoundSeqs ? 2 : 1;
+    const int cap = min(rounds * warps / P.h_kv, (int)decode_max_splits(P.B, P.h_kv));
+    if (cap >= P.B) {
+      // the least size with at most cap pieces: between what an even cut of all
+      // chunks gives and what leaves each sequence a piece for its remainder
+      const int spare = cap - P.B;
+      int lo = (int)max((long long)kOneRoundMin, (C + cap - 1) / cap), hi = kMaxChunks;
+      if (spare > 0) hi = (int)min((long long)hi, max((long long)lo, (C + spare - 1) / spare));
 #pragma unroll 1
-  for (int b = b0; b < b1; ++b) {
-    const int n = rng[b].y < 0 ? 0 : rng[b].y / kChunk - rng[b].x / kChunk + 1;
-    TP += (tail_chunks(n) + small - 1) / small;
+      while (lo < hi) {
+        const int mid = (lo + hi) >> 1;
+        int pieces = 0;
+#pragma unroll 1
+        for (int b = b0; b < b1; ++b) {
+          const int n = rng[b].y < 0 ? 0 : rng[b].y / kChunk - rng[b].x / kChunk + 1;
+          pieces += (n + mid - 1) / mid;
+        }
+        if (__reduce_add_sync(0xffffffffu, pieces) <= cap) hi = mid;
+        else lo = mid + 1;
+      }
+      one = lo;
+    }
   }
-  TP = warp_sum64(TP);
-  const long long budget = (long long)target_splits + P.B - TP;
-  const long long sb = (C - T + budget - 1) / budget;
-  const int split = (int)(sb < kMinSplitChunks ? kMinSplitChunks : sb);
+  const long long half = max(target_splits / 2, 1);
+  const int small = one ? 0 : (int)max((long long)kSmallChunks, (T + P.B + half - 1) / half);
+  auto tail_of = [&](int n) { return ONE_ROUND ? tail_chunks(n, small) : tail_chunks(n); };
+  auto small_pieces = [&](int tail) { return tail > 0 ? (tail + small - 1) / small : 0; };
+  int split = one;
+  if (!one) {
+    long long TP = 0;
+#pragma unroll 1
+    for (int b = b0; b < b1; ++b) {
+      const int n = rng[b].y < 0 ? 0 : rng[b].y / kChunk - rng[b].x / kChunk + 1;
+      TP += small_pieces(tail_of(n));
+    }
+    TP = warp_sum64(TP);
+    const long long budget = (long long)target_splits + P.B - TP;
+    const long long sb = (C - T + budget - 1) / budget;
+    split = (int)(sb < kMinSplitChunks ? kMinSplitChunks : sb);
+  }
   long long x = 0;  // this lane's (bulk << 32 | small) pieces
 #pragma unroll 1
   for (int b = b0; b < b1; ++b) {
     const int n = rng[b].y < 0 ? 0 : rng[b].y / kChunk - rng[b].x / kChunk + 1;
-    const int t = tail_chunks(n);
-    x += ((long long)((n - t + split - 1) / split) << 32) | ((t + small - 1) / small);
+    const int t = tail_of(n);
+    x += ((long long)((n - t + split - 1) / split) << 32) | small_pieces(t);
   }
   long long inc = x;
 #pragma unroll
@@ -445,8 +500,8 @@ __device__ __forceinline__ void warp_plan(const DecodeParams& P, int target_spli
 #pragma unroll 1
     for (int b = b0; b < b1; ++b) {
       const int n = rng[b].y < 0 ? 0 : rng[b].y / kChunk - rng[b].x / kChunk + 1;
-      const int t = tail_chunks(n);
-      const int nb = (n - t + split - 1) / split, ntl = (t + small - 1) / small;
+      const int t = tail_of(n);
+      const int nb = (n - t + split - 1) / split, ntl = small_pieces(t);
       const int pos_b = (int)(pos >> 32), pos_t = (int)(pos & 0xffffffffll);
       if (publish) P.ws.split_off[b] = pos_b + pos_t;
       rec[b] = make_int4(pos_b, pos_t, nb, ntl);
@@ -690,16 +745,6 @@ static __global__ void __launch_bounds__(1024) decode_plan_kernel(DecodeParams P
   }
 }
 
-// Sequences up to which an EX call has no plan launch: its CTAs plan for
-// themselves (one sequence a lane of one warp) and take a fixed share of the
-// items, which saves a launch and its 4-5 us but not the counter's evenness.
-// Measured with / without it (us a call, 32 query and 8 KV heads of 128): 128
-// selected pages of 1, 4, 8, 16, 32 sequences 17.2 / 19.5, 18.5 / 21.0, 19.8 /
-// 22.0, 31.6 / 33.1, 52.6 / 53.9; weight-gathering over whole bf16 contexts of
-// up to 8,192 keys 21.3 / 23.6, 29.1 / 31.1, 40.9 / 42.7, 68.1 / 69.1 and, at
-// 32, 128.9 / 122.9 (e4m3: 53.4 / 54.2 at 16, 89.5 / 83.1 at 32).
-constexpr int kSelfPlanMax = 16;
-
 struct ItemInfo {
   int b, g, lo, p, c_begin, c_end;  // chunks [c_begin, c_end)
   int s_global, nsplits;            // split index in the partial arrays; splits of b
@@ -732,7 +777,7 @@ __device__ __forceinline__ void describe_planned(const DecodeParams& P, const in
   const int4 r = rec[j];
   const int lo = rng[j].x, p = rng[j].y;
   const int n = p / kChunk - lo / kChunk + 1, c0 = lo / kChunk, c1 = c0 + n;
-  const int cm = c1 - tail_chunks(n);
+  const int cm = c1 - tail_chunks(n, s_plan[1]);
   const int k = pidx - (bulk ? r.x : r.y);
   it.g = item - s * P.h_kv;
   it.b = j;
@@ -973,8 +1018,8 @@ __global__ void __launch_bounds__(DecodeShape<TWO_ROWS, KV8>::kWarps * 32, 1)
   // EX with few sequences: every CTA plans for itself, CTA 0 also for the
   // launches that follow
   constexpr bool self_plan = EX == 2;
-  __shared__ int4 plan_rec[self_plan ? kSelfPlanMax : 1];
-  __shared__ int2 plan_rng[self_plan ? kSelfPlanMax : 1];
+  __shared__ int4 plan_rec[self_plan ? self_plan_max(KV8) : 1];
+  __shared__ int2 plan_rng[self_plan ? self_plan_max(KV8) : 1];
   __shared__ int plan_out[4];
   if constexpr (self_plan) {
     if (threadIdx.x < P.B) {
@@ -984,11 +1029,12 @@ __global__ void __launch_bounds__(DecodeShape<TWO_ROWS, KV8>::kWarps * 32, 1)
     }
     __syncthreads();
     if (w == 0)
-      warp_plan(P, P.target_splits, 0, plan_rng, plan_rec, plan_out, blockIdx.x == 0, lane);
+      warp_plan<true>(P, P.target_splits, 0, plan_rng, plan_rec, plan_out, blockIdx.x == 0, lane,
+                      gridDim.x * (blockDim.x >> 5));
     __syncthreads();
     if (blockIdx.x == 0 && plan_out[2] >= 0)
-      write_piece_descs(P, plan_rec, plan_rng, 0, P.B, 0, plan_out[2], 0, plan_out[3], plan_out[2],
-                        plan_out[0], plan_out[1], threadIdx.x, blockDim.x);
+      write_piece_descs<true>(P, plan_rec, plan_rng, 0, P.B, 0, plan_out[2], 0, plan_out[3],
+                              plan_out[2], plan_out[0], plan_out[1], threadIdx.x, blockDim.x);
   }
 
   // launched as a programmatic dependent of the plan kernel: its results
@@ -2396,7 +2442,7 @@ struct NewRows {
 };
 
 // Dynamic shared memory a bf16 / one-byte kernel variant may take: 227 KiB
-// less 2 KiB for the static state, the int8 scale rings and (EX) 1 KiB for the
+// less 2 KiB for the static state, the int8 scale rings and (EX) 2 KiB for the
 // pieces it plans itself.  A kernel is given all of it, whatever a call's own
 // part: threads that launch different sizes at once set the same attribute.
 template <int D, bool TWO, bool K8, bool I8, bool EX>
@@ -2405,7 +2451,7 @@ static constexpr int decode_smem_max() {
   using L = WarpSmem<D, K8, I8, S::kRing>;
   static_assert(sizeof(WarpShared<S::kWarps, S::kRing>) <= 2048, "static state over 2 KiB");
   const int scales = I8 ? S::kWarps * S::kRing * L::kScaleBytes : 0;
-  return 227 * 1024 - 2048 - (EX ? 1024 : 0) - scales;
+  return 227 * 1024 - 2048 - (EX ? 2048 : 0) - scales;
 }
 
 // Warps per CTA: the shape's count, or as many as that memory holds besides
@@ -2430,11 +2476,11 @@ static int decode_warps(int rows) {
 // lengths, so no item waits for another, nothing is atomic and the order of
 // the additions is fixed (row 0, 1, ...).
 // Bound: L2 (the scores, 4 bytes a row and key) and the masses' 8 bytes a key
-// and head.  Measured: 14 of a call's 123 us for 64 e4m3 contexts of 512-8,192
+// and head.  Measured: 14 of a call's 118 us for 64 e4m3 contexts of 512-8,192
 // keys, 32 query and 8 KV heads (37 MB of scores, 19 of masses); a bf16 context
-// of 32,768 takes 35.5 us in all (136 MB).  One launch for the merge and this
+// of 32,768 takes 33.9 us in all (136 MB).  One launch for the merge and this
 // (blocks of either kind, these folding the pieces' statistics themselves)
-// took 39.5 and 124.7 us a call where two launches took 36.7 and 121: every
+// took 39.5 and 124.7 us where two launches then took 36.7 and 121: every
 // block then holds the merge's registers.
 static __global__ void __launch_bounds__(256) decode_mass_kernel(DecodeParams P, float* mass,
                                                                  int64_t mass_len) {
@@ -2664,7 +2710,7 @@ static tl_status decode_impl(const void* q, const void* k_cache, const void* v_c
   const int64_t write_ctas =
       P.n_new > 0 ? std::min<int64_t>(num_sms(), (write_warps + wpc - 1) / wpc) : 0;
   P.target_splits = target_splits;
-  P.self_plan = EX && dtype != TL_F32 && B <= kSelfPlanMax ? 1 : 0;
+  P.self_plan = EX && dtype != TL_F32 && B <= self_plan_max(kv8) ? 1 : 0;
   if (!P.self_plan) {
     decode_plan_kernel<<<(unsigned)(1 + write_ctas), plan_threads, 0, st>>>(P, target_splits,
                                                                             num_sms() * warps);

@@ -531,3 +531,24 @@ def test_pages_past_32_bit_offsets():
     assert torch.equal(pages.cpu(), torch.where(want_t >= 0, P - 1 - want_t, -1))
     out = tl.tl_paged_attn_decode_pages(q.cuda(), k, v, pages, ln, 0.09)
     check_pages(out, pools, q, want_t, want_l, 0.09, "far")
+
+
+@pytest.mark.parametrize("kind,B,hkv,group", [
+    ("bf16", 31, 2, 4), ("bf16", 32, 4, 2), ("bf16", 33, 2, 1), ("e4m3", 32, 2, 4),
+    ("e4m3", 33, 2, 8), ("int8", 64, 2, 4), ("int8", 65, 1, 4), ("e4m3", 64, 1, 16),
+    # more heads and sequences than warps: a piece of each sequence is no longer one item a warp
+    ("bf16", 30, 64, 1), ("e4m3", 61, 48, 1), ("int8", 2, 300, 1),
+])
+def test_attention_over_pages_of_any_batch(kind, B, hkv, group):
+    """Batches on both sides of the call's own planning, one sequence much longer than the rest,
+    some empty."""
+    rng = np.random.default_rng(B)
+    lens = [int(n) for n in rng.integers(1, 120, B)]
+    lens[B // 2], lens[0], lens[-1] = 2000, 0, 16
+    table, P = ref.tables(lens, 16, seed=3)
+    pools = ref.Pools(kind, P, 16, hkv, 128, seed=4)
+    q = torch.randn((B, hkv * group, 128), generator=torch.Generator().manual_seed(5)).bfloat16()
+    pages, ln = head_pages(table, lens, hkv, 110, 16, seed=6)
+    out = run_pages(pools, q, pages, ln, 0.09)
+    check_pages(out, pools, q, pages, ln, 0.09, f"{kind} b{B}")
+    assert torch.equal(out, run_pages(pools, q, pages, ln, 0.09))
