@@ -2471,14 +2471,14 @@ static int decode_warps(int rows) {
 // statistics that the EX form left in the workspace: the probabilities of the
 // softmax, each with its row's final max and sum (a piece's own max would
 // leave a factor per row, so the rows could not be added before the merge).
-// One warp per work item of the plan (piece x KV head): the plan's pieces
-// cover every live key of every sequence once and are balanced whatever the
-// lengths, so no item waits for another, nothing is atomic and the order of
-// the additions is fixed (row 0, 1, ...).
+// One warp per work item of the plan (piece x KV head), or a part of one: the
+// plan's pieces cover every live key of every sequence once and are balanced
+// whatever the lengths, so no item waits for another, nothing is atomic and the
+// order of the additions is fixed (row 0, 1, ...).
 // Bound: L2 (the scores, 4 bytes a row and key) and the masses' 8 bytes a key
-// and head.  Measured: 14 of a call's 118 us for 64 e4m3 contexts of 512-8,192
+// and head.  Measured: 14 of a call's 117 us for 64 e4m3 contexts of 512-8,192
 // keys, 32 query and 8 KV heads (37 MB of scores, 19 of masses); a bf16 context
-// of 32,768 takes 33.9 us in all (136 MB).  One launch for the merge and this
+// of 32,768 takes 34.3 us in all (136 MB).  One launch for the merge and this
 // (blocks of either kind, these folding the pieces' statistics themselves)
 // took 39.5 and 124.7 us where two launches then took 36.7 and 121: every
 // block then holds the merge's registers.
@@ -2488,11 +2488,22 @@ static __global__ void __launch_bounds__(256) decode_mass_kernel(DecodeParams P,
   asm volatile("griddepcontrol.wait;\n" ::: "memory");
   const int lane = threadIdx.x & 31;
   const int nwarps = gridDim.x * (blockDim.x >> 5);
-  const int total = __ldcg(P.ws.ctrl + 1) * P.h_kv;
-  for (int item = blockIdx.x * (blockDim.x >> 5) + (threadIdx.x >> 5); item < total;
-       item += nwarps) {
+  // the items, long ones of more than 8 rows in four parts where there are warps
+  // for them: a call of 16 sequences with 16 rows takes 82 us (84 undivided), one
+  // of 32 157 (169); with 4 rows the parts cost 1-2%, in short pieces 2-4 us
+  const int items = __ldcg(P.ws.ctrl + 1) * P.h_kv, size = __ldcg(P.ws.ctrl);
+  const int shift = P.rows > 8 && size >= 16 && 4 * (int64_t)items <= nwarps ? 2 : 0;
+  const int part_chunks = (size + 3) >> 2, total = items << shift;
+  for (int unit = blockIdx.x * (blockDim.x >> 5) + (threadIdx.x >> 5); unit < total;
+       unit += nwarps) {
     ItemInfo it;
-    describe_item(P, item, it);
+    describe_item(P, unit >> shift, it);
+    if (shift) {
+      const int part = unit & 3;
+      it.c_begin += part * part_chunks;
+      // (the last part takes what is left: a small piece may be the longer one)
+      if (part < 3) it.c_end = min(it.c_end, it.c_begin + part_chunks);
+    }
     float m = 0.f, inv = 0.f;  // lane r: row r's max and 1 / sum (0: it sees no key)
     if (lane < P.rows) {
       const float2 st = __ldcg(reinterpret_cast<const float2*>(P.stats) +

@@ -652,3 +652,19 @@ def test_v_scales_of_any_size(group, T):
         mass = mass0.cuda()
         out = run_mass(pools, q, table, lens, mass, 0.09)
         check_mass(out, mass, mass0, pools, q, table, lens, 0.09, 0, f"scales {sign}")
+
+
+@pytest.mark.parametrize("kind,B,T", [("bf16", 3, 4), ("e4m3", 40, 3), ("bf16", 700, 4),
+                                      ("bf16", 700, 1)])
+def test_mass_of_pieces_in_parts(kind, B, T):
+    """Fewer pieces than the warps that add the weights up: each piece goes in parts.  One long
+    sequence (its pieces' sizes differ from the others'), short ones and empty ones."""
+    lens = [(53 * b) % 90 for b in range(B)]
+    lens[1] = 9000
+    table, P = ref.tables(lens, 16, seed=1)
+    pools = ref.Pools(kind, P, 16, 1, 128, seed=2)
+    q = torch.randn((B, T, 4, 128), generator=torch.Generator().manual_seed(3)).bfloat16()
+    mass0 = torch.rand((B, 1, 9000), generator=torch.Generator().manual_seed(4))
+    mass = mass0.cuda()
+    out = run_mass(pools, q, table, lens, mass, 0.09)
+    check_mass(out, mass, mass0, pools, q, table, lens, 0.09, 0, f"{kind} b{B}")
