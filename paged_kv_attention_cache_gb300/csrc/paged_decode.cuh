@@ -2482,15 +2482,15 @@ static int decode_warps(int rows) {
 // (blocks of either kind, these folding the pieces' statistics themselves)
 // took 39.5 and 124.7 us where two launches then took 36.7 and 121: every
 // block then holds the merge's registers.
-static __global__ void __launch_bounds__(256) decode_mass_kernel(DecodeParams P, float* mass,
-                                                                 int64_t mass_len) {
+static __global__ void __launch_bounds__(256, 4) decode_mass_kernel(DecodeParams P, float* mass,
+                                                                    int64_t mass_len) {
   constexpr int U = 4, R = 4;  // keys per lane and rows per round of loads
   asm volatile("griddepcontrol.wait;\n" ::: "memory");
   const int lane = threadIdx.x & 31;
   const int nwarps = gridDim.x * (blockDim.x >> 5);
   // the items, long ones of more than 8 rows in four parts where there are warps
-  // for them: a call of 16 sequences with 16 rows takes 82 us (84 undivided), one
-  // of 32 157 (169); with 4 rows the parts cost 1-2%, in short pieces 2-4 us
+  // for them: a call of 16 sequences with 16 rows takes 79 us (84 undivided), one
+  // of 32 150 (169); with 4 rows the parts cost 1-2%, in short pieces 2-4 us
   const int items = __ldcg(P.ws.ctrl + 1) * P.h_kv, size = __ldcg(P.ws.ctrl);
   const int shift = P.rows > 8 && size >= 16 && 4 * (int64_t)items <= nwarps ? 2 : 0;
   const int part_chunks = (size + 3) >> 2, total = items << shift;
