@@ -1581,8 +1581,9 @@ __global__ void __launch_bounds__(DecodeShape<TWO_ROWS, KV8>::kWarps * 32, 1)
           v0 = fminf(fmaxf(v0, 0.f), 3.0e38f);
           v1 = fminf(fmaxf(v1, 0.f), 3.0e38f);
           if constexpr (kFitV) {
-            v0 = p[jc][0] + p[jc][1] > 0.f ? v0 : 0.f;
-            v1 = p[jc][2] + p[jc][3] > 0.f ? v1 : 0.f;
+            // (a NaN of one row is not to hide another row's weight)
+            v0 = p[jc][0] > 0.f || p[jc][1] > 0.f ? v0 : 0.f;
+            v1 = p[jc][2] > 0.f || p[jc][3] > 0.f ? v1 : 0.f;
             fit_v(fmaxf(v0, v1));
             v0 *= vfit;
             v1 *= vfit;
@@ -1888,8 +1889,8 @@ __global__ void __launch_bounds__(DecodeShape<TWO_ROWS, KV8>::kWarps * 32, 1)
   #pragma unroll
                 for (int e = 0; e < 2; ++e) {
                   v[n][e] = fminf(fmaxf(v[n][e], 0.f), 3.0e38f);
-                  const float any = TWO_ROWS ? p[jc][n][e] + p[jc][n][2 + e] : p[jc][n][e];
-                  if (any > 0.f) big = fmaxf(big, v[n][e]);
+                  if (p[jc][n][e] > 0.f || (TWO_ROWS && p[jc][n][2 + e] > 0.f))
+                    big = fmaxf(big, v[n][e]);
                 }
               fit_v(big);
   #pragma unroll

@@ -552,3 +552,46 @@ def test_attention_over_pages_of_any_batch(kind, B, hkv, group):
     out = run_pages(pools, q, pages, ln, 0.09)
     check_pages(out, pools, q, pages, ln, 0.09, f"{kind} b{B}")
     assert torch.equal(out, run_pages(pools, q, pages, ln, 0.09))
+
+
+@pytest.mark.parametrize("kind,group", [("bf16", 4), ("e4m3", 4), ("e4m3", 6), ("int8", 4),
+                                        ("int8", 5), ("int8", 12), ("f32", 3)])
+def test_a_nan_in_one_head_leaves_the_others(kind, group):
+    lens = [500, 33]
+    table, P = ref.tables(lens, 16, seed=3)
+    pools = ref.Pools(kind, P, 16, 2, 128, seed=4)
+    pools.poison(ref.used_slots(table, lens, P, 16))
+    q = torch.randn((2, 2 * group, 128), generator=torch.Generator().manual_seed(5))
+    q = q if kind == "f32" else q.bfloat16()
+    pages, ln = head_pages(table, lens, 2, 20, 16, seed=6)
+    want = run_pages(pools, q, pages, ln, 0.09)
+    bad = q.clone()
+    bad[:, 1, 7] = float("nan")
+    p, w = pools.gpu(), word()
+    attend = tl.tl_paged_attn_decode_pages_int8 if kind == "int8" else tl.tl_paged_attn_decode_pages
+    scales = (p["ks"], p["vs"]) if kind == "int8" else ()
+    got = attend(bad.cuda(), p["k"], p["v"], *scales, pages.cuda(), i32(ln), 0.09, error_word=w)
+    heads = [h for h in range(2 * group) if h != 1]
+    assert torch.equal(got[:, heads], want[:, heads])
+
+
+@pytest.mark.parametrize("kind,group,T", [("int8", 3, 2), ("int8", 1, 7), ("e4m3", 3, 2)])
+def test_weights_with_columns_left_over(kind, group, T):
+    """Tokens times heads that leave columns of the keys-as-rows form empty, over pools whose
+    unread slots hold NaN."""
+    lens = [9, 100, 1000]
+    table, P = ref.tables(lens, 16, seed=3)
+    pools = ref.Pools(kind, P, 16, 2, 128, seed=4)
+    clean = ref.Pools(kind, P, 16, 2, 128, seed=4)
+    pools.poison(ref.used_slots(table, lens, P, 16))
+    q = torch.randn((3, T, 2 * group, 128), generator=torch.Generator().manual_seed(5)).bfloat16()
+    res = []
+    for x in (pools, clean):
+        p, w, mass = x.gpu(), word(), torch.zeros((3, 2, 1000), device="cuda")
+        gather = tl.tl_paged_attn_decode_mass_int8 if kind == "int8" else tl.tl_paged_attn_decode_mass
+        scales = (p["ks"], p["vs"]) if kind == "int8" else ()
+        out = gather(q.cuda(), p["k"], p["v"], *scales, table.cuda(), i32(lens), mass, 0.09,
+                     error_word=w)
+        assert int(w.item()) == 0 and torch.isfinite(out).all() and torch.isfinite(mass).all()
+        res.append((out, mass))
+    assert torch.equal(res[0][0], res[1][0]) and torch.equal(res[0][1], res[1][1])
