@@ -205,16 +205,51 @@ def tl_kv_cache_write_int8(k_new: torch.Tensor, v_new: torch.Tensor, k_codes: to
          _err_word(error_word, dev))
 
 
-def _decode_out(out, shape, device):
+def _alloc_stream(stream, device):
+    """The stream to allocate a call's own buffers on, or None: the current one.
+    A block that was allocated on one stream goes, once dropped, to that
+    stream's next allocation, whose work may run while another stream still
+    uses it; so what a call allocates belongs to the stream it runs on."""
+    if stream is None:
+        return None
+    with torch.cuda.device(device):
+        handle = _stream(stream)
+        if handle == torch.cuda.current_stream().cuda_stream:
+            return None
+        if isinstance(stream, torch.cuda.Stream):
+            return stream
+        return torch.cuda.ExternalStream(handle, device=device) if handle else \
+            torch.cuda.default_stream(device)
+
+
+def _returned(shape, dtype, device, stream):
+    """A tensor that the call returns.  The caller uses it on the current stream
+    too: it is not reused before that stream's work so far at its release."""
+    on = _alloc_stream(stream, device)
+    if on is None:
+        return torch.empty(shape, dtype=dtype, device=device)
+    with torch.cuda.device(device):
+        current = torch.cuda.current_stream()
+    with torch.cuda.stream(on):
+        t = torch.empty(shape, dtype=dtype, device=device)
+    t.record_stream(current)
+    return t
+
+
+def _decode_out(out, shape, device, stream=None):
     if out is None:
-        return torch.empty(shape, dtype=torch.float32, device=device)
+        return _returned(shape, torch.float32, device, stream)
     _need(out, "out", torch.float32, shape, device)
     return out
 
 
-def _workspace(workspace, nbytes, device):
+def _workspace(workspace, nbytes, device, stream=None):
     if workspace is None:
-        return alloc_workspace(nbytes, device)
+        on = _alloc_stream(stream, device)
+        if on is None:
+            return alloc_workspace(nbytes, device)
+        with torch.cuda.stream(on):
+            return alloc_workspace(nbytes, device)
     _need(workspace, "workspace", None, None, device)
     return workspace
 
@@ -237,8 +272,9 @@ def tl_paged_attn_decode_int8(q: torch.Tensor, k_codes: torch.Tensor, v_codes: t
     _need(q, "q", torch.bfloat16, (None, None, d), dev)
     B, hq, _ = q.shape
     _need_table(block_table, context_lens, B, dev)
-    out = _decode_out(out, (B, hq, d), dev)
-    workspace = _workspace(workspace, tl_paged_attn_decode_workspace_size(B, hq, hkv, d), dev)
+    out = _decode_out(out, (B, hq, d), dev, stream)
+    workspace = _workspace(workspace, tl_paged_attn_decode_workspace_size(B, hq, hkv, d),
+                            dev, stream)
     _run("tl_paged_attn_decode_int8", dev, stream,
          _ptr(q), _ptr(k_codes), _ptr(v_codes), _ptr(k_scales), _ptr(v_scales), _ptr(block_table),
          block_table.shape[1], _ptr(context_lens), _ptr(out), B, hq, hkv, d, P, ps, int(window),
@@ -264,8 +300,9 @@ def tl_paged_attn_decode_write_int8(q: torch.Tensor, k_new: torch.Tensor, v_new:
     _need_new_rows(k_new, v_new, slot_mapping, hkv, d, dev)
     B, hq, _ = q.shape
     _need_table(block_table, context_lens, B, dev)
-    out = _decode_out(out, (B, hq, d), dev)
-    workspace = _workspace(workspace, tl_paged_attn_decode_workspace_size(B, hq, hkv, d), dev)
+    out = _decode_out(out, (B, hq, d), dev, stream)
+    workspace = _workspace(workspace, tl_paged_attn_decode_workspace_size(B, hq, hkv, d),
+                            dev, stream)
     _run("tl_paged_attn_decode_write_int8", dev, stream,
          _ptr(q), _ptr(k_new), _ptr(v_new), _DTYPES.get(k_new.dtype, -1), _ptr(slot_mapping),
          slot_mapping.numel(), _ptr(k_codes), _ptr(v_codes), _ptr(k_scales), _ptr(v_scales),
@@ -326,8 +363,9 @@ def tl_paged_attn_decode(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.
     """out[B, H_q, d] (float32): one query per sequence, causal length context_lens[b]."""
     dev, P, ps, hkv, d = _decode_args(q, k_cache, v_cache, block_table, context_lens)
     B, hq, _ = q.shape
-    out = _decode_out(out, (B, hq, d), dev)
-    workspace = _workspace(workspace, tl_paged_attn_decode_workspace_size(B, hq, hkv, d), dev)
+    out = _decode_out(out, (B, hq, d), dev, stream)
+    workspace = _workspace(workspace, tl_paged_attn_decode_workspace_size(B, hq, hkv, d),
+                            dev, stream)
     _run("tl_paged_attn_decode", dev, stream,
          _ptr(q), _ptr(k_cache), _ptr(v_cache), _ptr(block_table), block_table.shape[1],
          _ptr(context_lens), _ptr(out), B, hq, hkv, d, P, ps, int(window), float(scale),
@@ -351,8 +389,9 @@ def tl_paged_attn_decode_write(q: torch.Tensor, k_new: torch.Tensor, v_new: torc
     dev, P, ps, hkv, d = _decode_args(q, k_cache, v_cache, block_table, context_lens)
     _need_new_rows(k_new, v_new, slot_mapping, hkv, d, dev)
     B, hq, _ = q.shape
-    out = _decode_out(out, (B, hq, d), dev)
-    workspace = _workspace(workspace, tl_paged_attn_decode_workspace_size(B, hq, hkv, d), dev)
+    out = _decode_out(out, (B, hq, d), dev, stream)
+    workspace = _workspace(workspace, tl_paged_attn_decode_workspace_size(B, hq, hkv, d),
+                            dev, stream)
     _run("tl_paged_attn_decode_write", dev, stream,
          _ptr(q), _ptr(k_new), _ptr(v_new), _DTYPES.get(k_new.dtype, -1), _ptr(slot_mapping),
          slot_mapping.numel(), _ptr(k_cache), _ptr(v_cache), _ptr(block_table),
@@ -409,12 +448,12 @@ def tl_paged_attn_prefill(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch
     or, with max_row_keys, as wide as rows reading at most that many keys."""
     dev, P, ps, hkv, d = _prefill_args(q, k_cache, v_cache, block_table, positions)
     B, T, hq, _ = q.shape
-    out = _decode_out(out, (B, T, hq, d), dev)
+    out = _decode_out(out, (B, T, hq, d), dev, stream)
     dt = _DTYPES.get(k_cache.dtype, -1)
     workspace = _workspace(workspace, tl_paged_attn_prefill_workspace_size_keys(
         B, T, hq, hkv, d, max_row_keys, dt) if max_row_keys else
         tl_paged_attn_prefill_workspace_size_ex(B, T, hq, hkv, d, block_table.shape[1], ps, 0,
-                                                dt), dev)
+                                                dt), dev, stream)
     _run("tl_paged_attn_prefill", dev, stream,
          _ptr(q), _ptr(k_cache), _ptr(v_cache), _ptr(block_table), block_table.shape[1],
          _ptr(positions), _ptr(out), B, T, hq, hkv, d, P, ps, int(window), float(scale),
@@ -440,9 +479,9 @@ def tl_paged_attn_prefill_int8(q: torch.Tensor, k_codes: torch.Tensor, v_codes: 
     if block_table.shape[1] < 1:
         raise ValueError("block_table needs at least one column")
     _need(positions, "positions", torch.int32, (B, T), dev)
-    out = _decode_out(out, (B, T, hq, d), dev)
+    out = _decode_out(out, (B, T, hq, d), dev, stream)
     workspace = _workspace(workspace, tl_paged_attn_prefill_workspace_size_ex(
-        B, T, hq, hkv, d, block_table.shape[1], ps, 0, TL_INT8), dev)
+        B, T, hq, hkv, d, block_table.shape[1], ps, 0, TL_INT8), dev, stream)
     _run("tl_paged_attn_prefill_int8", dev, stream,
          _ptr(q), _ptr(k_codes), _ptr(v_codes), _ptr(k_scales), _ptr(v_scales), _ptr(block_table),
          block_table.shape[1], _ptr(positions), _ptr(out), B, T, hq, hkv, d, P, ps, int(window),
@@ -460,8 +499,9 @@ def tl_paged_attn_decode_ring(q: torch.Tensor, k_cache: torch.Tensor, v_cache: t
     the sequence's ring (logical block k on entry k % ring_pages)."""
     dev, P, ps, hkv, d = _decode_args(q, k_cache, v_cache, block_table, context_lens)
     B, hq, _ = q.shape
-    out = _decode_out(out, (B, hq, d), dev)
-    workspace = _workspace(workspace, tl_paged_attn_decode_workspace_size(B, hq, hkv, d), dev)
+    out = _decode_out(out, (B, hq, d), dev, stream)
+    workspace = _workspace(workspace, tl_paged_attn_decode_workspace_size(B, hq, hkv, d),
+                            dev, stream)
     _run("tl_paged_attn_decode_ring", dev, stream,
          _ptr(q), _ptr(k_cache), _ptr(v_cache), _ptr(block_table), block_table.shape[1],
          _ptr(context_lens), _ptr(out), B, hq, hkv, d, P, ps, int(window), int(ring_pages),
@@ -486,10 +526,10 @@ def tl_paged_attn_prefill_ring(q: torch.Tensor, k_cache: torch.Tensor, v_cache: 
     """Batched prefill over rings (see tl_paged_attn_decode_ring)."""
     dev, P, ps, hkv, d = _prefill_args(q, k_cache, v_cache, block_table, positions)
     B, T, hq, _ = q.shape
-    out = _decode_out(out, (B, T, hq, d), dev)
+    out = _decode_out(out, (B, T, hq, d), dev, stream)
     workspace = _workspace(workspace, tl_paged_attn_prefill_workspace_size_ex(
         B, T, hq, hkv, d, block_table.shape[1], ps, ring_pages,
-        _DTYPES.get(k_cache.dtype, -1)), dev)
+        _DTYPES.get(k_cache.dtype, -1)), dev, stream)
     _run("tl_paged_attn_prefill_ring", dev, stream,
          _ptr(q), _ptr(k_cache), _ptr(v_cache), _ptr(block_table), block_table.shape[1],
          _ptr(positions), _ptr(out), B, T, hq, hkv, d, P, ps, int(window), int(ring_pages),
@@ -511,8 +551,9 @@ def tl_paged_attn_decode_write_ring(q: torch.Tensor, k_new: torch.Tensor, v_new:
     dev, P, ps, hkv, d = _decode_args(q, k_cache, v_cache, block_table, context_lens)
     _need_new_rows(k_new, v_new, slot_mapping, hkv, d, dev)
     B, hq, _ = q.shape
-    out = _decode_out(out, (B, hq, d), dev)
-    workspace = _workspace(workspace, tl_paged_attn_decode_workspace_size(B, hq, hkv, d), dev)
+    out = _decode_out(out, (B, hq, d), dev, stream)
+    workspace = _workspace(workspace, tl_paged_attn_decode_workspace_size(B, hq, hkv, d),
+                            dev, stream)
     _run("tl_paged_attn_decode_write_ring", dev, stream,
          _ptr(q), _ptr(k_new), _ptr(v_new), _DTYPES.get(k_new.dtype, -1), _ptr(slot_mapping),
          slot_mapping.numel(), _ptr(k_cache), _ptr(v_cache), _ptr(block_table),
@@ -537,8 +578,9 @@ def tl_paged_attn_decode_ring_int8(q: torch.Tensor, k_codes: torch.Tensor, v_cod
     _need(q, "q", torch.bfloat16, (None, None, d), dev)
     B, hq, _ = q.shape
     _need_table(block_table, context_lens, B, dev)
-    out = _decode_out(out, (B, hq, d), dev)
-    workspace = _workspace(workspace, tl_paged_attn_decode_workspace_size(B, hq, hkv, d), dev)
+    out = _decode_out(out, (B, hq, d), dev, stream)
+    workspace = _workspace(workspace, tl_paged_attn_decode_workspace_size(B, hq, hkv, d),
+                            dev, stream)
     _run("tl_paged_attn_decode_ring_int8", dev, stream,
          _ptr(q), _ptr(k_codes), _ptr(v_codes), _ptr(k_scales), _ptr(v_scales), _ptr(block_table),
          block_table.shape[1], _ptr(context_lens), _ptr(out), B, hq, hkv, d, P, ps, int(window),
@@ -565,9 +607,9 @@ def tl_paged_attn_prefill_ring_int8(q: torch.Tensor, k_codes: torch.Tensor,
     if block_table.shape[1] < 1:
         raise ValueError("block_table needs at least one column")
     _need(positions, "positions", torch.int32, (B, T), dev)
-    out = _decode_out(out, (B, T, hq, d), dev)
+    out = _decode_out(out, (B, T, hq, d), dev, stream)
     workspace = _workspace(workspace, tl_paged_attn_prefill_workspace_size_ex(
-        B, T, hq, hkv, d, block_table.shape[1], ps, ring_pages, TL_INT8), dev)
+        B, T, hq, hkv, d, block_table.shape[1], ps, ring_pages, TL_INT8), dev, stream)
     _run("tl_paged_attn_prefill_ring_int8", dev, stream,
          _ptr(q), _ptr(k_codes), _ptr(v_codes), _ptr(k_scales), _ptr(v_scales), _ptr(block_table),
          block_table.shape[1], _ptr(positions), _ptr(out), B, T, hq, hkv, d, P, ps, int(window),
@@ -592,9 +634,9 @@ def tl_paged_attn_decode_multi(q: torch.Tensor, k_cache: torch.Tensor, v_cache: 
     dev, P, ps, hkv, d = _decode_args(q, k_cache, v_cache, block_table, context_lens,
                                       q_tokens=True)
     B, q_len, hq, _ = q.shape
-    out = _decode_out(out, (B, q_len, hq, d), dev)
+    out = _decode_out(out, (B, q_len, hq, d), dev, stream)
     workspace = _workspace(
-        workspace, tl_paged_attn_decode_multi_workspace_size(B, q_len, hq, hkv, d), dev)
+        workspace, tl_paged_attn_decode_multi_workspace_size(B, q_len, hq, hkv, d), dev, stream)
     _run("tl_paged_attn_decode_multi", dev, stream,
          _ptr(q), _ptr(k_cache), _ptr(v_cache), _ptr(block_table), block_table.shape[1],
          _ptr(context_lens), _ptr(out), B, q_len, hq, hkv, d, P, ps, int(window), float(scale),
@@ -618,9 +660,9 @@ def tl_paged_attn_decode_multi_int8(q: torch.Tensor, k_codes: torch.Tensor,
     _need(q, "q", torch.bfloat16, (None, None, None, d), dev)
     B, q_len, hq, _ = q.shape
     _need_table(block_table, context_lens, B, dev)
-    out = _decode_out(out, (B, q_len, hq, d), dev)
+    out = _decode_out(out, (B, q_len, hq, d), dev, stream)
     workspace = _workspace(
-        workspace, tl_paged_attn_decode_multi_workspace_size(B, q_len, hq, hkv, d), dev)
+        workspace, tl_paged_attn_decode_multi_workspace_size(B, q_len, hq, hkv, d), dev, stream)
     _run("tl_paged_attn_decode_multi_int8", dev, stream,
          _ptr(q), _ptr(k_codes), _ptr(v_codes), _ptr(k_scales), _ptr(v_scales), _ptr(block_table),
          block_table.shape[1], _ptr(context_lens), _ptr(out), B, q_len, hq, hkv, d, P, ps,
@@ -689,9 +731,9 @@ def tl_kv_page_select_workspace_size(B: int, h_q: int, h_kv: int, d: int,
     return int(_lib.load().tl_kv_page_select_workspace_size(B, h_q, h_kv, d, max_pages_per_seq))
 
 
-def _int_out(t, name, shape, device):
+def _int_out(t, name, shape, device, stream=None):
     if t is None:
-        return torch.empty(shape, dtype=torch.int32, device=device)
+        return _returned(shape, torch.int32, device, stream)
     _need(t, name, torch.int32, shape, device)
     return t
 
@@ -714,10 +756,11 @@ def tl_kv_page_select(q: torch.Tensor, bounds: torch.Tensor, bound_scales: torch
     P, hkv = bounds.shape[:2]
     _need_table(block_table, context_lens, B, dev)
     n = int(n_select)
-    page_table = _int_out(page_table, "page_table", (B, hkv, n), dev)
-    page_lens = _int_out(page_lens, "page_lens", (B,), dev)
+    page_table = _int_out(page_table, "page_table", (B, hkv, n), dev, stream)
+    page_lens = _int_out(page_lens, "page_lens", (B,), dev, stream)
     width = block_table.shape[1]
-    workspace = _workspace(workspace, tl_kv_page_select_workspace_size(B, hq, hkv, d, width), dev)
+    workspace = _workspace(workspace, tl_kv_page_select_workspace_size(B, hq, hkv, d, width),
+                            dev, stream)
     _run("tl_kv_page_select", dev, stream,
          _ptr(q), _DTYPES.get(q.dtype, -1), _ptr(bounds), _ptr(bound_scales), _ptr(block_table),
          width, _ptr(context_lens), n, int(keep_first), int(keep_last), _ptr(page_table),
@@ -746,8 +789,9 @@ def tl_paged_attn_decode_pages(q: torch.Tensor, k_cache: torch.Tensor, v_cache: 
     _need(q, "q", _query_dtype(k_cache.dtype), (None, None, d), dev)
     B, hq, _ = q.shape
     _need_page_table(page_table, page_lens, B, hkv, dev)
-    out = _decode_out(out, (B, hq, d), dev)
-    workspace = _workspace(workspace, tl_paged_attn_decode_workspace_size(B, hq, hkv, d), dev)
+    out = _decode_out(out, (B, hq, d), dev, stream)
+    workspace = _workspace(workspace, tl_paged_attn_decode_workspace_size(B, hq, hkv, d),
+                            dev, stream)
     _run("tl_paged_attn_decode_pages", dev, stream,
          _ptr(q), _ptr(k_cache), _ptr(v_cache), _ptr(page_table), page_table.shape[2],
          _ptr(page_lens), _ptr(out), B, hq, hkv, d, P, ps, float(scale),
@@ -770,8 +814,9 @@ def tl_paged_attn_decode_pages_int8(q: torch.Tensor, k_codes: torch.Tensor,
     _need(q, "q", torch.bfloat16, (None, None, d), dev)
     B, hq, _ = q.shape
     _need_page_table(page_table, page_lens, B, hkv, dev)
-    out = _decode_out(out, (B, hq, d), dev)
-    workspace = _workspace(workspace, tl_paged_attn_decode_workspace_size(B, hq, hkv, d), dev)
+    out = _decode_out(out, (B, hq, d), dev, stream)
+    workspace = _workspace(workspace, tl_paged_attn_decode_workspace_size(B, hq, hkv, d),
+                            dev, stream)
     _run("tl_paged_attn_decode_pages_int8", dev, stream,
          _ptr(q), _ptr(k_codes), _ptr(v_codes), _ptr(k_scales), _ptr(v_scales), _ptr(page_table),
          page_table.shape[2], _ptr(page_lens), _ptr(out), B, hq, hkv, d, P, ps, float(scale),
@@ -801,10 +846,10 @@ def tl_paged_attn_decode_mass(q: torch.Tensor, k_cache: torch.Tensor, v_cache: t
                                       q_tokens=True)
     B, q_len, hq, _ = q.shape
     _need(mass, "mass", torch.float32, (B, hkv, None), dev)
-    out = _decode_out(out, (B, q_len, hq, d), dev)
+    out = _decode_out(out, (B, q_len, hq, d), dev, stream)
     n = mass.shape[2]
     workspace = _workspace(
-        workspace, tl_paged_attn_decode_mass_workspace_size(B, q_len, hq, hkv, d, n), dev)
+        workspace, tl_paged_attn_decode_mass_workspace_size(B, q_len, hq, hkv, d, n), dev, stream)
     _run("tl_paged_attn_decode_mass", dev, stream,
          _ptr(q), _ptr(k_cache), _ptr(v_cache), _ptr(block_table), block_table.shape[1],
          _ptr(context_lens), _ptr(out), _ptr(mass), n, B, q_len, hq, hkv, d, P, ps, int(window),
@@ -828,10 +873,10 @@ def tl_paged_attn_decode_mass_int8(q: torch.Tensor, k_codes: torch.Tensor,
     B, q_len, hq, _ = q.shape
     _need_table(block_table, context_lens, B, dev)
     _need(mass, "mass", torch.float32, (B, hkv, None), dev)
-    out = _decode_out(out, (B, q_len, hq, d), dev)
+    out = _decode_out(out, (B, q_len, hq, d), dev, stream)
     n = mass.shape[2]
     workspace = _workspace(
-        workspace, tl_paged_attn_decode_mass_workspace_size(B, q_len, hq, hkv, d, n), dev)
+        workspace, tl_paged_attn_decode_mass_workspace_size(B, q_len, hq, hkv, d, n), dev, stream)
     _run("tl_paged_attn_decode_mass_int8", dev, stream,
          _ptr(q), _ptr(k_codes), _ptr(v_codes), _ptr(k_scales), _ptr(v_scales), _ptr(block_table),
          block_table.shape[1], _ptr(context_lens), _ptr(out), _ptr(mass), n, B, q_len, hq, hkv, d,
@@ -852,8 +897,8 @@ def tl_kv_evict_select(mass: torch.Tensor, context_lens: torch.Tensor, n_keep: i
     _need(mass, "mass", torch.float32, (None, None, None), dev)
     B, hkv, n = mass.shape
     _need(context_lens, "context_lens", torch.int32, (B,), dev)
-    keep = _int_out(keep, "keep", (B, hkv, int(n_keep)), dev)
-    new_lens = _int_out(new_lens, "new_lens", (B,), dev)
+    keep = _int_out(keep, "keep", (B, hkv, int(n_keep)), dev, stream)
+    new_lens = _int_out(new_lens, "new_lens", (B,), dev, stream)
     _run("tl_kv_evict_select", dev, stream,
          _ptr(mass), n, _ptr(context_lens), int(n_keep), int(keep_first), int(keep_last),
          _ptr(keep), _ptr(new_lens), B, hkv, _err_word(error_word, dev))
