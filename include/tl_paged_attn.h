@@ -730,7 +730,9 @@ size_t tl_kv_page_select_workspace_size(int32_t B, int32_t h_q, int32_t h_kv, in
  *   workspace     tl_kv_page_select_workspace_size bytes, 256-byte aligned;
  *                 calls that overlap in time must not share one
  * Supported: d in {64, 128}, h_q % h_kv == 0 with h_q/h_kv <= 16, page_size in
- * [1, 256], B*max_pages_per_seq < 2^31.  Otherwise TL_ERR_UNSUPPORTED.
+ * [1, 256], n_select and max_pages_per_seq up to 2^30, B*max_pages_per_seq,
+ * num_pages*page_size and n_select*page_size < 2^31, B*h_kv < 2^28.  Otherwise
+ * TL_ERR_UNSUPPORTED.
  */
 tl_status tl_kv_page_select(const void* q, tl_dtype q_dtype, const int8_t* bounds,
                             const float* bound_scales, const int32_t* block_table,

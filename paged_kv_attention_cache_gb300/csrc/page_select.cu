@@ -984,6 +984,8 @@ extern "C" tl_status tl_kv_page_select(const void* q, tl_dtype q_dtype, const in
       (int64_t)n_select * page_size >= ((int64_t)1 << 31) ||
       (int64_t)B * h_kv > INT32_MAX / 8 || (h_kv + kScoreWarps - 1) / kScoreWarps > 65535)
     return TL_ERR_UNSUPPORTED;
+  // places and blocks are counted in 32 bits, a step of all threads past the last one
+  if (n_select > (1 << 30) || max_pages_per_seq > (1 << 30)) return TL_ERR_UNSUPPORTED;
   if (!workspace || (reinterpret_cast<uintptr_t>(workspace) & 255u) ||
       workspace_bytes < tl_kv_page_select_workspace_size(B, h_q, h_kv, d, max_pages_per_seq))
     return TL_ERR_WORKSPACE;
