@@ -786,7 +786,7 @@ tl_status tl_paged_attn_decode_pages_int8(const void* q, const int8_t* k_codes,
  *                 sizes): the decode's, and one float32 per query head, token
  *                 and mass place for the scores
  *   other arguments, support (f32 pools with q_len 1) and errors as
- *   tl_paged_attn_decode_multi / _int8.
+ *   tl_paged_attn_decode_multi / _int8; mass_len past 2^30: TL_ERR_UNSUPPORTED.
  */
 size_t tl_paged_attn_decode_mass_workspace_size(int32_t B, int32_t q_len, int32_t h_q,
                                                 int32_t h_kv, int32_t d, int32_t mass_len);

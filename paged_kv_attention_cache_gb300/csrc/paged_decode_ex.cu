@@ -23,9 +23,10 @@ static MassWorkspace mass_ws_layout(int B, int q_len, int h_q, int h_kv, int d, 
   return w;
 }
 
+// (positions are counted in 32 bits, some steps of a warp past the last one)
 static bool mass_sizes_ok(int B, int q_len, int h_q, int h_kv, int d, int mass_len) {
   return B > 0 && q_len > 0 && h_q > 0 && h_kv > 0 && d > 0 && mass_len > 0 && h_q % h_kv == 0 &&
-         mass_len <= INT32_MAX - 32 && (int64_t)q_len * (h_q / h_kv) <= 16;
+         mass_len <= (1 << 30) && (int64_t)q_len * (h_q / h_kv) <= 16;
 }
 
 static tl_status decode_pages(const void* q, const void* k_cache, const void* v_cache,

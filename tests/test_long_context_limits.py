@@ -34,3 +34,21 @@ def test_page_select_counts_places_and_blocks(lib):
     assert s(n=2**31 - 1) == UNS and s(n=2**31 - 8192) == UNS and s(n=MOST + 1) == UNS
     assert s(maxp=2**31 - 1) == UNS and s(maxp=MOST + 1) == UNS
     assert s(n=MOST) == WS and s(maxp=MOST) == WS  # the checks behind it: no workspace
+
+
+def test_decode_mass_counts_positions(lib):
+    """A warp of the adding kernel steps 128 positions at a time: past a length near 2^31 the next
+    position would be negative."""
+    base = dict(q=256, k=512, v=768, ks=12288, vs=16384, bt=1024, maxp=1 << 27, cl=1280, out=1536,
+                m=2048, ml=64, B=1, T=1, hq=1, hkv=1, d=128, P=8, ps=16, w=0, sc=0.1,
+                dt=tl.TL_BF16, ws=4096, wsb=2**62, err=None, st=None)
+    a = caller(lib.tl_paged_attn_decode_mass,
+               "q k v bt maxp cl out m ml B T hq hkv d P ps w sc dt ws wsb err st", base)
+    i = caller(lib.tl_paged_attn_decode_mass_int8,
+               "q k v ks vs bt maxp cl out m ml B T hq hkv d P ps w sc ws wsb err st", base)
+    size = tl.tl_paged_attn_decode_mass_workspace_size
+    for ml in (2**31 - 33, 2**31 - 130, MOST + 1):
+        assert a(ml=ml) == UNS and i(ml=ml) == UNS, ml
+        assert size(1, 1, 1, 1, 128, ml) == 0, ml
+    assert a(ml=MOST, wsb=0) == WS and i(ml=MOST, wsb=0) == WS
+    assert size(1, 1, 1, 1, 128, MOST) > 4 * MOST
