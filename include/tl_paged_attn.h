@@ -850,7 +850,7 @@ tl_status tl_kv_evict_select(const float* mass, int32_t mass_len, const int32_t*
  *   mass              NULL, or [B][h_kv][mass_len] float32, in place
  * TL_ERR_INVALID_ARG when d * elem is not a multiple of 16 bytes;
  * TL_ERR_UNSUPPORTED past 4,096 bytes a row, page_size > 256,
- * num_pages*page_size >= 2^31 or n_keep > 2^30.
+ * num_pages*page_size >= 2^31, n_keep > 2^30 or (with a mass) mass_len > 2^30.
  */
 tl_status tl_kv_cache_compact(void* k_cache, void* v_cache, const int32_t* block_table,
                               int32_t max_pages_per_seq, const int32_t* context_lens,

@@ -207,7 +207,7 @@ static tl_status compact_impl(void* k, void* v, float* k_scales, float* v_scales
   if (row_bytes % 16 != 0) return TL_ERR_INVALID_ARG;
   if (row_bytes > 4096 || page_size > 256 ||
       (int64_t)num_pages * page_size >= ((int64_t)1 << 31) || (int64_t)B * h_kv > INT32_MAX ||
-      n_keep > (1 << 30))
+      n_keep > (1 << 30) || (mass && mass_len > (1 << 30)))
     return TL_ERR_UNSUPPORTED;
   CompactParams P;
   P.pool[0] = k;

@@ -1,6 +1,7 @@
 """Sizes of the long-context calls at which a 32-bit counter of a kernel would pass its range: refused
 before any launch (no GPU; made-up addresses that no kernel ever sees)."""
 import pytest
+import torch
 
 import paged_kv_attention_cache_gb300 as tl
 from paged_kv_attention_cache_gb300 import _lib, build
@@ -52,3 +53,21 @@ def test_decode_mass_counts_positions(lib):
         assert size(1, 1, 1, 1, 128, ml) == 0, ml
     assert a(ml=MOST, wsb=0) == WS and i(ml=MOST, wsb=0) == WS
     assert size(1, 1, 1, 1, 128, MOST) > 4 * MOST
+
+
+def test_compact_counts_positions_of_the_mass(lib):
+    """Zeroing the mass behind the kept rows steps up to 1,024 positions at a time up to the
+    length, which mass_len bounds."""
+    base = dict(k=256, v=512, ks=12288, vs=16384, bt=1024, maxp=1 << 27, cl=1280, keep=1536, n=8,
+                new=1792, m=2048, ml=128, B=1, hkv=1, d=128, P=16, ps=16, dt=tl.TL_INT8, err=None,
+                st=None)
+    c = caller(lib.tl_kv_cache_compact,
+               "k v bt maxp cl keep n new m ml B hkv d P ps dt err st", base)
+    i = caller(lib.tl_kv_cache_compact_int8,
+               "k v ks vs bt maxp cl keep n new m ml B hkv d P ps err st", base)
+    for ml in (2**31 - 1, 2**31 - 1024, MOST + 1):
+        assert c(ml=ml, dt=tl.TL_BF16) == UNS and i(ml=ml) == UNS, ml
+    # at the limit, and without a mass whatever the number, the checks pass: the launch itself
+    # fails here, where there is no GPU
+    if not torch.cuda.is_available():
+        assert i(ml=MOST) == tl.TL_ERR_CUDA and i(m=None, ml=2**31 - 1) == tl.TL_ERR_CUDA
