@@ -81,7 +81,8 @@ typedef enum {
 /* Bits OR-ed into *error_word by the device-side checks. */
 #define TL_DEVERR_SLOT_RANGE 1u    /* a slot outside [0, num_pages*page_size), not -1 */
 #define TL_DEVERR_PAGE_RANGE 2u    /* a needed block-table entry outside [0, num_pages) */
-#define TL_DEVERR_CONTEXT_RANGE 4u /* a length / position past max_pages_per_seq*page_size */
+#define TL_DEVERR_CONTEXT_RANGE 4u /* a length / position past max_pages_per_seq*page_size
+                                      (decode: or past 2^31 - 64) */
 #define TL_DEVERR_TIMEOUT 8u       /* an internal pipeline wait gave up (outputs invalid) */
 #define TL_DEVERR_VALUE_RANGE 16u  /* a finite value beyond fp16's +-65504 where the path rounds to
                                       fp16: V in prefill, q in decode over e4m3 or int8 pools

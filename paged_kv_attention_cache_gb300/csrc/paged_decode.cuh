@@ -209,6 +209,10 @@ __device__ __forceinline__ int32_t table_entry(const DecodeParams& P, int b, int
   return __ldg(P.block_table + row * P.max_pages_per_seq + e);
 }
 
+// Positions are 32-bit numbers, and a stage's last chunk may end 31 behind the
+// last key: the longest sequence leaves room for it.
+constexpr int kMaxLength = INT32_MAX - 63;
+
 // Key range of sequence b: lo..p, the union over its q_len queries (the last
 // at position p = L - 1, the first at L - q_len); empty when L <= 0 or L is
 // past the table.
@@ -216,7 +220,8 @@ __device__ __forceinline__ void seq_range(const DecodeParams& P, int b, int& lo,
                                           bool report_errors) {
   const int L = P.context_lens[b];
   p = L - 1;
-  if (P.ring_pages == 0 && L > P.key_cap) {  // a ring's positions are not bounded by its width
+  // (a ring's positions are not bounded by its width)
+  if (L > kMaxLength || (P.ring_pages == 0 && L > P.key_cap)) {
     if (report_errors) report(P.error_word, TL_DEVERR_CONTEXT_RANGE);
     p = -1;
   }
