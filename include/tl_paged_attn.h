@@ -819,6 +819,8 @@ tl_status tl_paged_attn_decode_mass_int8(const void* q, const int8_t* k_codes,
  *   keep      [B][h_kv][n_keep] int32: the positions in ascending order, then -1
  *   new_lens  [B] int32: min(L, n_keep), 0 for L <= 0
  *   keep_first + keep_last <= n_keep
+ * Neither output may overlap the other or an input (new_lens is not
+ * context_lens in place): TL_ERR_INVALID_ARG.
  * Supported: mass_len and n_keep up to 2^30, B*h_kv < 2^28.  Otherwise
  * TL_ERR_UNSUPPORTED.
  */

@@ -267,6 +267,15 @@ extern "C" tl_status tl_kv_evict_select(const float* mass, int32_t mass_len,
     return TL_ERR_INVALID_ARG;
   if ((int64_t)B * h_kv > INT32_MAX / 8 || mass_len > (1 << 30) || n_keep > (1 << 30))
     return TL_ERR_UNSUPPORTED;
+  // a row's CTAs read the lengths and masses while others write: in place, a
+  // head could see the length that another one's CTA has already cut
+  const size_t rows_bytes = sizeof(int32_t) * (size_t)B * h_kv, lens_bytes = sizeof(int32_t) * (size_t)B;
+  if (overlap(new_lens, lens_bytes, context_lens, lens_bytes) ||
+      overlap(keep, rows_bytes * n_keep, context_lens, lens_bytes) ||
+      overlap(keep, rows_bytes * n_keep, new_lens, lens_bytes) ||
+      overlap(keep, rows_bytes * n_keep, mass, rows_bytes * mass_len) ||
+      overlap(new_lens, lens_bytes, mass, rows_bytes * mass_len))
+    return TL_ERR_INVALID_ARG;
   EvictParams P;
   P.mass = mass;
   P.context_lens = context_lens;

@@ -1,0 +1,46 @@
+"""Outputs that overlap what other blocks of the same launch still read: refused before any launch
+(no GPU; made-up addresses that no kernel ever sees)."""
+import pytest
+import torch
+
+import paged_kv_attention_cache_gb300 as tl
+from paged_kv_attention_cache_gb300 import _lib, build
+
+BAD = tl.TL_ERR_INVALID_ARG
+
+
+@pytest.fixture(scope="module")
+def lib():
+    build.build()
+    return _lib.load()
+
+
+def caller(fn, order, base):
+    def call(**kw):
+        assert set(kw) <= set(base), kw
+        a = dict(base, **kw)
+        return fn(*(a[n] for n in order.split()))
+    return call
+
+
+def passes(status):
+    """All checks passed; the launch itself fails where there is no GPU."""
+    return status == tl.TL_ERR_CUDA
+
+
+def test_evict_select_is_not_in_place(lib):
+    """Each head's CTAs read the sequence's length; one of them writes the new one."""
+    M = 1 << 20
+    base = dict(m=1 * M, ml=100, cl=2 * M, n=8, first=1, last=2, keep=3 * M, new=4 * M, B=4, hkv=2,
+                err=None, st=None)
+    e = caller(lib.tl_kv_evict_select, "m ml cl n first last keep new B hkv err st", base)
+    mass, keep, lens = 4 * 4 * 2 * 100, 4 * 4 * 2 * 8, 4 * 4
+    assert e(new=base["cl"]) == BAD
+    assert e(cl=4 * M + 12) == BAD and e(cl=4 * M - 12) == BAD  # one element in common
+    assert e(keep=2 * M) == BAD and e(keep=2 * M - keep + 16) == BAD
+    assert e(keep=4 * M) == BAD and e(new=3 * M + keep - 16) == BAD
+    assert e(keep=1 * M) == BAD and e(keep=1 * M + mass - 16) == BAD and e(new=1 * M + 64) == BAD
+    if not torch.cuda.is_available():
+        for kw in (dict(), dict(cl=4 * M + lens), dict(cl=4 * M - lens), dict(new=3 * M + keep),
+                   dict(keep=1 * M + mass), dict(keep=2 * M - keep)):
+            assert passes(e(**kw)), kw
