@@ -727,6 +727,8 @@ size_t tl_kv_page_select_workspace_size(int32_t B, int32_t h_q, int32_t h_kv, in
  *   page_lens     [B] int32: the keys they hold (the last block, always
  *                 selected, may be part full); 0 for a sequence of length <= 0
  *                 or longer than its table (TL_DEVERR_CONTEXT_RANGE)
+ *   Neither output may overlap the other, context_lens, block_table or the
+ *   workspace (page_lens is not context_lens in place): TL_ERR_INVALID_ARG.
  *   keep_last     at least 1; keep_first + keep_last <= n_select
  *   workspace     tl_kv_page_select_workspace_size bytes, 256-byte aligned;
  *                 calls that overlap in time must not share one

@@ -989,6 +989,20 @@ extern "C" tl_status tl_kv_page_select(const void* q, tl_dtype q_dtype, const in
   if (!workspace || (reinterpret_cast<uintptr_t>(workspace) & 255u) ||
       workspace_bytes < tl_kv_page_select_workspace_size(B, h_q, h_kv, d, max_pages_per_seq))
     return TL_ERR_WORKSPACE;
+  // the selection's CTAs read lengths, tables and scores while others write: in
+  // place, a head could see the length that another one's CTA has already cut
+  const struct {
+    const void* p;
+    size_t bytes;
+  } outs[] = {{page_table, sizeof(int32_t) * (size_t)B * h_kv * n_select},
+              {page_lens, sizeof(int32_t) * (size_t)B}},
+    read[] = {{context_lens, sizeof(int32_t) * (size_t)B},
+              {block_table, sizeof(int32_t) * (size_t)B * max_pages_per_seq},
+              {workspace, tl_kv_page_select_workspace_size(B, h_q, h_kv, d, max_pages_per_seq)}};
+  for (const auto& o : outs)
+    for (const auto& r : read)
+      if (overlap(o.p, o.bytes, r.p, r.bytes)) return TL_ERR_INVALID_ARG;
+  if (overlap(page_table, outs[0].bytes, page_lens, outs[1].bytes)) return TL_ERR_INVALID_ARG;
   cudaStream_t st = (cudaStream_t)stream;
   ScoreParams S;
   S.q = q;

@@ -44,3 +44,23 @@ def test_evict_select_is_not_in_place(lib):
         for kw in (dict(), dict(cl=4 * M + lens), dict(cl=4 * M - lens), dict(new=3 * M + keep),
                    dict(keep=1 * M + mass), dict(keep=2 * M - keep)):
             assert passes(e(**kw)), kw
+
+
+def test_page_select_is_not_in_place(lib):
+    M = 1 << 20
+    base = dict(q=1 * M, qd=tl.TL_BF16, bnd=2 * M, sc=3 * M, bt=4 * M, maxp=8, cl=5 * M, n=4,
+                first=1, last=1, pt=6 * M, pl=7 * M, B=4, hq=8, hkv=2, d=128, P=16, ps=16,
+                ws=8 * M, wsb=1 << 18, err=None, st=None)
+    s = caller(lib.tl_kv_page_select,
+               "q qd bnd sc bt maxp cl n first last pt pl B hq hkv d P ps ws wsb err st", base)
+    table, block, lens = 4 * 4 * 2 * 4, 4 * 4 * 8, 4 * 4
+    need = tl.tl_kv_page_select_workspace_size(4, 8, 2, 128, 8)
+    assert s(pl=base["cl"]) == BAD and s(cl=7 * M - 4) == BAD and s(cl=7 * M + 12) == BAD
+    assert s(pt=base["bt"]) == BAD and s(bt=6 * M + table - 4) == BAD
+    assert s(pt=5 * M) == BAD and s(pl=4 * M + block - 16) == BAD
+    assert s(pt=8 * M) == BAD and s(pl=8 * M + need - 16) == BAD
+    assert s(pl=6 * M) == BAD and s(pl=6 * M + table - 16) == BAD
+    if not torch.cuda.is_available():
+        for kw in (dict(), dict(cl=7 * M + lens), dict(bt=6 * M + table), dict(pl=6 * M + table),
+                   dict(pt=4 * M + block), dict(pl=8 * M + need)):
+            assert passes(s(**kw)), kw
