@@ -1340,28 +1340,72 @@ __global__ void __launch_bounds__(DecodeShape<TWO_ROWS, KV8>::kWarps * 32, 1)
     const int pr1 = it.p - (P.q_len - 1 - rb / P.group);
     const int lr0 = (P.window > 0 && pr0 - P.window + 1 > 0) ? pr0 - P.window + 1 : 0;
     const int lr1 = (P.window > 0 && pr1 - P.window + 1 > 0) ? pr1 - P.window + 1 : 0;
-    // EX, int8: what P' = p x V scale is multiplied by before it is split into
-    // fp16 parts, a power of two (0: no live key yet).  The largest scale so
-    // far lies in [32, 64) after it, so that neither part falls below fp16's
-    // normal range (outputs within 5 x 10^-7 of exact; 2-5 x 10^-6 without) and
-    // p, at most 2^kLazyLog2, does not pass its largest value, whatever the
-    // pool's scales; 2% of a call, 5% with 16 rows.
+    // EX, int8: the power of two that rows ra's and rb's P' = p x V scale is
+    // multiplied by before it is split into fp16 parts, and O carries until the
+    // item's end.  It goes by the row's largest product, not by the scales: a
+    // key's scale counts only as far as its weight does.  It starts at 2^126;
+    // when a product passes kFitMost it is lowered so that the row's largest so
+    // far comes to [2^8, 2^10) (and O by as much), and when the softmax base
+    // moves, and with it every earlier product, it is raised by the same power.
+    // A part is off by at most 2^-25 then, against a largest product of 2^8 or
+    // more: 2^-33 of it per key, whatever the pool's scales (below 2^-118 the
+    // factor ends at 2^126).  A fit to the largest scale alone, shared by the
+    // rows, took 0.1-3.5% less of a call (64 sequences of 2,048-8,192 keys, 32
+    // query and 8 KV heads: 70.6 and 70.7 us over 128 pages, 153.1 and 154.1
+    // with weights, 281.1 and 283.7 with 4 tokens) and lost a row whose weight
+    // lies on keys of small scale: 10^-4 of it at scales 2^16 apart.
     constexpr bool kFitV = I8 && EX != 0;
-    [[maybe_unused]] float vfit = 0.f, vlim = 0.f;
-    [[maybe_unused]] auto fit_v = [&](float big) {  // big: the largest scale of this lane's live keys
-      if (!__any_sync(0xffffffffu, big > vlim)) return;
-      const uint32_t most = __reduce_max_sync(0xffffffffu, __float_as_uint(big));
-      const int e = min(5 - ((int)(most >> 23) - 127), 126);  // at least -122
-      const float f = __uint_as_float((uint32_t)(e + 127) << 23);
-      if (vfit > 0.f) {
-        const float r = f / vfit;
+    constexpr float kFitMost = 32768.f;  // fp16 ends at 65,504
+    [[maybe_unused]] float fit0 = __uint_as_float(253u << 23), fit1 = fit0;
+    // rescales O by r0 in the row of ra and by r1 in that of rb
+    [[maybe_unused]] auto rescale = [&](float r0, float r1) {
 #pragma unroll
-        for (int n = 0; n < NO; ++n)
-#pragma unroll
-          for (int x = 0; x < 4; ++x) o[n][x] *= r;
+      for (int n = 0; n < NO; ++n) {
+        o[n][0] *= r0;
+        o[n][1] *= KT ? r1 : r0;
+        o[n][2] *= KT ? r0 : r1;
+        o[n][3] *= r1;
       }
-      vfit = f;
-      vlim = 64.f / f;
+    };
+    // p x (V scale x fit); 0 stays 0 where the second product is infinite, and
+    // a NaN of a row is that row's alone
+    [[maybe_unused]] auto weigh = [](float p, float v_fit) { return p > 0.f ? p * v_fit : p; };
+    // exponent of p x v, at most (denormal values count as 2^-127)
+    [[maybe_unused]] auto product_exp = [](float p, float v) {
+      return p > 0.f && v > 0.f
+                 ? (int)(__float_as_uint(p) >> 23) + (int)(__float_as_uint(v) >> 23) - 254
+                 : -1000;
+    };
+    // The fits of the rows whose largest P' of the chunk passes kFitMost (a row's
+    // fit depends on nothing of the others), lowered.  Given: this lane's largest
+    // P' and exponent in each row.
+    [[maybe_unused]] auto lower_fits = [&](float most0, float most1, int e0, int e1) {
+#pragma unroll
+      for (int x = KT ? 4 : 1; x < (KT ? 32 : 4); x <<= 1) {
+        most0 = fmaxf(most0, __shfl_xor_sync(0xffffffffu, most0, x));
+        most1 = fmaxf(most1, __shfl_xor_sync(0xffffffffu, most1, x));
+        e0 = max(e0, __shfl_xor_sync(0xffffffffu, e0, x));
+        e1 = max(e1, __shfl_xor_sync(0xffffffffu, e1, x));
+      }
+      const float n0 =
+          most0 > kFitMost ? __uint_as_float((uint32_t)(max(min(8 - e0, 126), -126) + 127) << 23)
+                           : fit0;
+      const float n1 =
+          most1 > kFitMost ? __uint_as_float((uint32_t)(max(min(8 - e1, 126), -126) + 127) << 23)
+                           : fit1;
+      // (1 / fit: the exponent's mirror)
+      rescale(n0 * __uint_as_float((254u << 23) - __float_as_uint(fit0)),
+              n1 * __uint_as_float((254u << 23) - __float_as_uint(fit1)));
+      fit0 = n0;
+      fit1 = n1;
+    };
+    // the fit for products that shrank by f in [0, 1]: raised by 2^k, f x 2^k in
+    // [1, 2); f is multiplied by what it was raised by
+    [[maybe_unused]] auto raise_fit = [](float& fit, float& f) {
+      const uint32_t was = __float_as_uint(fit) >> 23;
+      const uint32_t now = min(was + 127u - (__float_as_uint(f) >> 23), 253u);
+      fit = __uint_as_float(now << 23);
+      f *= __uint_as_float((now - was + 127u) << 23);
     };
     // EX: the score rows of rows ra and rb (null: none, or not this lane's)
     float *srow0 = nullptr, *srow1 = nullptr;
@@ -1561,13 +1605,12 @@ __global__ void __launch_bounds__(DecodeShape<TWO_ROWS, KV8>::kWarps * 32, 1)
         l0 = l0 * f0 + sum0;
         l1 = l1 * f1 + sum1;
         if (__any_sync(0xffffffffu, f0 != 1.f || f1 != 1.f)) {
-#pragma unroll
-          for (int n = 0; n < NO; ++n) {
-            o[n][0] *= f0;
-            o[n][1] *= f1;
-            o[n][2] *= f0;
-            o[n][3] *= f1;
+          float r0 = f0, r1 = f1;
+          if constexpr (kFitV) {
+            raise_fit(fit0, r0);
+            raise_fit(fit1, r1);
           }
+          rescale(r0, r1);
         }
       }
 #pragma unroll
@@ -1586,17 +1629,29 @@ __global__ void __launch_bounds__(DecodeShape<TWO_ROWS, KV8>::kWarps * 32, 1)
           v0 = fminf(fmaxf(v0, 0.f), 3.0e38f);
           v1 = fminf(fmaxf(v1, 0.f), 3.0e38f);
           if constexpr (kFitV) {
-            // (a NaN of one row is not to hide another row's weight)
-            v0 = p[jc][0] > 0.f || p[jc][1] > 0.f ? v0 : 0.f;
-            v1 = p[jc][2] > 0.f || p[jc][3] > 0.f ? v1 : 0.f;
-            fit_v(fmaxf(v0, v1));
-            v0 *= vfit;
-            v1 *= vfit;
+            float x[4];
+            auto weigh_all = [&]() {
+              x[0] = weigh(p[jc][0], v0 * fit0);
+              x[1] = weigh(p[jc][1], v0 * fit1);
+              x[2] = weigh(p[jc][2], v1 * fit0);
+              x[3] = weigh(p[jc][3], v1 * fit1);
+            };
+            weigh_all();
+            const float most0 = fmaxf(x[0], x[2]), most1 = fmaxf(x[1], x[3]);
+            if (__any_sync(0xffffffffu, fmaxf(most0, most1) > kFitMost)) {
+              lower_fits(most0, most1,
+                         max(product_exp(p[jc][0], v0), product_exp(p[jc][2], v1)),
+                         max(product_exp(p[jc][1], v0), product_exp(p[jc][3], v1)));
+              weigh_all();
+            }
+#pragma unroll
+            for (int e = 0; e < 4; ++e) p[jc][e] = x[e];
+          } else {
+            p[jc][0] *= v0;
+            p[jc][1] *= v0;
+            p[jc][2] *= v1;
+            p[jc][3] *= v1;
           }
-          p[jc][0] *= v0;
-          p[jc][1] *= v0;
-          p[jc][2] *= v1;
-          p[jc][3] *= v1;
         }
         // P^T as the B operand: the fp16 pairs (columns 2t, 2t + 1) of keys g
         // and g + 8 form the 8 x 8 blocks P^T[keys 0-7] and P^T[keys 8-15];
@@ -1863,13 +1918,12 @@ __global__ void __launch_bounds__(DecodeShape<TWO_ROWS, KV8>::kWarps * 32, 1)
           // rows 8-15 hold either the second half of the group (TWO_ROWS) or
           // the low part of rows 0-7's probabilities; both rescale with their row
           if (__any_sync(0xffffffffu, c0 != 1.f || c1 != 1.f)) {
-  #pragma unroll
-            for (int n = 0; n < D / 8; ++n) {
-              o[n][0] *= c0;
-              o[n][1] *= c0;
-              o[n][2] *= c1;
-              o[n][3] *= c1;
+            float r0 = c0, r1 = c1;
+            if constexpr (kFitV) {
+              raise_fit(fit0, r0);
+              raise_fit(fit1, r1);
             }
+            rescale(r0, r1);
           }
         }
   #pragma unroll
@@ -1887,30 +1941,55 @@ __global__ void __launch_bounds__(DecodeShape<TWO_ROWS, KV8>::kWarps * 32, 1)
                            : "=f"(v[n][0]), "=f"(v[n][1])
                            : "r"(scale_ring + stage * L::kScaleBytes +
                                  ((CPS + sub0 + jc) * kChunk + n * 8 + qc) * 4));
-            if constexpr (kFitV) {
-              float big = 0.f;
+            if constexpr (kFitV) {  // int8 rows-as-rows are two rows a lane
+              float x[2][4], most0 = 0.f, most1 = 0.f;
+              auto weigh_all = [&]() {
+  #pragma unroll
+                for (int n = 0; n < 2; ++n)
+  #pragma unroll
+                  for (int e = 0; e < 2; ++e) {
+                    x[n][e] = weigh(p[jc][n][e], v[n][e] * fit0);
+                    x[n][2 + e] = weigh(p[jc][n][2 + e], v[n][e] * fit1);
+                  }
+              };
+  #pragma unroll
+              for (int n = 0; n < 2; ++n)
+  #pragma unroll
+                for (int e = 0; e < 2; ++e) v[n][e] = fminf(fmaxf(v[n][e], 0.f), 3.0e38f);
+              weigh_all();
   #pragma unroll
               for (int n = 0; n < 2; ++n)
   #pragma unroll
                 for (int e = 0; e < 2; ++e) {
-                  v[n][e] = fminf(fmaxf(v[n][e], 0.f), 3.0e38f);
-                  if (p[jc][n][e] > 0.f || (TWO_ROWS && p[jc][n][2 + e] > 0.f))
-                    big = fmaxf(big, v[n][e]);
+                  most0 = fmaxf(most0, x[n][e]);
+                  most1 = fmaxf(most1, x[n][2 + e]);
                 }
-              fit_v(big);
+              if (__any_sync(0xffffffffu, fmaxf(most0, most1) > kFitMost)) {
+                int e0 = -1000, e1 = -1000;
+  #pragma unroll
+                for (int n = 0; n < 2; ++n)
+  #pragma unroll
+                  for (int e = 0; e < 2; ++e) {
+                    e0 = max(e0, product_exp(p[jc][n][e], v[n][e]));
+                    e1 = max(e1, product_exp(p[jc][n][2 + e], v[n][e]));
+                  }
+                lower_fits(most0, most1, e0, e1);
+                weigh_all();
+              }
   #pragma unroll
               for (int n = 0; n < 2; ++n)
   #pragma unroll
-                for (int e = 0; e < 2; ++e) v[n][e] *= vfit;
-            }
+                for (int e = 0; e < 4; ++e) p[jc][n][e] = x[n][e];
+            } else {
   #pragma unroll
-            for (int n = 0; n < 2; ++n) {
-              const float v0 = v[n][0], v1 = v[n][1];
-              p[jc][n][0] = p[jc][n][0] > 0.f ? p[jc][n][0] * v0 : 0.f;
-              p[jc][n][1] = p[jc][n][1] > 0.f ? p[jc][n][1] * v1 : 0.f;
-              if (TWO_ROWS) {
-                p[jc][n][2] = p[jc][n][2] > 0.f ? p[jc][n][2] * v0 : 0.f;
-                p[jc][n][3] = p[jc][n][3] > 0.f ? p[jc][n][3] * v1 : 0.f;
+              for (int n = 0; n < 2; ++n) {
+                const float v0 = v[n][0], v1 = v[n][1];
+                p[jc][n][0] = p[jc][n][0] > 0.f ? p[jc][n][0] * v0 : 0.f;
+                p[jc][n][1] = p[jc][n][1] > 0.f ? p[jc][n][1] * v1 : 0.f;
+                if (TWO_ROWS) {
+                  p[jc][n][2] = p[jc][n][2] > 0.f ? p[jc][n][2] * v0 : 0.f;
+                  p[jc][n][3] = p[jc][n][3] > 0.f ? p[jc][n][3] * v1 : 0.f;
+                }
               }
             }
           }
@@ -2031,8 +2110,9 @@ __global__ void __launch_bounds__(DecodeShape<TWO_ROWS, KV8>::kWarps * 32, 1)
     }
     if (stop) break;
     // ------------------------------------------------------ finish the item
-    float unfit = 1.f;
-    if constexpr (kFitV) unfit = vfit > 0.f ? 1.f / vfit : 1.f;
+    if constexpr (kFitV)
+      rescale(__uint_as_float((254u << 23) - __float_as_uint(fit0)),
+              __uint_as_float((254u << 23) - __float_as_uint(fit1)));
     if constexpr (KT) {
       // a column's sum spans the 8 lanes of one t; with dup, the low parts
       // (columns 4-7, lanes t = 2, 3) join their rows (lanes t - 2)
@@ -2065,8 +2145,8 @@ __global__ void __launch_bounds__(DecodeShape<TWO_ROWS, KV8>::kWarps * 32, 1)
       };
       if (it.nsplits == 1) {
         const float i0 = l0 > 0.f ? 1.f / l0 : 0.f, i1 = l1 > 0.f ? 1.f / l1 : 0.f;
-        if (live0) write_col(P.out + ((size_t)it.b * P.hq_all + h0r) * D, 0, i0 * unfit, false, 0);
-        if (live1) write_col(P.out + ((size_t)it.b * P.hq_all + h1r) * D, 1, i1 * unfit, false, 0);
+        if (live0) write_col(P.out + ((size_t)it.b * P.hq_all + h0r) * D, 0, i0, false, 0);
+        if (live1) write_col(P.out + ((size_t)it.b * P.hq_all + h1r) * D, 1, i1, false, 0);
         if constexpr (EX) {
           float2* st = reinterpret_cast<float2*>(P.stats) + (size_t)it.b * P.hq_all;
           if (P.stats && live0 && qr == 0) st[h0r] = make_float2(m0, l0);
@@ -2076,12 +2156,12 @@ __global__ void __launch_bounds__(DecodeShape<TWO_ROWS, KV8>::kWarps * 32, 1)
         const uint64_t keep = l2_evict_last();
         if (live0) {
           const size_t rowi = (size_t)it.s_global * P.hq_all + h0r;
-          write_col(P.ws.acc + rowi * D, 0, unfit, true, keep);
+          write_col(P.ws.acc + rowi * D, 0, 1.f, true, keep);
           if (qr == 0) st_f32x2_hint(P.ws.ml + rowi * 2, m0, l0, keep);
         }
         if (live1) {
           const size_t rowi = (size_t)it.s_global * P.hq_all + h1r;
-          write_col(P.ws.acc + rowi * D, 1, unfit, true, keep);
+          write_col(P.ws.acc + rowi * D, 1, 1.f, true, keep);
           if (qr == 0) st_f32x2_hint(P.ws.ml + rowi * 2, m1, l1, keep);
         }
       }
@@ -2132,10 +2212,9 @@ __global__ void __launch_bounds__(DecodeShape<TWO_ROWS, KV8>::kWarps * 32, 1)
       };
       if (single) {
         const float i0 = l0 > 0.f ? 1.f / l0 : 0.f, i1 = l1 > 0.f ? 1.f / l1 : 0.f;
-        if (qr < P.rows)
-          write_row(P.out + ((size_t)it.b * P.hq_all + h0r) * D, false, i0 * unfit, false, 0);
+        if (qr < P.rows) write_row(P.out + ((size_t)it.b * P.hq_all + h0r) * D, false, i0, false, 0);
         if (TWO_ROWS && qr + 8 < P.rows)
-          write_row(P.out + ((size_t)it.b * P.hq_all + h1r) * D, true, i1 * unfit, false, 0);
+          write_row(P.out + ((size_t)it.b * P.hq_all + h1r) * D, true, i1, false, 0);
         if constexpr (EX) {
           float2* st = reinterpret_cast<float2*>(P.stats) + (size_t)it.b * P.hq_all;
           if (P.stats && qr < P.rows && (lane & 3) == 0) st[h0r] = make_float2(m0, l0);
@@ -2147,12 +2226,12 @@ __global__ void __launch_bounds__(DecodeShape<TWO_ROWS, KV8>::kWarps * 32, 1)
         const uint64_t keep = l2_evict_last();
         if (qr < P.rows) {
           const size_t rowi = (size_t)it.s_global * P.hq_all + h0r;
-          write_row(P.ws.acc + rowi * D, false, unfit, true, keep);
+          write_row(P.ws.acc + rowi * D, false, 1.f, true, keep);
           if ((lane & 3) == 0) st_f32x2_hint(P.ws.ml + rowi * 2, m0, l0, keep);
         }
         if (TWO_ROWS && qr + 8 < P.rows) {
           const size_t rowi = (size_t)it.s_global * P.hq_all + h1r;
-          write_row(P.ws.acc + rowi * D, true, unfit, true, keep);
+          write_row(P.ws.acc + rowi * D, true, 1.f, true, keep);
           if ((lane & 3) == 0) st_f32x2_hint(P.ws.ml + rowi * 2, m1, l1, keep);
         }
       }
