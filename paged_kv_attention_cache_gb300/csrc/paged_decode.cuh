@@ -179,10 +179,10 @@ struct DecodeParams {
   // log2 units, [B][H_kv][rows][score_stride] by key position (-inf where a
   // row does not see a key of the pieces' chunks).  stats: each output row's
   // running max (log2 units) and sum, [B][hq_all][2].
-  // self_plan: no plan launch; every attention CTA derives the pieces itself
-  // (at most self_plan_max sequences).
+  // target_splits: of the form without a plan launch, whose CTAs derive the
+  // pieces themselves.
   int32_t head_tables;
-  int32_t self_plan, target_splits;
+  int32_t target_splits;
   float* scores;
   int64_t score_stride;
   float* stats;
@@ -395,18 +395,34 @@ constexpr int kMaxChunks = 1 << 27;  // of a sequence: 2^31 keys
 constexpr int kWarpPlanMax = 128;
 constexpr int kWriteWarps = 8;  // writing warps per CTA of a warp-planned launch
 
-// Sequences up to which an EX call has no plan launch: its CTAs plan for
-// themselves and each warp takes one piece (two past 32 sequences), all of one
-// size.  It saves a launch and its 4-5 us and gives every warp work where there
-// is little; a long batch is dealt more evenly by the plan's counter and its
-// round of small pieces.  Measured without / with the plan's launch (us a call,
-// 32 query and 8 KV heads of 128): 128 selected pages of 1, 4, 16, 32, 64
-// sequences 11.6 / 19.5, 14.3 / 20.8, 29.7 / 33.2, 51.0 / 53.5, 95.0 / 93.7;
-// weight-gathering over whole bf16 contexts of 2,048-8,192 keys of 1, 8, 16,
-// 32, 64 sequences 17.3 / 23.6, 39.3 / 42.7, 66.3 / 69.3, 125 / 122, 254 / 234;
-// e4m3 contexts 18.1 / 24.1, 27.1 / 36.5, 40.5 / 54.2, 71.5 / 84.1 and, in two
-// rounds, 136 / 145.
+// An EX call of few sequences has no plan launch: its CTAs plan for themselves
+// and each warp takes one piece (two past 32 sequences), all of one size.  It
+// saves a launch and its 4-5 us and gives every warp work where there is
+// little; a long batch is dealt more evenly by the plan's counter and its round
+// of small pieces, the sooner the more KV heads there are to deal.  Measured
+// without / with the plan's launch (us a call, 32 query and 8 KV heads of 128,
+// sequences of 2,048-8,192 keys):
+//                           1          16          32          48          64
+// 128 pages, bf16   11.6/20.0   30.2/32.8   51.1/53.1   72.4/73.4   96.2/91.9
+// weights, bf16     19.2/25.2   66.8/71.0   125.4/122.7 182.5/177.1 241.2/233.9
+//   4 tokens        22.7/30.6   79.2/100.8  149.6/165.3 224.3/232.0 298.4/298.3
+// 128 pages, e4m3   12.1/19.7   23.7/29.5   38.9/43.4   54.8/60.0   68.2/69.4
+// weights, e4m3     19.6/24.9   43.1/55.0   73.3/84.3   102.2/113.6 135.3/146.4
+//   4 tokens        21.9/29.2   62.5/91.8   111.5/140.4 168.2/181.1 221.5/223.3
+// 128 pages, int8   13.1/25.7   25.4/32.4   38.9/47.7   57.7/69.3   70.8/78.1
+// weights, int8     21.6/31.0   50.3/65.4   86.9/99.1   118.8/139.3 153.9/176.8
+//   4 tokens        24.6/33.6   79.0/119.9  145.2/184.8 215.4/238.4 283.7/291.7
+// and over 16 heads of one query head: 128 pages, bf16, 16 sequences 50.8/52.5
+// and 32 91.4/90.7; weights, bf16, 117.1/118.0 and 230.5/218.5, e4m3 67.0/78.3
+// and 121.5/127.7, int8 80.2/92.8 and 156.3/149.8; over 2 heads without is
+// faster throughout (weights, bf16, 32 sequences 39.9/45.5).
 __host__ __device__ constexpr int self_plan_max(bool one_byte) { return one_byte ? 64 : 32; }
+static inline bool plans_itself(bool one_byte, bool weights, int rows, int B, int h_kv) {
+  if (B > self_plan_max(one_byte)) return false;
+  // 16-bit pools: sequences x heads up to which it is faster (weights in up to
+  // 8 rows: 24 x 8, not 32 x 8; else 32 x 8, not 32 x 16)
+  return one_byte || (int64_t)B * h_kv <= (weights && rows <= 8 ? 192 : 256);
+}
 constexpr int kOneRoundSeqs = 32;
 constexpr int kOneRoundMin = 2;  // chunks of a piece; 1 measured no faster
 
@@ -2806,8 +2822,10 @@ static tl_status decode_impl(const void* q, const void* k_cache, const void* v_c
   const int64_t write_ctas =
       P.n_new > 0 ? std::min<int64_t>(num_sms(), (write_warps + wpc - 1) / wpc) : 0;
   P.target_splits = target_splits;
-  P.self_plan = EX && dtype != TL_F32 && B <= self_plan_max(kv8) ? 1 : 0;
-  if (!P.self_plan) {
+  const bool self_plan =
+      EX && dtype != TL_F32 && plans_itself(kv8, ex.mass != nullptr, rows, B, h_kv) &&
+      warps * 32 >= B;  // a CTA's thread reads a sequence's length each
+  if (!self_plan) {
     decode_plan_kernel<<<(unsigned)(1 + write_ctas), plan_threads, 0, st>>>(P, target_splits,
                                                                             num_sms() * warps);
     if (launch_status() != TL_OK) return TL_ERR_CUDA;
@@ -2831,7 +2849,7 @@ static tl_status decode_impl(const void* q, const void* k_cache, const void* v_c
   do {                                                                                    \
     auto kern = decode_bf16_kernel<DD, TWO, K8, I8V, EX ? 1 : 0>;                         \
     if constexpr (EX)                                                                     \
-      if (P.self_plan) kern = decode_bf16_kernel<DD, TWO, K8, I8V, 2>;                    \
+      if (self_plan) kern = decode_bf16_kernel<DD, TWO, K8, I8V, 2>;                    \
     const int sm =                                                                        \
         warps * WarpSmem<DD, K8, I8V, DecodeShape<TWO, K8>::kRing>::warp_bytes(rows) + 1024; \
     if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize,           \
@@ -2846,7 +2864,7 @@ static tl_status decode_impl(const void* q, const void* k_cache, const void* v_c
     cfg.dynamicSmemBytes = sm;                                                            \
     cfg.stream = st;                                                                      \
     cfg.attrs = attr;                                                                     \
-    cfg.numAttrs = P.self_plan ? 0 : 1; /* its predecessor is not the call's plan */      \
+    cfg.numAttrs = self_plan ? 0 : 1; /* its predecessor is not the call's plan */      \
     if (cudaLaunchKernelEx(&cfg, kern, P, kmap, vmap, box_rows) != cudaSuccess)           \
       return TL_ERR_CUDA;                                                                 \
   } while (0)
