@@ -304,6 +304,11 @@ TL_DEVINLINE uint32_t even_share(uint32_t n, uint32_t i, uint32_t shares) {
 }
 
 constexpr int kBoundsThreads = 256;
+// CTAs an SM holds at once (one-byte vectors are 16 channels a lane: 80
+// registers instead of 64).
+__host__ __device__ constexpr int bounds_ctas(int kind) {
+  return kind == kInt8 || kind == kE4m3 ? 3 : 4;
+}
 constexpr int kBoundsSeqs = 1024;  // sequences placed per round
 
 // Blocks first_new / page_size .. (L - 1) / page_size of every sequence,
@@ -311,12 +316,16 @@ constexpr int kBoundsSeqs = 1024;  // sequences placed per round
 // sequences' block counts into shared memory, and a warp finds the sequence
 // of its run by a binary search.  The batch may be ragged (a prompt among
 // decode steps): the work is even whatever the lengths, and the host needs to
-// know none of them.  Bound: HBM; one wave of CTAs, as many as an SM takes.
-// 8 prompts of 6,144-8,192 keys (125 MB, bf16, 8 KV heads of 128) take 24.5 us,
-// 5.1 TB/s; a decode step of 64 sequences, a page each, 4.9 us: a launch and
+// know none of them.  One wave of CTAs, as many as an SM takes.  8 prompts of
+// 6,144-8,192 keys (8 KV heads of 128) take 24.3 us in bf16 (125 MB, 5.1 TB/s)
+// and 42.5 in f32 (242 MB, 5.7 TB/s), bound by HBM; 36.1 in e4m3 (66 MB) and
+// 56.9 in int8 (68 MB), bound by the arithmetic: 16 conversions (int8: and
+// products with the key's scale) a lane and 16 bytes.  With a CTA an SM more
+// than fit, a second wave of a third, they took 41.0 and 67.3.  A decode step
+// of 64 sequences, a page each, takes 4.8 us (bf16) to 7.0 (int8): a launch and
 // three dependent reads.
 template <int D, int KIND>
-__global__ void __launch_bounds__(kBoundsThreads, KIND == kInt8 || KIND == kE4m3 ? 3 : 4) page_bounds_kernel(BoundsParams P) {
+__global__ void __launch_bounds__(kBoundsThreads, bounds_ctas(KIND)) page_bounds_kernel(BoundsParams P) {
   __shared__ int start[kBoundsSeqs + 1];  // first block of each sequence of the round
   __shared__ uint32_t tmp[32];
   const int tid = threadIdx.x, lane = tid & 31;
@@ -818,7 +827,7 @@ static tl_status bounds_impl(const void* k, const float* k_scales, const int32_t
   P.error_word = error_word;
   const int64_t most = ((int64_t)B * max_pages_per_seq * h_kv + kBoundsThreads / 32 - 1) /
                        (kBoundsThreads / 32);
-  const unsigned grid = (unsigned)std::min<int64_t>(most, (int64_t)num_sms() * 4);  // one wave
+  const unsigned grid = (unsigned)std::min<int64_t>(most, (int64_t)num_sms() * bounds_ctas(kind));  // one wave
   cudaStream_t st = (cudaStream_t)stream;
 #define TL_BOUNDS(K)                                                              \
   do {                                                                            \
