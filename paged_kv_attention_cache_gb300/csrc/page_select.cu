@@ -57,19 +57,6 @@ TL_DEVINLINE void widen_vec(const uint4& x, float scale, float* f) {
   }
 }
 
-// Four int8 codes as two fp16 pairs (codes 0, 1 and 2, 3), exact: a code c +
-// 128 as the low byte under the high byte 0x64 is the fp16 1024 + c + 128.
-// The biased form leaves the 1152 in.
-TL_DEVINLINE void i8x4_as_f16x2x2_biased(uint32_t w, uint32_t& lo, uint32_t& hi) {
-  const uint32_t u = w ^ 0x80808080u;
-  lo = __byte_perm(u, 0x64646464u, 0x4140u);
-  hi = __byte_perm(u, 0x64646464u, 0x4342u);
-}
-TL_DEVINLINE void i8x4_as_f16x2x2(uint32_t w, uint32_t& lo, uint32_t& hi) {
-  i8x4_as_f16x2x2_biased(w, lo, hi);
-  asm("sub.rn.f16x2 %0, %0, %1;\n" : "+r"(lo) : "r"(0x64806480u));
-  asm("sub.rn.f16x2 %0, %0, %1;\n" : "+r"(hi) : "r"(0x64806480u));
-}
 // D(16x8, s32) += A(16x32, s8, row) * B(32x8, s8, col)
 TL_DEVINLINE void mma_s8_16832(int* c, const uint32_t* a, const uint32_t* b) {
   asm("mma.sync.aligned.m16n8k32.row.col.s32.s8.s8.s32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, "
@@ -79,9 +66,11 @@ TL_DEVINLINE void mma_s8_16832(int* c, const uint32_t* a, const uint32_t* b) {
 }
 
 // round-half-even(x / s) as the f32 quotient rounds, clamped to +-127, for s >
-// 0 and |x / s| <= 128: the product with 1 / s is within 2 x 10^-5 of the
-// quotient, so it rounds alike unless it lies within 5 x 10^-4 of a half,
-// where (and for an s whose reciprocal is out of range) the division is done.
+// 0 and |x / s| <= 128: __fdividef is documented within 2 ulp (2^-22 of the
+// value) and the product adds half a one, 3 x 10^-7 together, so x * (1 / s) is
+// within 4 x 10^-5 of the quotient; it rounds alike unless it lies within 5 x
+// 10^-4 of a half, where (and for an s whose reciprocal is out of range) the
+// division is done.
 struct Quotient {
   float s, inv;
   bool fast;
