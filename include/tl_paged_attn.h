@@ -853,7 +853,8 @@ tl_status tl_kv_evict_select(const float* mass, int32_t mass_len, const int32_t*
  *                     TL_F32 or TL_FP8_E4M3; _int8: codes and scales), in place
  *   keep              [B][h_kv][n_keep] int32;  new_lens [B] int32
  *   mass              NULL, or [B][h_kv][mass_len] float32, in place
- * TL_ERR_INVALID_ARG when d * elem is not a multiple of 16 bytes;
+ * TL_ERR_INVALID_ARG when d * elem is not a multiple of 16 bytes, or when two of
+ * the pools, scales and mass overlap (keys and values in one pool);
  * TL_ERR_UNSUPPORTED past 4,096 bytes a row, page_size > 256,
  * num_pages*page_size >= 2^31, n_keep > 2^30 or (with a mass) mass_len > 2^30.
  */

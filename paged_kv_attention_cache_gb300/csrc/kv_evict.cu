@@ -209,6 +209,23 @@ static tl_status compact_impl(void* k, void* v, float* k_scales, float* v_scales
       (int64_t)num_pages * page_size >= ((int64_t)1 << 31) || (int64_t)B * h_kv > INT32_MAX ||
       n_keep > (1 << 30) || (mass && mass_len > (1 << 30)))
     return TL_ERR_UNSUPPORTED;
+  // each pool (and the mass) is moved by CTAs of its own: one buffer given for
+  // two of them would be moved twice at once
+  const size_t pool_bytes = (size_t)num_pages * page_size * h_kv * row_bytes;
+  const size_t scale_bytes = k_scales ? sizeof(float) * (size_t)num_pages * page_size * h_kv : 0;
+  const struct {
+    const void* p;
+    size_t bytes;
+  } moved[] = {{k, pool_bytes},
+               {v, pool_bytes},
+               {k_scales, scale_bytes},
+               {v_scales, scale_bytes},
+               {mass, mass ? sizeof(float) * (size_t)B * h_kv * mass_len : 0}};
+  for (int i = 0; i < 5; ++i)
+    for (int j = 0; j < i; ++j)
+      if (moved[i].bytes && moved[j].bytes &&
+          overlap(moved[i].p, moved[i].bytes, moved[j].p, moved[j].bytes))
+        return TL_ERR_INVALID_ARG;
   CompactParams P;
   P.pool[0] = k;
   P.pool[1] = v;

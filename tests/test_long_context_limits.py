@@ -58,9 +58,9 @@ def test_decode_mass_counts_positions(lib):
 def test_compact_counts_positions_of_the_mass(lib):
     """Zeroing the mass behind the kept rows steps up to 1,024 positions at a time up to the
     length, which mass_len bounds."""
-    base = dict(k=256, v=512, ks=12288, vs=16384, bt=1024, maxp=1 << 27, cl=1280, keep=1536, n=8,
-                new=1792, m=2048, ml=128, B=1, hkv=1, d=128, P=16, ps=16, dt=tl.TL_INT8, err=None,
-                st=None)
+    base = dict(k=1 << 20, v=1 << 21, ks=12288, vs=16384, bt=1024, maxp=1 << 27, cl=1280, keep=1536,
+                n=8, new=1792, m=1 << 22, ml=128, B=1, hkv=1, d=128, P=16, ps=16, dt=tl.TL_INT8,
+                err=None, st=None)
     c = caller(lib.tl_kv_cache_compact,
                "k v bt maxp cl keep n new m ml B hkv d P ps dt err st", base)
     i = caller(lib.tl_kv_cache_compact_int8,

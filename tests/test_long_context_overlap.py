@@ -64,3 +64,25 @@ def test_page_select_is_not_in_place(lib):
         for kw in (dict(), dict(cl=7 * M + lens), dict(bt=6 * M + table), dict(pl=6 * M + table),
                    dict(pt=4 * M + block), dict(pl=8 * M + need)):
             assert passes(s(**kw)), kw
+
+
+def test_compaction_moves_each_buffer_once(lib):
+    """K and V in one pool: two CTAs would gather the same rows at the same time."""
+    M = 1 << 20
+    base = dict(k=1 * M, v=2 * M, ks=3 * M, vs=4 * M, bt=5 * M, maxp=8, cl=6 * M, keep=7 * M, n=8,
+                new=8 * M, m=9 * M, ml=128, B=2, hkv=2, d=128, P=16, ps=16, dt=tl.TL_BF16,
+                err=None, st=None)
+    c = caller(lib.tl_kv_cache_compact,
+               "k v bt maxp cl keep n new m ml B hkv d P ps dt err st", base)
+    i = caller(lib.tl_kv_cache_compact_int8,
+               "k v ks vs bt maxp cl keep n new m ml B hkv d P ps err st", base)
+    slots = 16 * 16 * 2
+    assert c(v=1 * M) == BAD and c(v=1 * M + slots * 256 - 16) == BAD
+    assert i(v=1 * M) == BAD and i(v=1 * M + slots * 128 - 16) == BAD
+    assert i(vs=3 * M) == BAD and i(ks=4 * M + slots * 4 - 16) == BAD and i(ks=1 * M) == BAD
+    assert c(m=1 * M) == BAD and i(m=3 * M) == BAD
+    if not torch.cuda.is_available():
+        for call, kw in ((c, dict()), (i, dict()), (c, dict(v=1 * M + slots * 256)),
+                         (i, dict(v=1 * M + slots * 128)), (i, dict(vs=3 * M + slots * 4)),
+                         (c, dict(m=None)), (i, dict(m=None))):
+            assert passes(call(**kw)), kw
