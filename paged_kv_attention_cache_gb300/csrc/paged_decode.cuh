@@ -148,6 +148,7 @@ struct DecodeParams {
   const int32_t* context_lens;
   float* out;
   int32_t max_pages_per_seq;
+  int32_t key_cap;  // the longest sequence: the table's positions, or fewer (a ring: kMaxLength)
   int32_t B, h_q, h_kv, group, d;
   int32_t num_pages, page_size, window;
   int32_t ring_pages;  // > 0: the table's first ring_pages entries are a ring
@@ -172,8 +173,6 @@ struct DecodeParams {
   // int8 pools: the per-(slot, KV head) scales, [num_pages][H_kv][page_size]
   const float* k_scales;
   const float* v_scales;
-  // the longest sequence the call takes (the table's positions, or fewer)
-  int64_t key_cap;
   // EX form only.  head_tables: the table has a row per (sequence, KV head),
   // [B][H_kv][max_pages_per_seq].  scores (when not null): every score in
   // log2 units, [B][H_kv][rows][score_stride] by key position (-inf where a
@@ -220,8 +219,7 @@ __device__ __forceinline__ void seq_range(const DecodeParams& P, int b, int& lo,
                                           bool report_errors) {
   const int L = P.context_lens[b];
   p = L - 1;
-  // (a ring's positions are not bounded by its width)
-  if (L > kMaxLength || (P.ring_pages == 0 && L > P.key_cap)) {
+  if (L > P.key_cap) {
     if (report_errors) report(P.error_word, TL_DEVERR_CONTEXT_RANGE);
     p = -1;
   }
@@ -376,10 +374,14 @@ __device__ __forceinline__ void write_piece_descs(const DecodeParams& P, const i
     P.ws.desc[2 * slot + 1] = make_int4(lo_j, p_j, part, 0);
     const int blk = page_of(P, cb * kChunk);
     const int e = P.ring_pages > 0 ? blk % P.ring_pages : blk;
-    const int heads = P.head_tables ? P.h_kv : 1;  // one row of the table each
-    for (int g = 0; g < heads; ++g)
-      asm volatile("prefetch.global.L2 [%0];\n" ::"l"(
-          P.block_table + ((size_t)bj * heads + g) * P.max_pages_per_seq + e));
+    if constexpr (EX) {
+      const int heads = P.head_tables ? P.h_kv : 1;  // one row of the table each
+      for (int g = 0; g < heads; ++g)
+        asm volatile("prefetch.global.L2 [%0];\n" ::"l"(
+            P.block_table + ((size_t)bj * heads + g) * P.max_pages_per_seq + e));
+    } else {
+      asm volatile("prefetch.global.L2 [%0];\n" ::"l"(P.block_table + (size_t)bj * P.max_pages_per_seq + e));
+    }
   }
 }
 
@@ -474,7 +476,10 @@ __device__ __forceinline__ void warp_plan(const DecodeParams& P, int target_spli
   const long long half = max(target_splits / 2, 1);
   const int small = one ? 0 : (int)max((long long)kSmallChunks, (T + P.B + half - 1) / half);
   auto tail_of = [&](int n) { return ONE_ROUND ? tail_chunks(n, small) : tail_chunks(n); };
-  auto small_pieces = [&](int tail) { return tail > 0 ? (tail + small - 1) / small : 0; };
+  // (ONE_ROUND: small may be 0, and the tails then are)
+  auto small_pieces = [&](int tail) {
+    return !ONE_ROUND || tail > 0 ? (tail + small - 1) / small : 0;
+  };
   int split = one;
   if (!one) {
     long long TP = 0;
@@ -550,8 +555,9 @@ __device__ __forceinline__ void warp_plan(const DecodeParams& P, int target_spli
 // every piece.  Either way every thread then writes descriptors, one piece
 // at a time.  first_dynamic: items below it are taken without the counter
 // (the attention kernel's warp w starts with item w).
+template <bool EX>
 static __global__ void __launch_bounds__(1024) decode_plan_kernel(DecodeParams P, int target_splits,
-                                                           int first_dynamic) {
+                                                                  int first_dynamic) {
   __shared__ long long red[2][32];
   __shared__ long long tmp[32];
   __shared__ int4 rec[1024];  // per sequence of a round: first bulk / small position, counts
@@ -673,8 +679,8 @@ static __global__ void __launch_bounds__(1024) decode_plan_kernel(DecodeParams P
     __syncthreads();
     if (s_plan[2] < 0) return;
     if (tid == 0) TL_TRACE_SET(TL_TRACE_PLAN_PLACED);
-    write_piece_descs(P, rec, rng, 0, P.B, 0, s_plan[2], 0, s_plan[3], s_plan[2], s_plan[0],
-                      s_plan[1], tid, nt);
+    write_piece_descs<EX>(P, rec, rng, 0, P.B, 0, s_plan[2], 0, s_plan[3], s_plan[2], s_plan[0],
+                          s_plan[1], tid, nt);
 #if TL_DECODE_TRACE
     __syncthreads();
     if (tid == 0) TL_TRACE_SET(TL_TRACE_PLAN_END);
@@ -750,7 +756,7 @@ static __global__ void __launch_bounds__(1024) decode_plan_kernel(DecodeParams P
       rng[tid] = make_int2(lo, p);
     }
     __syncthreads();
-    write_piece_descs(P, rec, rng, base, min(nt, P.B - base), (int)(carry >> 32),
+    write_piece_descs<EX>(P, rec, rng, base, min(nt, P.B - base), (int)(carry >> 32),
                       (int)(tot >> 32), (int)(carry & 0xffffffffll), (int)(tot & 0xffffffffll),
                       (int)NB, split, small, tid, nt);
     __syncthreads();  // rec and rng are rewritten by the next round
@@ -2758,7 +2764,11 @@ static tl_status decode_impl(const void* q, const void* k_cache, const void* v_c
   P.row_units = 0;
   P.k_scales = k_scales;
   P.v_scales = v_scales;
-  P.key_cap = std::min((int64_t)max_pages_per_seq * page_size, ex.key_cap);
+  // (a ring's positions are not bounded by its width)
+  P.key_cap = (int32_t)std::min<int64_t>(
+      kMaxLength,
+      ring_pages > 0 ? kMaxLength
+                     : std::min((int64_t)max_pages_per_seq * page_size, ex.key_cap));
   P.head_tables = ex.head_tables ? 1 : 0;
   P.scores = ex.scores;
   P.score_stride = ex.score_stride;
@@ -2826,8 +2836,8 @@ static tl_status decode_impl(const void* q, const void* k_cache, const void* v_c
       EX && dtype != TL_F32 && plans_itself(kv8, ex.mass != nullptr, rows, B, h_kv) &&
       warps * 32 >= B;  // a CTA's thread reads a sequence's length each
   if (!self_plan) {
-    decode_plan_kernel<<<(unsigned)(1 + write_ctas), plan_threads, 0, st>>>(P, target_splits,
-                                                                            num_sms() * warps);
+    decode_plan_kernel<EX><<<(unsigned)(1 + write_ctas), plan_threads, 0, st>>>(
+        P, target_splits, num_sms() * warps);
     if (launch_status() != TL_OK) return TL_ERR_CUDA;
   }
 
