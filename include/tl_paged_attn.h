@@ -714,8 +714,12 @@ size_t tl_kv_page_select_workspace_size(int32_t B, int32_t h_q, int32_t h_kv, in
  *     I_h = sum_e a_h[e] x (a_h[e] >= 0 ? max code : min code of channel e)
  *     score = max over the heads h of g of (float(I_h) x bound scale) x t_h
  * (codes clamped to +-127, all in binary32, I_h exact: every implementation
- * gives the same bits): the largest score a key of the page could have, in
- * int8.  Blocks i < keep_first and i >= nb - keep_last are selected whatever
+ * gives the same bits).  It estimates the largest score that a key of the page
+ * could have, sum_e max(q[e] M[e], q[e] m[e]): codes are rounded to nearest, so
+ * it may lie above or below that, by up to bound scale x t_h x
+ * sum_e (|a_h[e]| + |code of e| + 1/2) / 2, and a channel whose values stay below
+ * 1/254 of the page's largest does not count.  Keys with a few channels far
+ * larger than the others are ranked more coarsely for it.  Blocks i < keep_first and i >= nb - keep_last are selected whatever
  * their score, then the largest scores, equal ones by the lowest i.  With nb
  * <= n_select every block is.  A non-finite query value counts as 0 and sets
  * TL_DEVERR_VALUE_RANGE; a table entry outside the pool sets

@@ -1,6 +1,9 @@
 // Eviction from the cache by accumulated attention weight: which keys of each
 // (sequence, KV head) stay, and the in-place move of their rows to the front
 // of the sequence's pages.  The weights come from tl_paged_attn_decode_mass.
+// (Eviction by accumulated weight with the newest keys protected: Zhang et al.,
+// "H2O: Heavy-Hitter Oracle for Efficient Generative Inference of Large Language
+// Models", 2023.)
 #include <algorithm>
 
 #include "common.cuh"

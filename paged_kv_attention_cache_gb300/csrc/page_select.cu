@@ -5,12 +5,15 @@
 // Mathematics.  For a page and KV head, M_d and m_d are the largest and
 // smallest live key value of channel d.  Any key k of the page has
 // <q, k> <= sum_d max(q_d M_d, q_d m_d), so the sum ranks pages by the
-// largest score a key of theirs could reach.  It is held in int8: codes of
-// (M, m) with one f32 scale per (page, head), and of q with one scale per
-// query head.  The sum is then a sum of whole numbers, below 2^24, with two
-// f32 products after it, so a page's score, and with it the selection, is the
-// same bit for bit however the work is split, at an eighth of the bytes of
-// one bf16 key page of 16.
+// largest score a key of theirs could reach (page selection by per-channel
+// minima and maxima: Tang et al., "Quest: Query-Aware Sparsity for Efficient
+// Long-Context LLM Inference", 2024).  It is estimated in int8: codes of (M, m)
+// with one f32 scale per (page, head), and of q with one scale per query head,
+// all rounded to nearest (so the estimate may lie below the sum).  It is then a
+// sum of whole numbers, below 2^24, with two f32 products after it, so a page's
+// score, and with it the selection, is the same bit for bit however the work is
+// split, at a sixteenth of the bytes of the page's keys (16 of bf16; an eighth
+// of one-byte ones).
 #include <algorithm>
 
 #include "common.cuh"

@@ -1,6 +1,6 @@
 // PAGED_ATTENTION, decode: one query token per sequence (or q_len tokens at
 // its end: the multi-token / speculative-verify shape), split-K over the
-// sequence's keys with a log-sum-exp merge of the splits.
+// sequence's keys ("flash-decoding") with a log-sum-exp merge of the splits.
 // The table may be a ring (the windowed pool of section 3): logical block k
 // is then read from entry k % ring_pages, keys still in position order.
 //
