@@ -4,6 +4,11 @@ Argument marshalling only: every function checks that the tensors are CUDA,
 contiguous and of the expected dtype, passes their device pointers and sizes to
 libtlpa.so, and raises TLError on a non-TL_OK status.  No arithmetic of the
 path happens here; torch provides the device memory and the stream.
+
+With stream= (a torch stream or a raw handle) a call runs on that stream, and
+what it allocates itself (outputs and workspaces not given) belongs to it; the
+tensors given are the caller's to order before it and to keep until its work is
+done, as with any kernel.
 """
 from __future__ import annotations
 

@@ -486,7 +486,7 @@ TL_DEVINLINE int blocks_of(int L, int max_pages, int page_size) {
 // code >= 0) and min code x (q code < 0) its k steps, in whole numbers.
 // Bound: HBM, and past 8 heads a group the int8 MMA.  With the query's kernel
 // and the selection, 64 sequences of 1,024-32,768 keys (142 MB of codes, 8 KV
-// heads of 128, 5 query heads each) take 39.4 us and one of 131,072 19.2 us.
+// heads of 128, 5 query heads each) take 39.2 us and one of 131,072 17.1 us.
 // The same sums by fp16 MMAs (the codes widened by byte permutes, exact with
 // two chains) take as long there and 20-25% longer at 16 query heads.
 template <int D, int NT>
