@@ -250,7 +250,8 @@ size_t tl_paged_attn_decode_workspace_size(int32_t B, int32_t h_q, int32_t h_kv,
  *     s_j = scale * <q[b][h], K_g(j)>,  j = lo..p,  K_g(j) found through
  *           page block_table[b][j / page_size], offset j % page_size
  *     out[b][h] = sum_j softmax(s)_j * V_g(j)
- * L <= 0 gives out[b][h] = 0.  Each sequence's keys are cut into pieces
+ * L <= 0 gives out[b][h] = 0.  Rows at positions outside lo..p, in these and in
+ * the pools' other slots, may hold anything.  Each sequence's keys are cut into pieces
  * attended independently (split-K) and merged with a log-sum-exp combine in a
  * fixed order; the result does not depend on where the pages are in the pool,
  * and repeats bit for bit.  The call enqueues three kernels on `stream` (a
@@ -548,7 +549,9 @@ tl_status tl_paged_attn_decode_ring(const void* q, const void* k_cache, const vo
  * prefill ("How serving works in Tlaloc", section 4); it gives the same
  * results as tl_paged_attn_prefill on the same tokens, within the tolerance,
  * and for q_len = 1 is tl_paged_attn_decode.  K and V of each sequence are
- * read once for all its tokens, as in decode.
+ * read once for all its tokens, as in decode.  Keys that no token of the call
+ * sees may hold anything; a V element that is not finite, of a key that some
+ * token sees, may make that element NaN for the other tokens of the KV head too.
  *   q    [B][q_len][h_q][d] bf16;  out [B][q_len][h_q][d] float32.
  * Supported: bf16 pools with d in {64, 128}, or TL_FP8_E4M3 pools with
  * d = 128 (bf16 q, as for tl_paged_attn_decode), q_len * (h_q / h_kv) <= 16
@@ -788,7 +791,8 @@ tl_status tl_paged_attn_decode_pages_int8(const void* q, const int8_t* k_codes,
  *   mass          [B][h_kv][mass_len] float32, in place.  A sequence longer
  *                 than mass_len (or its table) sets TL_DEVERR_CONTEXT_RANGE:
  *                 output 0, mass as it was.  Two calls that overlap in time
- *                 must not share a mass (or a workspace).
+ *                 must not share a mass (or a workspace).  After a
+ *                 TL_DEVERR_TIMEOUT the mass, like the output, is undefined.
  *   workspace     tl_paged_attn_decode_mass_workspace_size bytes (0: invalid
  *                 sizes): the decode's, and one float32 per query head, token
  *                 and mass place for the scores

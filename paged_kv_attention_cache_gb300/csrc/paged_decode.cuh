@@ -1458,19 +1458,21 @@ __global__ void __launch_bounds__(DecodeShape<TWO_ROWS, KV8>::kWarps * 32, 1)
       constexpr int nj = decltype(nj_c)::value;
 #pragma unroll
       for (int j = 0; j < NJ; ++j) {
-        if (j >= nj) break;
-        // V rows past the sequence's end (its last chunk only) may hold anything
-        const int c = c0 + sub0 + j;
+        if (I8 || j >= nj) break;  // (int8 codes are numbers, whatever they are)
+        // V rows past the sequence's end or before its first key (its last and
+        // first chunk only) may hold anything: a weight of 0 would make a NaN
+        // of an infinity there
         const uint32_t vaddr = ring + stage * L::kStageBytes + (CPS + sub0 + j) * L::kChunkBytes;
-        const int first_dead = it.p + 1 - c * kChunk;
-        if (first_dead < kChunk) {
-          const int n_dead = kChunk - max(first_dead, 0);
-          for (int idx = lane; idx < n_dead * L::kHalves * 8; idx += 32) {
-            const int row = kChunk - n_dead + idx / (L::kHalves * 8);
+        if (smask != (CPS == 2 ? 0xffffffffu : 0xffffu)) {
+          const uint32_t dead = ~(smask >> (16 * (sub0 + j)));
+#pragma unroll 1
+          for (int idx = lane; idx < kChunk * L::kHalves * 8; idx += 32) {
+            const int row = idx / (L::kHalves * 8);
             const int hu = idx % (L::kHalves * 8);
             const uint32_t a = vaddr + (hu >> 3) * L::kHalfBytes + row * 128 + ((hu & 7) << 4);
-            asm volatile("st.shared.v4.u32 [%0], {%1, %1, %1, %1};\n" ::"r"(a), "r"(0u)
-                         : "memory");
+            if (dead >> row & 1u)
+              asm volatile("st.shared.v4.u32 [%0], {%1, %1, %1, %1};\n" ::"r"(a), "r"(0u)
+                           : "memory");
           }
           fence_proxy_async_smem();  // these stores precede the stage's next TMA fill
           __syncwarp();
