@@ -151,3 +151,34 @@ def test_a_call_on_a_stream_that_is_not_current(name, handle, monkeypatch):
     torch.cuda.current_stream().wait_stream(side)
     for a, b in zip(got, first):
         assert torch.equal(a, b)
+
+
+@pytest.mark.gpu
+def test_a_passed_stream_inside_a_capture():
+    """A step captured with a forked stream passed to its calls, replayed over new inputs."""
+    build.build()
+    c = inputs("cuda")
+    main, side = torch.cuda.Stream(), torch.cuda.Stream()
+
+    def step(stream):
+        pages, lens = tl.tl_kv_page_select(c.q, c.bounds, c.bscales, c.table, c.lens, PS, 2,
+                                           stream=stream)
+        return tl.tl_paged_attn_decode_pages(c.q, c.k, c.v, pages, lens, 0.1, stream=stream)
+
+    main.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(main):
+        step(None)
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph, stream=main):
+            side.wait_stream(main)
+            step(side)  # its buffers are dropped inside the capture
+            out = step(side)
+            main.wait_stream(side)
+    torch.cuda.synchronize()
+    for seed in (1, 2):
+        g = torch.Generator().manual_seed(seed)
+        c.q.copy_(torch.randn((B, HQ, D), generator=g).to(BF))
+        torch.cuda.synchronize()
+        graph.replay()
+        torch.cuda.synchronize()
+        assert torch.equal(out, step(None))
