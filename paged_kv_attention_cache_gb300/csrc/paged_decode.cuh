@@ -2585,9 +2585,9 @@ static int decode_warps(int rows) {
 // whatever the lengths, so no item waits for another, nothing is atomic and the
 // order of the additions is fixed (row 0, 1, ...).
 // Bound: L2 (the scores, 4 bytes a row and key) and the masses' 8 bytes a key
-// and head.  Measured: 14 of a call's 118 us for 64 e4m3 contexts of 512-8,192
+// and head.  Measured: 14 of a call's 117 us for 64 e4m3 contexts of 512-8,192
 // keys, 32 query and 8 KV heads (37 MB of scores, 19 of masses); a bf16 context
-// of 32,768 takes 33.4 us in all (136 MB).  One launch for the merge and this
+// of 32,768 takes 33.3 us in all (136 MB).  One launch for the merge and this
 // (blocks of either kind, these folding the pieces' statistics themselves)
 // took 39.5 and 124.7 us where two launches then took 36.7 and 121: every
 // block then holds the merge's registers.
