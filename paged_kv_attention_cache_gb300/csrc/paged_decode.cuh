@@ -405,19 +405,20 @@ constexpr int kWriteWarps = 8;  // writing warps per CTA of a warp-planned launc
 // without / with the plan's launch (us a call, 32 query and 8 KV heads of 128,
 // sequences of 2,048-8,192 keys):
 //                           1          16          32          48          64
-// 128 pages, bf16   11.6/20.0   30.2/32.8   51.1/53.1   72.4/73.4   96.2/91.9
-// weights, bf16     19.2/25.2   66.8/71.0   125.4/122.7 182.5/177.1 241.2/233.9
-//   4 tokens        22.7/30.6   79.2/100.8  149.6/165.3 224.3/232.0 298.4/298.3
-// 128 pages, e4m3   12.1/19.7   23.7/29.5   38.9/43.4   54.8/60.0   68.2/69.4
-// weights, e4m3     19.6/24.9   43.1/55.0   73.3/84.3   102.2/113.6 135.3/146.4
-//   4 tokens        21.9/29.2   62.5/91.8   111.5/140.4 168.2/181.1 221.5/223.3
-// 128 pages, int8   13.1/25.7   25.4/32.4   38.9/47.7   57.7/69.3   70.8/78.1
-// weights, int8     21.6/31.0   50.3/65.4   86.9/99.1   118.8/139.3 153.9/176.8
-//   4 tokens        24.6/33.6   79.0/119.9  145.2/184.8 215.4/238.4 283.7/291.7
-// and over 16 heads of one query head: 128 pages, bf16, 16 sequences 50.8/52.5
-// and 32 91.4/90.7; weights, bf16, 117.1/118.0 and 230.5/218.5, e4m3 67.0/78.3
-// and 121.5/127.7, int8 80.2/92.8 and 156.3/149.8; over 2 heads without is
-// faster throughout (weights, bf16, 32 sequences 39.9/45.5).
+// 128 pages, bf16   11.5/19.2   29.4/32.4   49.2/52.4   69.8/71.7   94.0/89.3
+// weights, bf16     19.1/25.1   66.2/69.6   123.8/120.8 179.1/173.8 242.3/230.5
+//   4 tokens        22.5/30.1   78.3/100.6  148.4/164.3 222.9/229.3 295.5/294.5
+// 128 pages, e4m3   11.9/18.4   22.3/29.0   36.7/42.0   51.9/56.9   65.5/66.7
+// weights, e4m3     18.9/25.0   41.9/53.7   71.7/82.5   101.8/110.0 134.1/142.7
+//   4 tokens        21.7/28.9   62.1/91.2   112.1/139.4 169.4/180.0 223.6/222.3
+// 128 pages, int8   12.9/24.0   24.7/32.2   37.6/47.2   56.7/65.2   69.4/74.8
+// weights, int8     21.0/29.7   48.0/65.5   83.6/98.3   114.6/136.7 150.4/174.8
+//   4 tokens        24.0/34.2   77.9/115.0  142.4/177.9 212.9/234.6 280.2/288.1
+// (weights, bf16, 24 sequences 95.7/96.8); over 16 heads of one query head, 128
+// pages, bf16, 16 sequences 48.6/51.7 and 32 86.9/87.6; weights, bf16,
+// 115.5/114.6 and 228.0/213.7, e4m3 66.0/76.5 and 120.2/124.5, int8 78.2/94.4
+// and 152.9/148.6; over 2 heads without is faster throughout (weights, bf16, 32
+// sequences 39.7/44.9).
 __host__ __device__ constexpr int self_plan_max(bool one_byte) { return one_byte ? 64 : 32; }
 static inline bool plans_itself(bool one_byte, bool weights, int rows, int B, int h_kv) {
   if (B > self_plan_max(one_byte)) return false;
@@ -1372,10 +1373,11 @@ __global__ void __launch_bounds__(DecodeShape<TWO_ROWS, KV8>::kWarps * 32, 1)
     // A part is off by at most 2^-25 then, against a largest product of 2^8 or
     // more: 2^-33 of it per key, whatever the pool's scales (below 2^-118 the
     // factor ends at 2^126).  A fit to the largest scale alone, shared by the
-    // rows, took 0.1-3.5% less of a call (64 sequences of 2,048-8,192 keys, 32
-    // query and 8 KV heads: 70.6 and 70.7 us over 128 pages, 153.1 and 154.1
-    // with weights, 281.1 and 283.7 with 4 tokens) and lost a row whose weight
-    // lies on keys of small scale: 10^-4 of it at scales 2^16 apart.
+    // rows, took 0.1-3.5% less of a call (timed in turn, 64 sequences of
+    // 2,048-8,192 keys, 32 query and 8 KV heads: 70.6 for 70.7 us over 128 pages,
+    // 153.1 for 154.1 with weights, 281.1 for 283.7 with 4 tokens; they take 70,
+    // 150 and 280 now) and lost a row whose weight lies on keys of small scale:
+    // 10^-4 of it at scales 2^16 apart.
     constexpr bool kFitV = I8 && EX != 0;
     constexpr float kFitMost = 32768.f;  // fp16 ends at 65,504
     [[maybe_unused]] float fit0 = __uint_as_float(253u << 23), fit1 = fit0;
