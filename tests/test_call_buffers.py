@@ -136,7 +136,7 @@ def test_a_call_on_a_stream_that_is_not_current(name, handle, monkeypatch):
     side = torch.cuda.Stream()
     side.wait_stream(torch.cuda.current_stream())
     with torch.cuda.stream(side):
-        torch.cuda._sleep(200_000_000)  # some 100 ms
+        torch.cuda._sleep(400_000_000)  # some 200 ms
     c2 = inputs("cuda") if "write" in name or "mass" in name else c
     side.wait_stream(torch.cuda.current_stream())
     got = call(c2, side.cuda_stream if handle else side)
