@@ -880,6 +880,157 @@ tl_status tl_kv_cache_compact_int8(int8_t* k_codes, int8_t* v_codes, float* k_sc
                                    int32_t d, int32_t num_pages, int32_t page_size,
                                    uint32_t* error_word, void* stream);
 
+/* ---- Rotary positions ----------------------------------------------------
+ * Rotation of rows by their positions, the append of a step's or a prompt's
+ * rows to the pages with queries and keys rotated on the way, and the
+ * compaction whose kept keys are turned to the positions they move to.  No
+ * page describes them; they are defined here in full.
+ *
+ * The rotation at position p of a row x of d elements, whose first rot_dim
+ * (even) are rotated in pairs i = 0 .. rot_dim/2 - 1 of elements (lo, hi) =
+ *     (i, i + rot_dim/2)   interleaved = 0,   or   (2i, 2i + 1)   otherwise:
+ *     y[lo] = rope_scale x (x[lo] cos a - x[hi] sin a)
+ *     y[hi] = rope_scale x (x[hi] cos a + x[lo] sin a),   a = p x f_i
+ * and y[e] = x[e] for e >= rot_dim.  (Rotary position embedding: Su et al.,
+ * "RoFormer", 2021.)  Computed in binary32 from the row's values and rounded
+ * once to the output's type.
+ *
+ * freqs: [rot_dim/2] uint64, the turns that each pair makes per position as
+ * 64-bit fractions: freqs[i] = round(2^64 x f_i / 2 pi) mod 2^64.  p x freqs[i]
+ * mod 2^64 is the angle as a fraction of a turn, exact for every 32-bit p (an
+ * entry's own rounding moves it by at most 2^-34 turns).  A table of negated
+ * entries (mod 2^64) rotates backwards: the inverse, and the gradient, of the
+ * rotation.  tl_rope_freqs makes tables; a caller may make its own.
+ *
+ * positions: [n] int32.  A row at a negative position is padding: it is taken
+ * over as it is, neither rotated nor scaled (in place: left as it was).
+ */
+
+/* How a table stretches positions past the trained length. */
+typedef enum {
+  TL_ROPE_PLAIN = 0,  /* f_i = base^(-2i/rot_dim) */
+  TL_ROPE_LINEAR = 1, /* f_i / factor */
+  TL_ROPE_BASE = 2,   /* base x factor^(rot_dim/(rot_dim-2)) for base (rot_dim > 2) */
+  TL_ROPE_BANDS = 3,  /* a pair that makes t = trained_len x f_i / 2 pi turns over the trained
+                         length keeps f_i from t = high on, takes f_i / factor up to t = low, and
+                         between them the mix of the two that is linear in t */
+  TL_ROPE_RAMP = 4,   /* the same mix linear in i, from the pair that makes `high` turns (index
+                         rounded down, at least 0) to the one that makes `low` (rounded up, at
+                         most rot_dim - 1); rope_scale 0.1 ln(factor) + 1 (Peng et al., "YaRN",
+                         2023) */
+  TL_ROPE_FACTORS = 5 /* f_i / factors[i] */
+} tl_rope_scaling;
+
+/*
+ * Fills the HOST arrays freqs [rot_dim/2] and *rope_scale (1 but for
+ * TL_ROPE_RAMP) of a rotary table; the caller copies freqs to the device.
+ * Computed in binary64, on the calling thread; nothing is launched.
+ * trained_len, low and high are read by TL_ROPE_BANDS and TL_ROPE_RAMP, factor
+ * by all kinds but TL_ROPE_PLAIN and TL_ROPE_FACTORS, factors [rot_dim/2] by
+ * TL_ROPE_FACTORS.  TL_ERR_INVALID_ARG for rot_dim odd or outside 2 .. 4096, a
+ * base not above 1, a factor (or factors entry) not above 0, trained_len not
+ * above 0, low not above 0 or not below high, a value that is not finite, a
+ * NULL array; TL_ERR_UNSUPPORTED for a kind not listed.
+ */
+tl_status tl_rope_freqs(int32_t rot_dim, double base, int32_t scaling, double factor,
+                        double trained_len, double low, double high, const double* factors,
+                        uint64_t* freqs, float* rope_scale);
+
+/*
+ * out[t][h] = the rotation of x[t][h] at positions[t], for n_tokens tokens of
+ * `heads` rows of d elements.
+ *   x, out        rows of one token contiguous; token t at x + t * x_stride
+ *                 (out + t * out_stride) elements, so that a part of a fused
+ *                 projection's rows is read where it lies.  out may be x (same
+ *                 pointer and stride: in place); otherwise the two must have
+ *                 no element in common.  Aligned to their elements.
+ *   dtype         TL_BF16 or TL_F32, of both
+ * TL_ERR_INVALID_ARG for a negative n_tokens, sizes not positive, rot_dim odd
+ * or outside 2 .. d, a negative stride, an out_stride below heads * d (with
+ * more than one token), or an overlap.  n_tokens 0: nothing is done.
+ * TL_ERR_UNSUPPORTED for another dtype, d > 4096 or heads * d >= 2^31.
+ */
+tl_status tl_rope(const void* x, int64_t x_stride, void* out, int64_t out_stride,
+                  const int32_t* positions, const uint64_t* freqs, int32_t rot_dim,
+                  int32_t interleaved, float rope_scale, int32_t n_tokens, int32_t heads,
+                  int32_t d, tl_dtype dtype, void* stream);
+
+/*
+ * For every token t: q_out[t] = the rotation of q[t] (h_q heads), and for
+ * slot_mapping[t] != -1 the cache row slot_mapping[t] = the rotation of
+ * k_new[t], and v_new[t] as it is (h_kv heads each), at positions[t].  The
+ * pools' other rows stay as they are.
+ *   q, q_out      as tl_rope's x and out (src_dtype); NULL with h_q = 0: keys
+ *                 and values alone
+ *   k_new, v_new  [n_tokens][h_kv][d] in src_dtype (TL_BF16 or TL_F32), token t
+ *                 at k_stride (v_stride) elements times t
+ *   dtype         the pools': src_dtype, or TL_FP8_E4M3 (nearest with ties to
+ *                 even, clamped to +-448, NaN as 0x7F); tl_kv_cache_write_rope_int8:
+ *                 codes and scales as tl_kv_cache_write_int8, of the rotated row
+ *   slot_mapping  [n_tokens] int64; -1 writes nothing (the query is rotated all
+ *                 the same), a slot outside the pools sets TL_DEVERR_SLOT_RANGE
+ *                 and writes nothing
+ *   positions     a token with a slot at a negative position writes nothing and
+ *                 sets TL_DEVERR_CONTEXT_RANGE; its query is padding
+ * Two tokens with one slot are a caller error.  q_out must have no element in
+ * common with k_new, v_new or the pools, nor the pools (and scales) with one
+ * another or with q, k_new or v_new.
+ * Errors as tl_rope and tl_kv_cache_write; pools 16-byte aligned, scales 4-byte
+ * aligned, h_kv * d elements of a pool a multiple of 16 bytes (int8: d up to
+ * 1024); num_pages * page_size < 2^31, (h_q + 2 h_kv) * d < 2^31.
+ */
+tl_status tl_kv_cache_write_rope(const void* q, int64_t q_stride, void* q_out,
+                                 int64_t q_out_stride, const void* k_new, int64_t k_stride,
+                                 const void* v_new, int64_t v_stride, tl_dtype src_dtype,
+                                 void* k_cache, void* v_cache, const int64_t* slot_mapping,
+                                 const int32_t* positions, const uint64_t* freqs,
+                                 int32_t rot_dim, int32_t interleaved, float rope_scale,
+                                 int32_t n_tokens, int32_t num_pages, int32_t page_size,
+                                 int32_t h_q, int32_t h_kv, int32_t d, tl_dtype dtype,
+                                 uint32_t* error_word, void* stream);
+tl_status tl_kv_cache_write_rope_int8(const void* q, int64_t q_stride, void* q_out,
+                                      int64_t q_out_stride, const void* k_new, int64_t k_stride,
+                                      const void* v_new, int64_t v_stride, tl_dtype src_dtype,
+                                      int8_t* k_codes, int8_t* v_codes, float* k_scales,
+                                      float* v_scales, const int64_t* slot_mapping,
+                                      const int32_t* positions, const uint64_t* freqs,
+                                      int32_t rot_dim, int32_t interleaved, float rope_scale,
+                                      int32_t n_tokens, int32_t num_pages, int32_t page_size,
+                                      int32_t h_q, int32_t h_kv, int32_t d, uint32_t* error_word,
+                                      void* stream);
+
+/*
+ * tl_kv_cache_compact of a cache of rotated keys, whose positions close up: the
+ * K row that moves from position keep[b][g][j] to j is also rotated by
+ * j - keep[b][g][j] positions (backwards; rope_scale 1: a row has had its factor
+ * when it was written), so that a key rotated at its old place is one rotated
+ * at its new place, to the rounding of its type, and the sequence goes on at
+ * position new_lens[b].  Rows that stay (keep[b][g][j] = j) keep their bits.
+ * e4m3 rows are rounded and clamped anew; int8 rows get a new scale (of the
+ * values code x scale as rounded to binary32), and a row whose values are not
+ * all finite sets TL_DEVERR_VALUE_RANGE as tl_kv_cache_write_int8 does.
+ * V rows, their scales and the mass move as in tl_kv_cache_compact, whose other
+ * rules and errors hold; TL_ERR_INVALID_ARG for rot_dim odd or outside 2 .. d,
+ * TL_ERR_UNSUPPORTED when d or rot_dim is not a multiple of 16, and for int8
+ * pools when d is not a power of two up to 512.
+ */
+tl_status tl_kv_cache_compact_rope(void* k_cache, void* v_cache, const int32_t* block_table,
+                                   int32_t max_pages_per_seq, const int32_t* context_lens,
+                                   const int32_t* keep, int32_t n_keep, const int32_t* new_lens,
+                                   float* mass, int32_t mass_len, const uint64_t* freqs,
+                                   int32_t rot_dim, int32_t interleaved, int32_t B, int32_t h_kv,
+                                   int32_t d, int32_t num_pages, int32_t page_size,
+                                   tl_dtype dtype, uint32_t* error_word, void* stream);
+tl_status tl_kv_cache_compact_rope_int8(int8_t* k_codes, int8_t* v_codes, float* k_scales,
+                                        float* v_scales, const int32_t* block_table,
+                                        int32_t max_pages_per_seq, const int32_t* context_lens,
+                                        const int32_t* keep, int32_t n_keep,
+                                        const int32_t* new_lens, float* mass, int32_t mass_len,
+                                        const uint64_t* freqs, int32_t rot_dim,
+                                        int32_t interleaved, int32_t B, int32_t h_kv, int32_t d,
+                                        int32_t num_pages, int32_t page_size,
+                                        uint32_t* error_word, void* stream);
+
 #ifdef __cplusplus
 }
 #endif

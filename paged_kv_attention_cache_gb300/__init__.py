@@ -27,7 +27,10 @@ from .api import (TL_BF16, TL_FP8_E4M3, tl_kv_cache_write_fp8, TL_DEVERR_CONTEXT
                   tl_paged_attn_decode_pages_int8, tl_paged_attn_decode_mass,
                   tl_paged_attn_decode_mass_int8, tl_paged_attn_decode_mass_workspace_size,
                   tl_kv_evict_select, tl_kv_cache_compact, tl_kv_cache_compact_int8,
-                  tl_version)
+                  TL_ROPE_PLAIN, TL_ROPE_LINEAR, TL_ROPE_BASE, TL_ROPE_BANDS, TL_ROPE_RAMP,
+                  TL_ROPE_FACTORS, tl_rope_freqs, tl_rope, tl_kv_cache_write_rope,
+                  tl_kv_cache_write_rope_int8, tl_kv_cache_compact_rope,
+                  tl_kv_cache_compact_rope_int8, tl_version)
 from . import build as _build_module
 
 
@@ -46,5 +49,7 @@ __all__ = [
     "tl_paged_attn_decode_multi_int8", "tl_paged_attn_decode_write_ring",
     "tl_paged_attn_prefill_ring_workspace_size", "tl_paged_attn_decode_multi",
     "tl_paged_attn_decode_multi_workspace_size", "tl_paged_attn_prefill_workspace_size_keys",
+    "tl_rope_freqs", "tl_rope", "tl_kv_cache_write_rope", "tl_kv_cache_write_rope_int8",
+    "tl_kv_cache_compact_rope", "tl_kv_cache_compact_rope_int8",
     "tl_status_string", "tl_version", "tl_get_device_error", "TLError", "build_library", "alloc_workspace",
 ]

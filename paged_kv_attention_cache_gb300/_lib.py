@@ -16,6 +16,7 @@ _lib = None
 
 i32, i64, u32p, vp, sz, f32 = (ctypes.c_int32, ctypes.c_int64, ctypes.c_void_p, ctypes.c_void_p,
                                ctypes.c_size_t, ctypes.c_float)
+f64 = ctypes.c_double
 
 SIGNATURES = {
     "tl_status_string": ([ctypes.c_int], ctypes.c_char_p),
@@ -94,6 +95,19 @@ SIGNATURES = {
                              ctypes.c_int, u32p, vp], ctypes.c_int),
     "tl_kv_cache_compact_int8": ([vp, vp, vp, vp, vp, i32, vp, vp, i32, vp, vp, i32, i32, i32,
                                   i32, i32, i32, u32p, vp], ctypes.c_int),
+    "tl_rope_freqs": ([i32, f64, i32, f64, f64, f64, f64, vp, vp, vp], ctypes.c_int),
+    "tl_rope": ([vp, i64, vp, i64, vp, vp, i32, i32, f32, i32, i32, i32, ctypes.c_int, vp],
+                ctypes.c_int),
+    "tl_kv_cache_write_rope": ([vp, i64, vp, i64, vp, i64, vp, i64, ctypes.c_int, vp, vp, vp, vp,
+                                vp, i32, i32, f32, i32, i32, i32, i32, i32, i32, ctypes.c_int,
+                                u32p, vp], ctypes.c_int),
+    "tl_kv_cache_write_rope_int8": ([vp, i64, vp, i64, vp, i64, vp, i64, ctypes.c_int, vp, vp, vp,
+                                     vp, vp, vp, vp, i32, i32, f32, i32, i32, i32, i32, i32, i32,
+                                     u32p, vp], ctypes.c_int),
+    "tl_kv_cache_compact_rope": ([vp, vp, vp, i32, vp, vp, i32, vp, vp, i32, vp, i32, i32, i32,
+                                  i32, i32, i32, i32, ctypes.c_int, u32p, vp], ctypes.c_int),
+    "tl_kv_cache_compact_rope_int8": ([vp, vp, vp, vp, vp, i32, vp, vp, i32, vp, vp, i32, vp, i32,
+                                       i32, i32, i32, i32, i32, i32, u32p, vp], ctypes.c_int),
     "tl_paged_attn_prefill_ring": ([vp, vp, vp, vp, i32, vp, vp, i32, i32, i32, i32, i32, i32,
                                     i32, i32, i32, f32, ctypes.c_int, vp, sz, u32p, vp],
                                    ctypes.c_int),

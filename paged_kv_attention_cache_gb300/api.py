@@ -28,6 +28,8 @@ _current_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
 (TL_OK, TL_ERR_INVALID_ARG, TL_ERR_UNSUPPORTED, TL_ERR_CUDA, TL_ERR_DEVICE_BOUNDS,
  TL_ERR_WORKSPACE, TL_ERR_DEVICE_TIMEOUT) = range(7)
 TL_F32, TL_BF16, TL_FP8_E4M3, TL_INT8 = 0, 1, 2, 3
+(TL_ROPE_PLAIN, TL_ROPE_LINEAR, TL_ROPE_BASE, TL_ROPE_BANDS, TL_ROPE_RAMP,
+ TL_ROPE_FACTORS) = range(6)
 TL_DEVERR_SLOT_RANGE, TL_DEVERR_PAGE_RANGE, TL_DEVERR_CONTEXT_RANGE = 1, 2, 4
 TL_DEVERR_TIMEOUT, TL_DEVERR_VALUE_RANGE, TL_DEVERR_PLAN_CAPACITY = 8, 16, 32
 
@@ -954,3 +956,193 @@ def tl_kv_cache_compact_int8(k_codes: torch.Tensor, v_codes: torch.Tensor,
          _ptr(k_codes), _ptr(v_codes), _ptr(k_scales), _ptr(v_scales), _ptr(block_table),
          block_table.shape[1], _ptr(context_lens), _ptr(keep), keep.shape[2], _ptr(new_lens),
          mass_ptr, mass_len, B, hkv, d, P, ps, _err_word(error_word, dev))
+
+
+# --------------------------------------------------------- rotary positions --
+
+def tl_rope_freqs(rot_dim: int, base: float = 10000.0, scaling: int = TL_ROPE_PLAIN,
+                  factor: float = 1.0, trained_len: float = 0.0, low: float = 1.0,
+                  high: float = 32.0, factors=None, device="cuda"):
+    """(freqs [rot_dim/2] int64 on `device`, rope_scale): each pair's turns per
+    position as 64-bit fractions of a turn (the bits of an unsigned number),
+    and the factor of the rotated values.  -freqs rotates backwards."""
+    import ctypes
+    n = max(int(rot_dim) // 2, 0)
+    if factors is not None:
+        factors = [float(x) for x in factors]
+        if len(factors) != n:
+            raise ValueError(f"factors must have rot_dim / 2 = {n} entries, got {len(factors)}")
+        factors = (ctypes.c_double * n)(*factors)
+    freqs = torch.empty(max(n, 1), dtype=torch.int64)
+    scale = ctypes.c_float(0)
+    _check(_lib.load().tl_rope_freqs(int(rot_dim), float(base), int(scaling), float(factor),
+                                     float(trained_len), float(low), float(high), factors,
+                                     _ptr(freqs), ctypes.byref(scale)), "tl_rope_freqs")
+    return freqs.to(device), float(scale.value)
+
+
+def _need_rows(t, name, n, heads, d, device, dtype=None):
+    """A CUDA tensor [n, heads, d] (None: any) whose tokens' rows are contiguous,
+    the tokens at any stride; returns the stride."""
+    if not isinstance(t, torch.Tensor) or not t.is_cuda:
+        raise TypeError(f"{name} must be a CUDA tensor")
+    if dtype is not None and t.dtype != dtype:
+        raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
+    if t.dim() != 3 or any(w is not None and a != w for a, w in zip(t.shape, (n, heads, d))):
+        raise ValueError(f"{name} must have shape {(n, heads, d)} (None: any), got "
+                         f"{tuple(t.shape)}")
+    s = t.stride()
+    if t.numel() and ((t.shape[2] > 1 and s[2] != 1) or
+                      (t.shape[1] > 1 and s[1] != t.shape[2])):
+        raise ValueError(f"the rows of one token of {name} must be contiguous")
+    if t.get_device() != device.index:
+        raise ValueError(f"{name} is on {t.device}, the call's tensors are on {device}")
+    return s[0]
+
+
+def _need_table_of_turns(freqs, d, device):
+    """freqs [rot_dim / 2] int64; returns rot_dim."""
+    _need(freqs, "freqs", torch.int64, (None,), device)
+    if not 1 <= freqs.shape[0] <= d // 2:
+        raise ValueError(f"freqs must have 1 to d / 2 = {d // 2} entries, got {freqs.shape[0]}")
+    return 2 * freqs.shape[0]
+
+
+def _need_turns(positions, freqs, n, d, device):
+    """positions [n] int32 and the table of turns; returns rot_dim."""
+    _need(positions, "positions", torch.int32, (n,), device)
+    return _need_table_of_turns(freqs, d, device)
+
+
+def _rotated_out(out, name, shape, dtype, device, stream):
+    """The output of rotated rows and its tokens' stride."""
+    if out is None:
+        out = _returned(shape, dtype, device, stream)
+    return out, _need_rows(out, name, *shape, device, dtype)
+
+
+def tl_rope(x: torch.Tensor, positions: torch.Tensor, freqs: torch.Tensor,
+            interleaved: bool = False, rope_scale: float = 1.0,
+            out: Optional[torch.Tensor] = None, stream=None) -> torch.Tensor:
+    """out [N, H, d]: the rows of x [N, H, d] (bf16 or f32; the tokens at any
+    stride) rotated at positions [N] int32; rows at negative positions as they
+    are.  out may be x (in place)."""
+    dev = x.device
+    x_stride = _need_rows(x, "x", None, None, None, dev)
+    N, H, d = x.shape
+    rot = _need_turns(positions, freqs, N, d, dev)
+    out, out_stride = _rotated_out(out, "out", (N, H, d), x.dtype, dev, stream)
+    _run("tl_rope", dev, stream,
+         _ptr(x), x_stride, _ptr(out), out_stride, _ptr(positions), _ptr(freqs), rot,
+         int(bool(interleaved)), float(rope_scale), N, H, d, _DTYPES.get(x.dtype, -1))
+    return out
+
+
+def _write_rope_rows(q, k_new, v_new, slot_mapping, positions, freqs, q_out, hkv, d, dev, stream):
+    """The rows of an append, checked: (arguments up to v_stride, N, H_q, rot_dim, q_out)."""
+    k_stride = _need_rows(k_new, "k_new", None, hkv, d, dev)
+    N = k_new.shape[0]
+    v_stride = _need_rows(v_new, "v_new", N, hkv, d, dev, k_new.dtype)
+    _need(slot_mapping, "slot_mapping", torch.int64, (N,), dev)
+    rot = _need_turns(positions, freqs, N, d, dev)
+    hq = q_stride = out_stride = 0
+    if q is None:
+        if q_out is not None:
+            raise ValueError("q_out without q")
+    else:
+        q_stride = _need_rows(q, "q", N, None, d, dev, k_new.dtype)
+        hq = q.shape[1]
+        if hq < 1:
+            raise ValueError("q needs at least one head (None: keys and values alone)")
+        q_out, out_stride = _rotated_out(q_out, "q_out", (N, hq, d), q.dtype, dev, stream)
+    return (_ptr(q), q_stride, _ptr(q_out), out_stride, _ptr(k_new), k_stride, _ptr(v_new),
+            v_stride, _DTYPES.get(k_new.dtype, -1)), N, hq, rot, q_out
+
+
+def tl_kv_cache_write_rope(q: Optional[torch.Tensor], k_new: torch.Tensor, v_new: torch.Tensor,
+                           k_cache: torch.Tensor, v_cache: torch.Tensor,
+                           slot_mapping: torch.Tensor, positions: torch.Tensor,
+                           freqs: torch.Tensor, interleaved: bool = False,
+                           rope_scale: float = 1.0, q_out: Optional[torch.Tensor] = None,
+                           error_word: Optional[torch.Tensor] = None,
+                           stream=None) -> Optional[torch.Tensor]:
+    """q_out [N, H_q, d] = q rotated at positions [N]; in place, the cache row
+    slot_mapping[t] = k_new[t] rotated and v_new[t], for every t with slot !=
+    -1 (pools of the rows' type, or e4m3).  q, k_new, v_new [N, heads, d]: the
+    tokens at any stride, as parts of a fused projection's rows; q None: keys
+    and values alone (returns None)."""
+    dev = k_cache.device
+    P, ps, hkv, d = _need_pools(k_cache, v_cache, dev)
+    rows, N, hq, rot, q_out = _write_rope_rows(q, k_new, v_new, slot_mapping, positions, freqs,
+                                               q_out, hkv, d, dev, stream)
+    _run("tl_kv_cache_write_rope", dev, stream,
+         *rows, _ptr(k_cache), _ptr(v_cache), _ptr(slot_mapping), _ptr(positions), _ptr(freqs),
+         rot, int(bool(interleaved)), float(rope_scale), N, P, ps, hq, hkv, d,
+         _DTYPES.get(k_cache.dtype, -1), _err_word(error_word, dev))
+    return q_out
+
+
+def tl_kv_cache_write_rope_int8(q: Optional[torch.Tensor], k_new: torch.Tensor,
+                                v_new: torch.Tensor, k_codes: torch.Tensor,
+                                v_codes: torch.Tensor, k_scales: torch.Tensor,
+                                v_scales: torch.Tensor, slot_mapping: torch.Tensor,
+                                positions: torch.Tensor, freqs: torch.Tensor,
+                                interleaved: bool = False, rope_scale: float = 1.0,
+                                q_out: Optional[torch.Tensor] = None,
+                                error_word: Optional[torch.Tensor] = None,
+                                stream=None) -> Optional[torch.Tensor]:
+    """tl_kv_cache_write_rope into int8 pools: codes and scales as
+    tl_kv_cache_write_int8 writes them, of the rotated rows."""
+    dev = k_codes.device
+    P, ps, hkv, d = _need_int8_pools(k_codes, v_codes, k_scales, v_scales, dev)
+    rows, N, hq, rot, q_out = _write_rope_rows(q, k_new, v_new, slot_mapping, positions, freqs,
+                                               q_out, hkv, d, dev, stream)
+    _run("tl_kv_cache_write_rope_int8", dev, stream,
+         *rows, _ptr(k_codes), _ptr(v_codes), _ptr(k_scales), _ptr(v_scales), _ptr(slot_mapping),
+         _ptr(positions), _ptr(freqs), rot, int(bool(interleaved)), float(rope_scale), N, P, ps,
+         hq, hkv, d, _err_word(error_word, dev))
+    return q_out
+
+
+def tl_kv_cache_compact_rope(k_cache: torch.Tensor, v_cache: torch.Tensor,
+                             block_table: torch.Tensor, context_lens: torch.Tensor,
+                             keep: torch.Tensor, new_lens: torch.Tensor, freqs: torch.Tensor,
+                             interleaved: bool = False, mass: Optional[torch.Tensor] = None,
+                             error_word: Optional[torch.Tensor] = None, stream=None) -> None:
+    """tl_kv_cache_compact whose K rows are rotated by the positions they move
+    (from keep[b, g, j] to j): the sequence goes on at position new_lens[b]."""
+    dev = k_cache.device
+    P, ps, hkv, d = _need_pools(k_cache, v_cache, dev)
+    _need(context_lens, "context_lens", torch.int32, (None,), dev)
+    B = context_lens.shape[0]
+    _need_table(block_table, context_lens, B, dev)
+    mass_ptr, mass_len = _need_keep(keep, new_lens, mass, B, hkv, dev)
+    rot = _need_table_of_turns(freqs, d, dev)
+    _run("tl_kv_cache_compact_rope", dev, stream,
+         _ptr(k_cache), _ptr(v_cache), _ptr(block_table), block_table.shape[1],
+         _ptr(context_lens), _ptr(keep), keep.shape[2], _ptr(new_lens), mass_ptr, mass_len,
+         _ptr(freqs), rot, int(bool(interleaved)), B, hkv, d, P, ps,
+         _DTYPES.get(k_cache.dtype, -1), _err_word(error_word, dev))
+
+
+def tl_kv_cache_compact_rope_int8(k_codes: torch.Tensor, v_codes: torch.Tensor,
+                                  k_scales: torch.Tensor, v_scales: torch.Tensor,
+                                  block_table: torch.Tensor, context_lens: torch.Tensor,
+                                  keep: torch.Tensor, new_lens: torch.Tensor,
+                                  freqs: torch.Tensor, interleaved: bool = False,
+                                  mass: Optional[torch.Tensor] = None,
+                                  error_word: Optional[torch.Tensor] = None,
+                                  stream=None) -> None:
+    """tl_kv_cache_compact_rope over int8 pools: moved keys get new scales."""
+    dev = k_codes.device
+    P, ps, hkv, d = _need_int8_pools(k_codes, v_codes, k_scales, v_scales, dev)
+    _need(context_lens, "context_lens", torch.int32, (None,), dev)
+    B = context_lens.shape[0]
+    _need_table(block_table, context_lens, B, dev)
+    mass_ptr, mass_len = _need_keep(keep, new_lens, mass, B, hkv, dev)
+    rot = _need_table_of_turns(freqs, d, dev)
+    _run("tl_kv_cache_compact_rope_int8", dev, stream,
+         _ptr(k_codes), _ptr(v_codes), _ptr(k_scales), _ptr(v_scales), _ptr(block_table),
+         block_table.shape[1], _ptr(context_lens), _ptr(keep), keep.shape[2], _ptr(new_lens),
+         mass_ptr, mass_len, _ptr(freqs), rot, int(bool(interleaved)), B, hkv, d, P, ps,
+         _err_word(error_word, dev))

@@ -19,7 +19,8 @@ BUILD = os.path.join(HERE, "_build")
 LIB = os.path.join(BUILD, "libtlpa.so")
 
 SOURCES = ["api.cu", "kv_cache_write.cu", "paged_decode.cu", "paged_prefill.cu",
-           "decode_noalloc.cu", "paged_decode_ex.cu", "page_select.cu", "kv_evict.cu"]
+           "decode_noalloc.cu", "paged_decode_ex.cu", "page_select.cu", "kv_evict.cu",
+           "rope.cu"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 NVCC_FLAGS = ["-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC", "-I" + INCLUDE,
               "-I" + CSRC, "--expt-relaxed-constexpr"]

@@ -7,6 +7,7 @@
 #include <algorithm>
 
 #include "common.cuh"
+#include "rope.cuh"
 #include "row_select.cuh"
 
 namespace tl {
@@ -89,15 +90,17 @@ TL_DEVINLINE CompactPlace compact_place(const CompactParams& P, const int32_t* t
 
 // The walk: rows_per_pass rows of a pass, this thread's being row r of it
 // (r < 0: none), U passes a batch.  slot(j): where position j's element is
-// (-1: nowhere); at(slot): the element.  Entries outside [j, L) and positions
+// (-1: nowhere); get(slot): the element; put(slot, x, by): its new place, `by`
+// positions from the old one (put of every element, moved or not, in step with
+// the warp's other threads, where ALL).  Entries outside [j, L) and positions
 // without a page are reported by `reports` threads and skipped.
-template <int U, class Vec, class Index, class Slot, class At>
+template <int U, class Vec, class Index, bool ALL, class Slot, class Get, class Put>
 TL_DEVINLINE void compact_walk(const int32_t* keep, int new_len, int L, int rows_per_pass, int r,
-                               bool reports, uint32_t* error_word, Slot slot, At at) {
+                               bool reports, uint32_t* error_word, Slot slot, Get get, Put put) {
   const int batch = rows_per_pass * U;
   auto entry = [&](int j) { return r >= 0 && j < new_len ? __ldg(keep + j) : j; };
   // the rows of the batch at j0, whose list entries are s
-  auto load = [&](int j0, const int* s, Vec* x, Index* d) {
+  auto load = [&](int j0, const int* s, Vec* x, Index* d, int* by) {
 #pragma unroll
     for (int u = 0; u < U; ++u) {
       const int j = j0 + u * rows_per_pass + r;
@@ -113,80 +116,200 @@ TL_DEVINLINE void compact_walk(const int32_t* keep, int new_len, int L, int rows
         continue;
       }
       d[u] = to;
-      x[u] = __ldcg(at(from));
+      by[u] = j - s[u];
+      x[u] = get(from);
     }
   };
   Vec v[U], nv[U];
   Index dst[U], ndst[U];
-  int s[U], ns[U];
+  int s[U], ns[U], by[U], nby[U];
 #pragma unroll
   for (int u = 0; u < U; ++u) s[u] = entry(u * rows_per_pass + r);
 #pragma unroll
   for (int u = 0; u < U; ++u) ns[u] = entry(batch + u * rows_per_pass + r);
-  load(0, s, v, dst);
+  load(0, s, v, dst, by);
   for (int j0 = 0; j0 < new_len; j0 += batch) {
 #pragma unroll
     for (int u = 0; u < U; ++u) s[u] = entry(j0 + 2 * batch + u * rows_per_pass + r);
-    load(j0 + batch, ns, nv, ndst);
+    load(j0 + batch, ns, nv, ndst, nby);
     __syncthreads();  // every thread's loads of this batch come before any store of it
 #pragma unroll
     for (int u = 0; u < U; ++u) {
-      if (dst[u] >= 0) *at(dst[u]) = v[u];
+      if (ALL || dst[u] >= 0) put(dst[u], v[u], by[u]);
       v[u] = nv[u];
       dst[u] = ndst[u];
+      by[u] = nby[u];
       ns[u] = s[u];
     }
   }
 }
 
+// A sequence's lengths, checked; false: it stays as it is.
+TL_DEVINLINE bool compact_lens(const CompactParams& P, int b, int& L, int& new_len) {
+  L = P.context_lens[b];
+  new_len = P.new_lens[b];
+  const int64_t cap = (int64_t)P.max_pages_per_seq * P.page_size;
+  const bool bad = L > cap || (P.mass && L > P.mass_len) || new_len < 0 || new_len > P.n ||
+                   new_len > max(L, 0);
+  if (bad && blockIdx.y == 0 && threadIdx.x == 0) report(P.error_word, TL_DEVERR_CONTEXT_RANGE);
+  return !bad;
+}
+
+// Rows as they are: this CTA's slice (of `slices`) of one pool's rows.
+template <int T, int U>
+TL_DEVINLINE void compact_rows(const CompactParams& P, void* rows, int slices, int slice, int g,
+                               const int32_t* keep, const int32_t* table, int L, int new_len) {
+  const int tid = threadIdx.x;
+  const int lanes = P.row_vecs / slices;  // threads of a row
+  const int per = T / lanes;              // rows of a pass
+  uint4* pool =
+      static_cast<uint4*>(rows) + (size_t)g * P.row_vecs + slice * lanes + tid % lanes;
+  const int64_t stride = (int64_t)P.h_kv * P.row_vecs;
+  compact_walk<U, uint4, int, false>(
+      keep, new_len, L, per, tid / lanes < per ? tid / lanes : -1, tid % lanes == 0,
+      P.error_word,
+      [&](int j) {
+        const CompactPlace p = compact_place(P, table, j);
+        return p.page < 0 ? -1 : p.page * P.page_size + p.off;
+      },
+      [&](int slot) { return __ldcg(pool + slot * stride); },
+      [&](int slot, const uint4& x, int) { pool[slot * stride] = x; });
+}
+
+// The scales of an int8 pool's rows.
+template <int T, int U>
+TL_DEVINLINE void compact_scales(const CompactParams& P, float* scales, int g,
+                                 const int32_t* keep, const int32_t* table, int L, int new_len) {
+  float* scale = scales + (size_t)g * P.page_size;
+  compact_walk<U, float, int64_t, false>(
+      keep, new_len, L, T, threadIdx.x, false, nullptr,
+      [&](int j) -> int64_t {
+        const CompactPlace p = compact_place(P, table, j);
+        return p.page < 0 ? -1 : (int64_t)p.page * P.h_kv * P.page_size + p.off;
+      },
+      [&](int64_t slot) { return __ldcg(scale + slot); },
+      [&](int64_t slot, float x, int) { scale[slot] = x; });
+}
+
+template <int T, int U>
+TL_DEVINLINE void compact_mass(const CompactParams& P, int row, const int32_t* keep, int L,
+                               int new_len) {
+  float* m = P.mass + (size_t)row * P.mass_len;
+  compact_walk<U, float, int, false>(
+      keep, new_len, L, T, threadIdx.x, false, nullptr, [&](int j) { return j; },
+      [&](int j) { return __ldcg(m + j); }, [&](int j, float x, int) { m[j] = x; });
+  // positions that no key holds any more gather nothing; the last batch's
+  // loads are behind the walk's barrier
+  __syncthreads();
+  for (int j = new_len + (int)threadIdx.x; j < L; j += T) m[j] = 0.f;
+}
+
 template <int T, int U>
 __global__ void __launch_bounds__(T) compact_kernel(CompactParams P) {
-  const int tid = threadIdx.x;
   const int row = blockIdx.x, b = row / P.h_kv, g = row % P.h_kv;
-  const int L = P.context_lens[b], new_len = P.new_lens[b];
-  const int64_t cap = (int64_t)P.max_pages_per_seq * P.page_size;
-  const bool bad_len = L > cap || (P.mass && L > P.mass_len) || new_len < 0 || new_len > P.n ||
-                       new_len > max(L, 0);
-  if (bad_len) {  // the sequence stays as it is
-    if (blockIdx.y == 0 && tid == 0) report(P.error_word, TL_DEVERR_CONTEXT_RANGE);
-    return;
-  }
+  int L, new_len;
+  if (!compact_lens(P, b, L, new_len)) return;
   const int32_t* keep = P.keep + (size_t)row * P.n;
   const int32_t* table = P.block_table + (size_t)b * P.max_pages_per_seq;
   const int kind = blockIdx.y;  // the pools' slices, then K and V scales, then the mass
   if (kind < 2 * P.slices) {
     const bool is_v = kind >= P.slices;
-    const int lanes = P.row_vecs / P.slices;  // threads of a row
-    const int per = T / lanes;                // rows of a pass
-    uint4* pool = static_cast<uint4*>(is_v ? P.pool[1] : P.pool[0]) + (size_t)g * P.row_vecs +
-                  (kind - (is_v ? P.slices : 0)) * lanes + tid % lanes;
-    const int64_t stride = (int64_t)P.h_kv * P.row_vecs;
-    compact_walk<U, uint4, int>(
+    compact_rows<T, U>(P, is_v ? P.pool[1] : P.pool[0], P.slices, kind - (is_v ? P.slices : 0), g,
+                       keep, table, L, new_len);
+  } else if (P.scale[0] && kind < 2 * P.slices + 2) {
+    compact_scales<T, U>(P, kind == 2 * P.slices ? P.scale[0] : P.scale[1], g, keep, table, L,
+                         new_len);
+  } else {
+    compact_mass<T, U>(P, row, keep, L, new_len);
+  }
+}
+
+// The same with K rows turned by the positions they move (tl_kv_cache_compact_rope).
+// K rows are walked in rotary units (rope.cuh), one a thread, which turns its 8
+// pairs between the load and the store: a row that moves has an angle of its
+// own for every pair.  int8 rows are scaled anew over their threads, which lie
+// in one warp (d is a power of two up to 512).
+struct CompactTurn {
+  const uint64_t* freqs;
+  int32_t rot, interleaved;
+  int32_t units, slices;  // rotary units of a row, CTAs that share a K row
+};
+
+template <int E>
+struct CompactUnit : RopeUnit<E> {
+  float scale;  // int8
+};
+
+template <int T, int U, int E>
+__global__ void __launch_bounds__(T) compact_rope_kernel(CompactParams P, CompactTurn R) {
+  const int tid = threadIdx.x;
+  const int row = blockIdx.x, b = row / P.h_kv, g = row % P.h_kv;
+  int L, new_len;
+  if (!compact_lens(P, b, L, new_len)) return;
+  const int32_t* keep = P.keep + (size_t)row * P.n;
+  const int32_t* table = P.block_table + (size_t)b * P.max_pages_per_seq;
+  const int kind = blockIdx.y;  // K slices, V slices, V scales (int8), the mass
+  if (kind < R.slices) {
+    const int lanes = R.units / R.slices, per = T / lanes;
+    const int u = kind * lanes + tid % lanes;
+    const bool turned = 16 * u < R.rot, inter = R.interleaved != 0;
+    int at_a, at_b;
+    rope_unit_offsets(u, R.rot, inter, at_a, at_b);
+    const int64_t row_bytes = (int64_t)P.row_vecs * 16, stride = P.h_kv * row_bytes;
+    char* pool = static_cast<char*>(P.pool[0]) + g * row_bytes;
+    float* scales = E == kElemInt8 ? P.scale[0] + (size_t)g * P.page_size : nullptr;
+    auto scale_at = [&](int slot) {
+      const int page = P.ps_shift >= 0 ? slot >> P.ps_shift : slot / P.page_size;
+      return scales + (int64_t)page * (P.h_kv - 1) * P.page_size + slot;
+    };
+    compact_walk<U, CompactUnit<E>, int, E == kElemInt8>(
         keep, new_len, L, per, tid / lanes < per ? tid / lanes : -1, tid % lanes == 0,
         P.error_word,
         [&](int j) {
           const CompactPlace p = compact_place(P, table, j);
           return p.page < 0 ? -1 : p.page * P.page_size + p.off;
         },
-        [&](int slot) { return pool + slot * stride; });
-  } else if (P.scale[0] && kind < 2 * P.slices + 2) {
-    float* scale = (kind == 2 * P.slices ? P.scale[0] : P.scale[1]) + (size_t)g * P.page_size;
-    compact_walk<U, float, int64_t>(
-        keep, new_len, L, T, tid, false, nullptr,
-        [&](int j) -> int64_t {
-          const CompactPlace p = compact_place(P, table, j);
-          return p.page < 0 ? -1 : (int64_t)p.page * P.h_kv * P.page_size + p.off;
+        [&](int slot) {
+          CompactUnit<E> x;
+          x.load(pool + slot * stride, at_a, at_b);
+          if constexpr (E == kElemInt8) x.scale = __ldcg(scale_at(slot));
+          return x;
         },
-        [&](int64_t slot) { return scale + slot; });
+        [&](int slot, CompactUnit<E>& x, int by) {
+          float y[16];
+          if (E != kElemInt8 && !turned) {
+            x.store(pool + slot * stride, at_a, at_b);
+            return;
+          }
+          x.values(y);
+          if constexpr (E == kElemInt8) {
+#pragma unroll
+            for (int k = 0; k < 16; ++k) y[k] *= x.scale;
+          }
+          if (slot >= 0 && turned)
+            rope_unit_rotate(y, inter,
+                             [&](int k) { return rope_turn(__ldg(R.freqs + 8 * u + k), by); });
+          if constexpr (E == kElemInt8) {
+            bool bad = false;
+            float m = rope_unit_max(y, bad);
+            for (int o = lanes >> 1; o > 0; o >>= 1)
+              m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
+            if (slot < 0) return;
+            const float sc = __fdiv_rn(m, 127.f);
+            x.set_codes(y, sc);
+            if (tid % lanes == 0) *scale_at(slot) = sc;
+            if (bad) report(P.error_word, TL_DEVERR_VALUE_RANGE);
+          } else {
+            x.set(y);
+          }
+          x.store(pool + slot * stride, at_a, at_b);
+        });
+  } else if (kind < R.slices + P.slices) {
+    compact_rows<T, U>(P, P.pool[1], P.slices, kind - R.slices, g, keep, table, L, new_len);
+  } else if (E == kElemInt8 && kind == R.slices + P.slices) {
+    compact_scales<T, U>(P, P.scale[1], g, keep, table, L, new_len);
   } else {
-    float* m = P.mass + (size_t)row * P.mass_len;
-    compact_walk<U, float, int>(
-        keep, new_len, L, T, tid, false, nullptr, [&](int j) { return j; },
-        [&](int j) { return m + j; });
-    // positions that no key holds any more gather nothing; the last batch's
-    // loads are behind the walk's barrier
-    __syncthreads();
-    for (int j = new_len + tid; j < L; j += T) m[j] = 0.f;
+    compact_mass<T, U>(P, row, keep, L, new_len);
   }
 }
 
@@ -195,7 +318,8 @@ static tl_status compact_impl(void* k, void* v, float* k_scales, float* v_scales
                               const int32_t* context_lens, const int32_t* keep, int32_t n_keep,
                               const int32_t* new_lens, float* mass, int32_t mass_len, int32_t B,
                               int32_t h_kv, int32_t d, int32_t num_pages, int32_t page_size,
-                              int elem, uint32_t* error_word, void* stream) {
+                              int elem, uint32_t* error_word, void* stream,
+                              CompactTurn* turn = nullptr) {
   if (B <= 0 || h_kv <= 0 || d <= 0 || num_pages <= 0 || page_size <= 0 ||
       max_pages_per_seq <= 0 || n_keep <= 0 || (mass && mass_len <= 0))
     return TL_ERR_INVALID_ARG;
@@ -208,6 +332,13 @@ static tl_status compact_impl(void* k, void* v, float* k_scales, float* v_scales
   if (elem == 0) return TL_ERR_UNSUPPORTED;
   const int64_t row_bytes = (int64_t)d * elem;
   if (row_bytes % 16 != 0) return TL_ERR_INVALID_ARG;
+  if (turn) {
+    if (turn->rot < 2 || turn->rot % 2 || turn->rot > d || !turn->freqs ||
+        (reinterpret_cast<uintptr_t>(turn->freqs) & 7u))
+      return TL_ERR_INVALID_ARG;
+    if (d % 16 || turn->rot % 16 || (k_scales && ((d & (d - 1)) || d > 512)))
+      return TL_ERR_UNSUPPORTED;
+  }
   if (row_bytes > 4096 || page_size > 256 ||
       (int64_t)num_pages * page_size >= ((int64_t)1 << 31) || (int64_t)B * h_kv > INT32_MAX ||
       n_keep > (1 << 30) || (mass && mass_len > (1 << 30)))
@@ -257,6 +388,35 @@ static tl_status compact_impl(void* k, void* v, float* k_scales, float* v_scales
   while (P.row_vecs % (2 * P.slices) == 0 && P.row_vecs / (2 * P.slices) >= 2 &&
          rows * 2 * P.slices < 2 * num_sms())
     P.slices *= 2;
+  if (turn) {
+    // K rows alike, a slice being whole 32-byte sectors: units whose runs fill
+    // them (an int8 row is one slice, for its scale)
+    CompactTurn R = *turn;
+    R.units = d / 16;
+    R.slices = 1;
+    const int run = 8 * elem;  // bytes of a unit's run
+    const int least = R.interleaved ? std::max(1, 16 / run) : std::max(1, 32 / run);
+    if (!k_scales)
+      while (R.units % (2 * R.slices) == 0 && R.units / (2 * R.slices) >= least &&
+             rows * 2 * R.slices < 2 * num_sms())
+        R.slices *= 2;
+    const bool big = rows * 2 * P.slices <= 2 * num_sms() || P.row_vecs / P.slices > 128 ||
+                     R.units / R.slices > 128;
+    const dim3 grid((unsigned)rows, (unsigned)(R.slices + P.slices + (k_scales ? 1 : 0) +
+                                               (mass ? 1 : 0)));
+    cudaStream_t st = (cudaStream_t)stream;
+#define TL_COMPACT_ROPE(E)                                          \
+  do {                                                              \
+    if (big) compact_rope_kernel<512, 2, E><<<grid, 512, 0, st>>>(P, R); \
+    else compact_rope_kernel<128, 4, E><<<grid, 128, 0, st>>>(P, R);     \
+  } while (0)
+    if (k_scales) TL_COMPACT_ROPE(kElemInt8);
+    else if (elem == 1) TL_COMPACT_ROPE(kElemE4m3);
+    else if (elem == 2) TL_COMPACT_ROPE(kElemBf16);
+    else TL_COMPACT_ROPE(kElemF32);
+#undef TL_COMPACT_ROPE
+    return launch_status();
+  }
   const dim3 grid((unsigned)rows, (unsigned)(2 * P.slices + (k_scales ? 2 : 0) + (mass ? 1 : 0)));
   // otherwise small CTAs, whose barriers hold few rows back: one sequence of
   // 8,192 rows kept takes 23 us with 1,024 threads and 33 with 512, 64
@@ -345,4 +505,30 @@ extern "C" tl_status tl_kv_cache_compact_int8(int8_t* k_codes, int8_t* v_codes, 
   return tl::compact_impl(k_codes, v_codes, k_scales, v_scales, block_table, max_pages_per_seq,
                           context_lens, keep, n_keep, new_lens, mass, mass_len, B, h_kv, d,
                           num_pages, page_size, 1, error_word, stream);
+}
+
+extern "C" tl_status tl_kv_cache_compact_rope(
+    void* k_cache, void* v_cache, const int32_t* block_table, int32_t max_pages_per_seq,
+    const int32_t* context_lens, const int32_t* keep, int32_t n_keep, const int32_t* new_lens,
+    float* mass, int32_t mass_len, const uint64_t* freqs, int32_t rot_dim, int32_t interleaved,
+    int32_t B, int32_t h_kv, int32_t d, int32_t num_pages, int32_t page_size, tl_dtype dtype,
+    uint32_t* error_word, void* stream) {
+  const int elem = dtype == TL_F32 ? 4 : dtype == TL_BF16 ? 2 : dtype == TL_FP8_E4M3 ? 1 : 0;
+  tl::CompactTurn turn = {freqs, rot_dim, interleaved != 0, 0, 0};
+  return tl::compact_impl(k_cache, v_cache, nullptr, nullptr, block_table, max_pages_per_seq,
+                          context_lens, keep, n_keep, new_lens, mass, mass_len, B, h_kv, d,
+                          num_pages, page_size, elem, error_word, stream, &turn);
+}
+
+extern "C" tl_status tl_kv_cache_compact_rope_int8(
+    int8_t* k_codes, int8_t* v_codes, float* k_scales, float* v_scales,
+    const int32_t* block_table, int32_t max_pages_per_seq, const int32_t* context_lens,
+    const int32_t* keep, int32_t n_keep, const int32_t* new_lens, float* mass, int32_t mass_len,
+    const uint64_t* freqs, int32_t rot_dim, int32_t interleaved, int32_t B, int32_t h_kv,
+    int32_t d, int32_t num_pages, int32_t page_size, uint32_t* error_word, void* stream) {
+  if (!k_scales || !v_scales) return TL_ERR_INVALID_ARG;
+  tl::CompactTurn turn = {freqs, rot_dim, interleaved != 0, 0, 0};
+  return tl::compact_impl(k_codes, v_codes, k_scales, v_scales, block_table, max_pages_per_seq,
+                          context_lens, keep, n_keep, new_lens, mass, mass_len, B, h_kv, d,
+                          num_pages, page_size, 1, error_word, stream, &turn);
 }
