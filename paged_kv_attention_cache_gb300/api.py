@@ -988,12 +988,13 @@ def _need_rows(t, name, n, heads, d, device, dtype=None):
         raise TypeError(f"{name} must be a CUDA tensor")
     if dtype is not None and t.dtype != dtype:
         raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
-    if t.dim() != 3 or any(w is not None and a != w for a, w in zip(t.shape, (n, heads, d))):
-        raise ValueError(f"{name} must have shape {(n, heads, d)} (None: any), got "
-                         f"{tuple(t.shape)}")
+    ts = t.shape
+    if len(ts) != 3 or (n is not None and ts[0] != n) or (heads is not None and ts[1] != heads) \
+            or (d is not None and ts[2] != d):
+        raise ValueError(f"{name} must have shape {(n, heads, d)} (None: any), got {tuple(ts)}")
     s = t.stride()
-    if t.numel() and ((t.shape[2] > 1 and s[2] != 1) or
-                      (t.shape[1] > 1 and s[1] != t.shape[2])):
+    if (s[2] != 1 or s[1] != ts[2]) and t.numel() and \
+            ((ts[2] > 1 and s[2] != 1) or (ts[1] > 1 and s[1] != ts[2])):
         raise ValueError(f"the rows of one token of {name} must be contiguous")
     if t.get_device() != device.index:
         raise ValueError(f"{name} is on {t.device}, the call's tensors are on {device}")
@@ -1003,22 +1004,10 @@ def _need_rows(t, name, n, heads, d, device, dtype=None):
 def _need_table_of_turns(freqs, d, device):
     """freqs [rot_dim / 2] int64; returns rot_dim."""
     _need(freqs, "freqs", torch.int64, (None,), device)
-    if not 1 <= freqs.shape[0] <= d // 2:
-        raise ValueError(f"freqs must have 1 to d / 2 = {d // 2} entries, got {freqs.shape[0]}")
-    return 2 * freqs.shape[0]
-
-
-def _need_turns(positions, freqs, n, d, device):
-    """positions [n] int32 and the table of turns; returns rot_dim."""
-    _need(positions, "positions", torch.int32, (n,), device)
-    return _need_table_of_turns(freqs, d, device)
-
-
-def _rotated_out(out, name, shape, dtype, device, stream):
-    """The output of rotated rows and its tokens' stride."""
-    if out is None:
-        out = _returned(shape, dtype, device, stream)
-    return out, _need_rows(out, name, *shape, device, dtype)
+    n = freqs.shape[0]
+    if not 1 <= n <= d // 2:
+        raise ValueError(f"freqs must have 1 to d / 2 = {d // 2} entries, got {n}")
+    return 2 * n
 
 
 def tl_rope(x: torch.Tensor, positions: torch.Tensor, freqs: torch.Tensor,
@@ -1030,33 +1019,43 @@ def tl_rope(x: torch.Tensor, positions: torch.Tensor, freqs: torch.Tensor,
     dev = x.device
     x_stride = _need_rows(x, "x", None, None, None, dev)
     N, H, d = x.shape
-    rot = _need_turns(positions, freqs, N, d, dev)
-    out, out_stride = _rotated_out(out, "out", (N, H, d), x.dtype, dev, stream)
+    dtype = x.dtype
+    _need(positions, "positions", torch.int32, (N,), dev)
+    rot = _need_table_of_turns(freqs, d, dev)
+    if out is None:
+        out, out_stride = _returned((N, H, d), dtype, dev, stream), H * d
+    else:
+        out_stride = _need_rows(out, "out", N, H, d, dev, dtype)
     _run("tl_rope", dev, stream,
-         _ptr(x), x_stride, _ptr(out), out_stride, _ptr(positions), _ptr(freqs), rot,
-         int(bool(interleaved)), float(rope_scale), N, H, d, _DTYPES.get(x.dtype, -1))
+         x.data_ptr(), x_stride, out.data_ptr(), out_stride, positions.data_ptr(),
+         freqs.data_ptr(), rot, 1 if interleaved else 0, rope_scale, N, H, d,
+         _DTYPES.get(dtype, -1))
     return out
 
 
 def _write_rope_rows(q, k_new, v_new, slot_mapping, positions, freqs, q_out, hkv, d, dev, stream):
-    """The rows of an append, checked: (arguments up to v_stride, N, H_q, rot_dim, q_out)."""
+    """The rows of an append, checked: (arguments up to src_dtype, N, H_q, rot_dim, q_out)."""
     k_stride = _need_rows(k_new, "k_new", None, hkv, d, dev)
-    N = k_new.shape[0]
-    v_stride = _need_rows(v_new, "v_new", N, hkv, d, dev, k_new.dtype)
+    N, dtype = k_new.shape[0], k_new.dtype
+    v_stride = _need_rows(v_new, "v_new", N, hkv, d, dev, dtype)
     _need(slot_mapping, "slot_mapping", torch.int64, (N,), dev)
-    rot = _need_turns(positions, freqs, N, d, dev)
+    _need(positions, "positions", torch.int32, (N,), dev)
+    rot = _need_table_of_turns(freqs, d, dev)
     hq = q_stride = out_stride = 0
     if q is None:
         if q_out is not None:
             raise ValueError("q_out without q")
     else:
-        q_stride = _need_rows(q, "q", N, None, d, dev, k_new.dtype)
+        q_stride = _need_rows(q, "q", N, None, d, dev, dtype)
         hq = q.shape[1]
         if hq < 1:
             raise ValueError("q needs at least one head (None: keys and values alone)")
-        q_out, out_stride = _rotated_out(q_out, "q_out", (N, hq, d), q.dtype, dev, stream)
-    return (_ptr(q), q_stride, _ptr(q_out), out_stride, _ptr(k_new), k_stride, _ptr(v_new),
-            v_stride, _DTYPES.get(k_new.dtype, -1)), N, hq, rot, q_out
+        if q_out is None:
+            q_out, out_stride = _returned((N, hq, d), dtype, dev, stream), hq * d
+        else:
+            out_stride = _need_rows(q_out, "q_out", N, hq, d, dev, dtype)
+    return (_ptr(q), q_stride, _ptr(q_out), out_stride, k_new.data_ptr(), k_stride,
+            v_new.data_ptr(), v_stride, _DTYPES.get(dtype, -1)), N, hq, rot, q_out
 
 
 def tl_kv_cache_write_rope(q: Optional[torch.Tensor], k_new: torch.Tensor, v_new: torch.Tensor,
@@ -1077,7 +1076,7 @@ def tl_kv_cache_write_rope(q: Optional[torch.Tensor], k_new: torch.Tensor, v_new
                                                q_out, hkv, d, dev, stream)
     _run("tl_kv_cache_write_rope", dev, stream,
          *rows, _ptr(k_cache), _ptr(v_cache), _ptr(slot_mapping), _ptr(positions), _ptr(freqs),
-         rot, int(bool(interleaved)), float(rope_scale), N, P, ps, hq, hkv, d,
+         rot, 1 if interleaved else 0, rope_scale, N, P, ps, hq, hkv, d,
          _DTYPES.get(k_cache.dtype, -1), _err_word(error_word, dev))
     return q_out
 
@@ -1099,7 +1098,7 @@ def tl_kv_cache_write_rope_int8(q: Optional[torch.Tensor], k_new: torch.Tensor,
                                                q_out, hkv, d, dev, stream)
     _run("tl_kv_cache_write_rope_int8", dev, stream,
          *rows, _ptr(k_codes), _ptr(v_codes), _ptr(k_scales), _ptr(v_scales), _ptr(slot_mapping),
-         _ptr(positions), _ptr(freqs), rot, int(bool(interleaved)), float(rope_scale), N, P, ps,
+         _ptr(positions), _ptr(freqs), rot, 1 if interleaved else 0, rope_scale, N, P, ps,
          hq, hkv, d, _err_word(error_word, dev))
     return q_out
 

@@ -236,11 +236,11 @@ struct CompactTurn {
 };
 
 template <int E>
-struct CompactUnit : RopeUnit<E> {
+struct CompactUnit : RopeUnit<E, E == kElemF32 ? 4 : 8> {
   float scale;  // int8
 };
 
-template <int T, int U, int E>
+template <int T, int U, int E, bool INTER>
 __global__ void __launch_bounds__(T) compact_rope_kernel(CompactParams P, CompactTurn R) {
   const int tid = threadIdx.x;
   const int row = blockIdx.x, b = row / P.h_kv, g = row % P.h_kv;
@@ -252,9 +252,10 @@ __global__ void __launch_bounds__(T) compact_rope_kernel(CompactParams P, Compac
   if (kind < R.slices) {
     const int lanes = R.units / R.slices, per = T / lanes;
     const int u = kind * lanes + tid % lanes;
-    const bool turned = 16 * u < R.rot, inter = R.interleaved != 0;
-    int at_a, at_b;
-    rope_unit_offsets(u, R.rot, inter, at_a, at_b);
+    constexpr int W = 16 / CompactUnit<E>::NW;
+    using Pairs = RopePairs<INTER, W>;
+    int at[16 / W];
+    rope_unit_words<INTER, W>(u, R.units * 16, R.rot, at);
     const int64_t row_bytes = (int64_t)P.row_vecs * 16, stride = P.h_kv * row_bytes;
     char* pool = static_cast<char*>(P.pool[0]) + g * row_bytes;
     float* scales = E == kElemInt8 ? P.scale[0] + (size_t)g * P.page_size : nullptr;
@@ -271,14 +272,14 @@ __global__ void __launch_bounds__(T) compact_rope_kernel(CompactParams P, Compac
         },
         [&](int slot) {
           CompactUnit<E> x;
-          x.load(pool + slot * stride, at_a, at_b);
+          x.load(pool + slot * stride, at);
           if constexpr (E == kElemInt8) x.scale = __ldcg(scale_at(slot));
           return x;
         },
         [&](int slot, CompactUnit<E>& x, int by) {
           float y[16];
-          if (E != kElemInt8 && !turned) {
-            x.store(pool + slot * stride, at_a, at_b);
+          if (E != kElemInt8 && (INTER ? at[0] >= R.rot : 16 * u >= R.rot)) {
+            x.store(pool + slot * stride, at);
             return;
           }
           x.values(y);
@@ -286,9 +287,10 @@ __global__ void __launch_bounds__(T) compact_rope_kernel(CompactParams P, Compac
 #pragma unroll
             for (int k = 0; k < 16; ++k) y[k] *= x.scale;
           }
-          if (slot >= 0 && turned)
-            rope_unit_rotate(y, inter,
-                             [&](int k) { return rope_turn(__ldg(R.freqs + 8 * u + k), by); });
+          if (slot >= 0)
+            rope_unit_rotate<INTER, W>(
+                y, [&](int k) { return Pairs::turn(at, k, u, R.rot); },
+                [&](int k) { return rope_turn(__ldg(R.freqs + Pairs::index(at, k)), by); });
           if constexpr (E == kElemInt8) {
             bool bad = false;
             float m = rope_unit_max(y, bad);
@@ -296,13 +298,19 @@ __global__ void __launch_bounds__(T) compact_rope_kernel(CompactParams P, Compac
               m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
             if (slot < 0) return;
             const float sc = __fdiv_rn(m, 127.f);
-            x.set_codes(y, sc);
+            x.set_codes(y, sc, !bad);
             if (tid % lanes == 0) *scale_at(slot) = sc;
             if (bad) report(P.error_word, TL_DEVERR_VALUE_RANGE);
           } else {
+            const CompactUnit<E> was = x;
             x.set(y);
+            if (INTER) {  // words behind the rotated part keep their bits
+#pragma unroll
+              for (int w = 0; w < x.NW; ++w)
+                if (at[w] >= R.rot) x.w[w] = was.w[w];
+            }
           }
-          x.store(pool + slot * stride, at_a, at_b);
+          x.store(pool + slot * stride, at);
         });
   } else if (kind < R.slices + P.slices) {
     compact_rows<T, U>(P, P.pool[1], P.slices, kind - R.slices, g, keep, table, L, new_len);
@@ -389,13 +397,12 @@ static tl_status compact_impl(void* k, void* v, float* k_scales, float* v_scales
          rows * 2 * P.slices < 2 * num_sms())
     P.slices *= 2;
   if (turn) {
-    // K rows alike, a slice being whole 32-byte sectors: units whose runs fill
-    // them (an int8 row is one slice, for its scale)
+    // K rows alike, a slice being units whose words fill whole 32-byte sectors
+    // (an int8 row is one slice, for its scale)
     CompactTurn R = *turn;
     R.units = d / 16;
     R.slices = 1;
-    const int run = 8 * elem;  // bytes of a unit's run
-    const int least = R.interleaved ? std::max(1, 16 / run) : std::max(1, 32 / run);
+    const int least = elem == 1 ? 4 : 2;  // words of 8 bytes, or of 16
     if (!k_scales)
       while (R.units % (2 * R.slices) == 0 && R.units / (2 * R.slices) >= least &&
              rows * 2 * R.slices < 2 * num_sms())
@@ -407,8 +414,11 @@ static tl_status compact_impl(void* k, void* v, float* k_scales, float* v_scales
     cudaStream_t st = (cudaStream_t)stream;
 #define TL_COMPACT_ROPE(E)                                          \
   do {                                                              \
-    if (big) compact_rope_kernel<512, 2, E><<<grid, 512, 0, st>>>(P, R); \
-    else compact_rope_kernel<128, 4, E><<<grid, 128, 0, st>>>(P, R);     \
+    auto kern = big ? (R.interleaved ? compact_rope_kernel<512, 2, E, true>  \
+                                     : compact_rope_kernel<512, 2, E, false>) \
+                    : (R.interleaved ? compact_rope_kernel<128, 4, E, true>   \
+                                     : compact_rope_kernel<128, 4, E, false>); \
+    kern<<<grid, big ? 512 : 128, 0, st>>>(P, R);                             \
   } while (0)
     if (k_scales) TL_COMPACT_ROPE(kElemInt8);
     else if (elem == 1) TL_COMPACT_ROPE(kElemE4m3);

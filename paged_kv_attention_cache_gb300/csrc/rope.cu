@@ -20,19 +20,84 @@ __global__ void __launch_bounds__(256) rope_rows_kernel(RopeRows R, int heads) {
     rope_row<F32, KIND>(R, r / heads, (int)(r % heads), lane);
 }
 
-static tl_status launch_rope(const RopeRows& R, bool f32, int kind, cudaStream_t st) {
+// One warp per item: P passes over a token's heads.  Bound: HBM (each row read
+// and written once).  What it took, on 16,384 tokens of 32 bf16 heads of 128
+// (268 MB) and on a prompts' append of 12,288 such tokens with 8 KV heads (369
+// MB, copies included):
+//   one warp a (token, head), an element pair a lane  127 us   175 us
+//   one pass of 4 heads a warp, 256 threads            59        89
+//   two passes                                         46        63
+//   four, streaming accesses, 80 registers             43        56
+//   four, CTAs of two warps                            42.4      55.3 (6.68 TB/s)
+// Passes amortise a token's angles and keep more loads in flight; beyond the
+// registers of three 256-thread CTAs an SM they spill (four f32 passes 34 us
+// against 20 with two).  Small CTAs give their registers back as soon as their
+// own rows are written (512 threads: 51 and 69 us).
+constexpr int kRopeThreads = 64;
+template <bool F32, int KIND, bool INTER, int P>
+__global__ void __launch_bounds__(kRopeThreads, 768 / kRopeThreads)
+    rope_units_kernel(RopeRows R, int heads, int U, int HW, uint32_t per_token, uint32_t items) {
+  constexpr int warps = kRopeThreads / 32;
+  __shared__ float4 cs[warps][4 * kRopeMaxUnits];
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const uint32_t i = blockIdx.x * warps + warp;
+  if (i >= items) return;
+  const uint32_t t = i / per_token;
+  rope_units<F32, KIND, INTER, P>(R, t, (int)(i - t * per_token) * P * HW, heads, U, HW, lane,
+                                  cs[warp]);
+}
+
+// The most passes: as many as keep a kernel in its 80 registers.
+template <bool F32, int KIND>
+constexpr int kRopePasses = (KIND == kRopeSame ? 4 : 2) / (F32 ? 2 : 1);
+
+template <bool F32, int KIND>
+static tl_status launch_units(const RopeRows& R, int heads, cudaStream_t st) {
+  const int U = R.d / 16, HW = 32 / U, passes = (heads + HW - 1) / HW;
+  // fewer where a token has fewer, and while warps are few: 64 tokens of a
+  // decode step take 2.5 us with one pass, 2.7 with two and 3.4 with four
+  int P = kRopePasses<F32, KIND>;
+  while (P > 1 && (P > passes || (int64_t)R.n * ((passes + P - 1) / P) < 16 * (int64_t)num_sms()))
+    P /= 2;
+  const uint32_t per_token = (passes + P - 1) / P, items = R.n * per_token;
+  const unsigned grid = (items + kRopeThreads / 32 - 1) / (kRopeThreads / 32);
+  auto launch = [&](auto kern) {
+    kern<<<grid, kRopeThreads, 0, st>>>(R, heads, U, HW, per_token, items);
+    return launch_status();
+  };
+  if constexpr (kRopePasses<F32, KIND> >= 4)
+    if (P == 4)
+      return R.interleaved ? launch(rope_units_kernel<F32, KIND, true, 4>)
+                           : launch(rope_units_kernel<F32, KIND, false, 4>);
+  if constexpr (kRopePasses<F32, KIND> >= 2)
+    if (P == 2)
+      return R.interleaved ? launch(rope_units_kernel<F32, KIND, true, 2>)
+                           : launch(rope_units_kernel<F32, KIND, false, 2>);
+  return R.interleaved ? launch(rope_units_kernel<F32, KIND, true, 1>)
+                       : launch(rope_units_kernel<F32, KIND, false, 1>);
+}
+
+template <bool F32, int KIND>
+static tl_status launch_rows(const RopeRows& R, cudaStream_t st) {
   const int heads = R.h_q + (R.slots ? 2 * R.h_kv : 0);
+  // (items of a pass are counted in 32 bits)
+  if (rope_in_units(R, F32 ? 4 : 2) && (int64_t)R.n * heads < ((int64_t)1 << 31))
+    return launch_units<F32, KIND>(R, heads, st);
+  // a warp a row, element by element
   const int64_t rows = (int64_t)R.n * heads;
-  const unsigned blocks =
-      (unsigned)std::min<int64_t>((rows + 7) / 8, (int64_t)num_sms() * 64);
-  auto kern = f32 ? (kind == kRopeSame   ? rope_rows_kernel<true, kRopeSame>
-                     : kind == kRopeE4m3 ? rope_rows_kernel<true, kRopeE4m3>
-                                         : rope_rows_kernel<true, kRopeInt8>)
-                  : (kind == kRopeSame   ? rope_rows_kernel<false, kRopeSame>
-                     : kind == kRopeE4m3 ? rope_rows_kernel<false, kRopeE4m3>
-                                         : rope_rows_kernel<false, kRopeInt8>);
-  kern<<<blocks, 256, 0, st>>>(R, heads);
+  const unsigned blocks = (unsigned)std::min<int64_t>((rows + 7) / 8, (int64_t)num_sms() * 64);
+  rope_rows_kernel<F32, KIND><<<blocks, 256, 0, st>>>(R, heads);
   return launch_status();
+}
+
+static tl_status launch_rope(const RopeRows& R, bool f32, int kind, cudaStream_t st) {
+  if (f32)
+    return kind == kRopeSame   ? launch_rows<true, kRopeSame>(R, st)
+           : kind == kRopeE4m3 ? launch_rows<true, kRopeE4m3>(R, st)
+                               : launch_rows<true, kRopeInt8>(R, st);
+  return kind == kRopeSame   ? launch_rows<false, kRopeSame>(R, st)
+         : kind == kRopeE4m3 ? launch_rows<false, kRopeE4m3>(R, st)
+                             : launch_rows<false, kRopeInt8>(R, st);
 }
 
 static tl_status write_rope_impl(const void* q, int64_t q_stride, void* q_out,

@@ -52,42 +52,60 @@ TL_DEVINLINE void rope_rotate(float& lo, float& hi, float c, float s) {
 
 // ----------------------------------------------------------------- units --
 //
-// A unit is 16 elements of a row that hold 8 whole pairs: in the layout of
-// halves the 8 elements from 8u and their partners from rot/2 + 8u, otherwise
-// the 16 from 16u, for u < rot/16; behind the rotated part the 16 from 16u.
-// Rows whose d and rot are multiples of 16 are made of such units, each two
-// contiguous runs of 8 elements (16 bytes in 16 bits).
+// A row whose d and rot are multiples of 16 is moved in units of 16 elements
+// with 8 whole pairs, one a lane: 16 / W words of W elements (16 bytes of 16 or
+// 32 bits), each beside the next unit's, so that a warp's access to one word
+// of its units is contiguous.  In the layout of halves, for unit u < rot/16,
+// words of the lower half (at W u, and for W = 4 at rot/4 + W u) and their
+// partners rot/2 further; otherwise word w at w d W / 16 + W u.  Units behind
+// the rotated part of the halves lie in it as the latter do in the whole row.
+constexpr int kRopeMaxUnits = 16;  // of a row moved in units (d up to 256)
 enum RopeElem { kElemBf16, kElemF32, kElemE4m3, kElemInt8 };
 
-TL_DEVINLINE void rope_unit_offsets(int u, int rot, bool interleaved, int& a, int& b) {
-  const bool halves = !interleaved && 16 * u < rot;
-  a = halves ? 8 * u : 16 * u;
-  b = halves ? (rot >> 1) + 8 * u : 16 * u + 8;
+template <bool INTER, int W>
+TL_DEVINLINE void rope_unit_words(int u, int d, int rot, int* at) {
+  constexpr int NW = 16 / W;
+  if (!INTER && 16 * u < rot) {
+#pragma unroll
+    for (int w = 0; w < NW; ++w)
+      at[w] = W * u + (w % (NW / 2)) * (rot >> 2) + (w >= NW / 2 ? rot >> 1 : 0);
+  } else {
+    const int from = INTER ? 0 : rot;
+#pragma unroll
+    for (int w = 0; w < NW; ++w) at[w] = from + w * ((d - from) / NW) + W * (u - (from >> 4));
+  }
 }
 
-// A unit as it lies in memory: run a, then run b.
-template <int E>
+// The 8 pairs of a unit are n consecutive ones per word (of the lower half).
+template <bool INTER, int W>
+struct RopePairs {
+  static constexpr int n = INTER ? W / 2 : W;
+  // of the pairs from the k-th on: whether they turn, and the first one's index
+  static TL_DEVINLINE bool turn(const int* at, int k, int u, int rot) {
+    return INTER ? at[k / n] < rot : 16 * u < rot;
+  }
+  static TL_DEVINLINE int index(const int* at, int k) {
+    return (INTER ? at[k / n] >> 1 : at[k / n]) + k % n;
+  }
+};
+
+// A unit as it lies in memory.
+template <int E, int W>
 struct RopeUnit {
-  using W = typename std::conditional<E == kElemBf16 || E == kElemF32, uint4, uint2>::type;
   static constexpr int kBytes = E == kElemF32 ? 4 : E == kElemBf16 ? 2 : 1;  // of an element
-  static constexpr int kRun = E == kElemF32 ? 2 : 1;                        // words of a run
-  W w[2 * kRun];
-  // row: the row's first element; a, b: the runs' first elements
-  TL_DEVINLINE void load(const char* row, int a, int b) {
+  static constexpr int NW = 16 / W;
+  using Word = typename std::conditional<
+      W * kBytes == 16, uint4, typename std::conditional<W * kBytes == 8, uint2, uint32_t>::type>::type;
+  Word w[NW];
+  TL_DEVINLINE void load(const char* row, const int* at) {
 #pragma unroll
-    for (int i = 0; i < kRun; ++i) {
-      w[i] = __ldcg(reinterpret_cast<const W*>(row + a * kBytes) + i);
-      w[kRun + i] = __ldcg(reinterpret_cast<const W*>(row + b * kBytes) + i);
-    }
+    for (int i = 0; i < NW; ++i) w[i] = __ldcs(reinterpret_cast<const Word*>(row + at[i] * kBytes));
   }
-  TL_DEVINLINE void store(char* row, int a, int b) const {
+  TL_DEVINLINE void store(char* row, const int* at) const {
 #pragma unroll
-    for (int i = 0; i < kRun; ++i) {
-      reinterpret_cast<W*>(row + a * kBytes)[i] = w[i];
-      reinterpret_cast<W*>(row + b * kBytes)[i] = w[kRun + i];
-    }
+    for (int i = 0; i < NW; ++i) __stcs(reinterpret_cast<Word*>(row + at[i] * kBytes), w[i]);
   }
-  // the values, run a then run b (int8: codes)
+  // the values, word by word (int8: codes)
   TL_DEVINLINE void values(float* x) const {
     const uint32_t* v = reinterpret_cast<const uint32_t*>(w);
     if constexpr (E == kElemF32) {
@@ -128,44 +146,69 @@ struct RopeUnit {
       for (int i = 0; i < 4; ++i) v[i] = e4m3x4(x[4 * i], x[4 * i + 1], x[4 * i + 2], x[4 * i + 3]);
     }
   }
-  // int8: the codes of values x with scale sc (as quantize4_int8)
-  TL_DEVINLINE void set_codes(const float* x, float sc) {
+  // int8: the codes of values x with scale sc, x / sc in binary32 rounded half
+  // to even as quantize4_int8's; finite: every x is.  The quotient comes from
+  // the reciprocal: with |x / sc| <= 127 it is within 3 x 2^-24 x 127 < 2^-15 of
+  // the correctly rounded one, so only values that near to the middle of two
+  // codes are divided.
+  TL_DEVINLINE void set_codes(const float* x, float sc, bool finite) {
+    constexpr float kWhole = 12582912.f;  // 1.5 x 2^23: adding it rounds to a whole number
     uint32_t* v = reinterpret_cast<uint32_t*>(w);
+    const float inv = __frcp_rn(sc);
+    const bool normal = finite && sc >= 1e-37f;  // so is the reciprocal
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
-      uint32_t word = 0;
+      uint32_t code[4];
+      bool divide = !normal;
 #pragma unroll
       for (int k = 0; k < 4; ++k) {
-        const float y = x[4 * i + k];
-        float r = 0.f;
-        if (isfinite(y) && sc > 0.f) r = fminf(fmaxf(rintf(__fdiv_rn(y, sc)), -127.f), 127.f);
-        word |= (uint32_t)(uint8_t)(int8_t)__float2int_rn(r) << (8 * k);
+        const float q = x[4 * i + k] * inv, r = q + kWhole;
+        divide |= fabsf(fabsf(q - (r - kWhole)) - 0.5f) < 0x1p-15f;
+        code[k] = __float_as_uint(r);
       }
-      v[i] = word;
+      if (divide)
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+          float r = 0.f;
+          if (isfinite(x[4 * i + k]) && sc > 0.f)
+            r = fminf(fmaxf(rintf(__fdiv_rn(x[4 * i + k], sc)), -127.f), 127.f);
+          code[k] = (uint32_t)__float2int_rn(r);
+        }
+      v[i] = __byte_perm(__byte_perm(code[0], code[1], 0x0040),
+                         __byte_perm(code[2], code[3], 0x0040), 0x5410);
     }
   }
 };
 
 // The largest finite magnitude of a unit's values; bad: one is not finite.
+// (Magnitudes compare as their bits do.)
 TL_DEVINLINE float rope_unit_max(const float* x, bool& bad) {
+  uint32_t top = 0;
+#pragma unroll
+  for (int i = 0; i < 16; ++i) top = max(top, __float_as_uint(x[i]) & 0x7fffffffu);
+  bad = top >= 0x7f800000u;
+  if (!bad) return __uint_as_float(top);
   float m = 0.f;
 #pragma unroll
-  for (int i = 0; i < 16; ++i) {
+  for (int i = 0; i < 16; ++i)
     if (isfinite(x[i])) m = fmaxf(m, fabsf(x[i]));
-    else bad = true;
-  }
   return m;
 }
 
-// The 8 pairs of a unit's values, turned by turn(k).
-template <class Turn>
-TL_DEVINLINE void rope_unit_rotate(float* x, bool interleaved, Turn turn) {
+// A unit's values with its pairs turned by turn(k), k of them where `turns(k)`.
+template <bool INTER, int W, class Turns, class Turn>
+TL_DEVINLINE void rope_unit_rotate(float* x, Turns turns, Turn turn) {
+  constexpr int n = RopePairs<INTER, W>::n;
 #pragma unroll
-  for (int k = 0; k < 8; ++k) {
-    const float2 cs = turn(k);
-    if (interleaved) rope_rotate(x[2 * k], x[2 * k + 1], cs.x, cs.y);
-    else rope_rotate(x[k], x[8 + k], cs.x, cs.y);
-  }
+  for (int g = 0; g < 8; g += n)
+    if (turns(g)) {
+#pragma unroll
+      for (int k = g; k < g + n; ++k) {
+        const float2 cs = turn(k);
+        if (INTER) rope_rotate(x[2 * k], x[2 * k + 1], cs.x, cs.y);
+        else rope_rotate(x[k], x[8 + k], cs.x, cs.y);
+      }
+    }
 }
 
 // The rows of one call: h_q query heads, then h_kv key heads, then h_kv value
@@ -190,6 +233,13 @@ struct RopeRows {
 // codes and scales.
 enum { kRopeSame = 0, kRopeE4m3 = 1, kRopeInt8 = 2 };
 
+// Where the scale of head g at `slot` lies, [num_pages][h_kv][page_size] (slots
+// are below 2^31: a 32-bit division).
+TL_DEVINLINE int64_t rope_scale_place(const RopeRows& R, int64_t slot, int g) {
+  const uint32_t page = (uint32_t)slot / (uint32_t)R.page_size;
+  return ((int64_t)page * R.h_kv + g) * R.page_size + ((uint32_t)slot - page * R.page_size);
+}
+
 // A token's slot (-1: none), checked; `tell`: this thread reports.
 TL_DEVINLINE int64_t rope_slot(const RopeRows& R, int64_t t, int pos, bool tell) {
   if (!R.slots) return -1;
@@ -204,6 +254,124 @@ TL_DEVINLINE int64_t rope_slot(const RopeRows& R, int64_t t, int pos, bool tell)
     return -1;
   }
   return slot;
+}
+
+// P passes over a token's heads by one warp, in rotary units: lane l takes unit
+// u = l % U of head h0 + p HW + l / U in pass p, for U = d / 16 units a row and
+// HW = 32 / U heads a pass.  Every load comes before the angles, which the
+// warp's lanes make once for the token and every head reads (cs: 8 U float2 of
+// shared memory of the warp; two pairs, 16 bytes, of each lane side by side).
+template <bool F32, int KIND, bool INTER, int P>
+TL_DEVINLINE void rope_units(const RopeRows& R, int64_t t, int h0, int heads, int U, int HW,
+                             int lane, float4* cs) {
+  constexpr int W = F32 ? 4 : 8;
+  using Src = RopeUnit<F32 ? kElemF32 : kElemBf16, W>;
+  using Pairs = RopePairs<INTER, W>;
+  const int sub = lane / U, u = lane - sub * U, turned = R.h_q + R.h_kv;
+  const int pos = __ldg(R.positions + t);
+  int64_t slot = -1;
+  if (h0 + P * HW > R.h_q) slot = rope_slot(R, t, pos, lane == 0);
+  int at[16 / W];
+  rope_unit_words<INTER, W>(u, R.d, R.rot, at);
+  Src x[P];
+#pragma unroll
+  for (int p = 0; p < P; ++p) {
+    const int h = h0 + p * HW + sub;
+    if (sub >= HW || h >= heads) continue;
+    const bool is_q = h < R.h_q, is_v = h >= turned;
+    // (a single pass reads rows without a slot too: it does not wait for the slot)
+    if (P > 1 && !is_q && slot < 0) continue;
+    const char* row = static_cast<const char*>(is_q ? R.q : is_v ? R.v : R.k) +
+                      Src::kBytes * (t * (is_q ? R.q_stride : is_v ? R.v_stride : R.k_stride) +
+                                     (int64_t)(is_q ? h : is_v ? h - turned : h - R.h_q) * R.d);
+    x[p].load(row, at);
+  }
+  float2 turn[8];
+  if (pos >= 0 && h0 < turned) {
+    // chunk c of two pairs at (c % per) * (rot/4 / per) + c / per, for the `per`
+    // chunks that a lane reads one behind the other
+    constexpr int per = Pairs::n / 2;
+    const int step = (R.rot >> 2) / per;
+    float2* cs2 = reinterpret_cast<float2*>(cs);
+    for (int i = lane; i < R.rot >> 1; i += 32) {
+      const float2 c = rope_turn(__ldg(R.freqs + i), pos);
+      cs2[2 * ((i >> 1) % per * step + (i >> 1) / per) + (i & 1)] =
+          make_float2(c.x * R.scale, c.y * R.scale);
+    }
+    __syncwarp();
+#pragma unroll
+    for (int k = 0; k < 8; k += 2) {
+      if (!Pairs::turn(at, k, u, R.rot)) continue;
+      const int c = Pairs::index(at, k) >> 1;
+      const float4 f = cs[c % per * step + c / per];
+      turn[k] = make_float2(f.x, f.y);
+      turn[k + 1] = make_float2(f.z, f.w);
+    }
+    __syncwarp();  // (cs is the warp's next item's too)
+  }
+  auto turns = [&](int k) { return Pairs::turn(at, k, u, R.rot); };
+  auto of = [&](int k) { return turn[k]; };
+#pragma unroll
+  for (int p = 0; p < P; ++p) {
+    const int h = h0 + p * HW + sub;
+    const bool here = sub < HW && h < heads;
+    const bool is_q = h < R.h_q, is_v = h >= turned, rotates = pos >= 0 && !is_v;
+    if (KIND != kRopeInt8 && (!here || (!is_q && slot < 0))) continue;
+    float y[16];
+    if (KIND == kRopeSame || is_q) {
+      if (here) {
+        // (units behind the rotated part keep their bits)
+        if (rotates && (INTER || turns(0))) {
+          x[p].values(y);
+          rope_unit_rotate<INTER, W>(y, turns, of);
+          const Src was = x[p];
+          x[p].set(y);
+          if (INTER) {
+#pragma unroll
+            for (int w = 0; w < Src::NW; ++w)
+              if (at[w] >= R.rot) x[p].w[w] = was.w[w];
+          }
+        }
+        char* row =
+            is_q ? static_cast<char*>(R.q_out) + Src::kBytes * (t * R.out_stride + (int64_t)h * R.d)
+                 : static_cast<char*>(is_v ? R.v_dst : R.k_dst) +
+                       Src::kBytes * ((slot * R.h_kv + (is_v ? h - turned : h - R.h_q)) * R.d);
+        x[p].store(row, at);
+      }
+      // (an int8 pass with key or value rows goes on with all its lanes)
+      if (KIND != kRopeInt8 || h0 + (p + 1) * HW <= R.h_q) continue;
+    }
+    if constexpr (KIND != kRopeSame) {
+      const bool row = here && !is_q && slot >= 0;
+      const int g = is_v ? h - turned : h - R.h_q;
+      if (row) {
+        x[p].values(y);
+        if (rotates) rope_unit_rotate<INTER, W>(y, turns, of);
+      }
+      RopeUnit<KIND == kRopeInt8 ? kElemInt8 : kElemE4m3, W> codes;
+      if constexpr (KIND == kRopeE4m3) {
+        codes.set(y);
+      } else {
+        // the row's scale over its U lanes, in step with the warp's other lanes
+        bool bad = false;
+        float m = row ? rope_unit_max(y, bad) : 0.f;
+        if ((U & (U - 1)) == 0) {
+          for (int o = U >> 1; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
+        } else {
+          const float own = m;
+          for (int i = 0; i < U; ++i)
+            m = fmaxf(m, __shfl_sync(0xffffffffu, own, (sub * U + i) & 31));
+        }
+        if (!row) continue;
+        const float sc = __fdiv_rn(m, 127.f);
+        codes.set_codes(y, sc, !bad);
+        if (u == 0)
+          (is_v ? R.v_scales : R.k_scales)[rope_scale_place(R, slot, g)] = sc;
+        if (bad) report(R.error_word, TL_DEVERR_VALUE_RANGE);
+      }
+      codes.store(static_cast<char*>(is_v ? R.v_dst : R.k_dst) + (slot * R.h_kv + g) * R.d, at);
+    }
+  }
 }
 
 // One row (token t, head h of the h_q + 2 h_kv) by one warp, element by
@@ -302,8 +470,7 @@ __device__ void rope_row(const RopeRows& R, int64_t t, int h, int lane) {
     }
     for (int e = rot + lane; e < R.d; e += 32) dst[e] = code(value(e));
     if (lane == 0)
-      (is_v ? R.v_scales : R.k_scales)[(slot / R.page_size * R.h_kv + g) * R.page_size +
-                                       slot % R.page_size] = sc;
+      (is_v ? R.v_scales : R.k_scales)[rope_scale_place(R, slot, g)] = sc;
     if (__any_sync(0xffffffffu, bad) && lane == 0) report(R.error_word, TL_DEVERR_VALUE_RANGE);
   }
 }

@@ -27,6 +27,14 @@ inline bool aligned_to(const void* p, int bytes) {
   return (reinterpret_cast<uintptr_t>(p) & (uintptr_t)(bytes - 1)) == 0;
 }
 
+// Whether a call's rows are made of whole rotary units at 16-byte boundaries.
+inline bool rope_in_units(const RopeRows& R, int elem) {
+  auto row = [&](const void* p, int64_t stride) { return aligned16(p) && stride * elem % 16 == 0; };
+  return R.d % 16 == 0 && R.d <= 16 * kRopeMaxUnits && R.rot % 16 == 0 &&
+         row(R.q, R.q_stride) && row(R.q_out, R.out_stride) && row(R.k, R.k_stride) &&
+         row(R.v, R.v_stride);
+}
+
 // n > 0 rows of `row` elements read at x and written at out.
 inline tl_status rope_io_checked(const void* x, int64_t x_stride, const void* out,
                                  int64_t out_stride, int64_t n, int64_t row, int elem) {
