@@ -90,17 +90,15 @@ TL_DEVINLINE CompactPlace compact_place(const CompactParams& P, const int32_t* t
 
 // The walk: rows_per_pass rows of a pass, this thread's being row r of it
 // (r < 0: none), U passes a batch.  slot(j): where position j's element is
-// (-1: nowhere); get(slot): the element; put(slot, x, by): its new place, `by`
-// positions from the old one (put of every element, moved or not, in step with
-// the warp's other threads, where ALL).  Entries outside [j, L) and positions
+// (-1: nowhere); at(slot): the element.  Entries outside [j, L) and positions
 // without a page are reported by `reports` threads and skipped.
-template <int U, class Vec, class Index, bool ALL, class Slot, class Get, class Put>
+template <int U, class Vec, class Index, class Slot, class At>
 TL_DEVINLINE void compact_walk(const int32_t* keep, int new_len, int L, int rows_per_pass, int r,
-                               bool reports, uint32_t* error_word, Slot slot, Get get, Put put) {
+                               bool reports, uint32_t* error_word, Slot slot, At at) {
   const int batch = rows_per_pass * U;
   auto entry = [&](int j) { return r >= 0 && j < new_len ? __ldg(keep + j) : j; };
   // the rows of the batch at j0, whose list entries are s
-  auto load = [&](int j0, const int* s, Vec* x, Index* d, int* by) {
+  auto load = [&](int j0, const int* s, Vec* x, Index* d) {
 #pragma unroll
     for (int u = 0; u < U; ++u) {
       const int j = j0 + u * rows_per_pass + r;
@@ -116,209 +114,289 @@ TL_DEVINLINE void compact_walk(const int32_t* keep, int new_len, int L, int rows
         continue;
       }
       d[u] = to;
-      by[u] = j - s[u];
-      x[u] = get(from);
+      x[u] = __ldcg(at(from));
     }
   };
   Vec v[U], nv[U];
   Index dst[U], ndst[U];
-  int s[U], ns[U], by[U], nby[U];
+  int s[U], ns[U];
 #pragma unroll
   for (int u = 0; u < U; ++u) s[u] = entry(u * rows_per_pass + r);
 #pragma unroll
   for (int u = 0; u < U; ++u) ns[u] = entry(batch + u * rows_per_pass + r);
-  load(0, s, v, dst, by);
+  load(0, s, v, dst);
   for (int j0 = 0; j0 < new_len; j0 += batch) {
 #pragma unroll
     for (int u = 0; u < U; ++u) s[u] = entry(j0 + 2 * batch + u * rows_per_pass + r);
-    load(j0 + batch, ns, nv, ndst, nby);
+    load(j0 + batch, ns, nv, ndst);
     __syncthreads();  // every thread's loads of this batch come before any store of it
 #pragma unroll
     for (int u = 0; u < U; ++u) {
-      if (ALL || dst[u] >= 0) put(dst[u], v[u], by[u]);
+      if (dst[u] >= 0) *at(dst[u]) = v[u];
       v[u] = nv[u];
       dst[u] = ndst[u];
-      by[u] = nby[u];
       ns[u] = s[u];
     }
   }
 }
 
-// A sequence's lengths, checked; false: it stays as it is.
-TL_DEVINLINE bool compact_lens(const CompactParams& P, int b, int& L, int& new_len) {
-  L = P.context_lens[b];
-  new_len = P.new_lens[b];
-  const int64_t cap = (int64_t)P.max_pages_per_seq * P.page_size;
-  const bool bad = L > cap || (P.mass && L > P.mass_len) || new_len < 0 || new_len > P.n ||
-                   new_len > max(L, 0);
-  if (bad && blockIdx.y == 0 && threadIdx.x == 0) report(P.error_word, TL_DEVERR_CONTEXT_RANGE);
-  return !bad;
-}
-
-// Rows as they are: this CTA's slice (of `slices`) of one pool's rows.
-template <int T, int U>
-TL_DEVINLINE void compact_rows(const CompactParams& P, void* rows, int slices, int slice, int g,
-                               const int32_t* keep, const int32_t* table, int L, int new_len) {
-  const int tid = threadIdx.x;
-  const int lanes = P.row_vecs / slices;  // threads of a row
-  const int per = T / lanes;              // rows of a pass
-  uint4* pool =
-      static_cast<uint4*>(rows) + (size_t)g * P.row_vecs + slice * lanes + tid % lanes;
-  const int64_t stride = (int64_t)P.h_kv * P.row_vecs;
-  compact_walk<U, uint4, int, false>(
-      keep, new_len, L, per, tid / lanes < per ? tid / lanes : -1, tid % lanes == 0,
-      P.error_word,
-      [&](int j) {
-        const CompactPlace p = compact_place(P, table, j);
-        return p.page < 0 ? -1 : p.page * P.page_size + p.off;
-      },
-      [&](int slot) { return __ldcg(pool + slot * stride); },
-      [&](int slot, const uint4& x, int) { pool[slot * stride] = x; });
-}
-
-// The scales of an int8 pool's rows.
-template <int T, int U>
-TL_DEVINLINE void compact_scales(const CompactParams& P, float* scales, int g,
-                                 const int32_t* keep, const int32_t* table, int L, int new_len) {
-  float* scale = scales + (size_t)g * P.page_size;
-  compact_walk<U, float, int64_t, false>(
-      keep, new_len, L, T, threadIdx.x, false, nullptr,
-      [&](int j) -> int64_t {
-        const CompactPlace p = compact_place(P, table, j);
-        return p.page < 0 ? -1 : (int64_t)p.page * P.h_kv * P.page_size + p.off;
-      },
-      [&](int64_t slot) { return __ldcg(scale + slot); },
-      [&](int64_t slot, float x, int) { scale[slot] = x; });
-}
-
-template <int T, int U>
-TL_DEVINLINE void compact_mass(const CompactParams& P, int row, const int32_t* keep, int L,
-                               int new_len) {
-  float* m = P.mass + (size_t)row * P.mass_len;
-  compact_walk<U, float, int, false>(
-      keep, new_len, L, T, threadIdx.x, false, nullptr, [&](int j) { return j; },
-      [&](int j) { return __ldcg(m + j); }, [&](int j, float x, int) { m[j] = x; });
-  // positions that no key holds any more gather nothing; the last batch's
-  // loads are behind the walk's barrier
-  __syncthreads();
-  for (int j = new_len + (int)threadIdx.x; j < L; j += T) m[j] = 0.f;
-}
-
 template <int T, int U>
 __global__ void __launch_bounds__(T) compact_kernel(CompactParams P) {
+  const int tid = threadIdx.x;
   const int row = blockIdx.x, b = row / P.h_kv, g = row % P.h_kv;
-  int L, new_len;
-  if (!compact_lens(P, b, L, new_len)) return;
+  const int L = P.context_lens[b], new_len = P.new_lens[b];
+  const int64_t cap = (int64_t)P.max_pages_per_seq * P.page_size;
+  const bool bad_len = L > cap || (P.mass && L > P.mass_len) || new_len < 0 || new_len > P.n ||
+                       new_len > max(L, 0);
+  if (bad_len) {  // the sequence stays as it is
+    if (blockIdx.y == 0 && tid == 0) report(P.error_word, TL_DEVERR_CONTEXT_RANGE);
+    return;
+  }
   const int32_t* keep = P.keep + (size_t)row * P.n;
   const int32_t* table = P.block_table + (size_t)b * P.max_pages_per_seq;
   const int kind = blockIdx.y;  // the pools' slices, then K and V scales, then the mass
   if (kind < 2 * P.slices) {
     const bool is_v = kind >= P.slices;
-    compact_rows<T, U>(P, is_v ? P.pool[1] : P.pool[0], P.slices, kind - (is_v ? P.slices : 0), g,
-                       keep, table, L, new_len);
-  } else if (P.scale[0] && kind < 2 * P.slices + 2) {
-    compact_scales<T, U>(P, kind == 2 * P.slices ? P.scale[0] : P.scale[1], g, keep, table, L,
-                         new_len);
-  } else {
-    compact_mass<T, U>(P, row, keep, L, new_len);
-  }
-}
-
-// The same with K rows turned by the positions they move (tl_kv_cache_compact_rope).
-// K rows are walked in rotary units (rope.cuh), one a thread, which turns its 8
-// pairs between the load and the store: a row that moves has an angle of its
-// own for every pair.  int8 rows are scaled anew over their threads, which lie
-// in one warp (d is a power of two up to 512).
-struct CompactTurn {
-  const uint64_t* freqs;
-  int32_t rot, interleaved;
-  int32_t units, slices;  // rotary units of a row, CTAs that share a K row
-};
-
-template <int E>
-struct CompactUnit : RopeUnit<E, E == kElemF32 ? 4 : 8> {
-  float scale;  // int8
-};
-
-template <int T, int U, int E, bool INTER>
-__global__ void __launch_bounds__(T) compact_rope_kernel(CompactParams P, CompactTurn R) {
-  const int tid = threadIdx.x;
-  const int row = blockIdx.x, b = row / P.h_kv, g = row % P.h_kv;
-  int L, new_len;
-  if (!compact_lens(P, b, L, new_len)) return;
-  const int32_t* keep = P.keep + (size_t)row * P.n;
-  const int32_t* table = P.block_table + (size_t)b * P.max_pages_per_seq;
-  const int kind = blockIdx.y;  // K slices, V slices, V scales (int8), the mass
-  if (kind < R.slices) {
-    const int lanes = R.units / R.slices, per = T / lanes;
-    const int u = kind * lanes + tid % lanes;
-    constexpr int W = 16 / CompactUnit<E>::NW;
-    using Pairs = RopePairs<INTER, W>;
-    int at[16 / W];
-    rope_unit_words<INTER, W>(u, R.units * 16, R.rot, at);
-    const int64_t row_bytes = (int64_t)P.row_vecs * 16, stride = P.h_kv * row_bytes;
-    char* pool = static_cast<char*>(P.pool[0]) + g * row_bytes;
-    float* scales = E == kElemInt8 ? P.scale[0] + (size_t)g * P.page_size : nullptr;
-    auto scale_at = [&](int slot) {
-      const int page = P.ps_shift >= 0 ? slot >> P.ps_shift : slot / P.page_size;
-      return scales + (int64_t)page * (P.h_kv - 1) * P.page_size + slot;
-    };
-    compact_walk<U, CompactUnit<E>, int, E == kElemInt8>(
+    const int lanes = P.row_vecs / P.slices;  // threads of a row
+    const int per = T / lanes;                // rows of a pass
+    uint4* pool = static_cast<uint4*>(is_v ? P.pool[1] : P.pool[0]) + (size_t)g * P.row_vecs +
+                  (kind - (is_v ? P.slices : 0)) * lanes + tid % lanes;
+    const int64_t stride = (int64_t)P.h_kv * P.row_vecs;
+    compact_walk<U, uint4, int>(
         keep, new_len, L, per, tid / lanes < per ? tid / lanes : -1, tid % lanes == 0,
         P.error_word,
         [&](int j) {
           const CompactPlace p = compact_place(P, table, j);
           return p.page < 0 ? -1 : p.page * P.page_size + p.off;
         },
-        [&](int slot) {
-          CompactUnit<E> x;
-          x.load(pool + slot * stride, at);
-          if constexpr (E == kElemInt8) x.scale = __ldcg(scale_at(slot));
-          return x;
+        [&](int slot) { return pool + slot * stride; });
+  } else if (P.scale[0] && kind < 2 * P.slices + 2) {
+    float* scale = (kind == 2 * P.slices ? P.scale[0] : P.scale[1]) + (size_t)g * P.page_size;
+    compact_walk<U, float, int64_t>(
+        keep, new_len, L, T, tid, false, nullptr,
+        [&](int j) -> int64_t {
+          const CompactPlace p = compact_place(P, table, j);
+          return p.page < 0 ? -1 : (int64_t)p.page * P.h_kv * P.page_size + p.off;
         },
-        [&](int slot, CompactUnit<E>& x, int by) {
-          float y[16];
-          if (E != kElemInt8 && (INTER ? at[0] >= R.rot : 16 * u >= R.rot)) {
-            x.store(pool + slot * stride, at);
-            return;
-          }
-          x.values(y);
-          if constexpr (E == kElemInt8) {
-#pragma unroll
-            for (int k = 0; k < 16; ++k) y[k] *= x.scale;
-          }
-          if (slot >= 0)
-            rope_unit_rotate<INTER, W>(
-                y, [&](int k) { return Pairs::turn(at, k, u, R.rot); },
-                [&](int k) { return rope_turn(__ldg(R.freqs + Pairs::index(at, k)), by); });
-          if constexpr (E == kElemInt8) {
-            bool bad = false;
-            float m = rope_unit_max(y, bad);
-            for (int o = lanes >> 1; o > 0; o >>= 1)
-              m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
-            if (slot < 0) return;
-            const float sc = __fdiv_rn(m, 127.f);
-            x.set_codes(y, sc, !bad);
-            if (tid % lanes == 0) *scale_at(slot) = sc;
-            if (bad) report(P.error_word, TL_DEVERR_VALUE_RANGE);
-          } else {
-            const CompactUnit<E> was = x;
-            x.set(y);
-            if (INTER) {  // words behind the rotated part keep their bits
-#pragma unroll
-              for (int w = 0; w < x.NW; ++w)
-                if (at[w] >= R.rot) x.w[w] = was.w[w];
-            }
-          }
-          x.store(pool + slot * stride, at);
-        });
-  } else if (kind < R.slices + P.slices) {
-    compact_rows<T, U>(P, P.pool[1], P.slices, kind - R.slices, g, keep, table, L, new_len);
-  } else if (E == kElemInt8 && kind == R.slices + P.slices) {
-    compact_scales<T, U>(P, P.scale[1], g, keep, table, L, new_len);
+        [&](int64_t slot) { return scale + slot; });
   } else {
-    compact_mass<T, U>(P, row, keep, L, new_len);
+    float* m = P.mass + (size_t)row * P.mass_len;
+    compact_walk<U, float, int>(
+        keep, new_len, L, T, tid, false, nullptr, [&](int j) { return j; },
+        [&](int j) { return m + j; });
+    // positions that no key holds any more gather nothing; the last batch's
+    // loads are behind the walk's barrier
+    __syncthreads();
+    for (int j = new_len + tid; j < L; j += T) m[j] = 0.f;
   }
+}
+
+// ------------------------------------------- compact, positions closed up --
+//
+// The same move with every K row turned by the positions it moves.  All that
+// moves of a (sequence, KV head) is moved by one cluster of CTAs in one walk:
+// batches of positions are shared out among its CTAs and their rows' rotary
+// units (rope.cuh) among a row's threads, each of which takes the same words
+// of the K row and of the V row; the row's first thread takes the scales and
+// the mass.  So the list, the table and the checks are read once for all of it,
+// and every CTA has arithmetic (a row that moves has an angle of its own for
+// every pair) beside its loads.  A batch's rows are loaded while the batch
+// before it is turned (its list entries come three batches ahead, its pages
+// two); its stores come behind a barrier of the cluster that every thread
+// reaches with its rows loaded: positions below the batch's end, which no later
+// batch reads (every keep[j] >= j), as above.
+// Bound: HBM where rows are many, 2 x (K and V row) per moved row: 64 bf16
+// sequences of 512-8,192 keys cut to 2,048 take 151 us (858 MB, 5.7 TB/s; the
+// move alone 151), against 250 with K and V moved by CTAs of their own (the
+// index work twice, CTAs of K four times as long as those of V) and 196 where
+// pages were looked up in the batch that reads them.  One sequence of 32,768
+// cut to 8,192: 26 us; 24 sequences of up to 8,192 e4m3
+// keys cut to 1,500: 31 us.  There a batch's latency (some 2.5
+// us of loads, turns and the cluster's barrier) counts, times their number.
+struct CompactTurn {
+  const uint64_t* freqs;
+  int32_t rot, interleaved;
+  int32_t units, slices;  // rotary units of a row, clusters that share a row
+  int32_t cluster;        // CTAs of a cluster
+};
+
+template <int E>
+struct CompactRow {
+  static constexpr int W = E == kElemF32 ? 4 : 8;
+  RopeUnit<E, W> k, v;
+  float k_scale, v_scale, mass;
+};
+
+constexpr int kCompactRopeThreads = 256;
+template <int E, bool INTER>
+__global__ void __launch_bounds__(kCompactRopeThreads, E == kElemF32 ? 2 : 3) compact_rope_kernel(CompactParams P, CompactTurn R) {
+  constexpr int W = CompactRow<E>::W, T = kCompactRopeThreads;
+  using Pairs = RopePairs<INTER, W>;
+  const int tid = threadIdx.x;
+  const int group = (int)blockIdx.x / R.cluster, rank = (int)blockIdx.x - group * R.cluster;
+  const int row = group / R.slices, slice = group - row * R.slices;
+  const int b = row / P.h_kv, g = row - b * P.h_kv;
+  const int L = P.context_lens[b], new_len = P.new_lens[b];
+  const int64_t cap = (int64_t)P.max_pages_per_seq * P.page_size;
+  if (L > cap || (P.mass && L > P.mass_len) || new_len < 0 || new_len > P.n ||
+      new_len > max(L, 0)) {  // the sequence stays as it is (all of the cluster leaves)
+    if (rank == 0 && tid == 0) report(P.error_word, TL_DEVERR_CONTEXT_RANGE);
+    return;
+  }
+  const int32_t* keep = P.keep + (size_t)row * P.n;
+  const int32_t* table = P.block_table + (size_t)b * P.max_pages_per_seq;
+  const int lanes = R.units / R.slices, per = T / lanes;  // threads of a row, rows of a pass
+  const int u = slice * lanes + tid % lanes;
+  const int batch = per * R.cluster, r = rank * per + tid / lanes;
+  const bool mine = tid / lanes < per, first = u == 0;
+  int at[16 / W];
+  rope_unit_words<INTER, W>(u, R.units * 16, R.rot, at);
+  const int64_t row_bytes = (int64_t)P.row_vecs * 16, stride = P.h_kv * row_bytes;
+  char* k = static_cast<char*>(P.pool[0]) + g * row_bytes;
+  char* v = static_cast<char*>(P.pool[1]) + g * row_bytes;
+  float* mass = P.mass ? P.mass + (size_t)row * P.mass_len : nullptr;
+  auto scale_at = [&](int slot) {  // int8: [num_pages][h_kv][page_size]
+    const int page = P.ps_shift >= 0 ? slot >> P.ps_shift : slot / P.page_size;
+    return ((int64_t)page * (P.h_kv - 1) + g) * P.page_size + slot;
+  };
+  // the list's entry for position j
+  auto entry = [&](int j) { return mine && j < new_len ? __ldg(keep + j) : j; };
+  auto block_of = [&](int j) { return P.ps_shift >= 0 ? j >> P.ps_shift : j / P.page_size; };
+  // the pages that hold positions s and j; read here, looked at a batch later
+  auto pages = [&](int j, int s, int& from, int& to) {
+    from = to = -1;
+    if (s <= j || s >= L) return;
+    from = __ldg(table + block_of(s));
+    to = __ldg(table + block_of(j));
+  };
+  // the slots that entry s moves position j's row from and to, in place of the
+  // pages; to < 0: none
+  auto places = [&](int j, int s, int& from, int& to) {
+    if (s == j) return;  // stays, or not a row of this thread
+    if (s < j || s >= L) {
+      if (first) report(P.error_word, TL_DEVERR_CONTEXT_RANGE);
+      return;
+    }
+    if (from < 0 || from >= P.num_pages || to < 0 || to >= P.num_pages) {
+      if (first) report(P.error_word, TL_DEVERR_PAGE_RANGE);
+      to = -1;
+      return;
+    }
+    from = from * P.page_size + (s - block_of(s) * P.page_size);
+    to = to * P.page_size + (j - block_of(j) * P.page_size);
+  };
+  auto load = [&](CompactRow<E>& x, int s, int from, int to) {
+    if (to < 0) return;
+    x.k.load(k + from * stride, at);
+    x.v.load(v + from * stride, at);
+    if (E == kElemInt8) {
+      x.k_scale = __ldcg(P.scale[0] + scale_at(from));
+      if (first) x.v_scale = __ldcg(P.scale[1] + scale_at(from));
+    }
+    if (mass && first) x.mass = __ldcg(mass + s);
+  };
+  CompactRow<E> x, y;
+  int s = entry(r), s1 = entry(batch + r), s2 = entry(2 * batch + r);
+  int from, to, from1, to1;
+  pages(r, s, from, to);
+  pages(batch + r, s1, from1, to1);
+  places(r, s, from, to);
+  load(x, s, from, to);
+  for (int j = r; j - r < new_len; j += batch) {
+    // the next batch's row, the pages of the one behind it, the entry of a third
+    places(j + batch, s1, from1, to1);
+    load(y, s1, from1, to1);
+    int from2, to2;
+    pages(j + 2 * batch, s2, from2, to2);
+    const int s3 = entry(j + 3 * batch);
+    bool bad = false;
+    if (E == kElemInt8 || (to >= 0 && Pairs::turn(at, 0, u, R.rot))) {
+      float z[16];
+      x.k.values(z);
+      if constexpr (E == kElemInt8) {
+#pragma unroll
+        for (int e = 0; e < 16; ++e) z[e] *= x.k_scale;
+      }
+      if (to >= 0) rope_unit_turn_back<INTER, W>(z, at, u, R.rot, R.freqs, (uint32_t)(s - j));
+      if constexpr (E == kElemInt8) {
+        float m = to >= 0 ? rope_unit_max(z, bad) : 0.f;
+        for (int o = lanes >> 1; o > 0; o >>= 1)
+          m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
+        x.k_scale = __fdiv_rn(m, 127.f);
+        x.k.set_codes(z, x.k_scale, !bad);
+      } else {
+        const RopeUnit<E, W> was = x.k;
+        x.k.set(z);
+        if (INTER) {  // words behind the rotated part keep their bits
+#pragma unroll
+          for (int w = 0; w < 16 / W; ++w)
+            if (at[w] >= R.rot) x.k.w[w] = was.w[w];
+        }
+      }
+    }
+    if (E == kElemInt8 && bad) report(P.error_word, TL_DEVERR_VALUE_RANGE);
+    // every thread's row of this batch is loaded before any of it is stored
+    if (R.cluster > 1) {
+      asm volatile("barrier.cluster.arrive.release.aligned;\n" ::: "memory");
+      asm volatile("barrier.cluster.wait.acquire.aligned;\n" ::: "memory");
+    } else {
+      __syncthreads();
+    }
+    if (to >= 0) {
+      x.k.store(k + to * stride, at);
+      x.v.store(v + to * stride, at);
+      if (E == kElemInt8 && first) {
+        P.scale[0][scale_at(to)] = x.k_scale;
+        P.scale[1][scale_at(to)] = x.v_scale;
+      }
+      if (mass && first) mass[j] = x.mass;
+    }
+    x = y;
+    s = s1, s1 = s2, s2 = s3;
+    to = to1, from1 = from2, to1 = to2;
+  }
+  // positions that no key holds any more gather nothing (the masses that move
+  // are loaded: the last batch's barrier is past)
+  if (mass && slice == 0)
+    for (int j = new_len + rank * T + tid; j < L; j += R.cluster * T) mass[j] = 0.f;
+}
+
+static cudaError_t launch_compact_rope(const CompactParams& P, CompactTurn R, int64_t rows, int d,
+                                       int elem, cudaStream_t st) {
+  R.units = d / 16;
+  const bool i8 = P.scale[0] != nullptr;
+  // Few rows are shared by clusters of up to 8 CTAs, and by slices of a row
+  // (whole 32-byte sectors of words; an int8 row is one slice, for its scale),
+  // while every CTA has a place at once: three on an SM.  8 rows of 8,192 kept
+  // keys take 70 us with clusters of 8, 40 with two slices, 26 with four; 96
+  // rows of 1,500 e4m3 keys 49 us with clusters of 2, 31 with 4, and 33 with 8
+  // (two waves).
+  const int64_t ctas = (int64_t)num_sms() * 3;
+  R.cluster = R.slices = 1;
+  while (R.cluster < 8 && rows * 2 * R.cluster <= ctas) R.cluster *= 2;
+  const int least = elem == 1 ? 4 : 2;
+  while (!i8 && R.units % (2 * R.slices) == 0 && R.units / (2 * R.slices) >= least &&
+         rows * R.cluster * 2 * R.slices <= ctas)
+    R.slices *= 2;
+  auto kern = R.interleaved ? (i8          ? compact_rope_kernel<kElemInt8, true>
+                               : elem == 1 ? compact_rope_kernel<kElemE4m3, true>
+                               : elem == 2 ? compact_rope_kernel<kElemBf16, true>
+                                           : compact_rope_kernel<kElemF32, true>)
+                            : (i8          ? compact_rope_kernel<kElemInt8, false>
+                               : elem == 1 ? compact_rope_kernel<kElemE4m3, false>
+                               : elem == 2 ? compact_rope_kernel<kElemBf16, false>
+                                           : compact_rope_kernel<kElemF32, false>);
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeClusterDimension;
+  attr[0].val.clusterDim.x = R.cluster;
+  attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3((unsigned)(rows * R.slices * R.cluster));
+  cfg.blockDim = dim3(kCompactRopeThreads);
+  cfg.stream = st;
+  cfg.attrs = attr;
+  cfg.numAttrs = R.cluster > 1 ? 1 : 0;
+  return cudaLaunchKernelEx(&cfg, kern, P, R);
 }
 
 static tl_status compact_impl(void* k, void* v, float* k_scales, float* v_scales,
@@ -327,7 +405,7 @@ static tl_status compact_impl(void* k, void* v, float* k_scales, float* v_scales
                               const int32_t* new_lens, float* mass, int32_t mass_len, int32_t B,
                               int32_t h_kv, int32_t d, int32_t num_pages, int32_t page_size,
                               int elem, uint32_t* error_word, void* stream,
-                              CompactTurn* turn = nullptr) {
+                              const CompactTurn* turn = nullptr) {
   if (B <= 0 || h_kv <= 0 || d <= 0 || num_pages <= 0 || page_size <= 0 ||
       max_pages_per_seq <= 0 || n_keep <= 0 || (mass && mass_len <= 0))
     return TL_ERR_INVALID_ARG;
@@ -392,41 +470,14 @@ static tl_status compact_impl(void* k, void* v, float* k_scales, float* v_scales
   // a row is shared by more CTAs while the (sequence, head) rows leave SMs
   // empty, down to 32 bytes (a sector) of a row; then a CTA takes all of an SM's threads
   const int64_t rows = (int64_t)B * h_kv;
+  if (turn)
+    return launch_compact_rope(P, *turn, rows, d, elem, (cudaStream_t)stream) == cudaSuccess
+               ? launch_status()
+               : TL_ERR_CUDA;
   P.slices = 1;
   while (P.row_vecs % (2 * P.slices) == 0 && P.row_vecs / (2 * P.slices) >= 2 &&
          rows * 2 * P.slices < 2 * num_sms())
     P.slices *= 2;
-  if (turn) {
-    // K rows alike, a slice being units whose words fill whole 32-byte sectors
-    // (an int8 row is one slice, for its scale)
-    CompactTurn R = *turn;
-    R.units = d / 16;
-    R.slices = 1;
-    const int least = elem == 1 ? 4 : 2;  // words of 8 bytes, or of 16
-    if (!k_scales)
-      while (R.units % (2 * R.slices) == 0 && R.units / (2 * R.slices) >= least &&
-             rows * 2 * R.slices < 2 * num_sms())
-        R.slices *= 2;
-    const bool big = rows * 2 * P.slices <= 2 * num_sms() || P.row_vecs / P.slices > 128 ||
-                     R.units / R.slices > 128;
-    const dim3 grid((unsigned)rows, (unsigned)(R.slices + P.slices + (k_scales ? 1 : 0) +
-                                               (mass ? 1 : 0)));
-    cudaStream_t st = (cudaStream_t)stream;
-#define TL_COMPACT_ROPE(E)                                          \
-  do {                                                              \
-    auto kern = big ? (R.interleaved ? compact_rope_kernel<512, 2, E, true>  \
-                                     : compact_rope_kernel<512, 2, E, false>) \
-                    : (R.interleaved ? compact_rope_kernel<128, 4, E, true>   \
-                                     : compact_rope_kernel<128, 4, E, false>); \
-    kern<<<grid, big ? 512 : 128, 0, st>>>(P, R);                             \
-  } while (0)
-    if (k_scales) TL_COMPACT_ROPE(kElemInt8);
-    else if (elem == 1) TL_COMPACT_ROPE(kElemE4m3);
-    else if (elem == 2) TL_COMPACT_ROPE(kElemBf16);
-    else TL_COMPACT_ROPE(kElemF32);
-#undef TL_COMPACT_ROPE
-    return launch_status();
-  }
   const dim3 grid((unsigned)rows, (unsigned)(2 * P.slices + (k_scales ? 2 : 0) + (mass ? 1 : 0)));
   // otherwise small CTAs, whose barriers hold few rows back: one sequence of
   // 8,192 rows kept takes 23 us with 1,024 threads and 33 with 512, 64
@@ -524,7 +575,7 @@ extern "C" tl_status tl_kv_cache_compact_rope(
     int32_t B, int32_t h_kv, int32_t d, int32_t num_pages, int32_t page_size, tl_dtype dtype,
     uint32_t* error_word, void* stream) {
   const int elem = dtype == TL_F32 ? 4 : dtype == TL_BF16 ? 2 : dtype == TL_FP8_E4M3 ? 1 : 0;
-  tl::CompactTurn turn = {freqs, rot_dim, interleaved != 0, 0, 0};
+  const tl::CompactTurn turn = {freqs, rot_dim, interleaved != 0, 0, 0, 0};
   return tl::compact_impl(k_cache, v_cache, nullptr, nullptr, block_table, max_pages_per_seq,
                           context_lens, keep, n_keep, new_lens, mass, mass_len, B, h_kv, d,
                           num_pages, page_size, elem, error_word, stream, &turn);
@@ -537,7 +588,7 @@ extern "C" tl_status tl_kv_cache_compact_rope_int8(
     const uint64_t* freqs, int32_t rot_dim, int32_t interleaved, int32_t B, int32_t h_kv,
     int32_t d, int32_t num_pages, int32_t page_size, uint32_t* error_word, void* stream) {
   if (!k_scales || !v_scales) return TL_ERR_INVALID_ARG;
-  tl::CompactTurn turn = {freqs, rot_dim, interleaved != 0, 0, 0};
+  const tl::CompactTurn turn = {freqs, rot_dim, interleaved != 0, 0, 0, 0};
   return tl::compact_impl(k_codes, v_codes, k_scales, v_scales, block_table, max_pages_per_seq,
                           context_lens, keep, n_keep, new_lens, mass, mass_len, B, h_kv, d,
                           num_pages, page_size, 1, error_word, stream, &turn);

@@ -9,7 +9,7 @@
 // nearest quarter turn and a remainder t of at most half a quarter; sine and
 // cosine of t quarter turns are their Taylor series to t^9 and t^10, whose
 // first left-out terms are below 2^-28, and the quarter turns swap and negate
-// them.  27 instructions a pair for both.
+// them.
 #pragma once
 
 #include <cuda_fp16.h>
@@ -21,26 +21,61 @@
 
 namespace tl {
 
-// (cos, sin) of pos x freq / 2^64 turns, both within 2^-23 of exact.
-TL_DEVINLINE float2 rope_turn(uint64_t freq, int32_t pos) {
-  const uint32_t turn = (uint32_t)(((uint64_t)(int64_t)pos * freq) >> 32);
-  const uint32_t quarter = (turn + 0x20000000u) >> 30;
-  const float t = (float)(int32_t)(turn - (quarter << 30)) * 0x1p-30f;  // in [-1/2, 1/2]
-  const float x = t * t;
+// Two binary32 numbers in one 64-bit register, multiplied and added as two.
+TL_DEVINLINE uint64_t f2_pack(float a, float b) {
+  uint64_t r;
+  asm("mov.b64 %0, {%1, %2};\n" : "=l"(r) : "f"(a), "f"(b));
+  return r;
+}
+TL_DEVINLINE float2 f2_unpack(uint64_t v) {
+  float2 r;
+  asm("mov.b64 {%0, %1}, %2;\n" : "=f"(r.x), "=f"(r.y) : "l"(v));
+  return r;
+}
+TL_DEVINLINE uint64_t f2_fma(uint64_t a, uint64_t b, uint64_t c) {
+  uint64_t r;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;\n" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+  return r;
+}
+TL_DEVINLINE uint64_t f2_mul(uint64_t a, uint64_t b) {
+  uint64_t r;
+  asm("mul.rn.f32x2 %0, %1, %2;\n" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+
+// (cos, sin) of n x fa / 2^64 and n x fb / 2^64 turns, all within 2^-23 of exact.
+// The series of the two are evaluated in pairs of numbers.
+TL_DEVINLINE void rope_turns(uint64_t fa, uint64_t fb, uint32_t n, float2& a, float2& b) {
+  // the phase's top 32 bits, half a quarter turn further: the nearest quarter in
+  // the top two
+  const uint32_t ua = (uint32_t)((fa * n) >> 32) + 0x20000000u;
+  const uint32_t ub = (uint32_t)((fb * n) >> 32) + 0x20000000u;
+  auto both = [](float x) { return f2_pack(x, x); };
+  const uint64_t t = f2_mul(f2_pack((float)((int32_t)(ua & 0x3fffffffu) - 0x20000000),
+                                    (float)((int32_t)(ub & 0x3fffffffu) - 0x20000000)),
+                            both(0x1p-30f));  // in [-1/2, 1/2]
+  const uint64_t x = f2_mul(t, t);
   // (pi/2)^k / k!, alternating; pi/2 in two parts
-  float s = fmaf(x, 1.6044118479e-4f, -4.6817541353e-3f);
-  s = fmaf(x, s, 7.9692626246e-2f);
-  s = fmaf(x, s, -6.4596409751e-1f);
-  s = fmaf(t, 1.5707963705f, t * fmaf(x, s, -4.3711388287e-8f));
-  float c = fmaf(x, -2.5202042374e-5f, 9.1926027483e-4f);
-  c = fmaf(x, c, -2.0863480763e-2f);
-  c = fmaf(x, c, 2.5366950790e-1f);
-  c = fmaf(x, c, -1.2337005501f);
-  c = fmaf(x, c, 1.f);
-  float a = quarter & 1 ? s : c, b = quarter & 1 ? c : s;
-  if ((quarter + 1) & 2) a = -a;
-  if (quarter & 2) b = -b;
-  return make_float2(a, b);
+  uint64_t s = f2_fma(x, both(1.6044118479e-4f), both(-4.6817541353e-3f));
+  s = f2_fma(x, s, both(7.9692626246e-2f));
+  s = f2_fma(x, s, both(-6.4596409751e-1f));
+  s = f2_fma(x, s, both(-4.3711388287e-8f));
+  s = f2_fma(t, both(1.5707963705f), f2_mul(t, s));
+  uint64_t c = f2_fma(x, both(-2.5202042374e-5f), both(9.1926027483e-4f));
+  c = f2_fma(x, c, both(-2.0863480763e-2f));
+  c = f2_fma(x, c, both(2.5366950790e-1f));
+  c = f2_fma(x, c, both(-1.2337005501f));
+  c = f2_fma(x, c, both(1.f));
+  const float2 s2 = f2_unpack(s), c2 = f2_unpack(c);
+  // quarters 1 and 3 swap, 1 and 2 negate the cosine, 2 and 3 the sine
+  auto place = [](float s, float c, uint32_t u) {
+    const bool odd = u & 0x40000000u;
+    return make_float2(
+        __uint_as_float(__float_as_uint(odd ? s : c) ^ ((u + 0x40000000u) & 0x80000000u)),
+        __uint_as_float(__float_as_uint(odd ? c : s) ^ (u & 0x80000000u)));
+  };
+  a = place(s2.x, c2.x, ua);
+  b = place(s2.y, c2.y, ub);
 }
 
 // The pair (lo, hi) turned.
@@ -211,6 +246,29 @@ TL_DEVINLINE void rope_unit_rotate(float* x, Turns turns, Turn turn) {
     }
 }
 
+// A unit's values turned back by n positions (two pairs at once).
+template <bool INTER, int W>
+TL_DEVINLINE void rope_unit_turn_back(float* x, const int* at, int u, int rot,
+                                      const uint64_t* freqs, uint32_t n) {
+  using Pairs = RopePairs<INTER, W>;
+  uint64_t f[8];
+#pragma unroll
+  for (int k = 0; k < 8; ++k)
+    f[k] = Pairs::turn(at, k, u, rot) ? __ldg(freqs + Pairs::index(at, k)) : 0;
+#pragma unroll
+  for (int k = 0; k < 8; k += 2) {
+    if (!Pairs::turn(at, k, u, rot)) continue;
+    float2 a, b;
+    rope_turns(f[k], f[k + 1], n, a, b);
+    float &la = INTER ? x[2 * k] : x[k], &ha = INTER ? x[2 * k + 1] : x[8 + k];
+    float &lb = INTER ? x[2 * k + 2] : x[k + 1], &hb = INTER ? x[2 * k + 3] : x[9 + k];
+    const uint64_t lo = f2_pack(la, lb), hi = f2_pack(ha, hb), c = f2_pack(a.x, b.x);
+    const float2 l = f2_unpack(f2_fma(lo, c, f2_mul(hi, f2_pack(a.y, b.y))));
+    const float2 h = f2_unpack(f2_fma(hi, c, f2_mul(lo, f2_pack(-a.y, -b.y))));
+    la = l.x, lb = l.y, ha = h.x, hb = h.y;
+  }
+}
+
 // The rows of one call: h_q query heads, then h_kv key heads, then h_kv value
 // heads of every token.  Without slots (slots null) there are queries alone.
 struct RopeRows {
@@ -292,11 +350,11 @@ TL_DEVINLINE void rope_units(const RopeRows& R, int64_t t, int h0, int heads, in
     // chunks that a lane reads one behind the other
     constexpr int per = Pairs::n / 2;
     const int step = (R.rot >> 2) / per;
-    float2* cs2 = reinterpret_cast<float2*>(cs);
-    for (int i = lane; i < R.rot >> 1; i += 32) {
-      const float2 c = rope_turn(__ldg(R.freqs + i), pos);
-      cs2[2 * ((i >> 1) % per * step + (i >> 1) / per) + (i & 1)] =
-          make_float2(c.x * R.scale, c.y * R.scale);
+    for (int c = lane; c < R.rot >> 2; c += 32) {
+      float2 y, z;
+      rope_turns(__ldg(R.freqs + 2 * c), __ldg(R.freqs + 2 * c + 1), (uint32_t)pos, y, z);
+      cs[c % per * step + c / per] =
+          make_float4(y.x * R.scale, y.y * R.scale, z.x * R.scale, z.y * R.scale);
     }
     __syncwarp();
 #pragma unroll
@@ -399,7 +457,9 @@ __device__ void rope_row(const RopeRows& R, int64_t t, int h, int lane) {
     eh = R.interleaved ? 2 * i + 1 : i + (rot >> 1);
     lo = value(el);
     hi = value(eh);
-    const float2 cs = rope_turn(__ldg(R.freqs + i), pos);
+    const uint64_t f = __ldg(R.freqs + i);
+    float2 cs, same;
+    rope_turns(f, f, (uint32_t)pos, cs, same);
     rope_rotate(lo, hi, cs.x * R.scale, cs.y * R.scale);
   };
   auto same = [&](T* dst) {
