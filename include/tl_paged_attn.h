@@ -999,6 +999,56 @@ tl_status tl_kv_cache_write_rope_int8(const void* q, int64_t q_stride, void* q_o
                                       int32_t h_q, int32_t h_kv, int32_t d, uint32_t* error_word,
                                       void* stream);
 
+/* Bytes of workspace the step calls below need (the decode's, and the rotated
+ * queries); 0 for invalid sizes. */
+size_t tl_paged_attn_decode_write_rope_workspace_size(int32_t B, int32_t h_q, int32_t h_kv,
+                                                      int32_t d);
+
+/*
+ * A decode step of raw queries and keys in one call: tl_kv_cache_write_rope of
+ * sequence b's new token (row b of q, k_new and v_new, at slot_mapping[b] and
+ * positions[b]), then tl_paged_attn_decode with the rotated queries: the same
+ * outputs, pools and error bits as the two calls, bit for bit, in the decode's
+ * three launches (the rows and queries are rotated beside the plan; the rotated
+ * queries, in q's type, lie in the workspace).  positions[b] is context_lens[b]
+ * - 1 where every key kept its position; a sequence without a key this step
+ * has slot -1 (and position -1 where its query does not count either).
+ *   q             [B][h_q][d], k_new, v_new [B][h_kv][d], token b at its stride
+ *                 (elements) times b; TL_F32 with TL_F32 pools, else TL_BF16
+ *   dtype         TL_BF16, TL_F32 or TL_FP8_E4M3 pools (_int8: codes and scales;
+ *                 _ring: the ring rule of tl_paged_attn_decode_write_ring)
+ *   workspace     tl_paged_attn_decode_write_rope_workspace_size bytes, 256-byte
+ *                 aligned, nowhere over the rows or the pools; calls that overlap
+ *                 in time must not share one
+ * Errors as tl_kv_cache_write_rope and tl_paged_attn_decode.
+ */
+tl_status tl_paged_attn_decode_write_rope(
+    const void* q, int64_t q_stride, const void* k_new, int64_t k_stride, const void* v_new,
+    int64_t v_stride, const int64_t* slot_mapping, const int32_t* positions,
+    const uint64_t* freqs, int32_t rot_dim, int32_t interleaved, float rope_scale, void* k_cache,
+    void* v_cache, const int32_t* block_table, int32_t max_pages_per_seq,
+    const int32_t* context_lens, float* out, int32_t B, int32_t h_q, int32_t h_kv, int32_t d,
+    int32_t num_pages, int32_t page_size, int32_t window, float scale, tl_dtype dtype,
+    void* workspace, size_t workspace_bytes, uint32_t* error_word, void* stream);
+tl_status tl_paged_attn_decode_write_rope_int8(
+    const void* q, int64_t q_stride, const void* k_new, int64_t k_stride, const void* v_new,
+    int64_t v_stride, const int64_t* slot_mapping, const int32_t* positions,
+    const uint64_t* freqs, int32_t rot_dim, int32_t interleaved, float rope_scale,
+    int8_t* k_codes, int8_t* v_codes, float* k_scales, float* v_scales,
+    const int32_t* block_table, int32_t max_pages_per_seq, const int32_t* context_lens,
+    float* out, int32_t B, int32_t h_q, int32_t h_kv, int32_t d, int32_t num_pages,
+    int32_t page_size, int32_t window, float scale, void* workspace, size_t workspace_bytes,
+    uint32_t* error_word, void* stream);
+tl_status tl_paged_attn_decode_write_rope_ring(
+    const void* q, int64_t q_stride, const void* k_new, int64_t k_stride, const void* v_new,
+    int64_t v_stride, const int64_t* slot_mapping, const int32_t* positions,
+    const uint64_t* freqs, int32_t rot_dim, int32_t interleaved, float rope_scale, void* k_cache,
+    void* v_cache, const int32_t* block_table, int32_t max_pages_per_seq,
+    const int32_t* context_lens, float* out, int32_t B, int32_t h_q, int32_t h_kv, int32_t d,
+    int32_t num_pages, int32_t page_size, int32_t window, int32_t ring_pages, float scale,
+    tl_dtype dtype, void* workspace, size_t workspace_bytes, uint32_t* error_word,
+    void* stream);
+
 /*
  * tl_kv_cache_compact of a cache of rotated keys, whose positions close up: the
  * K row that moves from position keep[b][g][j] to j is also rotated by

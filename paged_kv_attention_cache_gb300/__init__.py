@@ -30,7 +30,9 @@ from .api import (TL_BF16, TL_FP8_E4M3, tl_kv_cache_write_fp8, TL_DEVERR_CONTEXT
                   TL_ROPE_PLAIN, TL_ROPE_LINEAR, TL_ROPE_BASE, TL_ROPE_BANDS, TL_ROPE_RAMP,
                   TL_ROPE_FACTORS, tl_rope_freqs, tl_rope, tl_kv_cache_write_rope,
                   tl_kv_cache_write_rope_int8, tl_kv_cache_compact_rope,
-                  tl_kv_cache_compact_rope_int8, tl_version)
+                  tl_kv_cache_compact_rope_int8, tl_paged_attn_decode_write_rope,
+                  tl_paged_attn_decode_write_rope_int8, tl_paged_attn_decode_write_rope_ring,
+                  tl_paged_attn_decode_write_rope_workspace_size, tl_version)
 from . import build as _build_module
 
 
@@ -51,5 +53,7 @@ __all__ = [
     "tl_paged_attn_decode_multi_workspace_size", "tl_paged_attn_prefill_workspace_size_keys",
     "tl_rope_freqs", "tl_rope", "tl_kv_cache_write_rope", "tl_kv_cache_write_rope_int8",
     "tl_kv_cache_compact_rope", "tl_kv_cache_compact_rope_int8",
+    "tl_paged_attn_decode_write_rope", "tl_paged_attn_decode_write_rope_int8",
+    "tl_paged_attn_decode_write_rope_ring", "tl_paged_attn_decode_write_rope_workspace_size",
     "tl_status_string", "tl_version", "tl_get_device_error", "TLError", "build_library", "alloc_workspace",
 ]

@@ -104,6 +104,17 @@ SIGNATURES = {
     "tl_kv_cache_write_rope_int8": ([vp, i64, vp, i64, vp, i64, vp, i64, ctypes.c_int, vp, vp, vp,
                                      vp, vp, vp, vp, i32, i32, f32, i32, i32, i32, i32, i32, i32,
                                      u32p, vp], ctypes.c_int),
+    "tl_paged_attn_decode_write_rope_workspace_size": ([i32, i32, i32, i32], sz),
+    "tl_paged_attn_decode_write_rope": ([vp, i64, vp, i64, vp, i64, vp, vp, vp, i32, i32, f32, vp,
+                                         vp, vp, i32, vp, vp, i32, i32, i32, i32, i32, i32, i32,
+                                         f32, ctypes.c_int, vp, sz, u32p, vp], ctypes.c_int),
+    "tl_paged_attn_decode_write_rope_int8": ([vp, i64, vp, i64, vp, i64, vp, vp, vp, i32, i32, f32,
+                                              vp, vp, vp, vp, vp, i32, vp, vp, i32, i32, i32, i32,
+                                              i32, i32, i32, f32, vp, sz, u32p, vp], ctypes.c_int),
+    "tl_paged_attn_decode_write_rope_ring": ([vp, i64, vp, i64, vp, i64, vp, vp, vp, i32, i32, f32,
+                                              vp, vp, vp, i32, vp, vp, i32, i32, i32, i32, i32,
+                                              i32, i32, i32, f32, ctypes.c_int, vp, sz, u32p, vp],
+                                             ctypes.c_int),
     "tl_kv_cache_compact_rope": ([vp, vp, vp, i32, vp, vp, i32, vp, vp, i32, vp, i32, i32, i32,
                                   i32, i32, i32, i32, ctypes.c_int, u32p, vp], ctypes.c_int),
     "tl_kv_cache_compact_rope_int8": ([vp, vp, vp, vp, vp, i32, vp, vp, i32, vp, vp, i32, vp, i32,

@@ -1103,6 +1103,107 @@ def tl_kv_cache_write_rope_int8(q: Optional[torch.Tensor], k_new: torch.Tensor,
     return q_out
 
 
+@functools.lru_cache(maxsize=1024)
+def tl_paged_attn_decode_write_rope_workspace_size(B: int, h_q: int, h_kv: int, d: int) -> int:
+    return int(_lib.load().tl_paged_attn_decode_write_rope_workspace_size(B, h_q, h_kv, d))
+
+
+def _step_rope(where, q, k_new, v_new, slot_mapping, positions, freqs, interleaved, rope_scale,
+               pools, q_dtype, sizes, block_table, context_lens, tail, out, workspace, error_word,
+               stream):
+    """The step calls: pools (their pointers), sizes (num_pages, page_size, H_kv, d), tail (what
+    follows page_size up to the workspace)."""
+    P, ps, hkv, d = sizes
+    dev = block_table.device
+    q_stride = _need_rows(q, "q", None, None, d, dev, q_dtype)
+    B, hq = q.shape[0], q.shape[1]
+    k_stride = _need_rows(k_new, "k_new", B, hkv, d, dev, q_dtype)
+    v_stride = _need_rows(v_new, "v_new", B, hkv, d, dev, q_dtype)
+    _need(slot_mapping, "slot_mapping", torch.int64, (B,), dev)
+    _need(positions, "positions", torch.int32, (B,), dev)
+    rot = _need_table_of_turns(freqs, d, dev)
+    _need_table(block_table, context_lens, B, dev)
+    out = _decode_out(out, (B, hq, d), dev, stream)
+    workspace = _workspace(workspace,
+                           tl_paged_attn_decode_write_rope_workspace_size(B, hq, hkv, d), dev,
+                           stream)
+    _run(where, dev, stream,
+         q.data_ptr(), q_stride, k_new.data_ptr(), k_stride, v_new.data_ptr(), v_stride,
+         slot_mapping.data_ptr(), positions.data_ptr(), freqs.data_ptr(), rot,
+         1 if interleaved else 0, rope_scale, *pools, block_table.data_ptr(),
+         block_table.shape[1], context_lens.data_ptr(), out.data_ptr(), B, hq, hkv, d, P, ps,
+         *tail, workspace.data_ptr(), _ws_bytes(workspace), _err_word(error_word, dev))
+    return out
+
+
+def tl_paged_attn_decode_write_rope(q: torch.Tensor, k_new: torch.Tensor, v_new: torch.Tensor,
+                                    slot_mapping: torch.Tensor, positions: torch.Tensor,
+                                    freqs: torch.Tensor, k_cache: torch.Tensor,
+                                    v_cache: torch.Tensor, block_table: torch.Tensor,
+                                    context_lens: torch.Tensor, scale: float, window: int = 0,
+                                    interleaved: bool = False, rope_scale: float = 1.0,
+                                    out: Optional[torch.Tensor] = None,
+                                    workspace: Optional[torch.Tensor] = None,
+                                    error_word: Optional[torch.Tensor] = None,
+                                    stream=None) -> torch.Tensor:
+    """A decode step of raw queries and keys in one call: tl_kv_cache_write_rope
+    of row b of q [B, H_q, d], k_new and v_new [B, H_kv, d] (the tokens at any
+    stride) at slot_mapping [B] and positions [B], then tl_paged_attn_decode
+    with the rotated queries: out [B, H_q, d] float32."""
+    dev = block_table.device
+    sizes = _need_pools(k_cache, v_cache, dev)
+    return _step_rope("tl_paged_attn_decode_write_rope", q, k_new, v_new, slot_mapping, positions,
+                      freqs, interleaved, rope_scale, (k_cache.data_ptr(), v_cache.data_ptr()),
+                      _query_dtype(k_cache.dtype), sizes, block_table, context_lens,
+                      (int(window), scale, _DTYPES.get(k_cache.dtype, -1)), out, workspace,
+                      error_word, stream)
+
+
+def tl_paged_attn_decode_write_rope_ring(q: torch.Tensor, k_new: torch.Tensor,
+                                         v_new: torch.Tensor, slot_mapping: torch.Tensor,
+                                         positions: torch.Tensor, freqs: torch.Tensor,
+                                         k_cache: torch.Tensor, v_cache: torch.Tensor,
+                                         block_table: torch.Tensor, context_lens: torch.Tensor,
+                                         scale: float, window: int, ring_pages: int,
+                                         interleaved: bool = False, rope_scale: float = 1.0,
+                                         out: Optional[torch.Tensor] = None,
+                                         workspace: Optional[torch.Tensor] = None,
+                                         error_word: Optional[torch.Tensor] = None,
+                                         stream=None) -> torch.Tensor:
+    """tl_paged_attn_decode_write_rope over rings (see
+    tl_paged_attn_decode_write_ring)."""
+    dev = block_table.device
+    sizes = _need_pools(k_cache, v_cache, dev)
+    return _step_rope("tl_paged_attn_decode_write_rope_ring", q, k_new, v_new, slot_mapping,
+                      positions, freqs, interleaved, rope_scale,
+                      (k_cache.data_ptr(), v_cache.data_ptr()), _query_dtype(k_cache.dtype),
+                      sizes, block_table, context_lens,
+                      (int(window), int(ring_pages), scale, _DTYPES.get(k_cache.dtype, -1)), out,
+                      workspace, error_word, stream)
+
+
+def tl_paged_attn_decode_write_rope_int8(q: torch.Tensor, k_new: torch.Tensor,
+                                         v_new: torch.Tensor, slot_mapping: torch.Tensor,
+                                         positions: torch.Tensor, freqs: torch.Tensor,
+                                         k_codes: torch.Tensor, v_codes: torch.Tensor,
+                                         k_scales: torch.Tensor, v_scales: torch.Tensor,
+                                         block_table: torch.Tensor, context_lens: torch.Tensor,
+                                         scale: float, window: int = 0,
+                                         interleaved: bool = False, rope_scale: float = 1.0,
+                                         out: Optional[torch.Tensor] = None,
+                                         workspace: Optional[torch.Tensor] = None,
+                                         error_word: Optional[torch.Tensor] = None,
+                                         stream=None) -> torch.Tensor:
+    """tl_paged_attn_decode_write_rope over int8 pools (bf16 rows)."""
+    dev = block_table.device
+    sizes = _need_int8_pools(k_codes, v_codes, k_scales, v_scales, dev)
+    return _step_rope("tl_paged_attn_decode_write_rope_int8", q, k_new, v_new, slot_mapping,
+                      positions, freqs, interleaved, rope_scale,
+                      (k_codes.data_ptr(), v_codes.data_ptr(), k_scales.data_ptr(),
+                       v_scales.data_ptr()), torch.bfloat16, sizes, block_table, context_lens,
+                      (int(window), scale), out, workspace, error_word, stream)
+
+
 def tl_kv_cache_compact_rope(k_cache: torch.Tensor, v_cache: torch.Tensor,
                              block_table: torch.Tensor, context_lens: torch.Tensor,
                              keep: torch.Tensor, new_lens: torch.Tensor, freqs: torch.Tensor,

@@ -2,6 +2,72 @@
 // paged_decode.cuh.
 #include "paged_decode.cuh"
 
+namespace tl {
+
+// Workspace of a step that rotates: the decode's, then the rotated queries (of
+// up to 4 bytes an element).
+static size_t rope_ws_queries(int32_t B, int32_t h_q, int32_t h_kv, int32_t d) {
+  return align_up(decode_ws_layout(B, h_q, h_kv, d, nullptr, nullptr), 256);
+}
+
+static tl_status decode_write_rope(
+    const void* q, int64_t q_stride, const void* k_new, int64_t k_stride, const void* v_new,
+    int64_t v_stride, const int64_t* slot_mapping, const int32_t* positions,
+    const uint64_t* freqs, int32_t rot_dim, int32_t interleaved, float rope_scale, void* k_cache,
+    void* v_cache, float* k_scales, float* v_scales, const int32_t* block_table,
+    int32_t max_pages_per_seq, const int32_t* context_lens, float* out, int32_t B, int32_t h_q,
+    int32_t h_kv, int32_t d, int32_t num_pages, int32_t page_size, int32_t window,
+    int32_t ring_pages, float scale, tl_dtype dtype, void* workspace, size_t workspace_bytes,
+    uint32_t* error_word, void* stream) {
+  if (B <= 0 || h_q <= 0 || h_kv <= 0 || d <= 0 || num_pages <= 0 || page_size <= 0 ||
+      h_q % h_kv || !q)
+    return TL_ERR_INVALID_ARG;
+  if (dtype != TL_BF16 && dtype != TL_F32 && dtype != TL_FP8_E4M3 && dtype != TL_INT8)
+    return TL_ERR_UNSUPPORTED;
+  if (d > 16 * kRopeStepUnits) return TL_ERR_UNSUPPORTED;
+  const tl_dtype q_dtype = dtype == TL_F32 ? TL_F32 : TL_BF16;
+  const size_t queries = rope_ws_queries(B, h_q, h_kv, d);
+  // a missing, small or misaligned workspace is refused by decode_impl after
+  // its other checks: it is told that it has none
+  if (workspace_bytes < queries + sizeof(float) * (size_t)B * h_q * d ||
+      (reinterpret_cast<uintptr_t>(workspace) & 255u))
+    workspace = nullptr;
+  if (!aligned_to(q, q_dtype == TL_F32 ? 4 : 2) || q_stride < 0) return TL_ERR_INVALID_ARG;
+  void* q_out = workspace ? static_cast<char*>(workspace) + queries : nullptr;
+  RopeStep step;
+  const tl_status ok = rope_rows_checked(
+      workspace ? q : nullptr, q_stride, q_out, (int64_t)h_q * d, k_new, k_stride, v_new,
+      v_stride, q_dtype, k_cache, v_cache, k_scales, v_scales, slot_mapping, positions, freqs,
+      rot_dim, interleaved, rope_scale, B, num_pages, page_size, workspace ? h_q : 0, h_kv, d,
+      dtype, error_word, &step.rows, &step.kind);
+  if (ok != TL_OK) return ok;
+  // the plan writes the workspace beside the CTAs that read the rows
+  const int64_t row = (int64_t)h_kv * d;
+  const size_t pool = (size_t)num_pages * page_size * row *
+                      (dtype == TL_F32 ? 4 : dtype == TL_BF16 ? 2 : 1);
+  const int elem = q_dtype == TL_F32 ? 4 : 2;
+  const struct {
+    const void* p;
+    size_t bytes;
+  } spans[] = {{q, (size_t)((B - 1) * q_stride + (int64_t)h_q * d) * elem},
+               {k_new, (size_t)((B - 1) * k_stride + row) * elem},
+               {v_new, (size_t)((B - 1) * v_stride + row) * elem},
+               {k_cache, pool},
+               {v_cache, pool}};
+  for (const auto& s : spans)
+    if (workspace && overlap(workspace, queries, s.p, s.bytes)) return TL_ERR_INVALID_ARG;
+  step.units = rope_in_units(step.rows, elem) ? d / 16 : 0;
+  // (q_out stands for q: 256-byte aligned, where q need not be)
+  return decode_impl<false>(workspace ? q_out : k_cache, k_cache, v_cache, block_table,
+                            max_pages_per_seq, context_lens, out, B, 1, h_q, h_kv, d, num_pages,
+                            page_size, window, ring_pages, scale,
+                            dtype == TL_INT8 ? TL_FP8_E4M3 : dtype, workspace, workspace_bytes,
+                            error_word, stream, NewRows(), k_scales, v_scales, DecodeExtra(),
+                            &step);
+}
+
+}  // namespace tl
+
 // ------------------------------------------------------------------- host --
 
 extern "C" tl_status tl_decode_trace_reset(void) {
@@ -189,4 +255,65 @@ extern "C" tl_status tl_paged_attn_decode_multi(
   return tl::decode_impl<false>(q, k_cache, v_cache, block_table, max_pages_per_seq, context_lens, out,
                          B, q_len, h_q, h_kv, d, num_pages, page_size, window, 0, scale, dtype,
                          workspace, workspace_bytes, error_word, stream);
+}
+
+extern "C" size_t tl_paged_attn_decode_write_rope_workspace_size(int32_t B, int32_t h_q,
+                                                                 int32_t h_kv, int32_t d) {
+  if (B <= 0 || h_q <= 0 || h_kv <= 0 || d <= 0 || h_q % h_kv) return 0;
+  return tl::rope_ws_queries(B, h_q, h_kv, d) + sizeof(float) * (size_t)B * h_q * d;
+}
+
+extern "C" tl_status tl_paged_attn_decode_write_rope(
+    const void* q, int64_t q_stride, const void* k_new, int64_t k_stride, const void* v_new,
+    int64_t v_stride, const int64_t* slot_mapping, const int32_t* positions,
+    const uint64_t* freqs, int32_t rot_dim, int32_t interleaved, float rope_scale, void* k_cache,
+    void* v_cache, const int32_t* block_table, int32_t max_pages_per_seq,
+    const int32_t* context_lens, float* out, int32_t B, int32_t h_q, int32_t h_kv, int32_t d,
+    int32_t num_pages, int32_t page_size, int32_t window, float scale, tl_dtype dtype,
+    void* workspace, size_t workspace_bytes, uint32_t* error_word, void* stream) {
+  if (dtype == TL_INT8) return TL_ERR_UNSUPPORTED;
+  return tl::decode_write_rope(q, q_stride, k_new, k_stride, v_new, v_stride, slot_mapping,
+                               positions, freqs, rot_dim, interleaved, rope_scale, k_cache,
+                               v_cache, nullptr, nullptr, block_table, max_pages_per_seq,
+                               context_lens, out, B, h_q, h_kv, d, num_pages, page_size, window,
+                               0, scale, dtype, workspace, workspace_bytes, error_word, stream);
+}
+
+extern "C" tl_status tl_paged_attn_decode_write_rope_int8(
+    const void* q, int64_t q_stride, const void* k_new, int64_t k_stride, const void* v_new,
+    int64_t v_stride, const int64_t* slot_mapping, const int32_t* positions,
+    const uint64_t* freqs, int32_t rot_dim, int32_t interleaved, float rope_scale,
+    int8_t* k_codes, int8_t* v_codes, float* k_scales, float* v_scales,
+    const int32_t* block_table, int32_t max_pages_per_seq, const int32_t* context_lens,
+    float* out, int32_t B, int32_t h_q, int32_t h_kv, int32_t d, int32_t num_pages,
+    int32_t page_size, int32_t window, float scale, void* workspace, size_t workspace_bytes,
+    uint32_t* error_word, void* stream) {
+  if (!k_scales || !v_scales) return TL_ERR_INVALID_ARG;
+  return tl::decode_write_rope(q, q_stride, k_new, k_stride, v_new, v_stride, slot_mapping,
+                               positions, freqs, rot_dim, interleaved, rope_scale, k_codes,
+                               v_codes, k_scales, v_scales, block_table, max_pages_per_seq,
+                               context_lens, out, B, h_q, h_kv, d, num_pages, page_size, window,
+                               0, scale, TL_INT8, workspace, workspace_bytes, error_word,
+                               stream);
+}
+
+extern "C" tl_status tl_paged_attn_decode_write_rope_ring(
+    const void* q, int64_t q_stride, const void* k_new, int64_t k_stride, const void* v_new,
+    int64_t v_stride, const int64_t* slot_mapping, const int32_t* positions,
+    const uint64_t* freqs, int32_t rot_dim, int32_t interleaved, float rope_scale, void* k_cache,
+    void* v_cache, const int32_t* block_table, int32_t max_pages_per_seq,
+    const int32_t* context_lens, float* out, int32_t B, int32_t h_q, int32_t h_kv, int32_t d,
+    int32_t num_pages, int32_t page_size, int32_t window, int32_t ring_pages, float scale,
+    tl_dtype dtype, void* workspace, size_t workspace_bytes, uint32_t* error_word,
+    void* stream) {
+  if (ring_pages <= 0 || ring_pages > max_pages_per_seq || window <= 0 || page_size <= 0 ||
+      (int64_t)ring_pages * page_size < window)
+    return TL_ERR_INVALID_ARG;
+  if (dtype == TL_INT8) return TL_ERR_UNSUPPORTED;
+  return tl::decode_write_rope(q, q_stride, k_new, k_stride, v_new, v_stride, slot_mapping,
+                               positions, freqs, rot_dim, interleaved, rope_scale, k_cache,
+                               v_cache, nullptr, nullptr, block_table, max_pages_per_seq,
+                               context_lens, out, B, h_q, h_kv, d, num_pages, page_size, window,
+                               ring_pages, scale, dtype, workspace, workspace_bytes, error_word,
+                               stream);
 }

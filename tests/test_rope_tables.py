@@ -13,6 +13,7 @@ from paged_kv_attention_cache_gb300 import _lib, api, build
 from tests import rope_ref as ref
 
 BAD, UNS, OK = tl.TL_ERR_INVALID_ARG, tl.TL_ERR_UNSUPPORTED, tl.TL_OK
+WS = tl.TL_ERR_WORKSPACE
 
 
 @pytest.fixture(scope="module", autouse=True)
@@ -254,6 +255,50 @@ def test_write_rope_refusals(lib):
     assert i(ksc=None) == BAD and i(vsc=None) == BAD and i(ksc=7 * M + 2) == BAD
     assert i(d=1040, rot=2) == UNS
     assert i(ksc=8 * M) == BAD and i(ksc=5 * M + 64) == BAD and i(vsc=3 * M) == BAD
+
+
+def test_step_refusals(lib):
+    M = 1 << 24
+    base = dict(q=M, qs=1024, k=3 * M, ks=256, v=4 * M, vs=256, sm=9 * M, pos=10 * M, f=11 * M,
+                rot=128, il=0, m=1.0, kc=5 * M, vc=6 * M, ksc=7 * M, vsc=8 * M, bt=12 * M, maxp=8,
+                cl=13 * M, out=14 * M, B=3, hq=8, hkv=2, d=128, P=16, ps=16, w=0, rp=8, sc=0.1,
+                dt=tl.TL_BF16, ws=None, wsb=0, err=None, st=None)
+    a = caller(lib.tl_paged_attn_decode_write_rope,
+               "q qs k ks v vs sm pos f rot il m kc vc bt maxp cl out B hq hkv d P ps w sc dt ws "
+               "wsb err st", base)
+    i = caller(lib.tl_paged_attn_decode_write_rope_int8,
+               "q qs k ks v vs sm pos f rot il m kc vc ksc vsc bt maxp cl out B hq hkv d P ps w sc "
+               "ws wsb err st", base)
+    g = caller(lib.tl_paged_attn_decode_write_rope_ring,
+               "q qs k ks v vs sm pos f rot il m kc vc bt maxp cl out B hq hkv d P ps w rp sc dt "
+               "ws wsb err st", dict(base, w=100))
+    size = tl.tl_paged_attn_decode_write_rope_workspace_size
+    need = size(3, 8, 2, 128)
+    assert need >= tl.tl_paged_attn_decode_workspace_size(3, 8, 2, 128) + 4 * 3 * 8 * 128
+    assert size(0, 8, 2, 128) == 0 and size(3, 7, 2, 128) == 0 and size(3, 8, 2, 0) == 0
+    for call in (a, i, g):
+        assert call() == WS and call(ws=1 << 30, wsb=need - 1) == WS
+        assert call(ws=(1 << 30) + 128, wsb=need) == WS
+        for name in ("q", "k", "v", "sm", "pos", "f", "kc", "vc", "bt", "cl", "out"):
+            assert call(**{name: None}) == BAD, name
+        for name in ("B", "hq", "hkv", "d", "P", "ps", "maxp"):
+            assert call(**{name: 0}) == BAD and call(**{name: -1}) == BAD, name
+        assert call(hq=7) == BAD and call(w=-1) == BAD
+        for rot in (0, 3, 130):
+            assert call(rot=rot) == BAD
+        for name, off in (("sm", 4), ("pos", 2), ("f", 4), ("q", 1), ("k", 1), ("kc", 8),
+                          ("out", 8), ("bt", 2), ("cl", 2)):
+            assert call(**{name: base[name] + off}) == BAD, name
+        for name in ("qs", "ks", "vs"):
+            assert call(**{name: -1}) == BAD
+        assert call(d=256, rot=128) == UNS and call(hq=34) == UNS and call(ps=257) == UNS
+        assert call(d=96, rot=96) == UNS
+        # the workspace over the rows or the pools
+        assert call(ws=3 * M - 4096, wsb=need) == BAD and call(ws=5 * M, wsb=need) == BAD
+    for call in (a, g):
+        assert call(dt=tl.TL_INT8) == UNS and call(dt=9) == UNS
+    assert i(ksc=None) == BAD and i(vsc=None) == BAD and i(ps=24) == UNS and i(ps=8) == UNS
+    assert g(w=0) == BAD and g(rp=0) == BAD and g(rp=9) == BAD and g(w=129) == BAD
 
 
 def test_compact_rope_refusals(lib):
