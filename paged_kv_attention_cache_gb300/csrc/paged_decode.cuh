@@ -551,122 +551,131 @@ __device__ __forceinline__ void warp_plan(const DecodeParams& P, int target_spli
   }
 }
 
-// The CTAs past the first of a plan launch write the call's new rows: one warp
-// per token (per token and KV head for int8 pools), slot -1 skipped, a slot
-// outside the pools reported and skipped.
-static __device__ __forceinline__ void write_new_rows(const DecodeParams& P) {
-  const int lane = threadIdx.x & 31, wid = threadIdx.x >> 5, nw = blockDim.x >> 5;
-  // a block enlarged for the warp plan writes with kWriteWarps of its
-  // warps, so the rows still spread over as many SMs
-  const int wpc = P.B <= kWarpPlanMax ? min(nw, kWriteWarps) : nw;
-  if (wid >= wpc) return;
-  const int64_t first = (int64_t)(blockIdx.x - 1) * wpc + wid;
-  const int64_t stride = (int64_t)(gridDim.x - 1) * wpc;
-  const int64_t n_slots = (int64_t)P.num_pages * P.page_size;
-  if (P.new_kind >= 3) {
-    // int8 pools: one warp per (token, KV head) row; the scales written
-    // here are read by the attention kernel after this grid
-    for (int64_t r = first; r < (int64_t)P.n_new * P.h_kv; r += stride) {
-      const int64_t t = r / P.h_kv;
-      const int g = (int)(r % P.h_kv);
-      const int64_t slot = P.slot_mapping[t];
-      if (slot == -1) continue;
-      if (slot < 0 || slot >= n_slots) {
-        if (lane == 0 && g == 0) report(P.error_word, TL_DEVERR_SLOT_RANGE);
-        continue;
-      }
-      int8_t* kd = static_cast<int8_t*>(P.k_dst);
-      int8_t* vd = static_cast<int8_t*>(P.v_dst);
-      float* ksc = const_cast<float*>(P.k_scales);
-      float* vsc = const_cast<float*>(P.v_scales);
-      if (P.d == 128) {
-        if (P.new_kind == 3)
-          write_head_rows_int8_d128<false>(P.k_new, P.v_new, kd, vd, ksc, vsc, t, g, slot,
-                                           P.page_size, P.h_kv, lane, P.error_word);
-        else
-          write_head_rows_int8_d128<true>(P.k_new, P.v_new, kd, vd, ksc, vsc, t, g, slot,
-                                          P.page_size, P.h_kv, lane, P.error_word);
-      } else if (P.new_kind == 3) {
-        write_head_rows_int8<false>(P.k_new, P.v_new, kd, vd, ksc, vsc, t, g, slot,
-                                    P.page_size, P.h_kv, P.d, lane, P.error_word);
-      } else {
-        write_head_rows_int8<true>(P.k_new, P.v_new, kd, vd, ksc, vsc, t, g, slot,
-                                   P.page_size, P.h_kv, P.d, lane, P.error_word);
-      }
-    }
-    return;
-  }
-  // rows of 32 x 1, 2, 4 (or 8) units: every load before any store
-  const int u = P.row_units;
-  const int upl = u % 32 == 0 ? u / 32 : 0;
-  if (P.new_kind == 0 && (upl == 1 || upl == 2 || upl == 4 || upl == 8)) {
-    const int4* kn = static_cast<const int4*>(P.k_new);
-    const int4* vn = static_cast<const int4*>(P.v_new);
-    int4* kd = static_cast<int4*>(P.k_dst);
-    int4* vd = static_cast<int4*>(P.v_dst);
-    for (int64_t t = first; t < P.n_new; t += stride) {
-      if (upl == 1) write_tokens_vec<1, 1>(kn, vn, kd, vd, P.slot_mapping, t, P.n_new, n_slots, lane, P.error_word);
-      else if (upl == 2) write_tokens_vec<2, 1>(kn, vn, kd, vd, P.slot_mapping, t, P.n_new, n_slots, lane, P.error_word);
-      else if (upl == 4) write_tokens_vec<4, 1>(kn, vn, kd, vd, P.slot_mapping, t, P.n_new, n_slots, lane, P.error_word);
-      else write_tokens_vec<8, 1>(kn, vn, kd, vd, P.slot_mapping, t, P.n_new, n_slots, lane, P.error_word);
-    }
-    return;
-  }
-  if ((P.new_kind == 1 || P.new_kind == 2) && (upl == 1 || upl == 2 || upl == 4)) {
-    uint2* kd = static_cast<uint2*>(P.k_dst);
-    uint2* vd = static_cast<uint2*>(P.v_dst);
-    for (int64_t t = first; t < P.n_new; t += stride) {
-#define TL_E4M3_VEC(F32, U) \
-  write_tokens_e4m3_vec<F32, U, 1>(P.k_new, P.v_new, kd, vd, P.slot_mapping, t, P.n_new, n_slots, lane, P.error_word)
-      if (P.new_kind == 1) {
-        if (upl == 1) TL_E4M3_VEC(false, 1);
-        else if (upl == 2) TL_E4M3_VEC(false, 2);
-        else TL_E4M3_VEC(false, 4);
-      } else {
-        if (upl == 1) TL_E4M3_VEC(true, 1);
-        else if (upl == 2) TL_E4M3_VEC(true, 2);
-        else TL_E4M3_VEC(true, 4);
-      }
-#undef TL_E4M3_VEC
-    }
-    return;
-  }
-  for (int64_t t = first; t < P.n_new; t += stride) {
-    const int64_t slot = P.slot_mapping[t];
-    if (slot == -1) continue;
-    if (slot < 0 || slot >= n_slots) {
-      if (lane == 0) report(P.error_word, TL_DEVERR_SLOT_RANGE);
-      continue;
-    }
-    if (P.new_kind == 0)
-      write_token_rows(static_cast<const int4*>(P.k_new) + t * u,
-                       static_cast<const int4*>(P.v_new) + t * u,
-                       static_cast<int4*>(P.k_dst) + slot * u,
-                       static_cast<int4*>(P.v_dst) + slot * u, u, lane);
-    else if (P.new_kind == 1)
-      write_token_rows_e4m3<false>(P.k_new, P.v_new, static_cast<uint2*>(P.k_dst),
-                                   static_cast<uint2*>(P.v_dst), t, slot, u, lane);
-    else
-      write_token_rows_e4m3<true>(P.k_new, P.v_new, static_cast<uint2*>(P.k_dst),
-                                  static_cast<uint2*>(P.v_dst), t, slot, u, lane);
-  }
-}
-
 // One CTA.  Up to kWarpPlanMax sequences: warp 0 plans alone (above).
 // Larger batches: thread t keeps sequence t's range in registers (sequences
 // past the block size are re-read in each pass); three block reductions fix
 // the piece sizes, and one scan of (bulk pieces << 32 | small pieces) places
 // every piece.  Either way every thread then writes descriptors, one piece
 // at a time.  first_dynamic: items below it are taken without the counter
-// (the attention kernel's warp w starts with item w).
-template <bool EX>
-static __device__ __forceinline__ void plan_batch(const DecodeParams& P, int target_splits,
-                                                  int first_dynamic) {
+// (the attention kernel's warp w starts with item w).  Rows: the rows that the
+// launch's other CTAs move in place of P's new ones (rows.write(P)), or none.
+struct PlainRows {};
+template <bool EX, class Rows>
+static __global__ void __launch_bounds__(1024) decode_plan_kernel(DecodeParams P, int target_splits,
+                                                                  int first_dynamic, Rows rows) {
   __shared__ long long red[2][32];
   __shared__ long long tmp[32];
   __shared__ int4 rec[1024];  // per sequence of a round: first bulk / small position, counts
   __shared__ int2 rng[1024];  // its lo, p
-  const int tid = threadIdx.x, nt = blockDim.x, lane = tid & 31, wid = tid >> 5;
+  const int tid = threadIdx.x, nt = blockDim.x, lane = tid & 31, wid = tid >> 5, nw = nt >> 5;
+  if (blockIdx.x == 0 && tid == 0) TL_TRACE_SET(TL_TRACE_PLAN_START);
+  // the attention kernel may launch now: it waits for this grid's results
+  // (griddepcontrol.wait) after its own set-up
+  asm volatile("griddepcontrol.launch_dependents;\n" ::: "memory");
+  if (blockIdx.x > 0) {
+    if constexpr (!std::is_same<Rows, PlainRows>::value) {
+      rows.write(P);
+      return;
+    }
+    // CTAs past the first write the call's new rows: one warp per token (per
+    // token and KV head for int8 pools), slot -1 skipped, a slot outside the
+    // pools reported and skipped
+    // a block enlarged for the warp plan writes with kWriteWarps of its
+    // warps, so the rows still spread over as many SMs
+    const int wpc = P.B <= kWarpPlanMax ? min(nw, kWriteWarps) : nw;
+    if (wid >= wpc) return;
+    const int64_t first = (int64_t)(blockIdx.x - 1) * wpc + wid;
+    const int64_t stride = (int64_t)(gridDim.x - 1) * wpc;
+    const int64_t n_slots = (int64_t)P.num_pages * P.page_size;
+    if (P.new_kind >= 3) {
+      // int8 pools: one warp per (token, KV head) row; the scales written
+      // here are read by the attention kernel after this grid
+      for (int64_t r = first; r < (int64_t)P.n_new * P.h_kv; r += stride) {
+        const int64_t t = r / P.h_kv;
+        const int g = (int)(r % P.h_kv);
+        const int64_t slot = P.slot_mapping[t];
+        if (slot == -1) continue;
+        if (slot < 0 || slot >= n_slots) {
+          if (lane == 0 && g == 0) report(P.error_word, TL_DEVERR_SLOT_RANGE);
+          continue;
+        }
+        int8_t* kd = static_cast<int8_t*>(P.k_dst);
+        int8_t* vd = static_cast<int8_t*>(P.v_dst);
+        float* ksc = const_cast<float*>(P.k_scales);
+        float* vsc = const_cast<float*>(P.v_scales);
+        if (P.d == 128) {
+          if (P.new_kind == 3)
+            write_head_rows_int8_d128<false>(P.k_new, P.v_new, kd, vd, ksc, vsc, t, g, slot,
+                                             P.page_size, P.h_kv, lane, P.error_word);
+          else
+            write_head_rows_int8_d128<true>(P.k_new, P.v_new, kd, vd, ksc, vsc, t, g, slot,
+                                            P.page_size, P.h_kv, lane, P.error_word);
+        } else if (P.new_kind == 3) {
+          write_head_rows_int8<false>(P.k_new, P.v_new, kd, vd, ksc, vsc, t, g, slot,
+                                      P.page_size, P.h_kv, P.d, lane, P.error_word);
+        } else {
+          write_head_rows_int8<true>(P.k_new, P.v_new, kd, vd, ksc, vsc, t, g, slot,
+                                     P.page_size, P.h_kv, P.d, lane, P.error_word);
+        }
+      }
+      return;
+    }
+    // rows of 32 x 1, 2, 4 (or 8) units: every load before any store
+    const int u = P.row_units;
+    const int upl = u % 32 == 0 ? u / 32 : 0;
+    if (P.new_kind == 0 && (upl == 1 || upl == 2 || upl == 4 || upl == 8)) {
+      const int4* kn = static_cast<const int4*>(P.k_new);
+      const int4* vn = static_cast<const int4*>(P.v_new);
+      int4* kd = static_cast<int4*>(P.k_dst);
+      int4* vd = static_cast<int4*>(P.v_dst);
+      for (int64_t t = first; t < P.n_new; t += stride) {
+        if (upl == 1) write_tokens_vec<1, 1>(kn, vn, kd, vd, P.slot_mapping, t, P.n_new, n_slots, lane, P.error_word);
+        else if (upl == 2) write_tokens_vec<2, 1>(kn, vn, kd, vd, P.slot_mapping, t, P.n_new, n_slots, lane, P.error_word);
+        else if (upl == 4) write_tokens_vec<4, 1>(kn, vn, kd, vd, P.slot_mapping, t, P.n_new, n_slots, lane, P.error_word);
+        else write_tokens_vec<8, 1>(kn, vn, kd, vd, P.slot_mapping, t, P.n_new, n_slots, lane, P.error_word);
+      }
+      return;
+    }
+    if ((P.new_kind == 1 || P.new_kind == 2) && (upl == 1 || upl == 2 || upl == 4)) {
+      uint2* kd = static_cast<uint2*>(P.k_dst);
+      uint2* vd = static_cast<uint2*>(P.v_dst);
+      for (int64_t t = first; t < P.n_new; t += stride) {
+#define TL_E4M3_VEC(F32, U) \
+  write_tokens_e4m3_vec<F32, U, 1>(P.k_new, P.v_new, kd, vd, P.slot_mapping, t, P.n_new, n_slots, lane, P.error_word)
+        if (P.new_kind == 1) {
+          if (upl == 1) TL_E4M3_VEC(false, 1);
+          else if (upl == 2) TL_E4M3_VEC(false, 2);
+          else TL_E4M3_VEC(false, 4);
+        } else {
+          if (upl == 1) TL_E4M3_VEC(true, 1);
+          else if (upl == 2) TL_E4M3_VEC(true, 2);
+          else TL_E4M3_VEC(true, 4);
+        }
+#undef TL_E4M3_VEC
+      }
+      return;
+    }
+    for (int64_t t = first; t < P.n_new; t += stride) {
+      const int64_t slot = P.slot_mapping[t];
+      if (slot == -1) continue;
+      if (slot < 0 || slot >= n_slots) {
+        if (lane == 0) report(P.error_word, TL_DEVERR_SLOT_RANGE);
+        continue;
+      }
+      if (P.new_kind == 0)
+        write_token_rows(static_cast<const int4*>(P.k_new) + t * u,
+                         static_cast<const int4*>(P.v_new) + t * u,
+                         static_cast<int4*>(P.k_dst) + slot * u,
+                         static_cast<int4*>(P.v_dst) + slot * u, u, lane);
+      else if (P.new_kind == 1)
+        write_token_rows_e4m3<false>(P.k_new, P.v_new, static_cast<uint2*>(P.k_dst),
+                                     static_cast<uint2*>(P.v_dst), t, slot, u, lane);
+      else
+        write_token_rows_e4m3<true>(P.k_new, P.v_new, static_cast<uint2*>(P.k_dst),
+                                    static_cast<uint2*>(P.v_dst), t, slot, u, lane);
+    }
+    return;
+  }
   if (P.B <= kWarpPlanMax) {
     __shared__ int s_plan[4];  // split, small, bulk pieces (-1: refused), small pieces
     if (tid < P.B) {  // the block holds at least B threads
@@ -769,47 +778,6 @@ static __device__ __forceinline__ void plan_batch(const DecodeParams& P, int tar
     P.ws.ctrl[1] = total;
     P.ws.ctrl[2] = first_dynamic;
     TL_TRACE_SET(TL_TRACE_PLAN_END);  // after the last round's barrier
-  }
-}
-
-template <bool EX>
-static __global__ void __launch_bounds__(1024) decode_plan_kernel(DecodeParams P, int target_splits,
-                                                                  int first_dynamic) {
-  if (blockIdx.x == 0 && threadIdx.x == 0) TL_TRACE_SET(TL_TRACE_PLAN_START);
-  // the attention kernel may launch now: it waits for this grid's results
-  // (griddepcontrol.wait) after its own set-up
-  asm volatile("griddepcontrol.launch_dependents;\n" ::: "memory");
-  if (blockIdx.x > 0) write_new_rows(P);
-  else plan_batch<EX>(P, target_splits, first_dynamic);
-}
-
-// The plan launch of a step that rotates its queries and new keys itself: the
-// CTAs past the first rotate the queries into the workspace (the attention
-// kernel reads them there) and write the rows, one warp per pass over a token's
-// heads in rotary units, or per row where rows are not made of them.
-template <bool F32, int KIND, bool INTER>
-static __global__ void __launch_bounds__(1024) decode_plan_rope_kernel(DecodeParams P, RopeRows R,
-                                                                       int units,
-                                                                       int target_splits,
-                                                                       int first_dynamic) {
-  if (blockIdx.x == 0 && threadIdx.x == 0) TL_TRACE_SET(TL_TRACE_PLAN_START);
-  asm volatile("griddepcontrol.launch_dependents;\n" ::: "memory");
-  if (blockIdx.x == 0) {
-    plan_batch<false>(P, target_splits, first_dynamic);
-    return;
-  }
-  __shared__ float4 cs[32][4 * kRopeStepUnits];
-  const int lane = threadIdx.x & 31, wid = threadIdx.x >> 5;
-  const int warps = P.B <= kWarpPlanMax ? kWriteWarps : (int)(blockDim.x >> 5);
-  if (wid >= warps) return;
-  const int heads = R.h_q + 2 * R.h_kv, HW = units ? 32 / units : 1;
-  const int per = (heads + HW - 1) / HW;
-  const int64_t stride = (int64_t)(gridDim.x - 1) * warps;
-  for (int64_t i = (int64_t)(blockIdx.x - 1) * warps + wid; i < (int64_t)R.n * per; i += stride) {
-    const int64_t t = i / per;
-    const int h = (int)(i - t * per) * HW;
-    if (units) rope_units<F32, KIND, INTER, 1>(R, t, h, heads, units, HW, lane, cs[wid]);
-    else rope_row<F32, KIND>(R, t, h, lane);
   }
 }
 
@@ -2735,27 +2703,9 @@ struct RopeStep {
   int kind, units;
 };
 
-// Warps that they take: a pass over a token's heads each.
-static int64_t rope_step_warps(const RopeStep& r) {
-  const int heads = r.rows.h_q + 2 * r.rows.h_kv, HW = r.units ? 32 / r.units : 1;
-  return (int64_t)r.rows.n * ((heads + HW - 1) / HW);
-}
-
-template <bool EX>
-static cudaError_t launch_plan_rope(const DecodeParams& P, const RopeStep& r, unsigned grid,
-                                    int threads, int target_splits, int first_dynamic, bool f32,
-                                    cudaStream_t st) {
-  const bool inter = r.rows.interleaved != 0;
-#define TL_PLAN_ROPE(F32, K) \
-  (inter ? decode_plan_rope_kernel<F32, K, true> : decode_plan_rope_kernel<F32, K, false>)
-  auto kern = f32                   ? TL_PLAN_ROPE(true, kRopeSame)
-              : r.kind == kRopeSame ? TL_PLAN_ROPE(false, kRopeSame)
-              : r.kind == kRopeE4m3 ? TL_PLAN_ROPE(false, kRopeE4m3)
-                                    : TL_PLAN_ROPE(false, kRopeInt8);
-#undef TL_PLAN_ROPE
-  kern<<<grid, threads, 0, st>>>(P, r.rows, r.units, target_splits, first_dynamic);
-  return cudaGetLastError();
-}
+// Its plan launch (paged_decode.cu).
+cudaError_t launch_plan_rope(const DecodeParams& P, const RopeStep& r, int plan_threads,
+                             int target_splits, int first_dynamic, bool f32, cudaStream_t st);
 
 template <bool EX>
 static tl_status decode_impl(const void* q, const void* k_cache, const void* v_cache,
@@ -2905,20 +2855,18 @@ static tl_status decode_impl(const void* q, const void* k_cache, const void* v_c
   const int64_t write_warps = P.new_kind >= 3 ? (int64_t)P.n_new * h_kv : P.n_new;
   const int wpc = B <= kWarpPlanMax ? kWriteWarps : plan_threads / 32;
   const int64_t write_ctas =
-      rope ? std::min<int64_t>(num_sms(), (rope_step_warps(*rope) + wpc - 1) / wpc)
-      : P.n_new > 0 ? std::min<int64_t>(num_sms(), (write_warps + wpc - 1) / wpc) : 0;
+      P.n_new > 0 ? std::min<int64_t>(num_sms(), (write_warps + wpc - 1) / wpc) : 0;
   P.target_splits = target_splits;
   const bool self_plan =
       EX && dtype != TL_F32 && plans_itself(kv8, ex.mass != nullptr, rows, B, h_kv) &&
       warps * 32 >= B;  // a CTA's thread reads a sequence's length each
   if constexpr (!EX)
-    if (rope && launch_plan_rope<EX>(P, *rope, (unsigned)(1 + write_ctas), plan_threads,
-                                     target_splits, num_sms() * warps, dtype == TL_F32,
-                                     st) != cudaSuccess)
+    if (rope && launch_plan_rope(P, *rope, plan_threads, target_splits, num_sms() * warps,
+                                 dtype == TL_F32, st) != cudaSuccess)
       return TL_ERR_CUDA;
   if (!self_plan && !rope) {
     decode_plan_kernel<EX><<<(unsigned)(1 + write_ctas), plan_threads, 0, st>>>(
-        P, target_splits, num_sms() * warps);
+        P, target_splits, num_sms() * warps, PlainRows());
     if (launch_status() != TL_OK) return TL_ERR_CUDA;
   }
 
