@@ -76,7 +76,7 @@ def _need(t: torch.Tensor, name: str, dtype=None, shape=None, device=None):
         raise ValueError(f"{name} must be contiguous")
     if dtype is not None and t.dtype != dtype:
         raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
-    if shape is not None:
+    if shape is not None and t.shape != shape:
         ts = t.shape
         bad = len(ts) != len(shape)
         if not bad:
@@ -232,7 +232,7 @@ def _alloc_stream(stream, device):
 def _returned(shape, dtype, device, stream):
     """A tensor that the call returns.  The caller uses it on the current stream
     too: it is not reused before that stream's work so far at its release."""
-    on = _alloc_stream(stream, device)
+    on = None if stream is None else _alloc_stream(stream, device)
     if on is None:
         return torch.empty(shape, dtype=dtype, device=device)
     with torch.cuda.device(device):
@@ -1054,7 +1054,8 @@ def _write_rope_rows(q, k_new, v_new, slot_mapping, positions, freqs, q_out, hkv
             q_out, out_stride = _returned((N, hq, d), dtype, dev, stream), hq * d
         else:
             out_stride = _need_rows(q_out, "q_out", N, hq, d, dev, dtype)
-    return (_ptr(q), q_stride, _ptr(q_out), out_stride, k_new.data_ptr(), k_stride,
+    return (None if q is None else q.data_ptr(), q_stride,
+            None if q is None else q_out.data_ptr(), out_stride, k_new.data_ptr(), k_stride,
             v_new.data_ptr(), v_stride, _DTYPES.get(dtype, -1)), N, hq, rot, q_out
 
 
@@ -1075,9 +1076,10 @@ def tl_kv_cache_write_rope(q: Optional[torch.Tensor], k_new: torch.Tensor, v_new
     rows, N, hq, rot, q_out = _write_rope_rows(q, k_new, v_new, slot_mapping, positions, freqs,
                                                q_out, hkv, d, dev, stream)
     _run("tl_kv_cache_write_rope", dev, stream,
-         *rows, _ptr(k_cache), _ptr(v_cache), _ptr(slot_mapping), _ptr(positions), _ptr(freqs),
-         rot, 1 if interleaved else 0, rope_scale, N, P, ps, hq, hkv, d,
-         _DTYPES.get(k_cache.dtype, -1), _err_word(error_word, dev))
+         *rows, k_cache.data_ptr(), v_cache.data_ptr(), slot_mapping.data_ptr(),
+         positions.data_ptr(), freqs.data_ptr(), rot, 1 if interleaved else 0, rope_scale, N, P,
+         ps, hq, hkv, d, _DTYPES.get(k_cache.dtype, -1),
+         None if error_word is None else _err_word(error_word, dev))
     return q_out
 
 

@@ -767,3 +767,72 @@ def test_a_captured_step_replayed():
                 assert torch.equal(a, b)
             for x, b in pools.t.items():
                 assert torch.equal(b, held[x]), x
+
+
+@pytest.mark.parametrize("kind", ["bf16", "e4m3", "int8"])
+def test_compact_lists_in_any_order(kind):
+    """Entries at or behind their place, in no order and some of them twice; many heads and few."""
+    for lens, hkv in (([500, 300], 1), ([400] * 60, 3)):
+        n, d, ps = 120, 128, 16
+        tbl, P = lref.tables(lens, ps, seed=1)
+        g = np.random.default_rng(5)
+        keep = np.stack([[np.array([g.integers(j, L) for j in range(n)]) for _ in range(hkv)]
+                         for L in lens]).astype(np.int32)
+        keep[:, :, 7] = keep[:, :, 3] = 40
+        keep[:, :, ::10] = np.arange(0, n, 10)
+        new = np.full(len(lens), n, np.int32)
+        freqs, f = table(128)
+        pools = Pools(kind, P, ps, hkv, d, seed=2)
+        run_compact(pools, tbl, lens, keep, new, freqs, False)
+        check_compact(pools, tbl, lens, keep, new, f, False)
+
+
+def test_compact_by_the_largest_shift():
+    """The last of 200,000 keys moved to the front: 199,999 positions back."""
+    L, hkv, d, ps = 200_000, 1, 128, 64
+    tbl, P = lref.tables([L], ps, seed=1)
+    pools = Pools("bf16", P, ps, hkv, d, seed=2)
+    keep, new = np.array([[[L - 1, 1, L - 2]]], np.int32), np.array([3], np.int32)
+    freqs, f = table(128, 500000.0)
+    run_compact(pools, tbl, [L], keep, new, freqs, True)
+    check_compact(pools, tbl, [L], keep, new, f, True)
+
+
+def test_compact_of_nothing():
+    """No length, or nothing that moves: every byte stays."""
+    tbl, P = lref.tables([40, 30], 16, seed=1)
+    pools = Pools("bf16", P, 16, 2, 128, seed=2)
+    freqs, f = table(128)
+    keep = np.tile(np.arange(30, dtype=np.int32), (2, 2, 1))
+    for lens, new in (([40, 30], [30, 30]), ([0, 0], [0, 0]), ([40, 30], [0, 0]),
+                      ([-3, 30], [0, 30])):
+        run_compact(pools, tbl, lens, keep, new, freqs, False)
+        check_compact(pools, tbl, lens, keep, new, f, False)
+
+
+def test_appends_on_two_streams_at_once():
+    """Disjoint slots of one pool, written by two streams' calls that overlap."""
+    n, hq, hkv, d, ps = 2048, 8, 2, 128, 16
+    freqs, f = table(128)
+    pools = Pools("bf16", 2 * n // ps, ps, hkv, d)
+    halves = []
+    for i in range(2):
+        rows = ref.randn((n, hq + 2 * hkv, d), torch.bfloat16, i).cuda()
+        halves.append((rows, torch.arange(i, 2 * n, 2).cuda(), i32(np.arange(n) * 3 + i)))
+    streams = [torch.cuda.Stream() for _ in range(2)]
+    w = word()
+    torch.cuda.synchronize()
+    for _ in range(3):
+        for s, (rows, slots, pos) in zip(streams, halves):
+            with torch.cuda.stream(s):
+                q, k, v = rows.split([hq, hkv, hkv], 1)
+                pools.append(q, k, v, slots, pos, freqs, err=w)
+    torch.cuda.synchronize()
+    assert int(w.item()) == 0
+    k = torch.empty(2 * n, hkv, d, dtype=torch.bfloat16)
+    v = torch.empty_like(k)
+    pos = np.empty(2 * n, np.int64)
+    for i, (rows, slots, p) in enumerate(halves):
+        k[i::2], v[i::2] = rows[:, hq:hq + hkv].cpu(), rows[:, hq + hkv:].cpu()
+        pos[i::2] = p.cpu().numpy()
+    pools.check(k, v, np.arange(2 * n), pos, f, False, 1.0, "two streams")
