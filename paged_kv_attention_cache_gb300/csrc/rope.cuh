@@ -37,6 +37,11 @@ TL_DEVINLINE uint64_t f2_fma(uint64_t a, uint64_t b, uint64_t c) {
   asm("fma.rn.f32x2 %0, %1, %2, %3;\n" : "=l"(r) : "l"(a), "l"(b), "l"(c));
   return r;
 }
+TL_DEVINLINE uint64_t f2_add(uint64_t a, uint64_t b) {
+  uint64_t r;
+  asm("add.rn.f32x2 %0, %1, %2;\n" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
 TL_DEVINLINE uint64_t f2_mul(uint64_t a, uint64_t b) {
   uint64_t r;
   asm("mul.rn.f32x2 %0, %1, %2;\n" : "=l"(r) : "l"(a), "l"(b));
@@ -163,8 +168,17 @@ struct RopeUnit {
         x[2 * i + 1] = f.y;
       }
     } else {
+      // a code c as the float 2^23 + 128 + c, whose last byte is c + 128
 #pragma unroll
-      for (int i = 0; i < 16; ++i) x[i] = (float)(int8_t)(v[i >> 2] >> (8 * (i & 3)));
+      for (int i = 0; i < 16; i += 2) {
+        const uint32_t w4 = v[i >> 2] ^ 0x80808080u;
+        const float2 f = f2_unpack(f2_add(
+            f2_pack(__uint_as_float(__byte_perm(w4, 0x4b000000u, 0x7650 + (i & 3))),
+                    __uint_as_float(__byte_perm(w4, 0x4b000000u, 0x7651 + (i & 3)))),
+            f2_pack(-8388736.f, -8388736.f)));
+        x[i] = f.x;
+        x[i + 1] = f.y;
+      }
     }
   }
   // values rounded to the type (not int8)
@@ -177,8 +191,24 @@ struct RopeUnit {
 #pragma unroll
       for (int i = 0; i < 8; ++i) v[i] = pack_bf16x2(x[2 * i], x[2 * i + 1]);
     } else {
+      // (a sum that is a number has no NaN in it; otherwise each value is looked at)
+      uint64_t sum = f2_pack(x[0], x[1]);
 #pragma unroll
-      for (int i = 0; i < 4; ++i) v[i] = e4m3x4(x[4 * i], x[4 * i + 1], x[4 * i + 2], x[4 * i + 3]);
+      for (int i = 2; i < 16; i += 2) sum = f2_add(sum, f2_pack(x[i], x[i + 1]));
+      const float2 s = f2_unpack(sum);
+      if (s.x + s.y == s.x + s.y) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          uint16_t lo, hi;
+          asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;\n" : "=h"(lo) : "f"(x[4 * i + 1]), "f"(x[4 * i]));
+          asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;\n" : "=h"(hi) : "f"(x[4 * i + 3]), "f"(x[4 * i + 2]));
+          v[i] = (uint32_t)lo | ((uint32_t)hi << 16);
+        }
+      } else {
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+          v[i] = e4m3x4(x[4 * i], x[4 * i + 1], x[4 * i + 2], x[4 * i + 3]);
+      }
     }
   }
   // int8: the codes of values x with scale sc, x / sc in binary32 rounded half
@@ -196,10 +226,16 @@ struct RopeUnit {
       uint32_t code[4];
       bool divide = !normal;
 #pragma unroll
-      for (int k = 0; k < 4; ++k) {
-        const float q = x[4 * i + k] * inv, r = q + kWhole;
-        divide |= fabsf(fabsf(q - (r - kWhole)) - 0.5f) < 0x1p-15f;
-        code[k] = __float_as_uint(r);
+      for (int k = 0; k < 4; k += 2) {
+        const uint64_t q = f2_mul(f2_pack(x[4 * i + k], x[4 * i + k + 1]), f2_pack(inv, inv));
+        const uint64_t r = f2_add(q, f2_pack(kWhole, kWhole));
+        // q - (r - kWhole)
+        const float2 off = f2_unpack(f2_fma(f2_add(r, f2_pack(-kWhole, -kWhole)),
+                                            f2_pack(-1.f, -1.f), q));
+        divide |= fmaxf(fabsf(off.x), fabsf(off.y)) > 0.5f - 0x1p-15f;
+        const float2 c = f2_unpack(r);
+        code[k] = __float_as_uint(c.x);
+        code[k + 1] = __float_as_uint(c.y);
       }
       if (divide)
 #pragma unroll
