@@ -220,6 +220,51 @@ struct CompactTurn {
   int32_t cluster;        // CTAs of a cluster
 };
 
+// A row's units here: rot is a multiple of 16 too, so in the layout of halves a
+// unit turns as a whole (u < rot / 16: its lower words rot/4 apart, for W = 4) or
+// lies as a whole behind the rotated part; interleaved as in rope_unit_words.
+template <bool INTER, int W>
+struct CompactUnits {
+  static constexpr int NW = 16 / W, n = INTER ? W / 2 : W;
+  static TL_DEVINLINE void words(int u, int d, int rot, int* at) {
+    if (!INTER && 16 * u < rot) {
+#pragma unroll
+      for (int w = 0; w < NW; ++w)
+        at[w] = W * u + (w % (NW / 2)) * (rot >> 2) + (w >= NW / 2 ? rot >> 1 : 0);
+    } else {
+      const int from = INTER ? 0 : rot;
+#pragma unroll
+      for (int w = 0; w < NW; ++w) at[w] = from + w * ((d - from) / NW) + W * (u - (from >> 4));
+    }
+  }
+  // whether pair k turns, and its index
+  static TL_DEVINLINE bool turn(const int* at, int k, int u, int rot) {
+    return INTER ? at[k / n] < rot : 16 * u < rot;
+  }
+  static TL_DEVINLINE int index(const int* at, int k) {
+    return (INTER ? at[k / n] >> 1 : at[k / n]) + k % n;
+  }
+  // the unit's values turned back by m positions, two pairs at once
+  static TL_DEVINLINE void turn_back(float* x, const int* at, int u, int rot,
+                                     const uint64_t* freqs, uint32_t m) {
+    uint64_t f[8];
+#pragma unroll
+    for (int k = 0; k < 8; ++k) f[k] = turn(at, k, u, rot) ? __ldg(freqs + index(at, k)) : 0;
+#pragma unroll
+    for (int k = 0; k < 8; k += 2) {
+      if (!turn(at, k, u, rot)) continue;
+      float2 a, b;
+      rope_turns(f[k], f[k + 1], m, a, b);
+      float &la = INTER ? x[2 * k] : x[k], &ha = INTER ? x[2 * k + 1] : x[8 + k];
+      float &lb = INTER ? x[2 * k + 2] : x[k + 1], &hb = INTER ? x[2 * k + 3] : x[9 + k];
+      const uint64_t lo = f2_pack(la, lb), hi = f2_pack(ha, hb), c = f2_pack(a.x, b.x);
+      const float2 l = f2_unpack(f2_fma(lo, c, f2_mul(hi, f2_pack(a.y, b.y))));
+      const float2 h = f2_unpack(f2_fma(hi, c, f2_mul(lo, f2_pack(-a.y, -b.y))));
+      la = l.x, lb = l.y, ha = h.x, hb = h.y;
+    }
+  }
+};
+
 template <int E>
 struct CompactRow {
   static constexpr int W = E == kElemF32 ? 4 : 8;
@@ -231,7 +276,7 @@ constexpr int kCompactRopeThreads = 256;
 template <int E, bool INTER>
 __global__ void __launch_bounds__(kCompactRopeThreads, E == kElemF32 ? 2 : 3) compact_rope_kernel(CompactParams P, CompactTurn R) {
   constexpr int W = CompactRow<E>::W, T = kCompactRopeThreads;
-  using Pairs = RopePairs<INTER, W>;
+  using Units = CompactUnits<INTER, W>;
   const int tid = threadIdx.x;
   const int group = (int)blockIdx.x / R.cluster, rank = (int)blockIdx.x - group * R.cluster;
   const int row = group / R.slices, slice = group - row * R.slices;
@@ -250,7 +295,7 @@ __global__ void __launch_bounds__(kCompactRopeThreads, E == kElemF32 ? 2 : 3) co
   const int batch = per * R.cluster, r = rank * per + tid / lanes;
   const bool mine = tid / lanes < per, first = u == 0;
   int at[16 / W];
-  rope_unit_words<INTER, W>(u, R.units * 16, R.rot, at);
+  Units::words(u, R.units * 16, R.rot, at);
   const int64_t row_bytes = (int64_t)P.row_vecs * 16, stride = P.h_kv * row_bytes;
   char* k = static_cast<char*>(P.pool[0]) + g * row_bytes;
   char* v = static_cast<char*>(P.pool[1]) + g * row_bytes;
@@ -310,14 +355,14 @@ __global__ void __launch_bounds__(kCompactRopeThreads, E == kElemF32 ? 2 : 3) co
     pages(j + 2 * batch, s2, from2, to2);
     const int s3 = entry(j + 3 * batch);
     bool bad = false;
-    if (E == kElemInt8 || (to >= 0 && Pairs::turn(at, 0, u, R.rot))) {
+    if (E == kElemInt8 || (to >= 0 && Units::turn(at, 0, u, R.rot))) {
       float z[16];
       x.k.values(z);
       if constexpr (E == kElemInt8) {
 #pragma unroll
         for (int e = 0; e < 16; ++e) z[e] *= x.k_scale;
       }
-      if (to >= 0) rope_unit_turn_back<INTER, W>(z, at, u, R.rot, R.freqs, (uint32_t)(s - j));
+      if (to >= 0) Units::turn_back(z, at, u, R.rot, R.freqs, (uint32_t)(s - j));
       if constexpr (E == kElemInt8) {
         float m = to >= 0 ? rope_unit_max(z, bad) : 0.f;
         for (int o = lanes >> 1; o > 0; o >>= 1)

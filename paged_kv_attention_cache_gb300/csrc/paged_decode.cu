@@ -108,7 +108,7 @@ static tl_status decode_write_rope(
                {v_cache, pool}};
   for (const auto& s : spans)
     if (workspace && overlap(workspace, queries, s.p, s.bytes)) return TL_ERR_INVALID_ARG;
-  step.units = rope_in_units(step.rows, elem) ? d / 16 : 0;
+  step.units = rope_unit_width(step.rows, elem) == 16 / elem ? d / 16 : 0;
   // (q_out stands for q: 256-byte aligned, where q need not be)
   return decode_impl<false>(workspace ? q_out : k_cache, k_cache, v_cache, block_table,
                             max_pages_per_seq, context_lens, out, B, 1, h_q, h_kv, d, num_pages,

@@ -34,7 +34,7 @@ __global__ void __launch_bounds__(256) rope_rows_kernel(RopeRows R, int heads) {
 // against 20 with two).  Small CTAs give their registers back as soon as their
 // own rows are written (512 threads: 51 and 69 us).
 constexpr int kRopeThreads = 64;
-template <bool F32, int KIND, bool INTER, int P>
+template <bool F32, int KIND, bool INTER, int P, int W>
 __global__ void __launch_bounds__(kRopeThreads, 768 / kRopeThreads)
     rope_units_kernel(RopeRows R, int heads, int U, int HW, uint32_t per_token, uint32_t items) {
   constexpr int warps = kRopeThreads / 32;
@@ -43,20 +43,21 @@ __global__ void __launch_bounds__(kRopeThreads, 768 / kRopeThreads)
   const uint32_t i = blockIdx.x * warps + warp;
   if (i >= items) return;
   const uint32_t t = i / per_token;
-  rope_units<F32, KIND, INTER, P>(R, t, (int)(i - t * per_token) * P * HW, heads, U, HW, lane,
+  rope_units<F32, KIND, INTER, P, W>(R, t, (int)(i - t * per_token) * P * HW, heads, U, HW, lane,
                                   cs[warp]);
 }
 
-// The most passes: as many as keep a kernel in its 80 registers.
-template <bool F32, int KIND>
-constexpr int kRopePasses = (KIND == kRopeSame ? 4 : 2) / (F32 ? 2 : 1);
+// The most passes: as many as keep a kernel in its 80 registers (W: see
+// rope_unit_width; words of 2 elements take more addresses).
+template <bool F32, int KIND, int W>
+constexpr int kRopePasses = (KIND == kRopeSame && W > 2 ? 4 : 2) / (F32 ? 2 : 1);
 
-template <bool F32, int KIND>
+template <bool F32, int KIND, int W>
 static tl_status launch_units(const RopeRows& R, int heads, cudaStream_t st) {
   const int U = R.d / 16, HW = 32 / U, passes = (heads + HW - 1) / HW;
   // fewer where a token has fewer, and while warps are few: 64 tokens of a
   // decode step take 2.5 us with one pass, 2.7 with two and 3.4 with four
-  int P = kRopePasses<F32, KIND>;
+  int P = kRopePasses<F32, KIND, W>;
   while (P > 1 && (P > passes || (int64_t)R.n * ((passes + P - 1) / P) < 16 * (int64_t)num_sms()))
     P /= 2;
   const uint32_t per_token = (passes + P - 1) / P, items = R.n * per_token;
@@ -65,24 +66,27 @@ static tl_status launch_units(const RopeRows& R, int heads, cudaStream_t st) {
     kern<<<grid, kRopeThreads, 0, st>>>(R, heads, U, HW, per_token, items);
     return launch_status();
   };
-  if constexpr (kRopePasses<F32, KIND> >= 4)
+  if constexpr (kRopePasses<F32, KIND, W> >= 4)
     if (P == 4)
-      return R.interleaved ? launch(rope_units_kernel<F32, KIND, true, 4>)
-                           : launch(rope_units_kernel<F32, KIND, false, 4>);
-  if constexpr (kRopePasses<F32, KIND> >= 2)
+      return R.interleaved ? launch(rope_units_kernel<F32, KIND, true, 4, W>)
+                           : launch(rope_units_kernel<F32, KIND, false, 4, W>);
+  if constexpr (kRopePasses<F32, KIND, W> >= 2)
     if (P == 2)
-      return R.interleaved ? launch(rope_units_kernel<F32, KIND, true, 2>)
-                           : launch(rope_units_kernel<F32, KIND, false, 2>);
-  return R.interleaved ? launch(rope_units_kernel<F32, KIND, true, 1>)
-                       : launch(rope_units_kernel<F32, KIND, false, 1>);
+      return R.interleaved ? launch(rope_units_kernel<F32, KIND, true, 2, W>)
+                           : launch(rope_units_kernel<F32, KIND, false, 2, W>);
+  return R.interleaved ? launch(rope_units_kernel<F32, KIND, true, 1, W>)
+                       : launch(rope_units_kernel<F32, KIND, false, 1, W>);
 }
 
 template <bool F32, int KIND>
 static tl_status launch_rows(const RopeRows& R, cudaStream_t st) {
   const int heads = R.h_q + (R.slots ? 2 * R.h_kv : 0);
   // (items of a pass are counted in 32 bits)
-  if (rope_in_units(R, F32 ? 4 : 2) && (int64_t)R.n * heads < ((int64_t)1 << 31))
-    return launch_units<F32, KIND>(R, heads, st);
+  if ((int64_t)R.n * heads < ((int64_t)1 << 31)) {
+    const int W = rope_unit_width(R, F32 ? 4 : 2);
+    if (W > 2) return launch_units<F32, KIND, F32 ? 4 : 8>(R, heads, st);
+    if (W == 2) return launch_units<F32, KIND, 2>(R, heads, st);
+  }
   // a warp a row, element by element
   const int64_t rows = (int64_t)R.n * heads;
   const unsigned blocks = (unsigned)std::min<int64_t>((rows + 7) / 8, (int64_t)num_sms() * 64);

@@ -92,40 +92,49 @@ TL_DEVINLINE void rope_rotate(float& lo, float& hi, float c, float s) {
 
 // ----------------------------------------------------------------- units --
 //
-// A row whose d and rot are multiples of 16 is moved in units of 16 elements
-// with 8 whole pairs, one a lane: 16 / W words of W elements (16 bytes of 16 or
-// 32 bits), each beside the next unit's, so that a warp's access to one word
-// of its units is contiguous.  In the layout of halves, for unit u < rot/16,
-// words of the lower half (at W u, and for W = 4 at rot/4 + W u) and their
-// partners rot/2 further; otherwise word w at w d W / 16 + W u.  Units behind
-// the rotated part of the halves lie in it as the latter do in the whole row.
+// A row of U = d / 16 units (d a multiple of 16) is moved a unit a lane: 16
+// elements with 8 whole pairs, in 16 / W words of W elements, word i of a unit
+// beside word i of the next, so that a warp's access to one word of its units
+// is contiguous.  Interleaved pairs: word i of unit u is the row's word i U + u.
+// Halves: words go in twos, the p-th (p = i U + u, i < 8 / W) at W p in the lower
+// half with its partner rot/2 further, and from p = rot / 2W on one behind the
+// other behind the rotated part.  So rot is a multiple of W (interleaved) or 2W.
 constexpr int kRopeMaxUnits = 16;  // of a row moved in units (d up to 256)
 enum RopeElem { kElemBf16, kElemF32, kElemE4m3, kElemInt8 };
 
+// The words' first elements (halves: the lower words, then their partners).
 template <bool INTER, int W>
 TL_DEVINLINE void rope_unit_words(int u, int d, int rot, int* at) {
   constexpr int NW = 16 / W;
-  if (!INTER && 16 * u < rot) {
+  const int U = d >> 4;
+  if (INTER) {
 #pragma unroll
-    for (int w = 0; w < NW; ++w)
-      at[w] = W * u + (w % (NW / 2)) * (rot >> 2) + (w >= NW / 2 ? rot >> 1 : 0);
+    for (int i = 0; i < NW; ++i) at[i] = (i * U + u) * W;
   } else {
-    const int from = INTER ? 0 : rot;
 #pragma unroll
-    for (int w = 0; w < NW; ++w) at[w] = from + w * ((d - from) / NW) + W * (u - (from >> 4));
+    for (int i = 0; i < NW / 2; ++i) {
+      const int e = (i * U + u) * W;
+      const bool turned = 2 * e < rot;
+      at[i] = turned ? e : 2 * e;  // behind: rot + 2 (e - rot/2)
+      at[i + NW / 2] = turned ? e + (rot >> 1) : 2 * e + W;
+    }
   }
 }
 
-// The 8 pairs of a unit are n consecutive ones per word (of the lower half).
+// The 8 pairs of a unit: n consecutive ones a word (halves: a word of the lower half).
 template <bool INTER, int W>
 struct RopePairs {
   static constexpr int n = INTER ? W / 2 : W;
-  // of the pairs from the k-th on: whether they turn, and the first one's index
-  static TL_DEVINLINE bool turn(const int* at, int k, int u, int rot) {
-    return INTER ? at[k / n] < rot : 16 * u < rot;
+  // whether pair k turns (the words of a unit turn up to some, in order)
+  static TL_DEVINLINE bool turn(const int* at, int k, int rot) {
+    return at[k / n] < (INTER ? rot : rot >> 1);
   }
   static TL_DEVINLINE int index(const int* at, int k) {
     return (INTER ? at[k / n] >> 1 : at[k / n]) + k % n;
+  }
+  // whether word i is one of those
+  static TL_DEVINLINE bool word(const int* at, int i, int rot) {
+    return INTER ? at[i] < rot : at[i % (8 / W)] < rot >> 1;
   }
 };
 
@@ -135,7 +144,10 @@ struct RopeUnit {
   static constexpr int kBytes = E == kElemF32 ? 4 : E == kElemBf16 ? 2 : 1;  // of an element
   static constexpr int NW = 16 / W;
   using Word = typename std::conditional<
-      W * kBytes == 16, uint4, typename std::conditional<W * kBytes == 8, uint2, uint32_t>::type>::type;
+      W * kBytes == 16, uint4,
+      typename std::conditional<
+          W * kBytes == 8, uint2,
+          typename std::conditional<W * kBytes == 4, uint32_t, uint16_t>::type>::type>::type;
   Word w[NW];
   TL_DEVINLINE void load(const char* row, const int* at) {
 #pragma unroll
@@ -266,15 +278,15 @@ TL_DEVINLINE float rope_unit_max(const float* x, bool& bad) {
   return m;
 }
 
-// A unit's values with its pairs turned by turn(k), k of them where `turns(k)`.
-template <bool INTER, int W, class Turns, class Turn>
-TL_DEVINLINE void rope_unit_rotate(float* x, Turns turns, Turn turn) {
-  constexpr int n = RopePairs<INTER, W>::n;
+// A unit's values with its pairs turned by turn(k).
+template <bool INTER, int W, class Turn>
+TL_DEVINLINE void rope_unit_rotate(float* x, const int* at, int rot, Turn turn) {
+  using Pairs = RopePairs<INTER, W>;
 #pragma unroll
-  for (int g = 0; g < 8; g += n)
-    if (turns(g)) {
+  for (int g = 0; g < 8; g += Pairs::n)
+    if (Pairs::turn(at, g, rot)) {
 #pragma unroll
-      for (int k = g; k < g + n; ++k) {
+      for (int k = g; k < g + Pairs::n; ++k) {
         const float2 cs = turn(k);
         if (INTER) rope_rotate(x[2 * k], x[2 * k + 1], cs.x, cs.y);
         else rope_rotate(x[k], x[8 + k], cs.x, cs.y);
@@ -282,27 +294,14 @@ TL_DEVINLINE void rope_unit_rotate(float* x, Turns turns, Turn turn) {
     }
 }
 
-// A unit's values turned back by n positions (two pairs at once).
-template <bool INTER, int W>
-TL_DEVINLINE void rope_unit_turn_back(float* x, const int* at, int u, int rot,
-                                      const uint64_t* freqs, uint32_t n) {
-  using Pairs = RopePairs<INTER, W>;
-  uint64_t f[8];
+// A unit's turned values in its words; words that do not turn keep their bits.
+template <bool INTER, int W, class Unit>
+TL_DEVINLINE void rope_unit_set(Unit& unit, const float* x, const int* at, int rot) {
+  const Unit was = unit;
+  unit.set(x);
 #pragma unroll
-  for (int k = 0; k < 8; ++k)
-    f[k] = Pairs::turn(at, k, u, rot) ? __ldg(freqs + Pairs::index(at, k)) : 0;
-#pragma unroll
-  for (int k = 0; k < 8; k += 2) {
-    if (!Pairs::turn(at, k, u, rot)) continue;
-    float2 a, b;
-    rope_turns(f[k], f[k + 1], n, a, b);
-    float &la = INTER ? x[2 * k] : x[k], &ha = INTER ? x[2 * k + 1] : x[8 + k];
-    float &lb = INTER ? x[2 * k + 2] : x[k + 1], &hb = INTER ? x[2 * k + 3] : x[9 + k];
-    const uint64_t lo = f2_pack(la, lb), hi = f2_pack(ha, hb), c = f2_pack(a.x, b.x);
-    const float2 l = f2_unpack(f2_fma(lo, c, f2_mul(hi, f2_pack(a.y, b.y))));
-    const float2 h = f2_unpack(f2_fma(hi, c, f2_mul(lo, f2_pack(-a.y, -b.y))));
-    la = l.x, lb = l.y, ha = h.x, hb = h.y;
-  }
+  for (int i = 0; i < Unit::NW; ++i)
+    if (!RopePairs<INTER, W>::word(at, i, rot)) unit.w[i] = was.w[i];
 }
 
 // The rows of one call: h_q query heads, then h_kv key heads, then h_kv value
@@ -355,10 +354,9 @@ TL_DEVINLINE int64_t rope_slot(const RopeRows& R, int64_t t, int pos, bool tell)
 // HW = 32 / U heads a pass.  Every load comes before the angles, which the
 // warp's lanes make once for the token and every head reads (cs: 8 U float2 of
 // shared memory of the warp; two pairs, 16 bytes, of each lane side by side).
-template <bool F32, int KIND, bool INTER, int P>
+template <bool F32, int KIND, bool INTER, int P, int W = F32 ? 4 : 8>
 TL_DEVINLINE void rope_units(const RopeRows& R, int64_t t, int h0, int heads, int U, int HW,
                              int lane, float4* cs) {
-  constexpr int W = F32 ? 4 : 8;
   using Src = RopeUnit<F32 ? kElemF32 : kElemBf16, W>;
   using Pairs = RopePairs<INTER, W>;
   const int sub = lane / U, u = lane - sub * U, turned = R.h_q + R.h_kv;
@@ -382,28 +380,41 @@ TL_DEVINLINE void rope_units(const RopeRows& R, int64_t t, int h0, int heads, in
   }
   float2 turn[8];
   if (pos >= 0 && h0 < turned) {
-    // chunk c of two pairs at (c % per) * (rot/4 / per) + c / per, for the `per`
-    // chunks that a lane reads one behind the other
-    constexpr int per = Pairs::n / 2;
-    const int step = (R.rot >> 2) / per;
-    for (int c = lane; c < R.rot >> 2; c += 32) {
-      float2 y, z;
-      rope_turns(__ldg(R.freqs + 2 * c), __ldg(R.freqs + 2 * c + 1), (uint32_t)pos, y, z);
-      cs[c % per * step + c / per] =
-          make_float4(y.x * R.scale, y.y * R.scale, z.x * R.scale, z.y * R.scale);
-    }
-    __syncwarp();
+    if constexpr (Pairs::n > 1) {
+      // chunk c of two pairs at (c % per) * (rot/4 / per) + c / per, for the `per`
+      // chunks that a lane reads one behind the other
+      constexpr int per = Pairs::n / 2;
+      const int step = (R.rot >> 2) / per;
+      for (int c = lane; c < R.rot >> 2; c += 32) {
+        float2 y, z;
+        rope_turns(__ldg(R.freqs + 2 * c), __ldg(R.freqs + 2 * c + 1), (uint32_t)pos, y, z);
+        cs[c % per * step + c / per] =
+            make_float4(y.x * R.scale, y.y * R.scale, z.x * R.scale, z.y * R.scale);
+      }
+      __syncwarp();
 #pragma unroll
-    for (int k = 0; k < 8; k += 2) {
-      if (!Pairs::turn(at, k, u, R.rot)) continue;
-      const int c = Pairs::index(at, k) >> 1;
-      const float4 f = cs[c % per * step + c / per];
-      turn[k] = make_float2(f.x, f.y);
-      turn[k + 1] = make_float2(f.z, f.w);
+      for (int k = 0; k < 8; k += 2) {
+        if (!Pairs::turn(at, k, R.rot)) continue;
+        const int c = Pairs::index(at, k) >> 1;
+        const float4 f = cs[c % per * step + c / per];
+        turn[k] = make_float2(f.x, f.y);
+        turn[k + 1] = make_float2(f.z, f.w);
+      }
+    } else {
+      float2* one = reinterpret_cast<float2*>(cs);
+      for (int c = lane; c < R.rot >> 1; c += 32) {
+        const uint64_t f = __ldg(R.freqs + c);
+        float2 y, same;
+        rope_turns(f, f, (uint32_t)pos, y, same);
+        one[c] = make_float2(y.x * R.scale, y.y * R.scale);
+      }
+      __syncwarp();
+#pragma unroll
+      for (int k = 0; k < 8; ++k)
+        if (Pairs::turn(at, k, R.rot)) turn[k] = one[Pairs::index(at, k)];
     }
     __syncwarp();  // (cs is the warp's next item's too)
   }
-  auto turns = [&](int k) { return Pairs::turn(at, k, u, R.rot); };
   auto of = [&](int k) { return turn[k]; };
 #pragma unroll
   for (int p = 0; p < P; ++p) {
@@ -414,17 +425,10 @@ TL_DEVINLINE void rope_units(const RopeRows& R, int64_t t, int h0, int heads, in
     float y[16];
     if (KIND == kRopeSame || is_q) {
       if (here) {
-        // (units behind the rotated part keep their bits)
-        if (rotates && (INTER || turns(0))) {
+        if (rotates && Pairs::turn(at, 0, R.rot)) {
           x[p].values(y);
-          rope_unit_rotate<INTER, W>(y, turns, of);
-          const Src was = x[p];
-          x[p].set(y);
-          if (INTER) {
-#pragma unroll
-            for (int w = 0; w < Src::NW; ++w)
-              if (at[w] >= R.rot) x[p].w[w] = was.w[w];
-          }
+          rope_unit_rotate<INTER, W>(y, at, R.rot, of);
+          rope_unit_set<INTER, W>(x[p], y, at, R.rot);
         }
         char* row =
             is_q ? static_cast<char*>(R.q_out) + Src::kBytes * (t * R.out_stride + (int64_t)h * R.d)
@@ -440,7 +444,7 @@ TL_DEVINLINE void rope_units(const RopeRows& R, int64_t t, int h0, int heads, in
       const int g = is_v ? h - turned : h - R.h_q;
       if (row) {
         x[p].values(y);
-        if (rotates) rope_unit_rotate<INTER, W>(y, turns, of);
+        if (rotates) rope_unit_rotate<INTER, W>(y, at, R.rot, of);
       }
       RopeUnit<KIND == kRopeInt8 ? kElemInt8 : kElemE4m3, W> codes;
       if constexpr (KIND == kRopeE4m3) {

@@ -27,12 +27,19 @@ inline bool aligned_to(const void* p, int bytes) {
   return (reinterpret_cast<uintptr_t>(p) & (uintptr_t)(bytes - 1)) == 0;
 }
 
-// Whether a call's rows are made of whole rotary units at 16-byte boundaries.
-inline bool rope_in_units(const RopeRows& R, int elem) {
-  auto row = [&](const void* p, int64_t stride) { return aligned16(p) && stride * elem % 16 == 0; };
-  return R.d % 16 == 0 && R.d <= 16 * kRopeMaxUnits && R.rot % 16 == 0 &&
-         row(R.q, R.q_stride) && row(R.q_out, R.out_stride) && row(R.k, R.k_stride) &&
-         row(R.v, R.v_stride);
+// The width W of the rotary units' words in which a call's rows can be moved: 16
+// bytes' elements, or 2; 0: neither (element by element).
+inline int rope_unit_width(const RopeRows& R, int elem) {
+  if (R.d % 16 || R.d > 16 * kRopeMaxUnits) return 0;
+  for (const int W : {16 / elem, 2}) {
+    auto row = [&](const void* p, int64_t stride) {
+      return aligned_to(p, W * elem) && stride % W == 0;
+    };
+    if (R.rot % (R.interleaved ? W : 2 * W) == 0 && row(R.q, R.q_stride) &&
+        row(R.q_out, R.out_stride) && row(R.k, R.k_stride) && row(R.v, R.v_stride))
+      return W;
+  }
+  return 0;
 }
 
 // n > 0 rows of `row` elements read at x and written at out.
