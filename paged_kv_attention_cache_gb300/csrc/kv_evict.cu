@@ -208,11 +208,14 @@ __global__ void __launch_bounds__(T) compact_kernel(CompactParams P) {
 // Bound: HBM where rows are many, 2 x (K and V row) per moved row: 64 bf16
 // sequences of 512-8,192 keys cut to 2,048 take 151 us (858 MB, 5.7 TB/s; the
 // move alone 151), against 250 with K and V moved by CTAs of their own (the
-// index work twice, CTAs of K four times as long as those of V) and 196 where
-// pages were looked up in the batch that reads them.  One sequence of 32,768
-// cut to 8,192: 26 us; 24 sequences of up to 8,192 e4m3
-// keys cut to 1,500: 31 us.  There a batch's latency (some 2.5
-// us of loads, turns and the cluster's barrier) counts, times their number.
+// index work twice, CTAs of K four times as long as those of V) and 169 where
+// pages were looked up in the batch that reads them.  f32 rows 304 us (1.7 GB,
+// 5.6 TB/s).  One-byte rows are bound by instructions, 420 a warp and unit: e4m3
+// 134 us (431 MB), int8 233 (a scale, 16 quotients and their checks more; two
+// units a thread spilled or left two CTAs an SM: 135-157 and 240-253 us).
+// One sequence of 32,768 cut to 8,192 takes 26 us, 24 of up to 8,192 e4m3 keys
+// cut to 1,500 31 us: a batch's latency (some 2.5 us of loads, turns and the
+// cluster's barrier) times their number.
 struct CompactTurn {
   const uint64_t* freqs;
   int32_t rot, interleaved;

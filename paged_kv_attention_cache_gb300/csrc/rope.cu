@@ -28,7 +28,11 @@ __global__ void __launch_bounds__(256) rope_rows_kernel(RopeRows R, int heads) {
 //   one pass of 4 heads a warp, 256 threads            59        89
 //   two passes                                         46        63
 //   four, streaming accesses, 80 registers             43        56
-//   four, CTAs of two warps                            42.4      55.3 (6.68 TB/s)
+//   four, CTAs of two warps                            41.5      54.8 (6.7 TB/s)
+// (f32, two passes: 78.4 and 107 us, 6.9 TB/s; e4m3 and int8 pools, two passes:
+// 61 and 74 us for the append, instruction issue beside the bytes, the int8
+// rows' quotients above all; rot 120 of 128, in words of two elements: 51 and
+// 70 us, element by element 135 and 179.)
 // Passes amortise a token's angles and keep more loads in flight; beyond the
 // registers of three 256-thread CTAs an SM they spill (four f32 passes 34 us
 // against 20 with two).  Small CTAs give their registers back as soon as their
