@@ -148,7 +148,7 @@ struct RopeUnit {
       typename std::conditional<
           W * kBytes == 8, uint2,
           typename std::conditional<W * kBytes == 4, uint32_t, uint16_t>::type>::type>::type;
-  Word w[NW];
+  alignas(16) Word w[NW];  // (read as 32-bit words too)
   TL_DEVINLINE void load(const char* row, const int* at) {
 #pragma unroll
     for (int i = 0; i < NW; ++i) w[i] = __ldcs(reinterpret_cast<const Word*>(row + at[i] * kBytes));
