@@ -91,6 +91,22 @@ def test_same_as_the_two_calls(kind, group, hkv, d, ps, rot, inter, window, lens
             assert torch.all(got[b] == 0)
 
 
+@pytest.mark.parametrize("kind", ["bf16", "f32", "int8"])
+def test_a_large_batch(kind):
+    """More sequences than a block of the plan has threads."""
+    lens = [1 + 13 * b % 70 for b in range(1100)]
+    tbl, P, slots, rows, pos = case(kind, lens, 2, 2, 128, 16, seed=1)
+    freqs, _ = table(128)
+    one, two = Pools(kind, P, 16, 2, 128, 3), Pools(kind, P, 16, 2, 128, 3)
+    e1, e2 = word(), word()
+    q = one.append(*rows, slots, pos, freqs, err=e1)
+    want = decode(one, q, tbl, i32(lens), 0.1, 0, 0, e1)
+    got = step(two, rows, slots, pos, freqs, tbl, i32(lens), 0.1, 0, 0, False, 1.0, e2)
+    assert int(e1.item()) == int(e2.item()) == 0 and torch.equal(got, want)
+    for n, x in one.t.items():
+        assert torch.equal(ref.bits(x), ref.bits(two.t[n])), n
+
+
 @pytest.mark.parametrize("kind", ["bf16", "f32", "e4m3"])
 def test_rings(kind):
     ps, ring, window = 16, 4, 50
