@@ -33,6 +33,7 @@ TL_F32, TL_BF16, TL_FP8_E4M3, TL_INT8 = 0, 1, 2, 3
 TL_DEVERR_SLOT_RANGE, TL_DEVERR_PAGE_RANGE, TL_DEVERR_CONTEXT_RANGE = 1, 2, 4
 TL_DEVERR_TIMEOUT, TL_DEVERR_VALUE_RANGE, TL_DEVERR_PLAN_CAPACITY = 8, 16, 32
 
+_Tensor = torch.Tensor
 _DTYPES = {torch.float32: TL_F32, torch.bfloat16: TL_BF16, torch.float8_e4m3fn: TL_FP8_E4M3}
 
 
@@ -70,13 +71,18 @@ def _stream(stream) -> Optional[int]:
 def _need(t: torch.Tensor, name: str, dtype=None, shape=None, device=None):
     """A contiguous CUDA tensor of the given dtype and shape (None entries of
     `shape` match any size) on `device`."""
+    # (what all of them are in a call that is right: one pass without a message;
+    # a CPU device has no index, a CPU tensor the device -1)
+    if isinstance(t, _Tensor) and device is not None and t.get_device() == device.index and \
+            t.dtype == dtype and t.shape == shape and t.is_contiguous():
+        return
     if not isinstance(t, torch.Tensor) or not t.is_cuda:
         raise TypeError(f"{name} must be a CUDA tensor")
     if not t.is_contiguous():
         raise ValueError(f"{name} must be contiguous")
     if dtype is not None and t.dtype != dtype:
         raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
-    if shape is not None and t.shape != shape:
+    if shape is not None:
         ts = t.shape
         bad = len(ts) != len(shape)
         if not bad:
@@ -119,9 +125,12 @@ def _need_table(block_table, lens, B, device, lens_name="context_lens"):
 
 def _need_pools(k_cache, v_cache, device, dtype=None):
     """k_cache / v_cache [num_pages, page_size, H_kv, d] of one dtype and shape."""
-    _need(k_cache, "k_cache", dtype, (None, None, None, None), device)
-    _need(v_cache, "v_cache", k_cache.dtype, tuple(k_cache.shape), device)
-    return k_cache.shape
+    shape = k_cache.shape
+    if len(shape) != 4:
+        shape = (None, None, None, None)
+    _need(k_cache, "k_cache", k_cache.dtype if dtype is None else dtype, shape, device)
+    _need(v_cache, "v_cache", k_cache.dtype, shape, device)
+    return shape
 
 
 def _need_new_rows(k_new, v_new, slot_mapping, hkv, d, device, dtype=None):
@@ -984,6 +993,12 @@ def tl_rope_freqs(rot_dim: int, base: float = 10000.0, scaling: int = TL_ROPE_PL
 def _need_rows(t, name, n, heads, d, device, dtype=None):
     """A CUDA tensor [n, heads, d] (None: any) whose tokens' rows are contiguous,
     the tokens at any stride; returns the stride."""
+    if isinstance(t, _Tensor) and t.get_device() == device.index and \
+            (dtype is None or t.dtype == dtype):
+        ts, s = t.shape, t.stride()
+        if len(ts) == 3 and s[2] == 1 and s[1] == ts[2] and (d is None or ts[2] == d) and \
+                (heads is None or ts[1] == heads) and (n is None or ts[0] == n):
+            return s[0]
     if not isinstance(t, torch.Tensor) or not t.is_cuda:
         raise TypeError(f"{name} must be a CUDA tensor")
     if dtype is not None and t.dtype != dtype:
@@ -1003,8 +1018,9 @@ def _need_rows(t, name, n, heads, d, device, dtype=None):
 
 def _need_table_of_turns(freqs, d, device):
     """freqs [rot_dim / 2] int64; returns rot_dim."""
-    _need(freqs, "freqs", torch.int64, (None,), device)
-    n = freqs.shape[0]
+    shape = freqs.shape
+    _need(freqs, "freqs", torch.int64, shape if len(shape) == 1 else (None,), device)
+    n = shape[0]
     if not 1 <= n <= d // 2:
         raise ValueError(f"freqs must have 1 to d / 2 = {d // 2} entries, got {n}")
     return 2 * n
