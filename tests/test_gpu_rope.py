@@ -836,3 +836,33 @@ def test_appends_on_two_streams_at_once():
         k[i::2], v[i::2] = rows[:, hq:hq + hkv].cpu(), rows[:, hq + hkv:].cpu()
         pos[i::2] = p.cpu().numpy()
     pools.check(k, v, np.arange(2 * n), pos, f, False, 1.0, "two streams")
+
+
+def test_compact_far_pages():
+    """Element offsets past 2^31 and 2^32: a sequence on the last pages of a long pool."""
+    P, ps, hkv, d = 140_000, 32, 8, 128  # 4.6 x 10^9 elements
+    pages = [139_999, 66_000, 5, 131_072]
+    n = 100
+    small = ref.randn((len(pages), ps, hkv, d), torch.float8_e4m3fn, 1)
+    pools = [torch.zeros((P, ps, hkv, d), dtype=torch.float8_e4m3fn, device="cuda")
+             for _ in range(2)]
+    at = torch.tensor(pages).cuda()
+    for x in pools:
+        x.view(torch.uint8)[at] = small.view(torch.uint8).cuda()
+    keep = np.tile(np.arange(0, n, 2, dtype=np.int32), (1, hkv, 1))
+    freqs, f = table(128)
+    w = word()
+    tl.tl_kv_cache_compact_rope(*pools, i32([pages]), i32([n]), i32(keep), i32([n // 2]), freqs,
+                                error_word=w)
+    assert int(w.item()) == 0
+    rows = ref.as_values(small).reshape(-1, hkv, d)
+    j = np.arange(1, n // 2)
+    got = [x.view(torch.uint8)[at].cpu().view(torch.float8_e4m3fn).reshape(-1, hkv, d)
+           for x in pools]
+    want, err = ref.rotate(rows[2 * j], -j[:, None], f, False)
+    ref.close(got[0][1:n // 2], want, err, "k")
+    assert np.array_equal(ref.as_values(got[1][1:n // 2]), rows[2 * j])
+    # nothing else of the long pools was written
+    for x in pools:
+        x.view(torch.uint8)[at] = 0
+        assert not bool(x.view(torch.int32).any())
