@@ -5,6 +5,7 @@
 // "H2O: Heavy-Hitter Oracle for Efficient Generative Inference of Large Language
 // Models", 2023.)
 #include <algorithm>
+#include <atomic>
 
 #include "common.cuh"
 #include "rope.cuh"
@@ -213,9 +214,10 @@ __global__ void __launch_bounds__(T) compact_kernel(CompactParams P) {
 // 5.6 TB/s).  One-byte rows are bound by instructions, 420 a warp and unit: e4m3
 // 134 us (431 MB), int8 233 (a scale, 16 quotients and their checks more; two
 // units a thread spilled or left two CTAs an SM: 135-157 and 240-253 us).
-// One sequence of 32,768 cut to 8,192 takes 26 us, 24 of up to 8,192 e4m3 keys
-// cut to 1,500 31 us: a batch's latency (some 2.5 us of loads, turns and the
-// cluster's barrier) times their number.
+// One sequence of 32,768 cut to 8,192 takes 25 us, 24 of up to 8,192 e4m3 keys
+// cut to 1,500 30 us: a batch's latency (some 2.5 us of loads, turns and the
+// cluster's barrier) times their number.  (The barrier is arrived at before the
+// next batch's loads, which its release would wait for: 2-9% less.)
 struct CompactTurn {
   const uint64_t* freqs;
   int32_t rot, interleaved;
@@ -351,6 +353,9 @@ __global__ void __launch_bounds__(kCompactRopeThreads, E == kElemF32 ? 2 : 3) co
   places(r, s, from, to);
   load(x, s, from, to);
   for (int j = r; j - r < new_len; j += batch) {
+    // this thread's row of the batch is loaded (the release is behind the load);
+    // what it loads from here on is for later batches
+    if (R.cluster > 1) asm volatile("barrier.cluster.arrive.release.aligned;\n" ::: "memory");
     // the next batch's row, the pages of the one behind it, the entry of a third
     places(j + batch, s1, from1, to1);
     load(y, s1, from1, to1);
@@ -384,12 +389,8 @@ __global__ void __launch_bounds__(kCompactRopeThreads, E == kElemF32 ? 2 : 3) co
     }
     if (E == kElemInt8 && bad) report(P.error_word, TL_DEVERR_VALUE_RANGE);
     // every thread's row of this batch is loaded before any of it is stored
-    if (R.cluster > 1) {
-      asm volatile("barrier.cluster.arrive.release.aligned;\n" ::: "memory");
-      asm volatile("barrier.cluster.wait.acquire.aligned;\n" ::: "memory");
-    } else {
-      __syncthreads();
-    }
+    if (R.cluster > 1) asm volatile("barrier.cluster.wait.acquire.aligned;\n" ::: "memory");
+    else __syncthreads();
     if (to >= 0) {
       x.k.store(k + to * stride, at);
       x.v.store(v + to * stride, at);
@@ -409,19 +410,52 @@ __global__ void __launch_bounds__(kCompactRopeThreads, E == kElemF32 ? 2 : 3) co
     for (int j = new_len + rank * T + tid; j < L; j += R.cluster * T) mass[j] = 0.f;
 }
 
+// Whether the current device holds a cluster of 16 of the int8 kernel's CTAs
+// (more than every device has to; asked once a device).
+template <bool INTER>
+static bool holds_16(cudaLaunchConfig_t cfg) {
+  static std::atomic<int> known[64];  // 0: not asked
+  int dev = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return false;
+  if (known[dev].load() == 0) {
+    auto kern = compact_rope_kernel<kElemInt8, INTER>;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeClusterDimension;
+    attr[0].val.clusterDim.x = 16;
+    attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
+    cfg.gridDim = dim3(16);
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    int n = 0;
+    const bool ok =
+        cudaFuncSetAttribute(kern, cudaFuncAttributeNonPortableClusterSizeAllowed, 1) ==
+            cudaSuccess &&
+        cudaOccupancyMaxActiveClusters(&n, kern, &cfg) == cudaSuccess && n > 0;
+    if (!ok) cudaGetLastError();
+    known[dev].store(ok ? 1 : -1);
+  }
+  return known[dev].load() > 0;
+}
+
 static cudaError_t launch_compact_rope(const CompactParams& P, CompactTurn R, int64_t rows, int d,
                                        int elem, cudaStream_t st) {
   R.units = d / 16;
   const bool i8 = P.scale[0] != nullptr;
+  cudaLaunchConfig_t cfg = {};
+  cfg.blockDim = dim3(kCompactRopeThreads);
+  cfg.stream = st;
   // Few rows are shared by clusters of up to 8 CTAs, and by slices of a row
   // (whole 32-byte sectors of words; an int8 row is one slice, for its scale),
-  // while every CTA has a place at once: three on an SM.  8 rows of 8,192 kept
-  // keys take 70 us with clusters of 8, 40 with two slices, 26 with four; 96
-  // rows of 1,500 e4m3 keys 49 us with clusters of 2, 31 with 4, and 33 with 8
-  // (two waves).
-  const int64_t ctas = (int64_t)num_sms() * 3;
-  R.cluster = R.slices = 1;
-  while (R.cluster < 8 && rows * 2 * R.cluster <= ctas) R.cluster *= 2;
+  // while every CTA has a place at once: three on an SM, f32 ones two.  8 rows of
+  // 8,192 kept keys take 70 us with clusters of 8, 40 with two slices, 25 with
+  // four (int8, one slice: 75, and 46 with the clusters of 16 that this GPU
+  // holds); 128 rows of 2,048 78 us with clusters of 2, 61 with 3; 96 rows of
+  // 1,500 e4m3 keys 49 with 2, 30 with 4, 33 with 8 (two waves).
+  const int64_t ctas = (int64_t)num_sms() * (elem == 4 ? 2 : 3);
+  const bool wide = i8 && rows * 16 <= num_sms() &&
+                    (R.interleaved ? holds_16<true>(cfg) : holds_16<false>(cfg));
+  R.cluster = (int)std::min<int64_t>(wide ? 16 : 8, std::max<int64_t>(1, ctas / rows));
+  R.slices = 1;
   const int least = elem == 1 ? 4 : 2;
   while (!i8 && R.units % (2 * R.slices) == 0 && R.units / (2 * R.slices) >= least &&
          rows * R.cluster * 2 * R.slices <= ctas)
@@ -438,10 +472,7 @@ static cudaError_t launch_compact_rope(const CompactParams& P, CompactTurn R, in
   attr[0].id = cudaLaunchAttributeClusterDimension;
   attr[0].val.clusterDim.x = R.cluster;
   attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
-  cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3((unsigned)(rows * R.slices * R.cluster));
-  cfg.blockDim = dim3(kCompactRopeThreads);
-  cfg.stream = st;
   cfg.attrs = attr;
   cfg.numAttrs = R.cluster > 1 ? 1 : 0;
   return cudaLaunchKernelEx(&cfg, kern, P, R);

@@ -866,3 +866,25 @@ def test_compact_far_pages():
     for x in pools:
         x.view(torch.uint8)[at] = 0
         assert not bool(x.view(torch.int32).any())
+
+
+@pytest.mark.parametrize("kind", ["bf16", "f32", "e4m3", "int8"])
+@pytest.mark.parametrize("B,hkv,n", [(1, 1, 700), (1, 8, 700), (1, 10, 300), (5, 3, 300), (8, 8, 200),
+                                     (16, 8, 150), (19, 8, 90), (25, 4, 90)])
+def test_compact_shared_by_clusters_of_every_size(kind, B, hkv, n):
+    """From few rows, each shared by many CTAs, to as many as there are places."""
+    lens = [n + 37 * b % 400 for b in range(B)]
+    tbl, P = lref.tables(lens, 16, seed=1)
+    pools = Pools(kind, P, 16, hkv, 128, seed=2)
+    keep, new = keep_lists(lens, hkv, n * 2 // 3, 3, seed=3)
+    freqs, f = table(64)
+    mass = torch.rand((B, hkv, 1200), generator=torch.Generator().manual_seed(1))
+    m = mass.cuda()
+    run_compact(pools, tbl, lens, keep, new, freqs, True, mass=m)
+    check_compact(pools, tbl, lens, keep, new, f, True)
+    for b in range(B):
+        for h in range(hkv):
+            want = mass[b, h].clone()
+            want[:new[b]] = mass[b, h][torch.as_tensor(keep[b, h, :new[b]]).long()]
+            want[new[b]:lens[b]] = 0
+            assert torch.equal(m[b, h].cpu(), want)
