@@ -436,9 +436,12 @@ TL_DEVINLINE void rope_units(const RopeRows& R, int64_t t, int h0, int heads, in
                        Src::kBytes * ((slot * R.h_kv + (is_v ? h - turned : h - R.h_q)) * R.d);
         x[p].store(row, at);
       }
-      // (an int8 pass with key or value rows goes on with all its lanes)
-      if (KIND != kRopeInt8 || h0 + (p + 1) * HW <= R.h_q) continue;
+      if (KIND != kRopeInt8) continue;
     }
+    // An int8 pass with key or value rows goes on with all of the warp's lanes, one of
+    // queries alone with none: lanes behind the last whole head stand at head
+    // h0 + (p + 1) HW, which may be a key's, and must not meet the shuffles alone.
+    if (KIND == kRopeInt8 && h0 + (p + 1) * HW <= R.h_q) continue;
     if constexpr (KIND != kRopeSame) {
       const bool row = here && !is_q && slot >= 0;
       const int g = is_v ? h - turned : h - R.h_q;
