@@ -125,9 +125,9 @@ def _need_table(block_table, lens, B, device, lens_name="context_lens"):
 
 def _need_pools(k_cache, v_cache, device, dtype=None):
     """k_cache / v_cache [num_pages, page_size, H_kv, d] of one dtype and shape."""
-    shape = k_cache.shape
-    if len(shape) != 4:
-        shape = (None, None, None, None)
+    shape = k_cache.shape if isinstance(k_cache, _Tensor) else ()
+    if len(shape) != 4:  # (says what is wrong)
+        _need(k_cache, "k_cache", dtype, (None, None, None, None), device)
     _need(k_cache, "k_cache", k_cache.dtype if dtype is None else dtype, shape, device)
     _need(v_cache, "v_cache", k_cache.dtype, shape, device)
     return shape
@@ -1018,7 +1018,7 @@ def _need_rows(t, name, n, heads, d, device, dtype=None):
 
 def _need_table_of_turns(freqs, d, device):
     """freqs [rot_dim / 2] int64; returns rot_dim."""
-    shape = freqs.shape
+    shape = freqs.shape if isinstance(freqs, _Tensor) else ()
     _need(freqs, "freqs", torch.int64, shape if len(shape) == 1 else (None,), device)
     n = shape[0]
     if not 1 <= n <= d // 2:
