@@ -943,11 +943,13 @@ tl_status tl_rope_freqs(int32_t rot_dim, double base, int32_t scaling, double fa
  *                 (out + t * out_stride) elements, so that a part of a fused
  *                 projection's rows is read where it lies.  out may be x (same
  *                 pointer and stride: in place); otherwise the two must have
- *                 no element in common.  Aligned to their elements.
+ *                 no element in common (of different strides, nor may the
+ *                 spans from their first to their last element).  positions
+ *                 and freqs lie outside out's span.  Aligned to their elements.
  *   dtype         TL_BF16 or TL_F32, of both
  * TL_ERR_INVALID_ARG for a negative n_tokens, sizes not positive, rot_dim odd
- * or outside 2 .. d, a negative stride, an out_stride below heads * d (with
- * more than one token), or an overlap.  n_tokens 0: nothing is done.
+ * or outside 2 .. d, an overlap, or, with more than one token, a stride negative
+ * or above 2^30 or an out_stride below heads * d.  n_tokens 0: nothing is done.
  * TL_ERR_UNSUPPORTED for another dtype, d > 4096 or heads * d >= 2^31.
  */
 tl_status tl_rope(const void* x, int64_t x_stride, void* out, int64_t out_stride,
@@ -974,7 +976,8 @@ tl_status tl_rope(const void* x, int64_t x_stride, void* out, int64_t out_stride
  *                 sets TL_DEVERR_CONTEXT_RANGE; its query is padding
  * Two tokens with one slot are a caller error.  q_out must have no element in
  * common with k_new, v_new or the pools, nor the pools (and scales) with one
- * another or with q, k_new or v_new.
+ * another or with q, k_new or v_new; slot_mapping, positions and freqs lie
+ * outside all that is written.
  * Errors as tl_rope and tl_kv_cache_write; pools 16-byte aligned, scales 4-byte
  * aligned, h_kv * d elements of a pool a multiple of 16 bytes (int8: d up to
  * 1024); num_pages * page_size < 2^31, (h_q + 2 h_kv) * d < 2^31.
@@ -1060,9 +1063,10 @@ tl_status tl_paged_attn_decode_write_rope_ring(
  * values code x scale as rounded to binary32), and a row whose values are not
  * all finite sets TL_DEVERR_VALUE_RANGE as tl_kv_cache_write_int8 does.
  * V rows, their scales and the mass move as in tl_kv_cache_compact, whose other
- * rules and errors hold; TL_ERR_INVALID_ARG for rot_dim odd or outside 2 .. d,
- * TL_ERR_UNSUPPORTED when d or rot_dim is not a multiple of 16, and for int8
- * pools when d is not a power of two up to 512.
+ * rules and errors hold; TL_ERR_INVALID_ARG for rot_dim odd or outside 2 .. d, or
+ * when a list or table lies over what moves; TL_ERR_UNSUPPORTED when d or rot_dim
+ * is not a multiple of 16, and for int8 pools when d is not a power of two up to
+ * 512.
  */
 tl_status tl_kv_cache_compact_rope(void* k_cache, void* v_cache, const int32_t* block_table,
                                    int32_t max_pages_per_seq, const int32_t* context_lens,

@@ -525,6 +525,21 @@ static tl_status compact_impl(void* k, void* v, float* k_scales, float* v_scales
       if (moved[i].bytes && moved[j].bytes &&
           overlap(moved[i].p, moved[i].bytes, moved[j].p, moved[j].bytes))
         return TL_ERR_INVALID_ARG;
+  if (turn) {
+    // the lists are read while other CTAs write
+    const size_t lens = sizeof(int32_t) * (size_t)B;
+    const struct {
+      const void* p;
+      size_t bytes;
+    } read[] = {{block_table, lens * max_pages_per_seq},
+                {context_lens, lens},
+                {keep, lens * h_kv * n_keep},
+                {new_lens, lens},
+                {turn->freqs, sizeof(uint64_t) * (size_t)(turn->rot / 2)}};
+    for (const auto& m : moved)
+      for (const auto& r : read)
+        if (m.bytes && overlap(m.p, m.bytes, r.p, r.bytes)) return TL_ERR_INVALID_ARG;
+  }
   CompactParams P;
   P.pool[0] = k;
   P.pool[1] = v;

@@ -203,6 +203,10 @@ extern "C" tl_status tl_rope(const void* x, int64_t x_stride, void* out, int64_t
   const int elem = dtype == TL_F32 ? 4 : 2;
   const tl_status ok = rope_io_checked(x, x_stride, out, out_stride, n_tokens, heads * d, elem);
   if (ok != TL_OK) return ok;
+  const int64_t row = (int64_t)heads * d;
+  if (over_rope_lists(out, (size_t)((n_tokens > 1 ? n_tokens - 1 : 0) * out_stride + row) * elem,
+                      nullptr, positions, freqs, n_tokens, rot_dim))
+    return TL_ERR_INVALID_ARG;
   RopeRows R = {};
   R.q = x;
   R.q_out = out;

@@ -56,6 +56,17 @@ inline tl_status rope_io_checked(const void* x, int64_t x_stride, const void* ou
   return TL_OK;
 }
 
+// Whether what a call of n tokens writes (bytes at p) has a byte in common with
+// the lists that its other warps read: positions, the frequencies, and slots
+// (null: none).
+inline bool over_rope_lists(const void* p, size_t bytes, const int64_t* slots,
+                            const int32_t* positions, const uint64_t* freqs, int32_t n,
+                            int32_t rot_dim) {
+  return overlap(p, bytes, positions, sizeof(int32_t) * (size_t)n) ||
+         overlap(p, bytes, freqs, sizeof(uint64_t) * (size_t)(rot_dim / 2)) ||
+         (slots && overlap(p, bytes, slots, sizeof(int64_t) * (size_t)n));
+}
+
 // The checks of an append's arguments (sizes positive, n_tokens >= 0); with
 // tokens, *R and the rows' kind.  dtype TL_INT8: codes and scales.
 inline tl_status rope_rows_checked(const void* q, int64_t q_stride, void* q_out,
@@ -121,6 +132,10 @@ inline tl_status rope_rows_checked(const void* q, int64_t q_stride, void* q_out,
       if (spans[i].bytes && spans[j].bytes &&
           overlap(spans[i].p, spans[i].bytes, spans[j].p, spans[j].bytes))
         return TL_ERR_INVALID_ARG;
+  for (int i : {0, 1, 2, 3, 7})
+    if (spans[i].bytes &&
+        over_rope_lists(spans[i].p, spans[i].bytes, slots, positions, freqs, n, rot_dim))
+      return TL_ERR_INVALID_ARG;
   *R = RopeRows();
   R->q = q;
   R->k = k_new;
