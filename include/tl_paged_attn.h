@@ -1021,8 +1021,9 @@ size_t tl_paged_attn_decode_write_rope_workspace_size(int32_t B, int32_t h_q, in
  *   dtype         TL_BF16, TL_F32 or TL_FP8_E4M3 pools (_int8: codes and scales;
  *                 _ring: the ring rule of tl_paged_attn_decode_write_ring)
  *   workspace     tl_paged_attn_decode_write_rope_workspace_size bytes, 256-byte
- *                 aligned, nowhere over the rows or the pools; calls that overlap
- *                 in time must not share one
+ *                 aligned, nowhere over the rows, the pools and their scales,
+ *                 slot_mapping, positions or freqs; calls that overlap in time
+ *                 must not share one
  * Errors as tl_kv_cache_write_rope and tl_paged_attn_decode.
  */
 tl_status tl_paged_attn_decode_write_rope(

@@ -79,10 +79,10 @@ static tl_status decode_write_rope(
   if (d > 16 * kRopeStepUnits) return TL_ERR_UNSUPPORTED;
   const tl_dtype q_dtype = dtype == TL_F32 ? TL_F32 : TL_BF16;
   const size_t queries = rope_ws_queries(B, h_q, h_kv, d);
+  const size_t need = queries + sizeof(float) * (size_t)B * h_q * d;
   // a missing, small or misaligned workspace is refused by decode_impl after
   // its other checks: it is told that it has none
-  if (workspace_bytes < queries + sizeof(float) * (size_t)B * h_q * d ||
-      (reinterpret_cast<uintptr_t>(workspace) & 255u))
+  if (workspace_bytes < need || (reinterpret_cast<uintptr_t>(workspace) & 255u))
     workspace = nullptr;
   if (!aligned_to(q, q_dtype == TL_F32 ? 4 : 2) || q_stride < 0) return TL_ERR_INVALID_ARG;
   void* q_out = workspace ? static_cast<char*>(workspace) + queries : nullptr;
@@ -105,9 +105,14 @@ static tl_status decode_write_rope(
                {k_new, (size_t)((B - 1) * k_stride + row) * elem},
                {v_new, (size_t)((B - 1) * v_stride + row) * elem},
                {k_cache, pool},
-               {v_cache, pool}};
+               {v_cache, pool},
+               {k_scales, k_scales ? pool / d * sizeof(float) : 0},
+               {v_scales, v_scales ? pool / d * sizeof(float) : 0}};
   for (const auto& s : spans)
-    if (workspace && overlap(workspace, queries, s.p, s.bytes)) return TL_ERR_INVALID_ARG;
+    if (workspace && s.bytes && overlap(workspace, need, s.p, s.bytes))
+      return TL_ERR_INVALID_ARG;
+  if (workspace && over_rope_lists(workspace, need, slot_mapping, positions, freqs, B, rot_dim))
+    return TL_ERR_INVALID_ARG;
   step.units = rope_unit_width(step.rows, elem) == 16 / elem ? d / 16 : 0;
   // (q_out stands for q: 256-byte aligned, where q need not be)
   return decode_impl<false>(workspace ? q_out : k_cache, k_cache, v_cache, block_table,

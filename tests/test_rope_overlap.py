@@ -79,3 +79,26 @@ def test_compaction(lib):
     check(a, base, lists, [("k", M, slots * 256), ("v", 2 * M, slots * 256), mass])
     check(i, base, lists, [("k", M, slots * 128), ("v", 2 * M, slots * 128),
                            ("ks", 3 * M, slots * 4), ("vs", 4 * M, slots * 4), mass])
+
+
+def test_step_workspace(lib):
+    """The plan writes the workspace beside the warps that write the rows and scales."""
+    B, hq, hkv, d = 3, 8, 2, 128
+    need = tl.tl_paged_attn_decode_write_rope_workspace_size(B, hq, hkv, d)
+    base = dict(q=M, qs=1024, k=3 * M, ks=256, v=4 * M, vs=256, sm=9 * M, pos=10 * M, f=11 * M,
+                rot=128, il=0, m=1.0, kc=5 * M, vc=6 * M, ksc=7 * M, vsc=8 * M, bt=12 * M, maxp=8,
+                cl=13 * M, out=14 * M, B=B, hq=hq, hkv=hkv, d=d, P=16, ps=16, w=0, sc=0.1,
+                dt=tl.TL_BF16, ws=64 * M, wsb=need, err=None, st=None)
+    a = caller(lib.tl_paged_attn_decode_write_rope,
+               "q qs k ks v vs sm pos f rot il m kc vc bt maxp cl out B hq hkv d P ps w sc dt ws "
+               "wsb err st", base)
+    i = caller(lib.tl_paged_attn_decode_write_rope_int8,
+               "q qs k ks v vs sm pos f rot il m kc vc ksc vsc bt maxp cl out B hq hkv d P ps w sc "
+               "ws wsb err st", base)
+    slots = 16 * 16 * hkv
+    lists = [("sm", 24, 8), ("pos", 12, 4), ("f", 512, 8), ("k", 2 * 256 * 2 + 512, 2),
+             ("q", 3 * 1024 * 2, 2)]
+    for call, size, scales in ((a, 2, []), (i, 1, [("ksc", slots * 4, 16), ("vsc", slots * 4, 16)])):
+        check(call, base, lists + scales + [("kc", slots * d * size, 16),
+                                            ("vc", slots * d * size, 16)],
+              [("ws", 64 * M, need)])
