@@ -916,8 +916,8 @@ typedef enum {
                          between them the mix of the two that is linear in t */
   TL_ROPE_RAMP = 4,   /* the same mix linear in i, from the pair that makes `high` turns (index
                          rounded down, at least 0) to the one that makes `low` (rounded up, at
-                         most rot_dim - 1); rope_scale 0.1 ln(factor) + 1 (Peng et al., "YaRN",
-                         2023) */
+                         most rot_dim - 1); rope_scale 0.1 ln(factor) + 1, and 1 for a factor
+                         up to 1 (Peng et al., "YaRN", 2023) */
   TL_ROPE_FACTORS = 5 /* f_i / factors[i] */
 } tl_rope_scaling;
 

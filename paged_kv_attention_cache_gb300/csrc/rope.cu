@@ -183,7 +183,8 @@ extern "C" tl_status tl_rope_freqs(int32_t rot_dim, double base, int32_t scaling
     const double part = std::rint((turns - std::floor(turns)) * 0x1p64);
     freqs[i] = part >= 0x1p64 ? 0 : (uint64_t)part;
   }
-  *rope_scale = scaling == TL_ROPE_RAMP ? (float)(0.1 * std::log(factor) + 1.0) : 1.f;
+  *rope_scale =
+      scaling == TL_ROPE_RAMP && factor > 1.0 ? (float)(0.1 * std::log(factor) + 1.0) : 1.f;
   return TL_OK;
 }
 
