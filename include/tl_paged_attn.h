@@ -897,10 +897,11 @@ tl_status tl_kv_cache_compact_int8(int8_t* k_codes, int8_t* v_codes, float* k_sc
  *
  * freqs: [rot_dim/2] uint64, the turns that each pair makes per position as
  * 64-bit fractions: freqs[i] = round(2^64 x f_i / 2 pi) mod 2^64.  p x freqs[i]
- * mod 2^64 is the angle as a fraction of a turn, exact for every 32-bit p (an
- * entry's own rounding moves it by at most 2^-34 turns).  A table of negated
- * entries (mod 2^64) rotates backwards: the inverse, and the gradient, of the
- * rotation.  tl_rope_freqs makes tables; a caller may make its own.
+ * mod 2^64 is the entry's angle at p as a fraction of a turn, exact for every
+ * 32-bit p; an entry that is off by e turns moves it by p x e (at most 2^-34
+ * turns where the entry is the nearest one).  A table of negated entries (mod
+ * 2^64) rotates backwards: the inverse, and the gradient, of the rotation.
+ * tl_rope_freqs makes tables; a caller may make its own.
  *
  * positions: [n] int32.  A row at a negative position is padding: it is taken
  * over as it is, neither rotated nor scaled (in place: left as it was).
@@ -924,7 +925,10 @@ typedef enum {
 /*
  * Fills the HOST arrays freqs [rot_dim/2] and *rope_scale (1 but for
  * TL_ROPE_RAMP) of a rotary table; the caller copies freqs to the device.
- * Computed in binary64, on the calling thread; nothing is launched.
+ * Computed in binary64, on the calling thread; nothing is launched.  An entry of
+ * a plain table is within 2^-53 turns of f_i / 2 pi (its angle at position p
+ * within p x 2^-53 turns: 7e-10 radians at a million, 1.5e-6 at 2^31); the other
+ * kinds add the roundings of their formulas.
  * trained_len, low and high are read by TL_ROPE_BANDS and TL_ROPE_RAMP, factor
  * by all kinds but TL_ROPE_PLAIN and TL_ROPE_FACTORS, factors [rot_dim/2] by
  * TL_ROPE_FACTORS.  TL_ERR_INVALID_ARG for rot_dim odd or outside 2 .. 4096, a
