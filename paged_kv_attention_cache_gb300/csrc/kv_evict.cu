@@ -279,7 +279,8 @@ struct CompactRow {
 
 constexpr int kCompactRopeThreads = 256;
 template <int E, bool INTER>
-__global__ void __launch_bounds__(kCompactRopeThreads, E == kElemF32 ? 2 : 3) compact_rope_kernel(CompactParams P, CompactTurn R) {
+__global__ void __launch_bounds__(kCompactRopeThreads, E == kElemF32 ? 2 : 3)
+    compact_rope_kernel(CompactParams P, CompactTurn R) {
   constexpr int W = CompactRow<E>::W, T = kCompactRopeThreads;
   using Units = CompactUnits<INTER, W>;
   const int tid = threadIdx.x;
